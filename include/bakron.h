@@ -345,6 +345,67 @@ int bakron_layer_report(int64_t m, int64_t n, const float* D_O, const float* D_I
                         const float* H_I, int64_t ldhi, const float* H_O, int64_t ldho, double* out,
                         void* stream);
 
+/*
+ * Serving a rounded layer: the codes and scales of the solve, packed once, and the
+ * products and the norm that use them. In the solve's rotated basis (bakron_rht above)
+ * a token x passes a layer as U_O^T (W' (U_I x)): bakron_rmsnorm applies U_I,
+ * bakron_matvec W', and bakron_rht (axis 1, seed_O, transpose) U_O^T to the rows of y.
+ *
+ * Element types of token rows. Rows are row-major with a leading dimension in elements.
+ */
+enum { BAKRON_F32 = 0, BAKRON_F16 = 1, BAKRON_BF16 = 2, BAKRON_I8 = 3, BAKRON_E4M3 = 4 /* OCP e4m3fn */ };
+
+/*
+ * bakron_pack: codes c_ij (m x n uint8, ldc >= n, values below 2^bits, bits 1..4) and their
+ *   scales into the layout that bakron_matvec reads: about n m / 4 bytes for bits 1 and 2,
+ *   n m / 2 for bits 3 and 4, and the scales in fp32. A larger value counts as 2^bits - 1.
+ *   group: columns that share a scale, a power of two >= 32, or 0 for one scale per row
+ *     (what bakron_solve returns). ng = ceil(n / group), or 1.
+ *   scales: [m x ng] fp32, lds >= ng; scale (i, g) is that of columns group g .. of row i.
+ *   packed: device, 16-byte aligned, bakron_packed_bytes(m, n, bits, group) bytes, all
+ *     written. It stands for w_ij = s_i,g(j) (c_ij - (2^bits - 1) / 2), the solve's grid.
+ * bakron_packed_bytes returns 0 for sizes or options that bakron_pack refuses.
+ *
+ * bakron_matvec: for T tokens (rows of X, T x n)
+ *     Y[t][i] = a_t sum_g s_ig sum_{j in g} X[t][j] (c_ij - (2^bits - 1) / 2).
+ *   m, n, bits, group: those that `packed` was made with (it holds no header).
+ *   X: BAKRON_F32, _F16, _BF16, _I8 or _E4M3, ldx >= n. xscale: [T] fp32 factors a_t, or
+ *     NULL for 1. Y: T x m, BAKRON_F32, _F16 or _BF16, ldy >= m; it must not overlap X.
+ *   The inner sums have exact products and fp32 accumulation (int32, exact, for _I8), the
+ *   outer sum is fp32, and Y is rounded once. Token t's result depends on its own row only.
+ *   For given sizes and types it is deterministic. T == 0 does nothing. Needs no workspace.
+ * Errors: INVALID_ARG for NULL pointers, m or n <= 0, T < 0, bad types, bits, group or ld,
+ *   a packed pointer that is not 16-byte aligned, overlapping Y, or more than 2^31 - 1
+ *   workgroups (ceil(m / 16) ceil(T / 16)); WORKSPACE if packed_bytes is too small.
+ */
+size_t bakron_packed_bytes(int64_t m, int64_t n, int32_t bits, int64_t group);
+int bakron_pack(const uint8_t* codes, int64_t m, int64_t n, int64_t ldc, int32_t bits, const float* scales,
+                int64_t lds, int64_t group, void* packed, size_t packed_bytes, void* stream);
+int bakron_matvec(const void* packed, size_t packed_bytes, int64_t m, int64_t n, int32_t bits, int64_t group,
+                  const void* X, int32_t xtype, int64_t T, int64_t ldx, const float* xscale, void* Y, int32_t ytype,
+                  int64_t ldy, void* stream);
+
+/*
+ * Root-mean-square norm of token rows with the residual's addition, the layer's rotation
+ * and an 8-bit output. For each row t of X (T x n):
+ *     h = x + r,  v = gain * h / sqrt(mean_j(h_j^2) + eps),  rotate: v <- U_n v.
+ *   X: BAKRON_F32, _F16 or _BF16. R: the residual, X's type, or NULL (r = 0). H: receives
+ *     h rounded to X's type, or NULL. gain: [n], type gtype = X's or BAKRON_F32, or NULL (1).
+ *   rotate != 0 applies U_n of `seed` as bakron_rht does (axis 1, no transpose); n <= 32768.
+ *   Y: T x n. ytype _F32, _F16, _BF16: v, rounded once. ytype _I8 or _E4M3: codes q and
+ *     yscale [T] (required): yscale = max_j |v_j| / 127 (448), q = v / yscale rounded to
+ *     nearest even; v is about yscale * q. A row of zeros gets scale 0 and codes 0; a row
+ *     with a v that is not finite gets scale NaN and codes 0.
+ *   The arithmetic is fp32 and uses the unrounded h. No workspace; deterministic.
+ *   H may be R or X itself, and Y may be X or R itself (same pointer, type and ld), but
+ *   no other overlap of H or Y with a buffer of the call is allowed.
+ * Errors: INVALID_ARG for NULL X or Y (T > 0), n <= 0, T < 0 or > 2^31 - 1, bad types or
+ *   ld, eps negative or not finite, missing yscale, rotation with n > 32768, or overlap.
+ */
+int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx, const void* R, int64_t ldr,
+                   void* H, int64_t ldh, const void* gain, int32_t gtype, float eps, int rotate, uint64_t seed,
+                   void* Y, int32_t ytype, int64_t ldy, float* yscale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -83,6 +83,16 @@ def _load() -> ctypes.CDLL:
     lib.bakron_solve_noalloc.restype = ctypes.c_int
     lib.bakron_solve_noalloc.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, ctypes.POINTER(_Quantizer),
                                          vp, i64, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    i32 = ctypes.c_int32
+    lib.bakron_packed_bytes.restype = sz
+    lib.bakron_packed_bytes.argtypes = [i64, i64, i32, i64]
+    lib.bakron_pack.restype = ctypes.c_int
+    lib.bakron_pack.argtypes = [vp, i64, i64, i64, i32, vp, i64, i64, vp, sz, vp]
+    lib.bakron_matvec.restype = ctypes.c_int
+    lib.bakron_matvec.argtypes = [vp, sz, i64, i64, i32, i64, vp, i32, i64, i64, vp, vp, i32, i64, vp]
+    lib.bakron_rmsnorm.restype = ctypes.c_int
+    lib.bakron_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i32, f32, ctypes.c_int,
+                                   ctypes.c_uint64, vp, i32, i64, vp, vp]
     return lib
 
 
@@ -97,7 +107,7 @@ EXPORTS = ("bakron_abi_version", "bakron_status_str", "bakron_hessian_accum_work
            "bakron_token_weights_workspace_bytes", "bakron_token_weights", "bakron_ldl_workspace_bytes", "bakron_ldl", "bakron_ldl_async",
            "bakron_ldl_pair_async",
            "bakron_solve_workspace_bytes", "bakron_solve", "bakron_solve_noalloc", "bakron_rht",
-           "bakron_layer_report")
+           "bakron_layer_report", "bakron_packed_bytes", "bakron_pack", "bakron_matvec", "bakron_rmsnorm")
 
 
 def abi_version() -> int:
@@ -549,3 +559,152 @@ def quantize_layer(W: torch.Tensor, X: torch.Tensor, G: Optional[torch.Tensor], 
         # factors of a failed factorisation; the failure is raised here
         check_ldl_pair(status)
     return res, (LO, DO, HI, DI)
+
+
+# --------------------------------------------------------------------------
+# serving a rounded layer
+ROW_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
+_WIDE = (torch.float32, torch.float16, torch.bfloat16)
+_CODED = (torch.int8, torch.float8_e4m3fn)
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
+    """Validate token rows on the current device; returns their leading dimension."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA/ROCm tensor" % name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current device" % name)
+    if t.dtype not in dtypes or t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor of %s" % (name, ", ".join(str(d) for d in dtypes)))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %d x %d" % ((name,) + tuple(shape)))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("%s must not have overlapping rows" % name)
+    return max(int(t.stride(0)), int(t.shape[1])) if t.shape[0] > 1 else max(int(t.shape[1]), 1)
+
+
+def _token_scales(t: Optional[torch.Tensor], name: str, T: int) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current device" % name)
+    return _vec(t, name, T)
+
+
+@dataclass
+class PackedWeight:
+    """A layer's codes and scales in bakron_matvec's layout (device bytes)."""
+    data: torch.Tensor
+    m: int
+    n: int
+    bits: int
+    group: int
+
+
+def pack(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -> PackedWeight:
+    """Lay out a solve's codes (m x n uint8) and scales for matvec().
+
+    group = 0: one scale per row, scales (m,) or (m, 1), as solve() returns them; else a
+    power of two >= 32, with scales (m, ceil(n / group)). bits 1..4.
+    """
+    ldc = _rows(codes, "codes", (torch.uint8,))
+    m, n = codes.shape
+    if isinstance(scales, torch.Tensor) and scales.dim() == 1 and group == 0:
+        scales = scales.reshape(-1, 1)
+    nb = LIB.bakron_packed_bytes(m, n, int(bits), int(group))
+    if nb == 0:
+        raise ValueError("pack takes m, n >= 1, bits 1..4 and group 0 or a power of two >= 32")
+    lds = _rows(scales, "scales", (torch.float32,), (m, -(-n // group) if group else 1))
+    data = torch.empty(nb, dtype=torch.uint8, device=codes.device)
+    _check("bakron_pack", LIB.bakron_pack(_ptr(codes), m, n, ldc, int(bits), _ptr(scales), lds, int(group),
+                                          _ptr(data), nb, _stream()))
+    return PackedWeight(data, int(m), int(n), int(bits), int(group))
+
+
+def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """x W^T for tokens x (T x n, or one token (n,)) and a packed layer W (m x n).
+
+    x: float32, float16, bfloat16, or int8 / float8_e4m3fn; x_scale (T,) float32 multiplies
+    each token's result. The result is T x m (or (m,)) in out_dtype (default: x's type, or
+    bfloat16 for an 8-bit x).
+    """
+    one = isinstance(x, torch.Tensor) and x.dim() == 1
+    if one:
+        x = x.unsqueeze(0)
+        out = out.unsqueeze(0) if isinstance(out, torch.Tensor) and out.dim() == 1 else out
+    ldx = _rows(x, "x", tuple(ROW_TYPES))
+    T = x.shape[0]
+    if x.shape[1] != w.n:
+        raise ValueError("x must have %d columns" % w.n)
+    if w.data.device != x.device:
+        raise ValueError("the packed layer must be on x's device")
+    xs = _token_scales(x_scale, "x_scale", T)
+    if out is None:
+        if out_dtype is None:
+            out_dtype = x.dtype if x.dtype in _WIDE else torch.bfloat16
+        if out_dtype not in _WIDE:
+            raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in _WIDE))
+        out = torch.empty((T, w.m), dtype=out_dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out must be a tensor of %s" % out_dtype)
+    ldy = _rows(out, "out", _WIDE, (T, w.m))
+    _check("bakron_matvec", LIB.bakron_matvec(_ptr(w.data), w.data.numel(), w.m, w.n, w.bits, w.group, _ptr(x),
+                                              ROW_TYPES[x.dtype], T, ldx, _ptr(xs), _ptr(out), ROW_TYPES[out.dtype],
+                                              ldy, _stream()))
+    return out[0] if one else out
+
+
+@dataclass
+class NormResult:
+    y: torch.Tensor
+    scale: Optional[torch.Tensor]     # (T,) float32 with an 8-bit y
+    sum: Optional[torch.Tensor]       # x + residual, rounded to x's type
+
+
+def rmsnorm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+            eps: float = 1e-6, rotate_seed: Optional[int] = None, out_dtype: Optional[torch.dtype] = None,
+            out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+            scale_out: Optional[torch.Tensor] = None) -> NormResult:
+    """gain * h / sqrt(mean(h^2) + eps) for the rows of h = x + residual (T x n).
+
+    rotate_seed applies the rotation that rht(..., axis=1, seed) applies to a layer's inputs.
+    out_dtype: float32, float16, bfloat16 (default: x's type), or int8 / float8_e4m3fn, which
+    come with one scale per token: the values are scale[:, None] * y. sum receives h in x's
+    type when a residual is given (sum_out=residual updates it in place).
+    """
+    ldx = _rows(x, "x", _WIDE)
+    T, n = x.shape
+    ldr = ldh = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", (x.dtype,), (T, n))
+        if sum_out is None:
+            sum_out = torch.empty((T, n), dtype=x.dtype, device=x.device)
+    if sum_out is not None:
+        ldh = _rows(sum_out, "sum_out", (x.dtype,), (T, n))
+    if gain is not None:
+        if (not isinstance(gain, torch.Tensor) or gain.device != x.device or gain.numel() != n
+                or not gain.is_contiguous() or gain.dtype not in (x.dtype, torch.float32)):
+            raise ValueError("gain must be a contiguous vector of length %d, float32 or x's type" % n)
+    if out is None:
+        out_dtype = x.dtype if out_dtype is None else out_dtype
+        if out_dtype not in ROW_TYPES:
+            raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in ROW_TYPES))
+        out = torch.empty((T, n), dtype=out_dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out must be a tensor of %s" % out_dtype)
+    ldy = _rows(out, "out", tuple(ROW_TYPES), (T, n))
+    if out.dtype in _CODED:
+        if scale_out is None:
+            scale_out = torch.empty(T, dtype=torch.float32, device=x.device)
+        _token_scales(scale_out, "scale_out", T)
+    elif scale_out is not None:
+        raise ValueError("scale_out goes with an 8-bit out")
+    _check("bakron_rmsnorm",
+           LIB.bakron_rmsnorm(_ptr(x), ROW_TYPES[x.dtype], T, n, ldx, _ptr(residual), ldr, _ptr(sum_out), ldh,
+                              _ptr(gain), ROW_TYPES[gain.dtype] if gain is not None else 0, eps,
+                              0 if rotate_seed is None else 1, int(rotate_seed or 0) & (2**64 - 1), _ptr(out),
+                              ROW_TYPES[out.dtype], ldy, _ptr(scale_out), _stream()))
+    return NormResult(out, scale_out, sum_out)

@@ -80,6 +80,51 @@ bk::SolveArgs solve_args(const float* W, int64_t m, int64_t n, int64_t ldw, cons
     return a;
 }
 
+// --- token rows (serving) ---
+size_t elem_size(int type) {
+    switch (type) {
+        case BAKRON_F32: return 4;
+        case BAKRON_F16:
+        case BAKRON_BF16: return 2;
+        case BAKRON_I8:
+        case BAKRON_E4M3: return 1;
+        default: return 0;
+    }
+}
+bool wide_type(int type) { return type == BAKRON_F32 || type == BAKRON_F16 || type == BAKRON_BF16; }
+
+// rows of `width` bytes, `pitch` bytes apart
+struct Rows {
+    const void* p;
+    int64_t rows, width, pitch;
+};
+Rows rows_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int type) {
+    const int64_t e = (int64_t)elem_size(type);
+    return {p, rows, cols * e, ld * e};
+}
+// Whether two arrays share a byte. Rows of one pitch may interleave (columns of one
+// buffer); with different pitches, ranges that cross count as overlapping.
+bool overlap(const Rows& a, const Rows& b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    const uintptr_t a1 = a0 + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
+    const uintptr_t b1 = b0 + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.pitch != b.pitch) return true;
+    const uintptr_t d = b0 >= a0 ? (b0 - a0) % (uintptr_t)a.pitch
+                                 : ((uintptr_t)a.pitch - (a0 - b0) % (uintptr_t)a.pitch) % (uintptr_t)a.pitch;
+    return d < (uintptr_t)a.width || d + (uintptr_t)b.width > (uintptr_t)a.pitch;
+}
+bool same_rows(const Rows& a, const Rows& b) { return a.p == b.p && a.pitch == b.pitch && a.width == b.width; }
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;
+
+bool bad_pack_shape(int64_t m, int64_t n, int32_t bits, int64_t group) {
+    if (m <= 0 || n <= 0 || m > kMaxDim || n > kMaxDim || bits < 1 || bits > 4) return true;
+    if (group != 0 && (group < 32 || group > kMaxDim || (group & (group - 1)) != 0)) return true;
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -237,6 +282,71 @@ int bakron_rht(float* A, int64_t rows, int64_t cols, int64_t lda, int axis, uint
         return BAKRON_E_INVALID_ARG;
     if (axis == 1 && (cols & -cols) > 16384) return BAKRON_E_INVALID_ARG;
     return bk::launch_rht(A, rows, cols, lda, axis, seed, transpose, (hipStream_t)stream);
+}
+
+size_t bakron_packed_bytes(int64_t m, int64_t n, int32_t bits, int64_t group) {
+    if (bad_pack_shape(m, n, bits, group)) return 0;
+    return bk::pack_shape(m, n, bits, group).bytes;
+}
+
+int bakron_pack(const uint8_t* codes, int64_t m, int64_t n, int64_t ldc, int32_t bits, const float* scales,
+                int64_t lds, int64_t group, void* packed, size_t packed_bytes, void* stream) {
+    if (!codes || !scales || !packed || bad_pack_shape(m, n, bits, group) || bad_ld(ldc, n))
+        return BAKRON_E_INVALID_ARG;
+    const bk::PackShape p = bk::pack_shape(m, n, bits, group);
+    if (bad_ld(lds, p.groups) || ((uintptr_t)packed & 15) != 0) return BAKRON_E_INVALID_ARG;
+    if (p.tiles * p.chunks > (int64_t)0x7fffffff || p.tiles * p.groups_padded > (int64_t)0x7fffffff)
+        return BAKRON_E_INVALID_ARG;
+    const Rows out = {packed, 1, (int64_t)p.bytes, (int64_t)p.bytes};
+    if (overlap(rows_of(codes, m, n, ldc, BAKRON_I8), out) || overlap(rows_of(scales, m, p.groups, lds, BAKRON_F32), out))
+        return BAKRON_E_INVALID_ARG;
+    if (packed_bytes < p.bytes) return BAKRON_E_WORKSPACE;
+    return bk::launch_pack(codes, m, n, ldc, bits, scales, lds, group, packed, (hipStream_t)stream);
+}
+
+int bakron_matvec(const void* packed, size_t packed_bytes, int64_t m, int64_t n, int32_t bits, int64_t group,
+                  const void* X, int32_t xtype, int64_t T, int64_t ldx, const float* xscale, void* Y, int32_t ytype,
+                  int64_t ldy, void* stream) {
+    if (!packed || ((uintptr_t)packed & 15) != 0 || bad_pack_shape(m, n, bits, group) || T < 0)
+        return BAKRON_E_INVALID_ARG;
+    if (elem_size(xtype) == 0 || !wide_type(ytype)) return BAKRON_E_INVALID_ARG;
+    if (T == 0) return BAKRON_OK;
+    if (!X || !Y || bad_ld(ldx, n) || bad_ld(ldy, m)) return BAKRON_E_INVALID_ARG;
+    if (T > 0x7fffffff || (m + 15) / 16 > 0x7fffffff / ((T + 15) / 16)) return BAKRON_E_INVALID_ARG;
+    const Rows y = rows_of(Y, T, m, ldy, ytype);
+    const Rows w = {packed, 1, (int64_t)packed_bytes, (int64_t)packed_bytes};
+    const Rows xs = {xscale, 1, 4 * T, 4 * T};
+    if (overlap(rows_of(X, T, n, ldx, xtype), y) || overlap(w, y) || overlap(xs, y)) return BAKRON_E_INVALID_ARG;
+    if (packed_bytes < bk::pack_shape(m, n, bits, group).bytes) return BAKRON_E_WORKSPACE;
+    return bk::launch_matvec(packed, m, n, bits, group, X, xtype, T, ldx, xscale, Y, ytype, ldy, (hipStream_t)stream);
+}
+
+int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx, const void* R, int64_t ldr,
+                   void* H, int64_t ldh, const void* gain, int32_t gtype, float eps, int rotate, uint64_t seed,
+                   void* Y, int32_t ytype, int64_t ldy, float* yscale, void* stream) {
+    if (n <= 0 || n > kMaxDim || T < 0 || T > 0x7fffffff || !wide_type(xtype) || elem_size(ytype) == 0)
+        return BAKRON_E_INVALID_ARG;
+    if (gain && gtype != xtype && gtype != BAKRON_F32) return BAKRON_E_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(eps < INFINITY) || (rotate && n > bk::kNormMaxBuffered)) return BAKRON_E_INVALID_ARG;
+    if (T == 0) return BAKRON_OK;
+    const bool coded = !wide_type(ytype);
+    if (!X || !Y || (coded && !yscale)) return BAKRON_E_INVALID_ARG;
+    if (bad_ld(ldx, n) || bad_ld(ldy, n) || (R && bad_ld(ldr, n)) || (H && bad_ld(ldh, n)))
+        return BAKRON_E_INVALID_ARG;
+    const Rows x = rows_of(X, T, n, ldx, xtype), r = rows_of(R, T, n, ldr, xtype), h = rows_of(H, T, n, ldh, xtype);
+    const Rows y = rows_of(Y, T, n, ldy, ytype), s = {coded ? yscale : nullptr, 1, 4 * T, 4 * T};
+    const Rows g = rows_of(gain, 1, n, n, gtype);
+    const auto clash = [&](const Rows& in, const Rows& out, int in_type, int out_type) {
+        return overlap(in, out) && !(same_rows(in, out) && in_type == out_type);
+    };
+    if (clash(x, h, xtype, xtype) || clash(r, h, xtype, xtype) || clash(x, y, xtype, ytype) ||
+        clash(r, y, xtype, ytype))
+        return BAKRON_E_INVALID_ARG;
+    if (overlap(h, y) || overlap(s, x) || overlap(s, r) || overlap(s, h) || overlap(s, y) || overlap(s, g) ||
+        overlap(g, h) || overlap(g, y))
+        return BAKRON_E_INVALID_ARG;
+    return bk::launch_rmsnorm(X, xtype, T, n, ldx, R, ldr, H, ldh, gain, gtype, eps, rotate != 0, seed, Y, ytype, ldy,
+                              yscale, (hipStream_t)stream);
 }
 
 }  // extern "C"

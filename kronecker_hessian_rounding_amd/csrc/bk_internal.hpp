@@ -68,6 +68,24 @@ int enqueue_ldl_pair(float* HA, int64_t dA, int64_t ldha, float* DA, void* wsA, 
 int launch_rht(float* A, int64_t rows, int64_t cols, int64_t lda, int axis, uint64_t seed, int transpose,
                hipStream_t stream);
 
+// --- packed layers and their products (bk_matvec.hip) ---
+struct PackShape {
+    int W;  // bits stored per weight
+    int64_t tiles, chunks, groups, groups_padded;
+    size_t scale_offset, bytes;
+};
+PackShape pack_shape(int64_t m, int64_t n, int bits, int64_t group);
+int launch_pack(const uint8_t* codes, int64_t m, int64_t n, int64_t ldc, int bits, const float* scales, int64_t lds,
+                int64_t group, void* packed, hipStream_t stream);
+int launch_matvec(const void* packed, int64_t m, int64_t n, int bits, int64_t group, const void* x, int xtype,
+                  int64_t T, int64_t ldx, const float* xs, void* y, int ytype, int64_t ldy, hipStream_t stream);
+
+// --- norm with residual, rotation and 8-bit output (bk_norm.hip) ---
+constexpr int64_t kNormMaxBuffered = 32768;  // longest row held in LDS as fp32 (128 KB)
+int launch_rmsnorm(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, const void* r, int64_t ldr, void* h,
+                   int64_t ldh, const void* gain, int gtype, float eps, int rotate, uint64_t seed, void* y, int ytype,
+                   int64_t ldy, float* ys, hipStream_t stream);
+
 // --- bound and sensitivity report (bk_report.hip) ---
 int launch_layer_report(int64_t m, int64_t n, const float* DO, const float* DI, const float* scales,
                         const float* HI, int64_t ldhi, const float* HO, int64_t ldho, double* out,
