@@ -25,9 +25,9 @@ def test_packed_bytes():
     assert f(16, 128, 4, 32) == 1024 + 4 * 64
     assert f(16, 129, 4, 32) == 2 * 1024 + 8 * 64      # groups of the padded columns
     assert f(16, 300, 4, 256) == 3 * 1024 + 2 * 64
-    # 2-bit: chunks of 256 columns
+    # 2-bit: 512 bytes
     assert f(16, 256, 2, 128) == 1024 + 2 * 64
-    assert f(16, 257, 1, 0) == 2 * 1024 + 64
+    assert f(16, 257, 1, 0) == 3 * 512 + 64
     for bad in ((0, 4, 4, 0), (4, 0, 4, 0), (4, 4, 0, 0), (4, 4, 5, 0), (4, 4, 4, 16), (4, 4, 4, 48), (4, 4, 4, -32)):
         assert f(*bad) == 0, bad
 
