@@ -143,7 +143,8 @@ def _vec(t: Optional[torch.Tensor], name: str, n: int, dtype=torch.float32):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle, without the Stream object around it (0.1 us instead of 3)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 _ws_cache: dict = {}
@@ -568,29 +569,38 @@ _WIDE = (torch.float32, torch.float16, torch.bfloat16)
 _CODED = (torch.int8, torch.float8_e4m3fn)
 
 
+# A call for one token takes the host about as long as the GPU, so these checks read each
+# property of a tensor once.
 def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
     """Validate token rows on the current device; returns their leading dimension."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA/ROCm tensor" % name)
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError("%s must be on the current device" % name)
-    if t.dtype not in dtypes or t.dim() != 2:
+    size = t.shape
+    if t.dtype not in dtypes or len(size) != 2:
         raise ValueError("%s must be a 2-D tensor of %s" % (name, ", ".join(str(d) for d in dtypes)))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %d x %d" % ((name,) + tuple(shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = size
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError("%s must be %d x %d" % ((name,) + shape))
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError("%s must not have overlapping rows" % name)
-    return max(int(t.stride(0)), int(t.shape[1])) if t.shape[0] > 1 else max(int(t.shape[1]), 1)
+    if rows > 1:
+        if ld < cols:
+            raise ValueError("%s must not have overlapping rows" % name)
+        return max(ld, 1)
+    return max(cols, 1)
 
 
-def _token_scales(t: Optional[torch.Tensor], name: str, T: int) -> Optional[torch.Tensor]:
+def _token_scales(t: Optional[torch.Tensor], name: str, T: int) -> Optional[int]:
+    """The address of a vector of T float32 factors on the current device."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device.index != torch.cuda.current_device():
-        raise ValueError("%s must be on the current device" % name)
-    return _vec(t, name, T)
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device()
+            or t.dtype != torch.float32 or t.numel() != T or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous float32 vector of length %d on the current device" % (name, T))
+    return t.data_ptr()
 
 
 @dataclass
@@ -611,16 +621,17 @@ def pack(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -
     """
     ldc = _rows(codes, "codes", (torch.uint8,))
     m, n = codes.shape
+    bits, group = int(bits), int(group)
     if isinstance(scales, torch.Tensor) and scales.dim() == 1 and group == 0:
         scales = scales.reshape(-1, 1)
-    nb = LIB.bakron_packed_bytes(m, n, int(bits), int(group))
+    nb = LIB.bakron_packed_bytes(m, n, bits, group)
     if nb == 0:
         raise ValueError("pack takes m, n >= 1, bits 1..4 and group 0 or a power of two >= 32")
     lds = _rows(scales, "scales", (torch.float32,), (m, -(-n // group) if group else 1))
     data = torch.empty(nb, dtype=torch.uint8, device=codes.device)
-    _check("bakron_pack", LIB.bakron_pack(_ptr(codes), m, n, ldc, int(bits), _ptr(scales), lds, int(group),
-                                          _ptr(data), nb, _stream()))
-    return PackedWeight(data, int(m), int(n), int(bits), int(group))
+    _check("bakron_pack", LIB.bakron_pack(codes.data_ptr(), m, n, ldc, bits, scales.data_ptr(), lds, group,
+                                          data.data_ptr(), nb, _stream()))
+    return PackedWeight(data, m, n, bits, group)
 
 
 def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = None,
@@ -635,11 +646,11 @@ def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = N
     if one:
         x = x.unsqueeze(0)
         out = out.unsqueeze(0) if isinstance(out, torch.Tensor) and out.dim() == 1 else out
-    ldx = _rows(x, "x", tuple(ROW_TYPES))
-    T = x.shape[0]
-    if x.shape[1] != w.n:
+    ldx = _rows(x, "x", ROW_TYPES)
+    T, n = x.shape
+    if n != w.n:
         raise ValueError("x must have %d columns" % w.n)
-    if w.data.device != x.device:
+    if w.data.get_device() != x.get_device():
         raise ValueError("the packed layer must be on x's device")
     xs = _token_scales(x_scale, "x_scale", T)
     if out is None:
@@ -647,13 +658,15 @@ def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = N
             out_dtype = x.dtype if x.dtype in _WIDE else torch.bfloat16
         if out_dtype not in _WIDE:
             raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in _WIDE))
-        out = torch.empty((T, w.m), dtype=out_dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out must be a tensor of %s" % out_dtype)
-    ldy = _rows(out, "out", _WIDE, (T, w.m))
-    _check("bakron_matvec", LIB.bakron_matvec(_ptr(w.data), w.data.numel(), w.m, w.n, w.bits, w.group, _ptr(x),
-                                              ROW_TYPES[x.dtype], T, ldx, _ptr(xs), _ptr(out), ROW_TYPES[out.dtype],
-                                              ldy, _stream()))
+        out = x.new_empty((T, w.m), dtype=out_dtype)
+        ldy = w.m
+    else:
+        ldy = _rows(out, "out", _WIDE, (T, w.m))
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must be a tensor of %s" % out_dtype)
+    _check("bakron_matvec", LIB.bakron_matvec(w.data.data_ptr(), w.data.numel(), w.m, w.n, w.bits, w.group,
+                                              x.data_ptr(), ROW_TYPES[x.dtype], T, ldx, xs, out.data_ptr(),
+                                              ROW_TYPES[out.dtype], ldy, _stream()))
     return out[0] if one else out
 
 
@@ -676,35 +689,43 @@ def rmsnorm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Opti
     type when a residual is given (sum_out=residual updates it in place).
     """
     ldx = _rows(x, "x", _WIDE)
-    T, n = x.shape
-    ldr = ldh = 0
+    T, n = shape = tuple(x.shape)
+    xtype = x.dtype
+    ldr = ldh = gtype = 0
+    r = h = g = None
     if residual is not None:
-        ldr = _rows(residual, "residual", (x.dtype,), (T, n))
+        ldr = _rows(residual, "residual", (xtype,), shape)
+        r = residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty((T, n), dtype=x.dtype, device=x.device)
+            sum_out = x.new_empty(shape)
     if sum_out is not None:
-        ldh = _rows(sum_out, "sum_out", (x.dtype,), (T, n))
+        ldh = _rows(sum_out, "sum_out", (xtype,), shape)
+        h = sum_out.data_ptr()
     if gain is not None:
         if (not isinstance(gain, torch.Tensor) or gain.device != x.device or gain.numel() != n
-                or not gain.is_contiguous() or gain.dtype not in (x.dtype, torch.float32)):
+                or not gain.is_contiguous() or gain.dtype not in (xtype, torch.float32)):
             raise ValueError("gain must be a contiguous vector of length %d, float32 or x's type" % n)
+        g, gtype = gain.data_ptr(), ROW_TYPES[gain.dtype]
     if out is None:
-        out_dtype = x.dtype if out_dtype is None else out_dtype
+        out_dtype = xtype if out_dtype is None else out_dtype
         if out_dtype not in ROW_TYPES:
             raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in ROW_TYPES))
-        out = torch.empty((T, n), dtype=out_dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out must be a tensor of %s" % out_dtype)
-    ldy = _rows(out, "out", tuple(ROW_TYPES), (T, n))
+        out = x.new_empty(shape, dtype=out_dtype)
+        ldy = max(n, 1)
+    else:
+        ldy = _rows(out, "out", ROW_TYPES, shape)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must be a tensor of %s" % out_dtype)
+    ys = None
     if out.dtype in _CODED:
         if scale_out is None:
-            scale_out = torch.empty(T, dtype=torch.float32, device=x.device)
-        _token_scales(scale_out, "scale_out", T)
+            scale_out = x.new_empty(T, dtype=torch.float32)
+        ys = _token_scales(scale_out, "scale_out", T)
     elif scale_out is not None:
         raise ValueError("scale_out goes with an 8-bit out")
+    seed = 0 if rotate_seed is None else int(rotate_seed) & (2**64 - 1)
     _check("bakron_rmsnorm",
-           LIB.bakron_rmsnorm(_ptr(x), ROW_TYPES[x.dtype], T, n, ldx, _ptr(residual), ldr, _ptr(sum_out), ldh,
-                              _ptr(gain), ROW_TYPES[gain.dtype] if gain is not None else 0, eps,
-                              0 if rotate_seed is None else 1, int(rotate_seed or 0) & (2**64 - 1), _ptr(out),
-                              ROW_TYPES[out.dtype], ldy, _ptr(scale_out), _stream()))
+           LIB.bakron_rmsnorm(x.data_ptr(), ROW_TYPES[xtype], T, n, ldx, r, ldr, h, ldh, g, gtype, eps,
+                              0 if rotate_seed is None else 1, seed, out.data_ptr(), ROW_TYPES[out.dtype], ldy, ys,
+                              _stream()))
     return NormResult(out, scale_out, sum_out)
