@@ -74,56 +74,72 @@ __device__ __forceinline__ void store8f(void* row, int c, int n, const float (&f
 
 constexpr float kMaxFinite = 3.402823466e38f;
 
-// |v| for the row's maximum: a value that is not finite counts as infinity.
-__device__ __forceinline__ float mag(float v) {
-    const float a = fabsf(v);
-    return a <= kMaxFinite ? a : INFINITY;
+// Over a wave: within 16 lanes by DPP (quad permutations, half-row and row mirrors), then
+// two exchanges; over the workgroup through `red`, whose values 16 lanes reduce again.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false);
 }
-
-template <int THREADS>
-__device__ __forceinline__ float block_reduce(float v, float* red, bool max) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const float w = __shfl_xor(v, o);
-        v = max ? fmaxf(v, w) : v + w;
-    }
-    if (THREADS == 64) return v;
+template <typename F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F op) {
+    v = op(v, dpp<0xB1>(v));
+    v = op(v, dpp<0x4E>(v));
+    v = op(v, dpp<0x141>(v));
+    return op(v, dpp<0x140>(v));
+}
+template <typename F>  // op(v, 0) is v
+__device__ __forceinline__ uint32_t block_reduce(uint32_t v, uint32_t* red, F op) {
+    v = row_reduce(v, op);
+    v = op(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = op(v, (uint32_t)__shfl_xor((int)v, 32));
+    const int waves = blockDim.x >> 6;  // at most 16
+    if (waves == 1) return v;
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    float s = red[0];
-#pragma unroll
-    for (int i = 1; i < THREADS / 64; ++i) s = max ? fmaxf(s, red[i]) : s + red[i];
-    return s;
+    const int i = threadIdx.x & 15;
+    return row_reduce(i < waves ? red[i] : 0u, op);
+}
+__device__ __forceinline__ float block_sum(float v, uint32_t* red) {
+    return __uint_as_float(block_reduce(__float_as_uint(v), red, [](uint32_t x, uint32_t y) {
+        return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+    }));
+}
+// The largest magnitude, as the bits of |v|: their order as integers is that of the values,
+// infinity and then NaN above all others.
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float block_max(uint32_t v, uint32_t* red) {
+    return __uint_as_float(block_reduce(v, red, [](uint32_t x, uint32_t y) { return max(x, y); }));
 }
 
 // The codes of a row with maximum mx = max|u| and factor f are (u * up) * inv, and its scale
 // is mx f / top. `up` is 2^64 for a maximum whose reciprocal fp32 may not hold. A row of
-// zeros: scale 0; a row that is not finite: scale NaN; codes 0 in both.
+// zeros: scale 0; a row that is not finite: scale NaN; inv 0 and codes 0 in both. A code
+// needs no clamping: |u| <= mx, so |u up inv| <= top (1 + 2^-22), which rounds to top.
 struct Coder {
-    float top, up, inv, scale;
+    float up, inv, scale;
     __device__ __forceinline__ Coder(float mx, float f, bool i8) {
-        top = i8 ? 127.0f : 448.0f;
+        const float top = i8 ? 127.0f : 448.0f;
         scale = mx * f / top;
         if (!(mx <= kMaxFinite) || !(scale <= kMaxFinite)) scale = NAN;
         up = mx < 0x1p-64f ? 0x1p64f : 1.0f;
         inv = scale >= 0.0f && mx > 0.0f ? top / (mx * up) : 0.0f;
     }
-    __device__ __forceinline__ float operator()(float u) const {
-        const float q = fminf(fmaxf(u * up * inv, -top), top);
-        return inv > 0.0f ? q : 0.0f;  // u may be infinite or NaN where inv is 0
-    }
 };
-__device__ __forceinline__ uint32_t e4m3_4(float a, float b, float c, float d) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+// Four codes of u. int8: behind 1.5 * 2^23 a float's low byte is the integer it was rounded to.
+__device__ __forceinline__ uint32_t e4m3_4(const float* u, float inv) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(u[0] * inv, u[1] * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(u[2] * inv, u[3] * inv, w, true);
 }
-__device__ __forceinline__ uint32_t int8_4(float a, float b, float c, float d) {
-    const auto q = [](float v) { return (uint32_t)(int)rintf(v) & 255u; };
-    return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
+__device__ __forceinline__ uint32_t int8_4(const float* u, float inv) {
+    uint32_t q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = __float_as_uint(fmaf(u[e], inv, 12582912.0f));
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[3], q[2], 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u), 0x05040100u);
 }
 
 // LDS address of element e of a row in floats: 8 floats of padding behind 64, so that the
-// strided reads of the lowest pass fall on all banks.
+// strided reads of the lowest pass fall on all banks. Additive over disjoint bits of e.
 __device__ __forceinline__ int at(int e) { return e + ((e >> 6) << 3); }
 
 // The butterflies of index bits [w0 + skip, w0 + 3) among the 8 values of a thread.
@@ -181,14 +197,15 @@ __device__ __forceinline__ float signed_gain(float g, uint32_t bit) {
 __device__ __forceinline__ void store_row(const NormArgs& a, int64_t row, int c, int n, float (&u)[8], float f,
                                           const Coder& code) {
     if (a.ys) {
-        float q[8];
+        uint32_t d[2] = {0, 0};
+        if (code.inv > 0.0f) {
+            if (code.up != 1.0f)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = code(u[e]);
-        uint32_t d[2];
+                for (int e = 0; e < 8; ++e) u[e] *= code.up;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            d[k] = a.ytype == BAKRON_I8 ? int8_4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3])
-                                        : e4m3_4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
+            for (int k = 0; k < 2; ++k)
+                d[k] = a.ytype == BAKRON_I8 ? int8_4(u + 4 * k, code.inv) : e4m3_4(u + 4 * k, code.inv);
+        }
         Vec<uint8_t>::type w;
         __builtin_memcpy(&w, d, 8);
         store8((uint8_t*)a.y + row * a.ldy, c, n, w);
@@ -202,105 +219,85 @@ __device__ __forceinline__ void store_row(const NormArgs& a, int64_t row, int c,
 }
 
 // A row per workgroup at a time, in registers: thread t holds columns 8 q .. 8 q + 7 of
-// the groups q = t + i THREADS. Workgroups take rows blockIdx.x, + gridDim.x, ...; the
-// signs stay in registers over them, and with one group a thread so does the gain, and the
-// next row's x and r are on the way while a row is worked on.
+// the groups q = t + i threads. Without rotation (kRot) a workgroup per row; with it,
+// workgroups take rows blockIdx.x, + gridDim.x, ... and keep the signs in registers.
 // Rotation: index bits 0..2 in registers, then passes over three bits each through LDS
 // (n % 8 == 0 whenever there are any): group q of a pass with window w0 holds the elements
 // that differ in bits w0..w0+2. Bits below 9 stay within a wave's 512 columns.
-template <typename TX, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS) void k_norm_rows(NormArgs a) {
-    using V = typename Vec<TX>::type;
-    extern __shared__ float buf[];
-    __shared__ float red[2][THREADS / 64];
-    const int n = (int)a.n;
-    constexpr bool kKeep = NV == 1;
-    // opaque where a thread holds several groups: their addresses are then computed where they are used
-    // instead of held in registers over the row and the loop
-    const auto tid = [] { return kKeep ? (int)threadIdx.x : tid_opaque(); };
-    const int c0 = 8 * (int)threadIdx.x;
-    V xv, rv;
-    const auto fetch = [&](int64_t row) {
-        xv = load8((const TX*)a.x + row * a.ldx, c0, n);
-        if (a.r) rv = load8((const TX*)a.r + row * a.ldr, c0, n);
-    };
-    float g0[8];
-    if (kKeep && c0 < n) {
-        fetch(blockIdx.x);
-        load_gain<TX>(a, c0, n, g0);
-    }
+template <typename TX, int NV, bool kRot>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 8 : 4))) void k_norm_rows(NormArgs a) {
+    extern __shared__ __align__(16) float buf[];
+    __shared__ uint32_t red[2][16];
+    const int n = (int)a.n, threads = blockDim.x;
     uint32_t neg = 0;  // 8 bits a group
-    if (a.rotate)
+    if (kRot)
 #pragma unroll 1
-        for (int i = 0; i < NV; ++i) neg |= sign_bits(a.seed, 8 * ((int)threadIdx.x + i * THREADS)) << (8 * i);
+        for (int i = 0; i < NV; ++i) neg |= sign_bits(a.seed, 8 * ((int)threadIdx.x + i * threads)) << (8 * i);
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        // opaque: addresses are then computed where they are used instead of held in registers over the row
+        const auto tid = [] { return tid_opaque(); };
         float v[NV][8];
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (tid() + i * THREADS);
+            const int c = 8 * (tid() + i * threads);
             if (c < n) {
                 float g[8];
-                if (kKeep) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        g[e] = g0[e];
-                        v[i][e] = a.r ? (float)xv[e] + (float)rv[e] : (float)xv[e];
-                    }
-                } else {
-                    load_sum<TX>(a, row, c, n, v[i]);
-                    load_gain<TX>(a, c, n, g);
-                }
+                load_sum<TX>(a, row, c, n, v[i]);
+                load_gain<TX>(a, c, n, g);
                 if (a.h) store8f<TX>((TX*)a.h + row * a.ldh, c, n, v[i]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     ss = fmaf(v[i][e], v[i][e], ss);
-                    v[i][e] *= signed_gain(g[e], neg >> (8 * i + e));
+                    v[i][e] *= kRot ? signed_gain(g[e], neg >> (8 * i + e)) : g[e];
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
             }
-            if (!kKeep) __builtin_amdgcn_sched_barrier(0);  // one group's loads at a time: registers
+            if (NV > 1) __builtin_amdgcn_sched_barrier(0);  // one group's loads at a time: registers
         }
-        if (kKeep && c0 < n && row + gridDim.x < a.T) fetch(row + gridDim.x);
-        ss = block_reduce<THREADS>(ss, red[0], false);
-        const float f = (a.rotate ? a.rscale : 1.0f) / sqrtf(ss / (float)n + a.eps);
-        if (a.rotate) {
+        ss = block_sum(ss, red[0]);
+        const float f = (kRot ? a.rscale : 1.0f) / sqrtf(ss / (float)n + a.eps);
+        if (kRot) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) butterflies(v[i], 0, a.kbits);
             if (a.kbits > 3) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int q = tid() + i * THREADS;
+                    const int q = tid() + i * threads;
                     if (8 * q < n) {
                         float* p = buf + at(8 * q);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) p[e] = v[i][e];
                     }
                 }
-                for (int done = 3; done < a.kbits;) {
-                    const int w0 = min(done, a.kbits - 3);
+                const auto pass = [&](int w0, int skip) {
                     if (w0 + 3 > 9) __syncthreads();
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
-                        const int q = tid() + i * THREADS;
+                        const int q = tid() + i * threads;
                         if (8 * q < n) {
-                            const int e0 = (q >> w0 << (w0 + 3)) | (q & ((1 << w0) - 1));
+                            float* p = buf + at((q >> w0 << (w0 + 3)) | (q & ((1 << w0) - 1)));
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) v[i][j] = buf[at(e0 + (j << w0))];
-                            butterflies(v[i], done - w0, 3);
+                            for (int j = 0; j < 8; ++j) v[i][j] = p[at(j << w0)];
+                            butterflies(v[i], skip, 3);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) buf[at(e0 + (j << w0))] = v[i][j];
+                            for (int j = 0; j < 8; ++j) p[at(j << w0)] = v[i][j];
                         }
-                        if (!kKeep) __builtin_amdgcn_sched_barrier(0);
+                        if (NV > 1) __builtin_amdgcn_sched_barrier(0);
                     }
-                    done = w0 + 3;
-                }
+                };
+                // whole windows at fixed places (their offsets are then constants), then one that ends at the
+                // top bit and skips the stages that are done
+                if (a.kbits >= 6) pass(3, 0);
+                if (a.kbits >= 9) pass(6, 0);
+                if (a.kbits >= 12) pass(9, 0);
+                if (a.kbits % 3) pass(a.kbits - 3, 3 - a.kbits % 3);
                 if (a.kbits > 9) __syncthreads();
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int q = tid() + i * THREADS;
+                    const int q = tid() + i * threads;
                     if (8 * q < n) {
                         const float* p = buf + at(8 * q);
 #pragma unroll
@@ -311,22 +308,23 @@ __global__ __launch_bounds__(THREADS) void k_norm_rows(NormArgs a) {
         }
         float mx = 0.0f;
         if (a.ys) {
+            uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, mag(v[i][e]));
-            mx = block_reduce<THREADS>(mx, red[1], true);
+                for (int e = 0; e < 8; ++e) top = max(top, mag(v[i][e]));
+            mx = block_max(top, red[1]);
         }
         const Coder code(mx, f, a.ytype == BAKRON_I8);
         if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (tid() + i * THREADS);
+            const int c = 8 * (tid() + i * threads);
             if (c < n) store_row(a, row, c, n, v[i], f, code);
-            if (!kKeep) __builtin_amdgcn_sched_barrier(0);
+            if (NV > 1) __builtin_amdgcn_sched_barrier(0);
         }
-        // the next row writes red and buf again
-        if (THREADS > 64) __syncthreads();
+        if (!kRot) break;
+        if (threads > 64) __syncthreads();  // the next row writes red and buf again
     }
 }
 
@@ -335,8 +333,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_rows(NormArgs a) {
 constexpr int kLongThreads = 1024;
 template <typename TX>
 __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
-    extern __shared__ float buf[];
-    __shared__ float red[2][kLongThreads / 64];
+    extern __shared__ __align__(16) float buf[];
+    __shared__ uint32_t red[2][kLongThreads / 64];
     const int n = (int)a.n, groups = (n + 7) / 8;
     const int64_t row = blockIdx.x;
     float ss = 0.0f;
@@ -357,7 +355,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = v[e];
     }
-    ss = block_reduce<kLongThreads>(ss, red[0], false);
+    ss = block_sum(ss, red[0]);
     const float f = (a.rotate ? a.rscale : 1.0f) / sqrtf(ss / (float)n + a.eps);
     if (a.rotate)
         for (int done = 3; done < a.kbits;) {
@@ -365,26 +363,27 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
             __syncthreads();
 #pragma unroll 1
             for (int q = threadIdx.x; q < groups; q += kLongThreads) {
-                const int e0 = (q >> w0 << (w0 + 3)) | (q & ((1 << w0) - 1));
+                float* p = buf + at((q >> w0 << (w0 + 3)) | (q & ((1 << w0) - 1)));
                 float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = buf[at(e0 + (j << w0))];
+                for (int j = 0; j < 8; ++j) v[j] = p[at(j << w0)];
                 butterflies(v, done - w0, 3);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) buf[at(e0 + (j << w0))] = v[j];
+                for (int j = 0; j < 8; ++j) p[at(j << w0)] = v[j];
             }
             done = w0 + 3;
         }
     __syncthreads();
     float mx = 0.0f;
     if (a.ys) {
+        uint32_t top = 0;
 #pragma unroll 1
         for (int q = threadIdx.x; q < groups; q += kLongThreads) {
             const float* p = buf + at(8 * q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, mag(p[e]));  // zeros from column n on
+            for (int e = 0; e < 8; ++e) top = max(top, mag(p[e]));  // zeros from column n on
         }
-        mx = block_reduce<kLongThreads>(mx, red[1], true);
+        mx = block_max(top, red[1]);
     }
     const Coder code(mx, f, a.ytype == BAKRON_I8);
     if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
@@ -401,7 +400,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
 // Rows too long for registers (no rotation): x and r are read again from cache, and each
 // element's loads precede its stores in the same thread, so in-place calls hold.
 __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
-    __shared__ float red[2][kLongThreads / 64];
+    __shared__ uint32_t red[2][kLongThreads / 64];
     const int64_t row = blockIdx.x;
     const auto h_of = [&](int64_t i) {
         float h = load_elem(a.x, a.xtype, row * a.ldx + i);
@@ -417,12 +416,13 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
         const float h = h_of(i);
         ss = fmaf(h, h, ss);
     }
-    const float f = 1.0f / sqrtf(block_reduce<kLongThreads>(ss, red[0], false) / (float)a.n + a.eps);
+    const float f = 1.0f / sqrtf(block_sum(ss, red[0]) / (float)a.n + a.eps);
     const bool i8 = a.ytype == BAKRON_I8;
     float mx = 0.0f;
     if (a.ys) {
-        for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) mx = fmaxf(mx, mag(u_of(i)));
-        mx = block_reduce<kLongThreads>(mx, red[1], true);
+        uint32_t top = 0;
+        for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) top = max(top, mag(u_of(i)));
+        mx = block_max(top, red[1]);
     }
     const Coder code(mx, f, i8);
     if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
@@ -432,28 +432,29 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
         if (!a.ys) {
             store_elem(a.y, a.ytype, row * a.ldy + i, u * f);
         } else {
-            const float q = code(u);
-            ((uint8_t*)a.y)[row * a.ldy + i] = (uint8_t)(i8 ? int8_4(q, 0, 0, 0) : e4m3_4(q, 0, 0, 0));
+            const float w[4] = {u * code.up, 0.0f, 0.0f, 0.0f};
+            const uint32_t q = i8 ? int8_4(w, code.inv) : e4m3_4(w, code.inv);
+            ((uint8_t*)a.y)[row * a.ldy + i] = code.inv > 0.0f ? (uint8_t)q : (uint8_t)0;
         }
     }
 }
 
-template <typename TX, int THREADS, int NV>
+template <typename TX, int NV>
 void launch_rows(const NormArgs& a, hipStream_t stream) {
+    const int threads = (int)((a.n + 512 * NV - 1) / (512 * NV)) * 64;
     // enough workgroups to fill the chip; each then keeps its signs and gain over its rows
-    const int per_cu = std::max(1, 2048 / THREADS / 2) * 2;
-    const unsigned grid = (unsigned)std::min<int64_t>(a.T, (int64_t)device_info().cus * per_cu);
+    const int64_t most = (int64_t)device_info().cus * (2048 / threads);
+    const int64_t per = a.rotate ? (a.T + most - 1) / most : 1;  // rows of a workgroup, as even as possible
+    const unsigned grid = (unsigned)((a.T + per - 1) / per);
     const size_t lds = a.rotate && a.kbits > 3 ? sizeof(float) * (a.n + (a.n >> 6 << 3)) : 0;
-    hipLaunchKernelGGL((k_norm_rows<TX, THREADS, NV>), dim3(grid), dim3(THREADS), lds, stream, a);
+    if (a.rotate) hipLaunchKernelGGL((k_norm_rows<TX, NV, true>), dim3(grid), dim3(threads), lds, stream, a);
+    else hipLaunchKernelGGL((k_norm_rows<TX, NV, false>), dim3(grid), dim3(threads), 0, stream, a);
 }
 
 template <typename TX>
 void launch_type(const NormArgs& a, hipStream_t stream) {
-    if (a.n <= 512) launch_rows<TX, 64, 1>(a, stream);
-    else if (a.n <= 2048) launch_rows<TX, 256, 1>(a, stream);
-    else if (a.n <= 4096) launch_rows<TX, 512, 1>(a, stream);
-    else if (a.n <= 8192) launch_rows<TX, 1024, 1>(a, stream);
-    else if (a.n <= 16384) launch_rows<TX, 1024, 2>(a, stream);
+    if (a.n <= 8192) launch_rows<TX, 1>(a, stream);
+    else if (a.n <= 16384) launch_rows<TX, 2>(a, stream);
     else
         hipLaunchKernelGGL(k_norm_lds<TX>, dim3((unsigned)a.T), dim3(kLongThreads),
                            sizeof(float) * (a.n + 8 + ((a.n + 7) >> 6 << 3)), stream, a);
