@@ -43,10 +43,11 @@ template <typename T> struct Vec { typedef T type __attribute__((ext_vector_type
 
 // 8 elements from column c on of a row of `type` T, zeros from column n on; no alignment
 // beyond the element's is assumed.
-template <typename T>
+// kWhole: n is a multiple of 8 (and c < n), so there is no tail.
+template <bool kWhole, typename T>
 __device__ __forceinline__ typename Vec<T>::type load8(const T* row, int c, int n) {
     typename Vec<T>::type v;
-    if (c + 8 <= n) {
+    if (kWhole || c + 8 <= n) {
         __builtin_memcpy(&v, row + c, sizeof v);
     } else {
 #pragma unroll
@@ -54,9 +55,9 @@ __device__ __forceinline__ typename Vec<T>::type load8(const T* row, int c, int 
     }
     return v;
 }
-template <typename T>
+template <bool kWhole, typename T>
 __device__ __forceinline__ void store8(T* row, int c, int n, typename Vec<T>::type v) {
-    if (c + 8 <= n) {
+    if (kWhole || c + 8 <= n) {
         __builtin_memcpy(row + c, &v, sizeof v);
     } else {
 #pragma unroll
@@ -64,12 +65,12 @@ __device__ __forceinline__ void store8(T* row, int c, int n, typename Vec<T>::ty
             if (c + e < n) row[c + e] = v[e];
     }
 }
-template <typename T>
+template <bool kWhole, typename T>
 __device__ __forceinline__ void store8f(void* row, int c, int n, const float (&f)[8]) {
     typename Vec<T>::type v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (T)f[e];
-    store8((T*)row, c, n, v);
+    store8<kWhole>((T*)row, c, n, v);
 }
 
 constexpr float kMaxFinite = 3.402823466e38f;
@@ -157,28 +158,28 @@ __device__ __forceinline__ void butterflies(float (&v)[8], int skip, int end) {
 }
 
 // h = x + r of 8 columns from c on, in fp32.
-template <typename TX>
+template <bool kWhole, typename TX>
 __device__ __forceinline__ void load_sum(const NormArgs& a, int64_t row, int c, int n, float (&v)[8]) {
-    const auto x = load8((const TX*)a.x + row * a.ldx, c, n);
+    const auto x = load8<kWhole>((const TX*)a.x + row * a.ldx, c, n);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
     if (a.r) {
-        const auto r = load8((const TX*)a.r + row * a.ldr, c, n);
+        const auto r = load8<kWhole>((const TX*)a.r + row * a.ldr, c, n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += (float)r[e];
     }
 }
-template <typename TX>
+template <bool kWhole, typename TX>
 __device__ __forceinline__ void load_gain(const NormArgs& a, int c, int n, float (&g)[8]) {
     if (!a.gain) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = 1.0f;
     } else if (a.gfloat) {
-        const auto w = load8((const float*)a.gain, c, n);
+        const auto w = load8<kWhole>((const float*)a.gain, c, n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = w[e];
     } else {
-        const auto w = load8((const TX*)a.gain, c, n);
+        const auto w = load8<kWhole>((const TX*)a.gain, c, n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = (float)w[e];
     }
@@ -194,6 +195,7 @@ __device__ __forceinline__ float signed_gain(float g, uint32_t bit) {
     return __uint_as_float(__float_as_uint(g) ^ (bit << 31));
 }
 // The outputs of columns c .. c + 7: u f, or the codes of u.
+template <bool kWhole>
 __device__ __forceinline__ void store_row(const NormArgs& a, int64_t row, int c, int n, float (&u)[8], float f,
                                           const Coder& code) {
     if (a.ys) {
@@ -208,14 +210,14 @@ __device__ __forceinline__ void store_row(const NormArgs& a, int64_t row, int c,
         }
         Vec<uint8_t>::type w;
         __builtin_memcpy(&w, d, 8);
-        store8((uint8_t*)a.y + row * a.ldy, c, n, w);
+        store8<kWhole>((uint8_t*)a.y + row * a.ldy, c, n, w);
         return;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) u[e] *= f;
-    if (a.ytype == BAKRON_F32) store8f<float>((float*)a.y + row * a.ldy, c, n, u);
-    else if (a.ytype == BAKRON_F16) store8f<_Float16>((_Float16*)a.y + row * a.ldy, c, n, u);
-    else store8f<__bf16>((__bf16*)a.y + row * a.ldy, c, n, u);
+    if (a.ytype == BAKRON_F32) store8f<kWhole, float>((float*)a.y + row * a.ldy, c, n, u);
+    else if (a.ytype == BAKRON_F16) store8f<kWhole, _Float16>((_Float16*)a.y + row * a.ldy, c, n, u);
+    else store8f<kWhole, __bf16>((__bf16*)a.y + row * a.ldy, c, n, u);
 }
 
 // A row per workgroup at a time, in registers: thread t holds columns 8 q .. 8 q + 7 of
@@ -223,9 +225,12 @@ __device__ __forceinline__ void store_row(const NormArgs& a, int64_t row, int c,
 // workgroups take rows blockIdx.x, + gridDim.x, ... and keep the signs in registers.
 // Rotation: index bits 0..2 in registers, then passes over three bits each through LDS
 // (n % 8 == 0 whenever there are any): group q of a pass with window w0 holds the elements
-// that differ in bits w0..w0+2. Bits below 9 stay within a wave's 512 columns.
-template <typename TX, int NV, bool kRot>
+// that differ in bits w0..w0+2. Bits below 9 stay within a wave's 512 columns. The order
+// 2^kbits is a template argument: the passes' bounds and offsets are then constants, which
+// as run-time values overflowed the scalar registers (4096 rows of 8192: 68 us, with it 62).
+template <typename TX, int NV, int kbits>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 8 : 4))) void k_norm_rows(NormArgs a) {
+    constexpr bool kRot = kbits >= 0, kWhole = kbits >= 3;
     extern __shared__ __align__(16) float buf[];
     __shared__ uint32_t red[2][16];
     const int n = (int)a.n, threads = blockDim.x;
@@ -233,9 +238,19 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
     if (kRot)
 #pragma unroll 1
         for (int i = 0; i < NV; ++i) neg |= sign_bits(a.seed, 8 * ((int)threadIdx.x + i * threads)) << (8 * i);
+    // one group a thread: its gain, signs applied, stays in registers too. Addresses are computed in each
+    // row (from an opaque thread index), with more groups where they are used, instead of held in registers
+    constexpr bool kKeep = NV == 1;
+    float g0[8] = {};
+    if (kKeep && 8 * (int)threadIdx.x < n) {
+        load_gain<kWhole, TX>(a, 8 * (int)threadIdx.x, n, g0);
+        if (kRot)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g0[e] = signed_gain(g0[e], neg >> e);
+    }
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-        // opaque: addresses are then computed where they are used instead of held in registers over the row
-        const auto tid = [] { return tid_opaque(); };
+        const int t0 = tid_opaque();
+        const auto tid = [&] { return kKeep ? t0 : tid_opaque(); };
         float v[NV][8];
         float ss = 0.0f;
 #pragma unroll
@@ -243,13 +258,13 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
             const int c = 8 * (tid() + i * threads);
             if (c < n) {
                 float g[8];
-                load_sum<TX>(a, row, c, n, v[i]);
-                load_gain<TX>(a, c, n, g);
-                if (a.h) store8f<TX>((TX*)a.h + row * a.ldh, c, n, v[i]);
+                load_sum<kWhole, TX>(a, row, c, n, v[i]);
+                if (!kKeep) load_gain<kWhole, TX>(a, c, n, g);
+                if (a.h) store8f<kWhole, TX>((TX*)a.h + row * a.ldh, c, n, v[i]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     ss = fmaf(v[i][e], v[i][e], ss);
-                    v[i][e] *= kRot ? signed_gain(g[e], neg >> (8 * i + e)) : g[e];
+                    v[i][e] *= kKeep ? g0[e] : kRot ? signed_gain(g[e], neg >> (8 * i + e)) : g[e];
                 }
             } else {
 #pragma unroll
@@ -261,8 +276,8 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
         const float f = (kRot ? a.rscale : 1.0f) / sqrtf(ss / (float)n + a.eps);
         if (kRot) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) butterflies(v[i], 0, a.kbits);
-            if (a.kbits > 3) {
+            for (int i = 0; i < NV; ++i) butterflies(v[i], 0, kbits);
+            if (kbits > 3) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int q = tid() + i * threads;
@@ -288,13 +303,12 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
                         if (NV > 1) __builtin_amdgcn_sched_barrier(0);
                     }
                 };
-                // whole windows at fixed places (their offsets are then constants), then one that ends at the
-                // top bit and skips the stages that are done
-                if (a.kbits >= 6) pass(3, 0);
-                if (a.kbits >= 9) pass(6, 0);
-                if (a.kbits >= 12) pass(9, 0);
-                if (a.kbits % 3) pass(a.kbits - 3, 3 - a.kbits % 3);
-                if (a.kbits > 9) __syncthreads();
+                // whole windows, then one that ends at the top bit and skips the stages that are done
+                if (kbits >= 6) pass(3, 0);
+                if (kbits >= 9) pass(6, 0);
+                if (kbits >= 12) pass(9, 0);
+                if (kbits % 3 != 0) pass(kbits - 3, 3 - kbits % 3);
+                if (kbits > 9) __syncthreads();
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int q = tid() + i * threads;
@@ -320,7 +334,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (tid() + i * threads);
-            if (c < n) store_row(a, row, c, n, v[i], f, code);
+            if (c < n) store_row<kWhole>(a, row, c, n, v[i], f, code);
             if (NV > 1) __builtin_amdgcn_sched_barrier(0);
         }
         if (!kRot) break;
@@ -341,9 +355,9 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
 #pragma unroll 1
     for (int q = threadIdx.x; q < groups; q += kLongThreads) {
         float v[8], g[8];
-        load_sum<TX>(a, row, 8 * q, n, v);
-        if (a.h) store8f<TX>((TX*)a.h + row * a.ldh, 8 * q, n, v);
-        load_gain<TX>(a, 8 * q, n, g);
+        load_sum<false, TX>(a, row, 8 * q, n, v);
+        if (a.h) store8f<false, TX>((TX*)a.h + row * a.ldh, 8 * q, n, v);
+        load_gain<false, TX>(a, 8 * q, n, g);
         const uint32_t neg = a.rotate ? sign_bits(a.seed, 8 * q) : 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -393,7 +407,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
         const float* p = buf + at(8 * q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = p[e];
-        store_row(a, row, 8 * q, n, v, f, code);
+        store_row<false>(a, row, 8 * q, n, v, f, code);
     }
 }
 
@@ -439,22 +453,28 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
     }
 }
 
-template <typename TX, int NV>
+template <typename TX, int NV, int kbits>
 void launch_rows(const NormArgs& a, hipStream_t stream) {
     const int threads = (int)((a.n + 512 * NV - 1) / (512 * NV)) * 64;
     // enough workgroups to fill the chip; each then keeps its signs and gain over its rows
     const int64_t most = (int64_t)device_info().cus * (2048 / threads);
-    const int64_t per = a.rotate ? (a.T + most - 1) / most : 1;  // rows of a workgroup, as even as possible
+    const int64_t per = kbits >= 0 ? (a.T + most - 1) / most : 1;  // rows of a workgroup, as even as possible
     const unsigned grid = (unsigned)((a.T + per - 1) / per);
-    const size_t lds = a.rotate && a.kbits > 3 ? sizeof(float) * (a.n + (a.n >> 6 << 3)) : 0;
-    if (a.rotate) hipLaunchKernelGGL((k_norm_rows<TX, NV, true>), dim3(grid), dim3(threads), lds, stream, a);
-    else hipLaunchKernelGGL((k_norm_rows<TX, NV, false>), dim3(grid), dim3(threads), 0, stream, a);
+    const size_t lds = kbits > 3 ? sizeof(float) * (a.n + (a.n >> 6 << 3)) : 0;
+    hipLaunchKernelGGL((k_norm_rows<TX, NV, kbits>), dim3(grid), dim3(threads), lds, stream, a);
+}
+
+template <typename TX, int NV, int kbits>
+void launch_order(const NormArgs& a, hipStream_t stream) {
+    if (!a.rotate) launch_rows<TX, NV, -1>(a, stream);
+    else if (a.kbits == kbits) launch_rows<TX, NV, kbits>(a, stream);
+    else if constexpr (kbits > 0) launch_order<TX, NV, kbits - 1>(a, stream);
 }
 
 template <typename TX>
 void launch_type(const NormArgs& a, hipStream_t stream) {
-    if (a.n <= 8192) launch_rows<TX, 1>(a, stream);
-    else if (a.n <= 16384) launch_rows<TX, 2>(a, stream);
+    if (a.n <= 8192) launch_order<TX, 1, 13>(a, stream);
+    else if (a.n <= 16384) launch_order<TX, 2, 14>(a, stream);
     else
         hipLaunchKernelGGL(k_norm_lds<TX>, dim3((unsigned)a.T), dim3(kLongThreads),
                            sizeof(float) * (a.n + 8 + ((a.n + 7) >> 6 << 3)), stream, a);
