@@ -357,134 +357,253 @@ __global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a, int64_t sla
     }
 }
 
-// More tokens: workgroup (R row tiles, block of 16 NT tokens), columns split over the
-// waves as above, x straight from memory in operand form; an operand of x serves R tiles.
-template <int MATH, int W, int FS, int NT, int R>
-__global__ __launch_bounds__(kMvThreads) void k_matvec(MvArgs a) {
+// More tokens: x tiles shared in LDS.
+//
+// A workgroup has KS x RW waves: wave (kg, rg) multiplies the R row tiles of row group rg
+// with the 16 NT tokens of the block over the chunks kg, kg + KS, ...; per iteration the
+// workgroup stages KS chunks of x, double buffered, one barrier an iteration. With many
+// workgroups at hand KS = 1 and all waves share the chunk; with few, the waves split the
+// columns and their sums meet in LDS at the end, in the order of kg.
+//
+// x lies in LDS in operand form, 1 KB for 64 lanes of 16 bytes, so an operand is one
+// conflict-free read. A thread stages 16 bytes of a row (u-th of the row's chunk); the
+// lane slot is (q, t ^ u) for token t, which spreads a row's units over the banks. fp32 is
+// cut into its three pieces on the way in. Of 8-bit types, 16 bytes of a lane are its
+// columns of two steps.
+template <int MATH, int FS>
+struct MmOp {  // the MFMA of a kSub-step operand
+    static constexpr int kSub = FS == 4 ? (MATH == kI8 ? 2 : MATH == kF8 ? 4 : 1) : 1;
+};
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ i32x4 mma_i8x64(u32x4 a, u32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ f32x4 mma_f8x128(u32x8 a, u32x8 b, f32x4 c) {
+    typedef int i32x8 __attribute__((ext_vector_type(8)));
+    // both operands e4m3, block scales 2^0
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a), __builtin_bit_cast(i32x8, b),
+                                                            c, 0, 0, 0, 127, 0, 127);
+}
+
+template <int MATH, int NT, int KS>
+struct MmTile {
+    // bytes of x in LDS a buffer: [chunk][token tile][piece or not][4 steps or 2 pairs][64 lanes][16 bytes]
+    static constexpr int kSlabs = MATH == kF32 ? 12 : Mt<MATH>::kBytes == 2 ? 4 : 2;  // of 1 KB a chunk and tile
+    static constexpr int kBytes = KS * NT * kSlabs * 1024;
+};
+
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW>
+__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(KS * RW >= 8 ? 2 : 1)))
+void k_matmul(MvArgs a, int token_blocks) {
     using M = Mt<MATH>;
-    constexpr int PF = 2;
-    using St = Stream<W, FS, R, PF>;
-    constexpr int kB = M::kBytes;
-    __shared__ float red[kWaves][16][17];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t groups = (a.tiles + R - 1) / R;
-    const int64_t tile0 = blockIdx.x % groups * R, t0 = (int64_t)(blockIdx.x / groups) * 16 * NT;
-    const char* row[NT];
+    using St = Stream<W, FS, R, 2>;
+    using Tile = MmTile<MATH, NT, KS>;
+    constexpr int kB = M::kBytes, kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
+    constexpr int kUnitCols = 16 / (kB == 4 ? 2 : kB);        // columns of a staged unit: 16 bytes, fp32 32
+    constexpr int kRowUnits = KS * kChunk / kUnitCols;        // units of a token row in an iteration
+    constexpr int kUnits = 16 * NT * kRowUnits / kThreads;    // units a thread stages
+    static_assert(16 * NT * kRowUnits % kThreads == 0, "units divide over the threads");
+    extern __shared__ __align__(16) char lds[];
+    float* red = reinterpret_cast<float*>(lds);               // [KS][16][kPitch], after the loop
+
+    // workgroups 8 apart share an XCD: give each XCD a run of row blocks, token blocks innermost, so that those
+    // that read the same weights run side by side
+    const uint32_t total = gridDim.x, per = total / 8, extra = total % 8;
+    const uint32_t xcd = blockIdx.x % 8, id = xcd * per + min(xcd, extra) + blockIdx.x / 8;
+    const int64_t tile_b = (int64_t)(id / token_blocks) * R * RW, t0 = (int64_t)(id % token_blocks) * 16 * NT;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kg = wave / RW, rg = wave % RW;
+    const int q = lane >> 4, t = lane & 15;
+
+    struct Unit { u32x4 v[kB == 4 ? 2 : 1]; };
+    Unit raw[kUnits];
+    // unit i of this thread: token row and unit in the row
+    const auto row_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) / kRowUnits; };
+    const auto unit_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) % kRowUnits; };
+    const auto load = [&](int64_t it) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        row[t] = a.x + (min(t0 + 16 * t + (lane & 15), a.T - 1) * a.ldx + 8 * (lane >> 4)) * kB;
-    St st(a, tile0, lane);
-    const int mine = a.nc > w ? (int)((a.nc - w + kWaves - 1) / kWaves) : 0;
-    const int64_t whole = a.n / kChunk;  // chunks without padding
+        for (int i = 0; i < kUnits; ++i) {
+            const int64_t row = min(t0 + row_of(i), a.T - 1);
+            const int64_t k = it * KS * kChunk + unit_of(i) * kUnitCols;
+            const char* src = a.x + (row * a.ldx + k) * kB;
+            if (k + kUnitCols <= a.n) {
+                __builtin_memcpy(&raw[i], src, sizeof(Unit));
+            } else {  // zeros from column n on
+                raw[i] = Unit{};
+                const int left = (int)max<int64_t>(0, (a.n - k) * kB);
 #pragma unroll
-    for (int p = 0; p < PF; ++p)
-        if (p < mine) st.fetch(p, w + p * kWaves);
+                for (int e = 0; e < (int)sizeof(Unit) / kB; ++e)
+                    if (e * kB < left) {
+                        uint32_t w = 0;
+                        __builtin_memcpy(&w, src + e * kB, kB);
+                        raw[i].v[e * kB / 16][e * kB / 4 % 4] |= w << (8 * (e * kB & 3));
+                    }
+            }
+        }
+    };
+    const auto store = [&](char* buf) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int row = row_of(i), u = unit_of(i) % (kChunk / kUnitCols), ck = unit_of(i) / (kChunk / kUnitCols);
+            char* dst = buf + (ck * NT + (row >> 4)) * Tile::kSlabs * 1024;
+            if constexpr (kB == 1) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
+                const u32x2 lo = {raw[i].v[0][0], raw[i].v[0][1]}, hi = {raw[i].v[0][2], raw[i].v[0][3]};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int step = u >> 1, qq = 2 * (u & 1) + h;
+                    const u32x2 v = h ? hi : lo;
+                    *reinterpret_cast<u32x2*>(dst + (step >> 1) * 1024 +
+                                              (qq * 16 + ((row ^ (4 * (step >> 1) + qq)) & 15)) * 16 + (step & 1) * 8) =
+                        W == 2 ? even_odd(v) : v;
+                }
+            } else {  // columns 8 u ..: step u / 4, lanes of q = u % 4
+                const int at = (u >> 2) * 1024 + ((u & 3) * 16 + ((row ^ u) & 15)) * 16;
+                if constexpr (kB == 4) {
+                    float x[8];
+                    __builtin_memcpy(x, &raw[i], sizeof x);
+                    bf16x8 p[3];
+                    split3(x, p);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) *reinterpret_cast<bf16x8*>(dst + c * 4096 + at) = p[c];
+                } else {
+                    *reinterpret_cast<u32x4*>(dst + at) = raw[i].v[0];
+                }
+            }
+        }
+    };
+
+    St st(a, tile_b + rg * R, lane);
+    const int iters = (int)((a.nc + KS - 1) / KS);
+    load(0);
+    if (kg < a.nc) st.fetch(0, kg);
+    store(lds);
+    __syncthreads();
+
     float sum[R][NT][4] = {};
-    for (int i = 0; i < mine; i += PF) {
-#pragma unroll
-        for (int p = 0; p < PF; ++p) {
-            const int64_t c = w + (int64_t)(i + p) * kWaves;
-            if (c >= whole) break;
+    const auto body = [&](int it, int slot) {
+        const int64_t c = (int64_t)it * KS + kg;
+        const bool more = it + 1 < iters;
+        if (more) load(it + 1);
+        if (c + KS < a.nc) st.fetch(slot ^ 1, c + KS);
+        const char* buf = lds + (it & 1) * Tile::kBytes + kg * NT * Tile::kSlabs * 1024 + q * 256;
+        if (c < a.nc) {
 #pragma unroll
             for (int f = 0; f < St::kUnits; ++f) {
                 typename M::Acc acc[R][NT] = {};
+                constexpr int kSub = MmOp<MATH, FS>::kSub;
 #pragma unroll
-                for (int j = 0; j < FS; ++j) {
+                for (int j = 0; j < FS; j += kSub) {
                     const int step = f * FS + j;
-                    typename M::Op b[R];
+                    if constexpr (kB == 1) {
+                        u32x4 x[NT][(kSub + 1) / 2];  // pairs of steps
 #pragma unroll
-                    for (int r = 0; r < R; ++r) b[r] = weights<MATH, W>(st.d[p][r], step);
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        struct alignas(16) { char d[8 * kB]; } raw;
-                        __builtin_memcpy(&raw, row[t] + (c * kChunk + step * kStep) * kB, 8 * kB);
-                        typename M::Op x[M::kPieces];
-                        operand<MATH, W>(raw.d, x);
+                            for (int h = 0; h < (kSub + 1) / 2; ++h) {
+                                const int pair = (step >> 1) + h;
+                                x[n][h] = *reinterpret_cast<const u32x4*>(buf + (n * 2 + pair) * 1024 +
+                                                                          ((t ^ (4 * pair + q)) & 15) * 16);
+                            }
 #pragma unroll
-                        for (int r = 0; r < R; ++r)
+                        for (int r = 0; r < R; ++r) {
+                            if constexpr (kSub == 1) {
+                                const u32x2 b = weights<MATH, W>(st.d[slot][r], step);
 #pragma unroll
-                            for (int q = 0; q < M::kPieces; ++q) acc[r][t] = M::mma(x[q], b[r], acc[r][t]);
+                                for (int n = 0; n < NT; ++n) {
+                                    const u32x2 v = step & 1 ? u32x2{x[n][0][2], x[n][0][3]}
+                                                             : u32x2{x[n][0][0], x[n][0][1]};
+                                    acc[r][n] = M::mma(v, b, acc[r][n]);
+                                }
+                            } else if constexpr (kSub == 2) {
+                                const u32x2 b0 = weights<MATH, W>(st.d[slot][r], step),
+                                            b1 = weights<MATH, W>(st.d[slot][r], step + 1);
+                                const u32x4 b = {b0[0], b0[1], b1[0], b1[1]};
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) acc[r][n] = mma_i8x64(x[n][0], b, acc[r][n]);
+                            } else {
+                                u32x8 b;
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    const u32x2 w = weights<MATH, W>(st.d[slot][r], h);
+                                    b[2 * h] = w[0];
+                                    b[2 * h + 1] = w[1];
+                                }
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const u32x4 lo = x[n][0], hi = x[n][(kSub + 1) / 2 - 1];
+                                    acc[r][n] = mma_f8x128(u32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]},
+                                                           b, acc[r][n]);
+                                }
+                            }
+                        }
+                    } else {
+                        typename M::Op x[NT][M::kPieces];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int p = 0; p < M::kPieces; ++p)
+                                x[n][p] = *reinterpret_cast<const typename M::Op*>(
+                                    buf + (n * Tile::kSlabs + p * 4 + step) * 1024 + ((t ^ (4 * step + q)) & 15) * 16);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const typename M::Op b = weights<MATH, W>(st.d[slot][r], step);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int p = 0; p < M::kPieces; ++p) acc[r][n] = M::mma(x[n][p], b, acc[r][n]);
+                        }
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            sum[r][t][v] = fmaf(st.s[p][r][f], (float)acc[r][t][v], sum[r][t][v]);
+                            sum[r][n][v] = fmaf(st.s[slot][r][f], (float)acc[r][n][v], sum[r][n][v]);
             }
-            if (i + p + PF < mine) st.fetch(p, c + PF * kWaves);
         }
+        if (more) store(lds + (~it & 1) * Tile::kBytes);
+        __syncthreads();
+    };
+    for (int it = 0; it < iters; it += 2) {
+        body(it, 0);
+        if (it + 1 < iters) body(it + 1, 1);
     }
-    if (whole < a.nc && whole % kWaves == w) {  // the chunk that the row ends in
-        st.fetch(0, whole);
-#pragma unroll 1
-        for (int step = 0; step < kSteps; ++step) {
-            const int k = (int)(a.n - whole * kChunk) - step * kStep - 8 * (lane >> 4);  // columns left
-            float s[R];
-            typename M::Op b[R];
+
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                s[r] = st.s[0][r][0];
+    for (int n = 0; n < NT; ++n) {
+        if (n) __syncthreads();
 #pragma unroll
-                for (int f = 1; f < St::kUnits; ++f) s[r] = f == step ? st.s[0][r][f] : s[r];
-                auto d = st.d[0][r];
-                constexpr int kPer = 4 / W;  // steps of a dword, less one
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int q = 1; q < W; ++q)
-                    if (step >> (kPer - 1) == q) d[0] = d[q];
-                b[r] = W == 2 && (step & 1) ? weights<MATH, W>(d, 1) : weights<MATH, W>(d, 0);
-            }
+            for (int v = 0; v < 4; ++v)
+                red[(kg * 16 + 4 * q + v) * kPitch + (rg * R + r) * 16 + t] = sum[r][n][v];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 16 * kRows; i += kThreads) {
+            const int tok = i / kRows, row = i % kRows;
+            const int64_t tt = t0 + 16 * n + tok, o = tile_b * 16 + row;
+            if (tt < a.T && o < a.m) {
+                float y = 0.0f;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                struct alignas(16) { char d[8 * kB]; } raw;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const char* src = row[t] + (whole * kChunk + step * kStep + e) * kB;
-                    if constexpr (kB == 4) reinterpret_cast<uint32_t*>(raw.d)[e] = e < k ? *(const uint32_t*)src : 0;
-                    else if constexpr (kB == 2) reinterpret_cast<uint16_t*>(raw.d)[e] = e < k ? *(const uint16_t*)src : 0;
-                    else raw.d[e] = e < k ? *src : 0;
-                }
-                typename M::Op x[M::kPieces];
-                operand<MATH, W>(raw.d, x);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    typename M::Acc acc = {0, 0, 0, 0};
-#pragma unroll
-                    for (int q = 0; q < M::kPieces; ++q) acc = M::mma(x[q], b[r], acc);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) sum[r][t][v] = fmaf(s[r], (float)acc[v], sum[r][t][v]);
-                }
+                for (int k = 0; k < KS; ++k) y += red[(k * 16 + tok) * kPitch + row];
+                y *= unit<MATH, W>();
+                if (a.xs) y *= a.xs[tt];
+                store_elem(a.y, a.ytype, tt * a.ldy + o, y);
             }
         }
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (r + t) __syncthreads();
-#pragma unroll
-            for (int v = 0; v < 4; ++v) red[w][4 * (lane >> 4) + v][lane & 15] = sum[r][t][v];
-            __syncthreads();
-            if (threadIdx.x < 256) {
-                const int64_t tt = t0 + 16 * t + (threadIdx.x >> 4), o = (tile0 + r) * 16 + (threadIdx.x & 15);
-                if (tt < a.T && o < a.m) {
-                    float y = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kWaves; ++k) y += red[k][threadIdx.x >> 4][threadIdx.x & 15];
-                    y *= unit<MATH, W>();
-                    if (a.xs) y *= a.xs[tt];
-                    store_elem(a.y, a.ytype, tt * a.ldy + o, y);
-                }
-            }
-        }
 }
 
-template <int MATH, int W, int FS, int NT, int R>
-void launch_many(const MvArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.tiles + R - 1) / R) * (unsigned)((a.T + 16 * NT - 1) / (16 * NT)));
-    hipLaunchKernelGGL((k_matvec<MATH, W, FS, NT, R>), grid, dim3(kMvThreads), 0, stream, a);
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW>
+void launch_mm(const MvArgs& a, hipStream_t stream) {
+    const unsigned rows = (unsigned)((a.tiles + R * RW - 1) / (R * RW));
+    const unsigned blocks = (unsigned)((a.T + 16 * NT - 1) / (16 * NT));
+    constexpr size_t red = sizeof(float) * KS * 16 * (16 * R * RW + 4);
+    constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, KS>::kBytes, red);
+    hipLaunchKernelGGL((k_matmul<MATH, W, FS, NT, R, KS, RW>), dim3(rows * blocks), dim3(64 * KS * RW), lds, stream, a,
+                       (int)blocks);
 }
 
 template <int MATH, int W, int FS, int R>
@@ -506,12 +625,14 @@ void launch_mv(const MvArgs& a, hipStream_t stream) {
         if (a.tiles >= 1024) launch_few<MATH, W, FS, 2>(a, stream);
         else launch_few<MATH, W, FS, 1>(a, stream);
     } else if (a.T <= 16) {
-        if (a.tiles >= 512) launch_many<MATH, W, FS, 1, 2>(a, stream);
-        else launch_many<MATH, W, FS, 1, 1>(a, stream);
-    } else if (a.T <= 32 || MATH == kF32 || FS == 1) {
-        launch_many<MATH, W, FS, 2, 2>(a, stream);
-    } else {
-        if constexpr (MATH != kF32 && FS != 1) launch_many<MATH, W, FS, 4, 2>(a, stream);
+        constexpr int KS = MATH == kF32 ? 4 : 8;
+        if (a.tiles >= 512) launch_mm<MATH, W, FS, 1, 2, KS, 1>(a, stream);
+        else launch_mm<MATH, W, FS, 1, 1, KS, 1>(a, stream);
+    } else if (a.T <= 32 || MATH == kF32) {
+        launch_mm<MATH, W, FS, 2, 2, MATH == kF32 ? 2 : 4, 2>(a, stream);
+    } else if constexpr (MATH != kF32) {
+        if (a.T <= 128) launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
+        else launch_mm<MATH, W, FS, 4, 4, 1, 4>(a, stream);
     }
 }
 
