@@ -120,7 +120,7 @@ bool same_rows(const Rows& a, const Rows& b) { return a.p == b.p && a.pitch == b
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 
 bool bad_pack_shape(int64_t m, int64_t n, int32_t bits, int64_t group) {
-    if (m <= 0 || n <= 0 || m > kMaxDim || n > kMaxDim || bits < 1 || bits > 4) return true;
+    if (m <= 0 || n <= 0 || m > kMaxDim || n > kMaxDim / 4 || bits < 1 || bits > 4) return true;  // 4 n fits 31 bits
     if (group != 0 && (group < 32 || group > kMaxDim || (group & (group - 1)) != 0)) return true;
     return false;
 }

@@ -37,6 +37,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRowTile = 16;
@@ -45,8 +46,6 @@ constexpr int kChunk = 128;       // columns of a chunk
 constexpr int kSteps = kChunk / kStep;
 constexpr int kWaves = 8;         // waves of a product workgroup that split the columns
 constexpr int kMvThreads = 64 * kWaves;
-constexpr int kFew = 4;           // tokens that the kernel with x in LDS takes
-constexpr int kFewLds = 65536;    // bytes of x that it stages at a time
 
 struct MvArgs {
     const char* codes;
@@ -196,19 +195,20 @@ __device__ __forceinline__ u32x2 even_odd(u32x2 x) {
 }
 
 // fp32 as three bf16 pieces, cut by truncation: 8 significant bits each, their sum is x
-// exactly. An infinity or NaN stays in the first piece (the others would be NaN).
-__device__ __forceinline__ void split3(const float (&x)[8], bf16x8 (&p)[3]) {
-    uint32_t h[8], m[8], l[8];
+// exactly. An infinity or NaN, whose remainder is NaN, stays in the first piece; a NaN is
+// quieted first, so that it does not lose its whole payload to the cut.
+__device__ __forceinline__ void split3(u32x8 x, bf16x8 (&p)[3]) {
+    u32x8 h, m, l;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, x[e]);
-        const bool special = (b & 0x7F800000u) == 0x7F800000u;
-        h[e] = (b & 0xFFFF0000u) | ((special && (b & 0x7FFFFFu)) ? 0x00400000u : 0u);
-        const float r = x[e] - __builtin_bit_cast(float, b & 0xFFFF0000u);
-        m[e] = special ? 0u : __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
-        l[e] = special ? 0u : __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, m[e]));
+        const float v = __uint_as_float(x[e]);
+        h[e] = __float_as_uint(__builtin_canonicalizef(v));
+        float r = v - __uint_as_float(x[e] & 0xFFFF0000u);
+        r = r == r ? r : 0.0f;
+        m[e] = __float_as_uint(r);
+        l[e] = __float_as_uint(r - __uint_as_float(m[e] & 0xFFFF0000u));
     }
-    const auto pack = [](const uint32_t (&a)[8]) {
+    const auto pack = [](u32x8 a) {
         u32x4 d;
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_perm(a[2 * e + 1], a[2 * e], 0x07060302u);
@@ -224,13 +224,28 @@ template <int MATH, int W>
 __device__ __forceinline__ void operand(const char* src, typename Mt<MATH>::Op (&p)[Mt<MATH>::kPieces]) {
     constexpr int kB = Mt<MATH>::kBytes;
     if constexpr (MATH == kF32) {
-        float x[8];
-        __builtin_memcpy(x, __builtin_assume_aligned(src, 16), sizeof x);
+        u32x8 x;
+        __builtin_memcpy(&x, __builtin_assume_aligned(src, 16), sizeof x);
         split3(x, p);
     } else {
         __builtin_memcpy(&p[0], __builtin_assume_aligned(src, 8 * kB), 8 * kB);
         if constexpr (W == 2 && kB == 1) p[0] = even_odd(p[0]);
     }
+}
+
+// The 16 bytes of a row of x from byte `at` on that the row's end, byte `end`, cuts: zeros
+// from there on. (All other units are whole, or past the end.)
+template <int kB>
+__device__ __forceinline__ u32x4 cut_unit(const char* __restrict__ row, int at, int end) {
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; e += kB)
+        if (at + e < end) {
+            uint32_t w = 0;
+            __builtin_memcpy(&w, row + at + e, kB);
+            v[e / 4] |= w << (8 * (e & 3));
+        }
+    return v;
 }
 
 // ---------------------------------------------------------------- the products
@@ -266,90 +281,109 @@ struct Stream {
     }
 };
 
-// Few tokens (T <= 4): the lanes of an A operand that stand for tokens past the last would
-// each fetch x again, and the address units, not HBM, would set the pace. So x is staged
-// in LDS, `slab` columns at a time (all of them up to 64 KB), where lanes share a read.
-// The 8 waves split the columns (wave w takes chunks w, w + 8, ...); their sums meet in
-// LDS and are added in a fixed order.
-template <int MATH, int W, int FS, int R>
-__global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a, int64_t slab, int pitch) {
+// Few tokens (T <= TB): the lanes of an A operand that stand for tokens past the last would
+// fetch x again, and rows a power of two apart fall on one memory channel, if operands came
+// straight from memory: the address units, not HBM, would set the pace. So each wave stages
+// x for its next PF chunks by rows in an LDS area of its own, where the surplus lanes share
+// a read: loads of a set are in flight while the set before is multiplied, and no wave
+// waits for another. The 8 waves split the columns (wave w takes chunks w, w + 8, ...);
+// their sums meet in LDS at the end and are added in a fixed order.
+template <int MATH, int PF, int TB>
+struct FewShape {
+    static constexpr int kB = Mt<MATH>::kBytes;
+    static constexpr int kRowUnits = PF * kChunk * kB / 16;           // 16-byte units of a token row in a set
+    static constexpr int kUnits = (TB * kRowUnits + 63) / 64;         // units of a lane
+    static constexpr int kPitch = kRowUnits * 16 + 16;                // rows 4 banks apart
+    static constexpr int kBytes = TB * kPitch;                        // of a wave
+};
+
+template <int MATH, int W, int FS, int R, int PF, int TB>
+__global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
     using M = Mt<MATH>;
-    constexpr int kB = M::kBytes, PF = 16 / (W * R);  // 4 KB of weights in flight per wave
     using St = Stream<W, FS, R, PF>;
-    extern __shared__ __align__(16) char xs[];
-    __shared__ float red[kWaves][R][kFew][16];
+    using Sh = FewShape<MATH, PF, TB>;
+    constexpr int kB = M::kBytes;
+    extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    char* xs = lds + w * Sh::kBytes;
     const int64_t tile0 = (int64_t)blockIdx.x * R;
-    St st(a, tile0, lane);
+    const int T = (int)a.T, end = (int)a.n * kB;  // bytes of a row
     const int mine = a.nc > w ? (int)((a.nc - w + kWaves - 1) / kWaves) : 0;  // this wave's chunks
+    u32x4 x[Sh::kUnits];
+    // unit i of this lane in the set from chunk i0 on: token, place in the token's LDS row, byte in the row of x
+    const auto token_of = [&](int i) { return (lane + i * 64) / Sh::kRowUnits; };
+    const auto place_of = [&](int i) { return (lane + i * 64) % Sh::kRowUnits; };
+    const auto byte_of = [&](int i, int i0) {
+        constexpr int kPer = kChunk * kB / 16;
+        const int u = place_of(i);
+        return ((i0 + u / kPer) * kWaves + w) * kChunk * kB + u % kPer * 16;
+    };
+    const auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < Sh::kUnits; ++i) {
+            x[i] = u32x4{0, 0, 0, 0};
+            if (token_of(i) < T && byte_of(i, i0) + 16 <= end)
+                __builtin_memcpy(&x[i], a.x + token_of(i) * a.ldx * kB + byte_of(i, i0), 16);
+        }
+    };
+    St st(a, tile0, lane);
+    load(0);
 #pragma unroll
     for (int p = 0; p < PF; ++p)
         if (p < mine) st.fetch(p, w + p * kWaves);
     float sum[R][4] = {};
-    const char* xl = xs + min((lane & 15), (int)a.T - 1) * pitch + (lane >> 4) * 8 * kB;
-    int i = 0;
-    for (int64_t k0 = 0; k0 < a.n; k0 += slab) {
-        if (k0) __syncthreads();
-        const int units = (int)(slab * kB / 16);
-        const int64_t left = (a.n - k0) * kB;
-        for (int t = 0; t < (int)a.T; ++t) {
-            const char* row = a.x + ((int64_t)t * a.ldx + k0) * kB;
-            for (int u = threadIdx.x; u < units; u += kMvThreads) {
-                u32x4 v = {0, 0, 0, 0};
-                if (u * 16 + 16 <= left) {
-                    __builtin_memcpy(&v, row + u * 16, 16);
-                } else {  // zeros from column n on
+    const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * kB;
+    for (int i0 = 0; i0 < mine; i0 += PF) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (u * 16 + e < left) v[e / 4] |= (uint32_t)(uint8_t)row[u * 16 + e] << (8 * (e & 3));
-                }
-                *reinterpret_cast<u32x4*>(xs + t * pitch + u * 16) = v;
-            }
+        for (int i = 0; i < Sh::kUnits; ++i)
+            if (token_of(i) < T) *reinterpret_cast<u32x4*>(xs + token_of(i) * Sh::kPitch + place_of(i) * 16) = x[i];
+        if (end % 16 != 0) {  // the unit that the row ends in, if it is in this set
+            const int at = end & ~15, c = at / (kChunk * kB), p = c / kWaves - i0;
+            if (c % kWaves == w && p >= 0 && p < PF && lane < T)
+                *reinterpret_cast<u32x4*>(xs + lane * Sh::kPitch + (p * kChunk - c * kChunk) * kB + at) =
+                    cut_unit<kB>(a.x + lane * a.ldx * kB, at, end);
         }
-        __syncthreads();
-        const int end = (int)min<int64_t>(mine, ((k0 + slab) / kChunk - w + kWaves - 1) / kWaves);
-        const char* xk = xl - k0 * kB;
-        for (; i < end; i += PF) {  // slabs are whole multiples of PF chunks per wave, or the last
+        if (i0 + PF < mine) load(i0 + PF);
 #pragma unroll
-            for (int p = 0; p < PF; ++p) {
-                if (i + p >= end) break;
-                const int64_t c = w + (int64_t)(i + p) * kWaves;
+        for (int p = 0; p < PF; ++p) {
+            if (i0 + p >= mine) break;
+            const char* xk = xl + p * kChunk * kB;
 #pragma unroll
-                for (int f = 0; f < St::kUnits; ++f) {
-                    typename M::Acc acc[R] = {};
+            for (int f = 0; f < St::kUnits; ++f) {
+                typename M::Acc acc[R] = {};
 #pragma unroll
-                    for (int j = 0; j < FS; ++j) {
-                        typename M::Op x[M::kPieces];
-                        operand<MATH, W>(xk + (c * kChunk + (f * FS + j) * kStep) * kB, x);
+                for (int j = 0; j < FS; ++j) {
+                    typename M::Op v[M::kPieces];
+                    operand<MATH, W>(xk + (f * FS + j) * kStep * kB, v);
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const typename M::Op b = weights<MATH, W>(st.d[p][r], f * FS + j);
+                    for (int r = 0; r < R; ++r) {
+                        const typename M::Op b = weights<MATH, W>(st.d[p][r], f * FS + j);
 #pragma unroll
-                            for (int q = 0; q < M::kPieces; ++q) acc[r] = M::mma(x[q], b, acc[r]);
-                        }
+                        for (int q = 0; q < M::kPieces; ++q) acc[r] = M::mma(v[q], b, acc[r]);
                     }
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) sum[r][v] = fmaf(st.s[p][r][f], (float)acc[r][v], sum[r][v]);
                 }
-                if (i + p + PF < mine) st.fetch(p, c + PF * kWaves);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sum[r][v] = fmaf(st.s[p][r][f], (float)acc[r][v], sum[r][v]);
             }
+            if (i0 + p + PF < mine) st.fetch(p, w + (int64_t)(i0 + p + PF) * kWaves);
         }
     }
-    if (lane < 16)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int v = 0; v < kFew; ++v) red[w][r][v][lane] = sum[r][v];
     __syncthreads();
-    if (threadIdx.x < R * kFew * 16) {
-        const int r = threadIdx.x / (kFew * 16), t = (threadIdx.x >> 4) % kFew;
-        const int64_t row = (tile0 + r) * 16 + (threadIdx.x & 15);
-        if (t < a.T && row < a.m) {
+    float* red = reinterpret_cast<float*>(lds);  // [wave][tile][token][16 rows + 1]
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[((w * R + r) * 16 + 4 * (lane >> 4) + v) * 17 + (lane & 15)] = sum[r][v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < T * R * 16; i += kMvThreads) {
+        const int t = i / (R * 16), r = i / 16 % R;
+        const int64_t row = (tile0 + r) * 16 + (i & 15);
+        if (row < a.m) {
             float y = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) y += red[k][r][t][threadIdx.x & 15];
+            for (int k = 0; k < kWaves; ++k) y += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
             y *= unit<MATH, W>();
             if (a.xs) y *= a.xs[t];
             store_elem(a.y, a.ytype, t * a.ldy + row, y);
@@ -374,8 +408,6 @@ template <int MATH, int FS>
 struct MmOp {  // the MFMA of a kSub-step operand
     static constexpr int kSub = FS == 4 ? (MATH == kI8 ? 2 : MATH == kF8 ? 4 : 1) : 1;
 };
-typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
-
 __device__ __forceinline__ i32x4 mma_i8x64(u32x4 a, u32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0,
                                                  0);
@@ -416,68 +448,76 @@ void k_matmul(MvArgs a, int token_blocks) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kg = wave / RW, rg = wave % RW;
     const int q = lane >> 4, t = lane & 15;
 
-    struct Unit { u32x4 v[kB == 4 ? 2 : 1]; };
-    Unit raw[kUnits];
+    constexpr int kParts = kB == 4 ? 2 : 1;  // 16-byte parts of a unit
+    u32x4 raw[kUnits][kParts];
     // unit i of this thread: token row and unit in the row
     const auto row_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) / kRowUnits; };
     const auto unit_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) % kRowUnits; };
-    const auto load = [&](int64_t it) {
+    const int end = (int)a.n * kB;  // bytes of a row
+    const auto load = [&](int it) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int64_t row = min(t0 + row_of(i), a.T - 1);
-            const int64_t k = it * KS * kChunk + unit_of(i) * kUnitCols;
-            const char* src = a.x + (row * a.ldx + k) * kB;
-            if (k + kUnitCols <= a.n) {
-                __builtin_memcpy(&raw[i], src, sizeof(Unit));
-            } else {  // zeros from column n on
-                raw[i] = Unit{};
-                const int left = (int)max<int64_t>(0, (a.n - k) * kB);
+            const int at = (it * KS * kChunk + unit_of(i) * kUnitCols) * kB;
 #pragma unroll
-                for (int e = 0; e < (int)sizeof(Unit) / kB; ++e)
-                    if (e * kB < left) {
-                        uint32_t w = 0;
-                        __builtin_memcpy(&w, src + e * kB, kB);
-                        raw[i].v[e * kB / 16][e * kB / 4 % 4] |= w << (8 * (e * kB & 3));
-                    }
+            for (int h = 0; h < kParts; ++h) {
+                raw[i][h] = u32x4{0, 0, 0, 0};
+                if (at + 16 * kParts <= end)
+                    __builtin_memcpy(&raw[i][h], a.x + row * a.ldx * kB + at + 16 * h, 16);
             }
         }
     };
-    const auto store = [&](char* buf) {
+    // unit `ru` of a token row's iteration, into its operands' slots
+    const auto put = [&](char* buf, int row, int ru, const u32x4 (&v)[kParts]) {
+        const int u = ru % (kChunk / kUnitCols), ck = ru / (kChunk / kUnitCols);
+        char* dst = buf + (ck * NT + (row >> 4)) * Tile::kSlabs * 1024;
+        if constexpr (kB == 1) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
+            const u32x2 lo = {v[0][0], v[0][1]}, hi = {v[0][2], v[0][3]};
+            const int step = u >> 1, pair = step >> 1;
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int row = row_of(i), u = unit_of(i) % (kChunk / kUnitCols), ck = unit_of(i) / (kChunk / kUnitCols);
-            char* dst = buf + (ck * NT + (row >> 4)) * Tile::kSlabs * 1024;
-            if constexpr (kB == 1) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
-                const u32x2 lo = {raw[i].v[0][0], raw[i].v[0][1]}, hi = {raw[i].v[0][2], raw[i].v[0][3]};
+            for (int h = 0; h < 2; ++h) {
+                const int qq = 2 * (u & 1) + h;
+                const u32x2 w = h ? hi : lo;
+                *reinterpret_cast<u32x2*>(dst + pair * 1024 + (qq * 16 + ((row ^ (4 * pair + qq)) & 15)) * 16 +
+                                          (step & 1) * 8) = W == 2 ? even_odd(w) : w;
+            }
+        } else {  // columns 8 u ..: step u / 4, lanes of q = u % 4
+            const int at = (u >> 2) * 1024 + ((u & 3) * 16 + ((row ^ u) & 15)) * 16;
+            if constexpr (kB == 4) {
+                u32x8 x;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int step = u >> 1, qq = 2 * (u & 1) + h;
-                    const u32x2 v = h ? hi : lo;
-                    *reinterpret_cast<u32x2*>(dst + (step >> 1) * 1024 +
-                                              (qq * 16 + ((row ^ (4 * (step >> 1) + qq)) & 15)) * 16 + (step & 1) * 8) =
-                        W == 2 ? even_odd(v) : v;
-                }
-            } else {  // columns 8 u ..: step u / 4, lanes of q = u % 4
-                const int at = (u >> 2) * 1024 + ((u & 3) * 16 + ((row ^ u) & 15)) * 16;
-                if constexpr (kB == 4) {
-                    float x[8];
-                    __builtin_memcpy(x, &raw[i], sizeof x);
-                    bf16x8 p[3];
-                    split3(x, p);
+                for (int e = 0; e < 8; ++e) x[e] = v[e >> 2][e & 3];
+                bf16x8 p[3];
+                split3(x, p);
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) *reinterpret_cast<bf16x8*>(dst + c * 4096 + at) = p[c];
-                } else {
-                    *reinterpret_cast<u32x4*>(dst + at) = raw[i].v[0];
-                }
+                for (int c = 0; c < 3; ++c) *reinterpret_cast<bf16x8*>(dst + c * 4096 + at) = p[c];
+            } else {
+                *reinterpret_cast<u32x4*>(dst + at) = v[0];
             }
         }
+    };
+    const auto store = [&](int it, char* buf) {
+        // the unit that a row's end cuts, if there is one in this iteration (else -1)
+        const int first = it * KS * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
+        const int cut = end != last && last >= first && last < first + KS * kChunk * kB ? (last - first) / (16 * kParts) : -1;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+            if (unit_of(i) != cut) put(buf, row_of(i), unit_of(i), raw[i]);
+        if (cut >= 0)
+            for (int row = threadIdx.x; row < 16 * NT; row += kThreads) {
+                const char* src = a.x + min(t0 + row, a.T - 1) * a.ldx * kB;
+                u32x4 v[kParts];
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) v[h] = cut_unit<kB>(src, last + 16 * h, end);
+                put(buf, row, cut, v);
+            }
     };
 
     St st(a, tile_b + rg * R, lane);
     const int iters = (int)((a.nc + KS - 1) / KS);
     load(0);
     if (kg < a.nc) st.fetch(0, kg);
-    store(lds);
+    store(0, lds);
     __syncthreads();
 
     float sum[R][NT][4] = {};
@@ -564,7 +604,7 @@ void k_matmul(MvArgs a, int token_blocks) {
                             sum[r][n][v] = fmaf(st.s[slot][r][f], (float)acc[r][n][v], sum[r][n][v]);
             }
         }
-        if (more) store(lds + (~it & 1) * Tile::kBytes);
+        if (more) store(it + 1, lds + (~it & 1) * Tile::kBytes);
         __syncthreads();
     };
     for (int it = 0; it < iters; it += 2) {
@@ -606,28 +646,24 @@ void launch_mm(const MvArgs& a, hipStream_t stream) {
                        (int)blocks);
 }
 
-template <int MATH, int W, int FS, int R>
+template <int MATH, int W, int FS, int R, int PF, int TB>
 void launch_few(const MvArgs& a, hipStream_t stream) {
-    constexpr int kB = Mt<MATH>::kBytes, kAll = kChunk * kWaves * (16 / (W * R));
-    // whole rounds of every wave's chunks in flight, unless the row ends first
-    int64_t slab = kFewLds / (a.T * kB) / kAll * kAll;
-    if (slab == 0) slab = kAll;
-    slab = std::min<int64_t>(slab, a.nc * kChunk);
-    const int pitch = (int)(slab * kB) + 16;
+    constexpr size_t red = sizeof(float) * kWaves * R * 16 * 17;
+    constexpr size_t lds = std::max<size_t>((size_t)kWaves * FewShape<MATH, PF, TB>::kBytes, red);
     const dim3 grid((unsigned)((a.tiles + R - 1) / R));
-    hipLaunchKernelGGL((k_matvec_few<MATH, W, FS, R>), grid, dim3(kMvThreads), (size_t)(a.T * pitch), stream, a, slab,
-                       pitch);
+    hipLaunchKernelGGL((k_matvec_few<MATH, W, FS, R, PF, TB>), grid, dim3(kMvThreads), lds, stream, a);
 }
 
 template <int MATH, int W, int FS>
 void launch_mv(const MvArgs& a, hipStream_t stream) {
-    if (a.T <= kFew) {
-        if (a.tiles >= 1024) launch_few<MATH, W, FS, 2>(a, stream);
-        else launch_few<MATH, W, FS, 1>(a, stream);
+    if (a.T <= 4) {
+        // 4 KB of weights in flight per wave
+        if (a.tiles >= 1024) launch_few<MATH, W, FS, 2, 8 / W, 4>(a, stream);
+        else launch_few<MATH, W, FS, 1, 16 / W, 4>(a, stream);
     } else if (a.T <= 16) {
-        constexpr int KS = MATH == kF32 ? 4 : 8;
-        if (a.tiles >= 512) launch_mm<MATH, W, FS, 1, 2, KS, 1>(a, stream);
-        else launch_mm<MATH, W, FS, 1, 1, KS, 1>(a, stream);
+        constexpr int PF = MATH == kF32 ? 1 : 2;
+        if (a.tiles >= 512) launch_few<MATH, W, FS, 2, PF, 16>(a, stream);
+        else launch_few<MATH, W, FS, 1, PF, 16>(a, stream);
     } else if (a.T <= 32 || MATH == kF32) {
         launch_mm<MATH, W, FS, 2, 2, MATH == kF32 ? 2 : 4, 2>(a, stream);
     } else if constexpr (MATH != kF32) {
