@@ -569,36 +569,39 @@ _WIDE = (torch.float32, torch.float16, torch.bfloat16)
 _CODED = (torch.int8, torch.float8_e4m3fn)
 
 
-# A call for one token takes the host about as long as the GPU, so these checks read each
-# property of a tensor once.
-def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
-    """Validate token rows on the current device; returns their leading dimension."""
+# A call for one token takes the host longer than the GPU, so these checks read each
+# property of a tensor once, and what a call allocates itself is not checked again.
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The current device, for a call whose first tensor is `t`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA/ROCm tensor" % name)
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s must be on the current device" % name)
+        raise ValueError("%s must be a CUDA/ROCm tensor on the current device" % name)
+    return torch._C._cuda_getDevice()
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, dev: int, shape=None) -> int:
+    """Validate token rows on the current device `dev`; returns their leading dimension."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError("%s must be a CUDA/ROCm tensor on the current device" % name)
     size = t.shape
     if t.dtype not in dtypes or len(size) != 2:
         raise ValueError("%s must be a 2-D tensor of %s" % (name, ", ".join(str(d) for d in dtypes)))
+    if shape is not None and size != shape:
+        raise ValueError("%s must be %d x %d" % ((name,) + tuple(shape)))
     rows, cols = size
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError("%s must be %d x %d" % ((name,) + shape))
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
     if rows > 1:
         if ld < cols:
             raise ValueError("%s must not have overlapping rows" % name)
-        return max(ld, 1)
-    return max(cols, 1)
+        return ld or 1
+    return cols or 1
 
 
-def _token_scales(t: Optional[torch.Tensor], name: str, T: int) -> Optional[int]:
+def _token_scales(t: torch.Tensor, name: str, T: int, dev: int) -> int:
     """The address of a vector of T float32 factors on the current device."""
-    if t is None:
-        return None
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device()
-            or t.dtype != torch.float32 or t.numel() != T or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.float32 or t.numel() != T
+            or not t.is_contiguous()):
         raise ValueError("%s must be a contiguous float32 vector of length %d on the current device" % (name, T))
     return t.data_ptr()
 
@@ -612,6 +615,9 @@ class PackedWeight:
     bits: int
     group: int
 
+    def __post_init__(self):
+        self.nbytes = self.data.numel()
+
 
 def pack(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -> PackedWeight:
     """Lay out a solve's codes (m x n uint8) and scales for matvec().
@@ -619,7 +625,8 @@ def pack(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -
     group = 0: one scale per row, scales (m,) or (m, 1), as solve() returns them; else a
     power of two >= 32, with scales (m, ceil(n / group)). bits 1..4.
     """
-    ldc = _rows(codes, "codes", (torch.uint8,))
+    dev = _device_of(codes, "codes")
+    ldc = _rows(codes, "codes", (torch.uint8,), dev)
     m, n = codes.shape
     bits, group = int(bits), int(group)
     if isinstance(scales, torch.Tensor) and scales.dim() == 1 and group == 0:
@@ -627,7 +634,7 @@ def pack(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -
     nb = LIB.bakron_packed_bytes(m, n, bits, group)
     if nb == 0:
         raise ValueError("pack takes m, n >= 1, bits 1..4 and group 0 or a power of two >= 32")
-    lds = _rows(scales, "scales", (torch.float32,), (m, -(-n // group) if group else 1))
+    lds = _rows(scales, "scales", (torch.float32,), dev, (m, -(-n // group) if group else 1))
     data = torch.empty(nb, dtype=torch.uint8, device=codes.device)
     _check("bakron_pack", LIB.bakron_pack(codes.data_ptr(), m, n, ldc, bits, scales.data_ptr(), lds, group,
                                           data.data_ptr(), nb, _stream()))
@@ -646,27 +653,32 @@ def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = N
     if one:
         x = x.unsqueeze(0)
         out = out.unsqueeze(0) if isinstance(out, torch.Tensor) and out.dim() == 1 else out
-    ldx = _rows(x, "x", ROW_TYPES)
+    dev = _device_of(x, "x")
+    ldx = _rows(x, "x", ROW_TYPES, dev)
     T, n = x.shape
+    m = w.m
     if n != w.n:
         raise ValueError("x must have %d columns" % w.n)
-    if w.data.get_device() != x.get_device():
+    if w.data.get_device() != dev:
         raise ValueError("the packed layer must be on x's device")
-    xs = _token_scales(x_scale, "x_scale", T)
+    xtype = x.dtype
     if out is None:
         if out_dtype is None:
-            out_dtype = x.dtype if x.dtype in _WIDE else torch.bfloat16
-        if out_dtype not in _WIDE:
+            out_dtype = xtype if xtype in _WIDE else torch.bfloat16
+        elif out_dtype not in _WIDE:
             raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in _WIDE))
-        out = x.new_empty((T, w.m), dtype=out_dtype)
-        ldy = w.m
+        out = x.new_empty((T, m), dtype=out_dtype)
+        ldy = m
     else:
-        ldy = _rows(out, "out", _WIDE, (T, w.m))
+        ldy = _rows(out, "out", _WIDE, dev, (T, m))
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out must be a tensor of %s" % out_dtype)
-    _check("bakron_matvec", LIB.bakron_matvec(w.data.data_ptr(), w.data.numel(), w.m, w.n, w.bits, w.group,
-                                              x.data_ptr(), ROW_TYPES[x.dtype], T, ldx, xs, out.data_ptr(),
-                                              ROW_TYPES[out.dtype], ldy, _stream()))
+        out_dtype = out.dtype
+    st = LIB.bakron_matvec(w.data.data_ptr(), w.nbytes, m, n, w.bits, w.group, x.data_ptr(), ROW_TYPES[xtype], T, ldx,
+                           None if x_scale is None else _token_scales(x_scale, "x_scale", T, dev), out.data_ptr(),
+                           ROW_TYPES[out_dtype], ldy, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("bakron_matvec", st)
     return out[0] if one else out
 
 
@@ -688,44 +700,50 @@ def rmsnorm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Opti
     come with one scale per token: the values are scale[:, None] * y. sum receives h in x's
     type when a residual is given (sum_out=residual updates it in place).
     """
-    ldx = _rows(x, "x", _WIDE)
-    T, n = shape = tuple(x.shape)
+    dev = _device_of(x, "x")
+    ldx = _rows(x, "x", _WIDE, dev)
+    T, n = shape = x.shape
     xtype = x.dtype
-    ldr = ldh = gtype = 0
-    r = h = g = None
+    code = gtype = ROW_TYPES[xtype]
+    ldr = ldh = 0
+    r = h = g = ys = None
     if residual is not None:
-        ldr = _rows(residual, "residual", (xtype,), shape)
+        ldr = _rows(residual, "residual", (xtype,), dev, shape)
         r = residual.data_ptr()
         if sum_out is None:
-            sum_out = x.new_empty(shape)
-    if sum_out is not None:
-        ldh = _rows(sum_out, "sum_out", (xtype,), shape)
+            sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            ldh, h = n, sum_out.data_ptr()
+    if h is None and sum_out is not None:
+        ldh = _rows(sum_out, "sum_out", (xtype,), dev, shape)
         h = sum_out.data_ptr()
     if gain is not None:
-        if (not isinstance(gain, torch.Tensor) or gain.device != x.device or gain.numel() != n
-                or not gain.is_contiguous() or gain.dtype not in (xtype, torch.float32)):
+        if (not isinstance(gain, torch.Tensor) or gain.get_device() != dev or gain.numel() != n
+                or not gain.is_contiguous() or (gain.dtype != xtype and gain.dtype != torch.float32)):
             raise ValueError("gain must be a contiguous vector of length %d, float32 or x's type" % n)
         g, gtype = gain.data_ptr(), ROW_TYPES[gain.dtype]
     if out is None:
-        out_dtype = xtype if out_dtype is None else out_dtype
-        if out_dtype not in ROW_TYPES:
+        if out_dtype is None:
+            out_dtype = xtype
+        elif out_dtype not in ROW_TYPES:
             raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in ROW_TYPES))
-        out = x.new_empty(shape, dtype=out_dtype)
-        ldy = max(n, 1)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
+        ldy = n or 1
     else:
-        ldy = _rows(out, "out", ROW_TYPES, shape)
+        ldy = _rows(out, "out", ROW_TYPES, dev, shape)
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out must be a tensor of %s" % out_dtype)
-    ys = None
-    if out.dtype in _CODED:
+        out_dtype = out.dtype
+    if out_dtype in _CODED:
         if scale_out is None:
             scale_out = x.new_empty(T, dtype=torch.float32)
-        ys = _token_scales(scale_out, "scale_out", T)
+            ys = scale_out.data_ptr()
+        else:
+            ys = _token_scales(scale_out, "scale_out", T, dev)
     elif scale_out is not None:
         raise ValueError("scale_out goes with an 8-bit out")
-    seed = 0 if rotate_seed is None else int(rotate_seed) & (2**64 - 1)
-    _check("bakron_rmsnorm",
-           LIB.bakron_rmsnorm(x.data_ptr(), ROW_TYPES[xtype], T, n, ldx, r, ldr, h, ldh, g, gtype, eps,
-                              0 if rotate_seed is None else 1, seed, out.data_ptr(), ROW_TYPES[out.dtype], ldy, ys,
-                              _stream()))
+    rotate, seed = (0, 0) if rotate_seed is None else (1, int(rotate_seed) & (2**64 - 1))
+    st = LIB.bakron_rmsnorm(x.data_ptr(), code, T, n, ldx, r, ldr, h, ldh, g, gtype, eps, rotate, seed, out.data_ptr(),
+                            ROW_TYPES[out_dtype], ldy, ys, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("bakron_rmsnorm", st)
     return NormResult(out, scale_out, sum_out)
