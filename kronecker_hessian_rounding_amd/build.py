@@ -34,7 +34,8 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(os.path.dirname(HERE), "include"),
 ]
-FILE_FLAGS = {"bk_ldl.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+FILE_FLAGS = {src: VGPR_FORM for src in SOURCES if src == "bk_ldl.hip" or src.startswith("bk_matvec_")}
 
 
 def _scratch_users(remarks: str):

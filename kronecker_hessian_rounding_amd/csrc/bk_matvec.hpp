@@ -25,6 +25,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bk_common.hpp"
 #include "bk_internal.hpp"
@@ -404,20 +405,66 @@ __global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
 // lane slot is (q, t ^ u) for token t, which spreads a row's units over the banks. fp32 is
 // cut into its three pieces on the way in. Of 8-bit types, 16 bytes of a lane are its
 // columns of two steps.
+//
+// MmOp: the MFMA of kSub steps, its operands from a share of weights and from LDS. Whole
+// chunks (FS = 4) take int8 two steps and e4m3 four steps at a time, at twice the rate.
 template <int MATH, int FS>
-struct MmOp {  // the MFMA of a kSub-step operand
+struct MmOp {
+    using M = Mt<MATH>;
+    static constexpr bool kByte = M::kBytes == 1;
     static constexpr int kSub = FS == 4 ? (MATH == kI8 ? 2 : MATH == kF8 ? 4 : 1) : 1;
+    using Op = std::conditional_t<kSub == 2, u32x4, std::conditional_t<kSub == 4, u32x8, typename M::Op>>;
+    template <int W>
+    static __device__ __forceinline__ Op weight(typename Share<W>::T d, int step) {
+        if constexpr (kSub == 1) {
+            return weights<MATH, W>(d, step);
+        } else {
+            Op b;
+#pragma unroll
+            for (int h = 0; h < kSub; ++h) {
+                const u32x2 w = weights<MATH, W>(d, step + h);
+                b[2 * h] = w[0];
+                b[2 * h + 1] = w[1];
+            }
+            return b;
+        }
+    }
+    static __device__ __forceinline__ void read(Op (&x)[M::kPieces], const char* buf, int step, int q, int t) {
+        if constexpr (kByte) {
+            Op v;
+#pragma unroll
+            for (int h = 0; h < (kSub + 1) / 2; ++h) {
+                const int pair = (step >> 1) + h;
+                const char* p = buf + pair * 1024 + ((t ^ (4 * pair + q)) & 15) * 16;
+                if constexpr (kSub == 1) {
+                    v = *reinterpret_cast<const u32x2*>(p + (step & 1) * 8);
+                } else {
+                    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * h + e] = w[e];
+                }
+            }
+            x[0] = v;
+        } else {
+#pragma unroll
+            for (int p = 0; p < M::kPieces; ++p)
+                x[p] = *reinterpret_cast<const Op*>(buf + (p * 4 + step) * 1024 + ((t ^ (4 * step + q)) & 15) * 16);
+        }
+    }
+    static __device__ __forceinline__ typename M::Acc mma(Op a, Op b, typename M::Acc c) {
+        if constexpr (kSub == 1) {
+            return M::mma(a, b, c);
+        } else if constexpr (kSub == 2) {
+            return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
+                                                         0, 0, 0);
+        } else {  // both operands e4m3, block scales 2^0
+            typedef int i32x8 __attribute__((ext_vector_type(8)));
+            return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a),
+                                                                    __builtin_bit_cast(i32x8, b), c, 0, 0, 0, 127, 0,
+                                                                    127);
+        }
+    }
 };
-__device__ __forceinline__ i32x4 mma_i8x64(u32x4 a, u32x4 b, i32x4 c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0,
-                                                 0);
-}
-__device__ __forceinline__ f32x4 mma_f8x128(u32x8 a, u32x8 b, f32x4 c) {
-    typedef int i32x8 __attribute__((ext_vector_type(8)));
-    // both operands e4m3, block scales 2^0
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a), __builtin_bit_cast(i32x8, b),
-                                                            c, 0, 0, 0, 127, 0, 127);
-}
 
 template <int MATH, int NT, int KS>
 struct MmTile {
@@ -427,7 +474,7 @@ struct MmTile {
 };
 
 template <int MATH, int W, int FS, int NT, int R, int KS, int RW>
-__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(KS * RW >= 8 ? 2 : 1)))
+__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)))
 void k_matmul(MvArgs a, int token_blocks) {
     using M = Mt<MATH>;
     using St = Stream<W, FS, R, 2>;
@@ -449,21 +496,22 @@ void k_matmul(MvArgs a, int token_blocks) {
     const int q = lane >> 4, t = lane & 15;
 
     constexpr int kParts = kB == 4 ? 2 : 1;  // 16-byte parts of a unit
-    u32x4 raw[kUnits][kParts];
+    constexpr int kAhead = KS > 1 ? 2 : 1;  // iterations that x is fetched ahead: few workgroups hide less
+    u32x4 raw[kAhead][kUnits][kParts];
     // unit i of this thread: token row and unit in the row
     const auto row_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) / kRowUnits; };
     const auto unit_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) % kRowUnits; };
     const int end = (int)a.n * kB;  // bytes of a row
-    const auto load = [&](int it) {
+    const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int64_t row = min(t0 + row_of(i), a.T - 1);
             const int at = (it * KS * kChunk + unit_of(i) * kUnitCols) * kB;
 #pragma unroll
             for (int h = 0; h < kParts; ++h) {
-                raw[i][h] = u32x4{0, 0, 0, 0};
+                to[i][h] = u32x4{0, 0, 0, 0};
                 if (at + 16 * kParts <= end)
-                    __builtin_memcpy(&raw[i][h], a.x + row * a.ldx * kB + at + 16 * h, 16);
+                    __builtin_memcpy(&to[i][h], a.x + row * a.ldx * kB + at + 16 * h, 16);
             }
         }
     };
@@ -496,13 +544,13 @@ void k_matmul(MvArgs a, int token_blocks) {
             }
         }
     };
-    const auto store = [&](int it, char* buf) {
+    const auto store = [&](int it, char* buf, const u32x4 (&from)[kUnits][kParts]) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
         const int first = it * KS * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
         const int cut = end != last && last >= first && last < first + KS * kChunk * kB ? (last - first) / (16 * kParts) : -1;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-            if (unit_of(i) != cut) put(buf, row_of(i), unit_of(i), raw[i]);
+            if (unit_of(i) != cut) put(buf, row_of(i), unit_of(i), from[i]);
         if (cut >= 0)
             for (int row = threadIdx.x; row < 16 * NT; row += kThreads) {
                 const char* src = a.x + min(t0 + row, a.T - 1) * a.ldx * kB;
@@ -515,96 +563,54 @@ void k_matmul(MvArgs a, int token_blocks) {
 
     St st(a, tile_b + rg * R, lane);
     const int iters = (int)((a.nc + KS - 1) / KS);
-    load(0);
+    load(0, raw[0]);
     if (kg < a.nc) st.fetch(0, kg);
-    store(0, lds);
+    if (kAhead == 2 && 1 < iters) load(1, raw[kAhead - 1]);
+    if (kg + KS < a.nc) st.fetch(1, kg + KS);
+    store(0, lds, raw[0]);
     __syncthreads();
 
     float sum[R][NT][4] = {};
     const auto body = [&](int it, int slot) {
         const int64_t c = (int64_t)it * KS + kg;
-        const bool more = it + 1 < iters;
-        if (more) load(it + 1);
-        if (c + KS < a.nc) st.fetch(slot ^ 1, c + KS);
+        if (it + kAhead < iters) load(it + kAhead, raw[kAhead == 2 ? slot : 0]);
         const char* buf = lds + (it & 1) * Tile::kBytes + kg * NT * Tile::kSlabs * 1024 + q * 256;
         if (c < a.nc) {
+            using Mm = MmOp<MATH, FS>;
+            constexpr int kParts = FS / Mm::kSub;  // MFMAs of a sum
+            typename Mm::Op b[St::kUnits][kParts][R];
+            float s[St::kUnits][R];
 #pragma unroll
-            for (int f = 0; f < St::kUnits; ++f) {
-                typename M::Acc acc[R][NT] = {};
-                constexpr int kSub = MmOp<MATH, FS>::kSub;
+            for (int f = 0; f < St::kUnits; ++f)
 #pragma unroll
-                for (int j = 0; j < FS; j += kSub) {
-                    const int step = f * FS + j;
-                    if constexpr (kB == 1) {
-                        u32x4 x[NT][(kSub + 1) / 2];  // pairs of steps
+                for (int r = 0; r < R; ++r) {
+                    s[f][r] = st.s[slot][r][f];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int h = 0; h < (kSub + 1) / 2; ++h) {
-                                const int pair = (step >> 1) + h;
-                                x[n][h] = *reinterpret_cast<const u32x4*>(buf + (n * 2 + pair) * 1024 +
-                                                                          ((t ^ (4 * pair + q)) & 15) * 16);
-                            }
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            if constexpr (kSub == 1) {
-                                const u32x2 b = weights<MATH, W>(st.d[slot][r], step);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    const u32x2 v = step & 1 ? u32x2{x[n][0][2], x[n][0][3]}
-                                                             : u32x2{x[n][0][0], x[n][0][1]};
-                                    acc[r][n] = M::mma(v, b, acc[r][n]);
-                                }
-                            } else if constexpr (kSub == 2) {
-                                const u32x2 b0 = weights<MATH, W>(st.d[slot][r], step),
-                                            b1 = weights<MATH, W>(st.d[slot][r], step + 1);
-                                const u32x4 b = {b0[0], b0[1], b1[0], b1[1]};
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) acc[r][n] = mma_i8x64(x[n][0], b, acc[r][n]);
-                            } else {
-                                u32x8 b;
-#pragma unroll
-                                for (int h = 0; h < 4; ++h) {
-                                    const u32x2 w = weights<MATH, W>(st.d[slot][r], h);
-                                    b[2 * h] = w[0];
-                                    b[2 * h + 1] = w[1];
-                                }
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    const u32x4 lo = x[n][0], hi = x[n][(kSub + 1) / 2 - 1];
-                                    acc[r][n] = mma_f8x128(u32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]},
-                                                           b, acc[r][n]);
-                                }
-                            }
-                        }
-                    } else {
-                        typename M::Op x[NT][M::kPieces];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int p = 0; p < M::kPieces; ++p)
-                                x[n][p] = *reinterpret_cast<const typename M::Op*>(
-                                    buf + (n * Tile::kSlabs + p * 4 + step) * 1024 + ((t ^ (4 * step + q)) & 15) * 16);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const typename M::Op b = weights<MATH, W>(st.d[slot][r], step);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int p = 0; p < M::kPieces; ++p) acc[r][n] = M::mma(x[n][p], b, acc[r][n]);
-                        }
-                    }
+                    for (int j = 0; j < kParts; ++j)
+                        b[f][j][r] = Mm::template weight<W>(st.d[slot][r], f * FS + j * Mm::kSub);
                 }
+            if (c + 2 * KS < a.nc) st.fetch(slot, c + 2 * KS);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int f = 0; f < St::kUnits; ++f) {
+                    typename M::Acc acc[R] = {};
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            sum[r][n][v] = fmaf(st.s[slot][r][f], (float)acc[r][n][v], sum[r][n][v]);
-            }
+                    for (int j = 0; j < kParts; ++j) {
+                        typename Mm::Op x[M::kPieces];
+                        Mm::read(x, buf + n * Tile::kSlabs * 1024, f * FS + j * Mm::kSub, q, t);
+#pragma unroll
+                        for (int p = 0; p < M::kPieces; ++p)
+#pragma unroll
+                            for (int r = 0; r < R; ++r) acc[r] = Mm::mma(x[p], b[f][j][r], acc[r]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) sum[r][n][v] = fmaf(s[f][r], (float)acc[r][v], sum[r][n][v]);
+                }
         }
-        if (more) store(it + 1, lds + (~it & 1) * Tile::kBytes);
+        if (it + 1 < iters) store(it + 1, lds + (~it & 1) * Tile::kBytes, raw[kAhead == 2 ? slot ^ 1 : 0]);
         __syncthreads();
     };
     for (int it = 0; it < iters; it += 2) {
@@ -664,11 +670,13 @@ void launch_mv(const MvArgs& a, hipStream_t stream) {
         constexpr int PF = MATH == kF32 ? 1 : 2;
         if (a.tiles >= 512) launch_few<MATH, W, FS, 2, PF, 16>(a, stream);
         else launch_few<MATH, W, FS, 1, PF, 16>(a, stream);
-    } else if (a.T <= 32 || MATH == kF32) {
+    } else if (MATH == kF32 || a.T <= 32) {
         launch_mm<MATH, W, FS, 2, 2, MATH == kF32 ? 2 : 4, 2>(a, stream);
     } else if constexpr (MATH != kF32) {
-        if (a.T <= 128) launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
-        else launch_mm<MATH, W, FS, 4, 4, 1, 4>(a, stream);
+        constexpr bool kByte = Mt<MATH>::kBytes == 1;
+        if (a.T <= 48) launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
+        else if (a.T <= 128) launch_mm<MATH, W, FS, 4, 2, kByte ? 4 : 2, 2>(a, stream);
+        else launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4>(a, stream);
     }
 }
 
