@@ -396,7 +396,7 @@ __global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
 //
 // A workgroup has KS x RW waves: wave (kg, rg) multiplies the R row tiles of row group rg
 // with the 16 NT tokens of the block over the chunks kg, kg + KS, ...; per iteration the
-// workgroup stages KS chunks of x, double buffered, one barrier an iteration. With many
+// workgroup stages KS CH chunks of x, double buffered, one barrier an iteration. With many
 // workgroups at hand KS = 1 and all waves share the chunk; with few, the waves split the
 // columns and their sums meet in LDS at the end, in the order of kg.
 //
@@ -466,22 +466,30 @@ struct MmOp {
     }
 };
 
-template <int MATH, int NT, int KS>
+template <int MATH, int NT, int KC>
 struct MmTile {
     // bytes of x in LDS a buffer: [chunk][token tile][piece or not][4 steps or 2 pairs][64 lanes][16 bytes]
     static constexpr int kSlabs = MATH == kF32 ? 12 : Mt<MATH>::kBytes == 2 ? 4 : 2;  // of 1 KB a chunk and tile
-    static constexpr int kBytes = KS * NT * kSlabs * 1024;
+    static constexpr int kBytes = KC * NT * kSlabs * 1024;
 };
 
-template <int MATH, int W, int FS, int NT, int R, int KS, int RW>
+// Token tiles of an output pass: as many as `room` bytes of LDS hold at `each`.
+constexpr int mm_pass(int tiles, int each, int room) {
+    int n = tiles;
+    while (n > 1 && n * each > room) n = (n + 1) / 2;
+    return n;
+}
+
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)))
 void k_matmul(MvArgs a, int token_blocks) {
     using M = Mt<MATH>;
     using St = Stream<W, FS, R, 2>;
-    using Tile = MmTile<MATH, NT, KS>;
+    constexpr int KC = KS * CH;  // chunks of an iteration
+    using Tile = MmTile<MATH, NT, KC>;
     constexpr int kB = M::kBytes, kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
     constexpr int kUnitCols = 16 / (kB == 4 ? 2 : kB);        // columns of a staged unit: 16 bytes, fp32 32
-    constexpr int kRowUnits = KS * kChunk / kUnitCols;        // units of a token row in an iteration
+    constexpr int kRowUnits = KC * kChunk / kUnitCols;        // units of a token row in an iteration
     constexpr int kUnits = 16 * NT * kRowUnits / kThreads;    // units a thread stages
     static_assert(16 * NT * kRowUnits % kThreads == 0, "units divide over the threads");
     extern __shared__ __align__(16) char lds[];
@@ -496,7 +504,8 @@ void k_matmul(MvArgs a, int token_blocks) {
     const int q = lane >> 4, t = lane & 15;
 
     constexpr int kParts = kB == 4 ? 2 : 1;  // 16-byte parts of a unit
-    constexpr int kAhead = KS > 1 ? 2 : 1;  // iterations that x is fetched ahead: few workgroups hide less
+    constexpr int kAhead = KS > 1 && kUnits * kParts <= 6 ? 2 : 1;  // iterations that x is fetched ahead: few
+                                                                   // workgroups hide less, and registers allow
     u32x4 raw[kAhead][kUnits][kParts];
     // unit i of this thread: token row and unit in the row
     const auto row_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) / kRowUnits; };
@@ -506,7 +515,7 @@ void k_matmul(MvArgs a, int token_blocks) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int64_t row = min(t0 + row_of(i), a.T - 1);
-            const int at = (it * KS * kChunk + unit_of(i) * kUnitCols) * kB;
+            const int at = (it * KC * kChunk + unit_of(i) * kUnitCols) * kB;
 #pragma unroll
             for (int h = 0; h < kParts; ++h) {
                 to[i][h] = u32x4{0, 0, 0, 0};
@@ -546,8 +555,8 @@ void k_matmul(MvArgs a, int token_blocks) {
     };
     const auto store = [&](int it, char* buf, const u32x4 (&from)[kUnits][kParts]) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
-        const int first = it * KS * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
-        const int cut = end != last && last >= first && last < first + KS * kChunk * kB ? (last - first) / (16 * kParts) : -1;
+        const int first = it * KC * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
+        const int cut = end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
             if (unit_of(i) != cut) put(buf, row_of(i), unit_of(i), from[i]);
@@ -562,7 +571,7 @@ void k_matmul(MvArgs a, int token_blocks) {
     };
 
     St st(a, tile_b + rg * R, lane);
-    const int iters = (int)((a.nc + KS - 1) / KS);
+    const int iters = (int)((a.nc + KC - 1) / KC);
     load(0, raw[0]);
     if (kg < a.nc) st.fetch(0, kg);
     if (kAhead == 2 && 1 < iters) load(1, raw[kAhead - 1]);
@@ -571,14 +580,17 @@ void k_matmul(MvArgs a, int token_blocks) {
     __syncthreads();
 
     float sum[R][NT][4] = {};
-    const auto body = [&](int it, int slot) {
-        const int64_t c = (int64_t)it * KS + kg;
-        if (it + kAhead < iters) load(it + kAhead, raw[kAhead == 2 ? slot : 0]);
-        const char* buf = lds + (it & 1) * Tile::kBytes + kg * NT * Tile::kSlabs * 1024 + q * 256;
-        if (c < a.nc) {
+    const auto body = [&](int it, int parity) {
+        if (it + kAhead < iters) load(it + kAhead, raw[kAhead == 2 ? parity : 0]);
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+            const int64_t c = (int64_t)it * KC + ch * KS + kg;
+            if (c >= a.nc) break;
+            const char* buf = lds + (it & 1) * Tile::kBytes + (ch * KS + kg) * NT * Tile::kSlabs * 1024 + q * 256;
+            const int slot = CH == 2 ? ch : parity;
             using Mm = MmOp<MATH, FS>;
-            constexpr int kParts = FS / Mm::kSub;  // MFMAs of a sum
-            typename Mm::Op b[St::kUnits][kParts][R];
+            constexpr int kMfma = FS / Mm::kSub;  // MFMAs of a sum
+            typename Mm::Op b[St::kUnits][kMfma][R];
             float s[St::kUnits][R];
 #pragma unroll
             for (int f = 0; f < St::kUnits; ++f)
@@ -586,31 +598,48 @@ void k_matmul(MvArgs a, int token_blocks) {
                 for (int r = 0; r < R; ++r) {
                     s[f][r] = st.s[slot][r][f];
 #pragma unroll
-                    for (int j = 0; j < kParts; ++j)
+                    for (int j = 0; j < kMfma; ++j)
                         b[f][j][r] = Mm::template weight<W>(st.d[slot][r], f * FS + j * Mm::kSub);
                 }
             if (c + 2 * KS < a.nc) st.fetch(slot, c + 2 * KS);
+            // token tiles one after the other, each behind the reads of the next one's x and in front of the scaling
+            // of the last one's sums, so that neither waits for the matrix core
+            constexpr int kSums = NT * St::kUnits;  // sum i: token tile i / kUnits, scale unit i % kUnits
+            typename Mm::Op x[2][kMfma][M::kPieces];
+            typename M::Acc acc[2][R];
+            const auto read = [&](int i) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int j = 0; j < kMfma; ++j)
+                    Mm::read(x[i & 1][j], buf + i / St::kUnits * Tile::kSlabs * 1024,
+                             i % St::kUnits * FS + j * Mm::kSub, q, t);
+            };
+            const auto flush = [&](int i) {
 #pragma unroll
-                for (int f = 0; f < St::kUnits; ++f) {
-                    typename M::Acc acc[R] = {};
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int j = 0; j < kParts; ++j) {
-                        typename Mm::Op x[M::kPieces];
-                        Mm::read(x, buf + n * Tile::kSlabs * 1024, f * FS + j * Mm::kSub, q, t);
+                    for (int v = 0; v < 4; ++v)
+                        sum[r][i / St::kUnits][v] =
+                            fmaf(s[i % St::kUnits][r], (float)acc[i & 1][r][v], sum[r][i / St::kUnits][v]);
+            };
+            read(0);
 #pragma unroll
-                        for (int p = 0; p < M::kPieces; ++p)
+            for (int i = 0; i < kSums; ++i) {
+                if (i + 1 < kSums) read(i + 1);
 #pragma unroll
-                            for (int r = 0; r < R; ++r) acc[r] = Mm::mma(x[p], b[f][j][r], acc[r]);
-                    }
+                for (int r = 0; r < R; ++r) acc[i & 1][r] = typename M::Acc{0, 0, 0, 0};
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
+                for (int j = 0; j < kMfma; ++j)
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) sum[r][n][v] = fmaf(s[f][r], (float)acc[r][v], sum[r][n][v]);
-                }
+                    for (int p = 0; p < M::kPieces; ++p)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            acc[i & 1][r] = Mm::mma(x[i & 1][j][p], b[i % St::kUnits][j][r], acc[i & 1][r]);
+                if (i > 0) flush(i - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            flush(kSums - 1);
         }
-        if (it + 1 < iters) store(it + 1, lds + (~it & 1) * Tile::kBytes, raw[kAhead == 2 ? slot ^ 1 : 0]);
+        if (it + 1 < iters) store(it + 1, lds + (~it & 1) * Tile::kBytes, raw[kAhead == 2 ? parity ^ 1 : 0]);
         __syncthreads();
     };
     for (int it = 0; it < iters; it += 2) {
@@ -618,37 +647,42 @@ void k_matmul(MvArgs a, int token_blocks) {
         if (it + 1 < iters) body(it + 1, 1);
     }
 
+    // the sums through LDS, NP token tiles at a time, so that a thread stores 4 rows of a token together
+    constexpr int NP = mm_pass(NT, KS * 16 * kPitch * 4, 2 * Tile::kBytes);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (n) __syncthreads();
+    for (int n0 = 0; n0 < NT; n0 += NP) {
+        if (n0) __syncthreads();
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int n = n0; n < n0 + NP && n < NT; ++n)
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-                red[(kg * 16 + 4 * q + v) * kPitch + (rg * R + r) * 16 + t] = sum[r][n][v];
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    red[(kg * 16 * NP + (n - n0) * 16 + 4 * q + v) * kPitch + (rg * R + r) * 16 + t] = sum[r][n][v];
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * kRows; i += kThreads) {
-            const int tok = i / kRows, row = i % kRows;
-            const int64_t tt = t0 + 16 * n + tok, o = tile_b * 16 + row;
+        const int toks = 16 * (NP < NT - n0 ? NP : NT - n0);
+        for (int i = threadIdx.x; i < toks * (kRows / 4); i += kThreads) {
+            const int tok = i / (kRows / 4), row = i % (kRows / 4) * 4;
+            const int64_t tt = t0 + 16 * n0 + tok, o = tile_b * 16 + row;
             if (tt < a.T && o < a.m) {
-                float y = 0.0f;
+                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) y += red[(k * 16 + tok) * kPitch + row];
+                for (int k = 0; k < KS; ++k) y += *reinterpret_cast<const f32x4*>(red + (k * 16 * NP + tok) * kPitch + row);
                 y *= unit<MATH, W>();
                 if (a.xs) y *= a.xs[tt];
-                store_elem(a.y, a.ytype, tt * a.ldy + o, y);
+                store4(a.y, a.ytype, tt * a.ldy + o, y, (int)min<int64_t>(4, a.m - o));
             }
         }
     }
 }
 
-template <int MATH, int W, int FS, int NT, int R, int KS, int RW>
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH = 1>
 void launch_mm(const MvArgs& a, hipStream_t stream) {
     const unsigned rows = (unsigned)((a.tiles + R * RW - 1) / (R * RW));
     const unsigned blocks = (unsigned)((a.T + 16 * NT - 1) / (16 * NT));
     constexpr size_t red = sizeof(float) * KS * 16 * (16 * R * RW + 4);
-    constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, KS>::kBytes, red);
-    hipLaunchKernelGGL((k_matmul<MATH, W, FS, NT, R, KS, RW>), dim3(rows * blocks), dim3(64 * KS * RW), lds, stream, a,
+    constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, KS * CH>::kBytes, red);
+    hipLaunchKernelGGL((k_matmul<MATH, W, FS, NT, R, KS, RW, CH>), dim3(rows * blocks), dim3(64 * KS * RW), lds, stream, a,
                        (int)blocks);
 }
 
@@ -674,9 +708,16 @@ void launch_mv(const MvArgs& a, hipStream_t stream) {
         launch_mm<MATH, W, FS, 2, 2, MATH == kF32 ? 2 : 4, 2>(a, stream);
     } else if constexpr (MATH != kF32) {
         constexpr bool kByte = Mt<MATH>::kBytes == 1;
-        if (a.T <= 48) launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
-        else if (a.T <= 128) launch_mm<MATH, W, FS, 4, 2, kByte ? 4 : 2, 2>(a, stream);
-        else launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4>(a, stream);
+        const int64_t big = (int64_t)((a.tiles + 7) / 8) * ((a.T + 127) / 128);   // workgroups of 128 x 128
+        const int64_t small = (int64_t)((a.tiles + 3) / 4) * ((a.T + 63) / 64);  // and of 64 x 64
+        if (a.T > 64 && big > 256)
+            launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4, kByte ? 2 : 1>(a, stream);
+        else if (a.T <= 48)
+            launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
+        else if (small > 256)
+            launch_mm<MATH, W, FS, 4, 2, 2, 2>(a, stream);
+        else
+            launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
     }
 }
 
