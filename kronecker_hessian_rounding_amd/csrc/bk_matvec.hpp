@@ -507,21 +507,36 @@ void k_matmul(MvArgs a, int token_blocks) {
     constexpr int kAhead = KS > 1 && kUnits * kParts <= 6 ? 2 : 1;  // iterations that x is fetched ahead: few
                                                                    // workgroups hide less, and registers allow
     u32x4 raw[kAhead][kUnits][kParts];
-    // unit i of this thread: token row and unit in the row
-    const auto row_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) / kRowUnits; };
-    const auto unit_of = [&](int i) { return (int)(threadIdx.x + i * kThreads) % kRowUnits; };
+    // this thread stages unit `un` of the token rows row0 + i kRowStep
+    constexpr int kRowStep = kThreads / kRowUnits;
+    static_assert(kThreads % kRowUnits == 0, "a thread keeps its unit");
+    const int row0 = threadIdx.x / kRowUnits, un = threadIdx.x % kRowUnits;
     const int end = (int)a.n * kB;  // bytes of a row
+    const int64_t ldb = a.ldx * kB;
+    const char* x0 = a.x + t0 * ldb;
+    const bool full = t0 + 16 * NT <= a.T;
     const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) {
+        const int at = (it * KC * kChunk + un * kUnitCols) * kB;
+        if (at + 16 * kParts <= end) {
+            if (full) {
+                const char* p = x0 + row0 * ldb + at;
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int64_t row = min(t0 + row_of(i), a.T - 1);
-            const int at = (it * KC * kChunk + unit_of(i) * kUnitCols) * kB;
+                for (int i = 0; i < kUnits; ++i, p += kRowStep * ldb)
 #pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-                to[i][h] = u32x4{0, 0, 0, 0};
-                if (at + 16 * kParts <= end)
-                    __builtin_memcpy(&to[i][h], a.x + row * a.ldx * kB + at + 16 * h, 16);
+                    for (int h = 0; h < kParts; ++h) __builtin_memcpy(&to[i][h], p + 16 * h, 16);
+            } else {  // rows past the last token repeat it
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h)
+                        __builtin_memcpy(&to[i][h], x0 + min<int64_t>(row0 + i * kRowStep, a.T - 1 - t0) * ldb + at + 16 * h,
+                                         16);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) to[i][h] = u32x4{0, 0, 0, 0};
         }
     };
     // unit `ru` of a token row's iteration, into its operands' slots
@@ -557,9 +572,9 @@ void k_matmul(MvArgs a, int token_blocks) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
         const int first = it * KC * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
         const int cut = end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
+        if (un != cut)
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-            if (unit_of(i) != cut) put(buf, row_of(i), unit_of(i), from[i]);
+            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i * kRowStep, un, from[i]);
         if (cut >= 0)
             for (int row = threadIdx.x; row < 16 * NT; row += kThreads) {
                 const char* src = a.x + min(t0 + row, a.T - 1) * a.ldx * kB;
