@@ -254,17 +254,21 @@ __device__ __forceinline__ u32x4 cut_unit(const char* __restrict__ row, int at, 
 // four tokens of one weight row and share its scale. The sums are scaled every FS steps: a
 // chunk (FS = 4), or a step where groups are shorter than a chunk (FS = 1).
 
-// A wave's chunks of R row tiles with their scales, PF chunks ahead of their use.
+// A wave's chunks of R row tiles with their scales, PF chunks ahead of their use. A chunk
+// past the last fetches the last again: the loads of the loops below are all unconditional
+// (clamped, not branched around), because behind a branch the compiler no longer knows how
+// many are in flight and waits for all of them before it uses the first.
 template <int W, int FS, int R, int PF>
 struct Stream {
     using Sh = typename Share<W>::T;
     static constexpr int kUnits = kSteps / FS;
     const Sh* wp[R];
     const float* sp[R];
+    int64_t nc;
     int gshift;
     Sh d[PF][R];
     float s[PF][R][kUnits];
-    __device__ __forceinline__ Stream(const MvArgs& a, int64_t tile0, int lane) : gshift(a.gshift) {
+    __device__ __forceinline__ Stream(const MvArgs& a, int64_t tile0, int lane) : nc(a.nc), gshift(a.gshift) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t tile = min(tile0 + r, (int64_t)a.tiles - 1);
@@ -273,6 +277,7 @@ struct Stream {
         }
     }
     __device__ __forceinline__ void fetch(int slot, int64_t c) {
+        c = min(c, nc - 1);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             d[slot][r] = wp[r][c * 64];
@@ -298,8 +303,8 @@ struct FewShape {
     static constexpr int kBytes = TB * kPitch;                        // of a wave
 };
 
-template <int MATH, int W, int FS, int R, int PF, int TB>
-__global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
+template <int MATH, int W, int FS, int R, int PF, int TB, int NW>
+__global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
     using M = Mt<MATH>;
     using St = Stream<W, FS, R, PF>;
     using Sh = FewShape<MATH, PF, TB>;
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
     char* xs = lds + w * Sh::kBytes;
     const int64_t tile0 = (int64_t)blockIdx.x * R;
     const int T = (int)a.T, end = (int)a.n * kB;  // bytes of a row
-    const int mine = a.nc > w ? (int)((a.nc - w + kWaves - 1) / kWaves) : 0;  // this wave's chunks
+    const int mine = a.nc > w ? (int)((a.nc - w + NW - 1) / NW) : 0;  // this wave's chunks
     u32x4 x[Sh::kUnits];
     // unit i of this lane in the set from chunk i0 on: token, place in the token's LDS row, byte in the row of x
     const auto token_of = [&](int i) { return (lane + i * 64) / Sh::kRowUnits; };
@@ -317,58 +322,62 @@ __global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
     const auto byte_of = [&](int i, int i0) {
         constexpr int kPer = kChunk * kB / 16;
         const int u = place_of(i);
-        return ((i0 + u / kPer) * kWaves + w) * kChunk * kB + u % kPer * 16;
+        return ((i0 + u / kPer) * NW + w) * kChunk * kB + u % kPer * 16;
     };
+    // a row below 16 bytes has no whole unit: the loads, whose values are then not used, go elsewhere
+    const char* xb = end >= 16 ? a.x : a.codes;
+    const int64_t ldb = end >= 16 ? a.ldx * kB : 0;
+    const int most = max(end - 16, 0);
     const auto load = [&](int i0) {
 #pragma unroll
-        for (int i = 0; i < Sh::kUnits; ++i) {
-            x[i] = u32x4{0, 0, 0, 0};
-            if (token_of(i) < T && byte_of(i, i0) + 16 <= end)
-                __builtin_memcpy(&x[i], a.x + token_of(i) * a.ldx * kB + byte_of(i, i0), 16);
-        }
+        for (int i = 0; i < Sh::kUnits; ++i)
+            __builtin_memcpy(&x[i], xb + min(token_of(i), T - 1) * ldb + min(byte_of(i, i0), most), 16);
     };
     St st(a, tile0, lane);
     load(0);
 #pragma unroll
-    for (int p = 0; p < PF; ++p)
-        if (p < mine) st.fetch(p, w + p * kWaves);
+    for (int p = 0; p < PF; ++p) st.fetch(p, w + p * NW);
     float sum[R][4] = {};
     const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * kB;
     for (int i0 = 0; i0 < mine; i0 += PF) {
+        if (((i0 + PF - 1) * NW + w + 1) * kChunk * kB > end)  // the set passes the row's end: zeros from there on
+#pragma unroll
+            for (int i = 0; i < Sh::kUnits; ++i)
+                if (byte_of(i, i0) + 16 > end) x[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < Sh::kUnits; ++i)
-            if (token_of(i) < T) *reinterpret_cast<u32x4*>(xs + token_of(i) * Sh::kPitch + place_of(i) * 16) = x[i];
+            if (token_of(i) < TB) *reinterpret_cast<u32x4*>(xs + token_of(i) * Sh::kPitch + place_of(i) * 16) = x[i];
         if (end % 16 != 0) {  // the unit that the row ends in, if it is in this set
-            const int at = end & ~15, c = at / (kChunk * kB), p = c / kWaves - i0;
-            if (c % kWaves == w && p >= 0 && p < PF && lane < T)
+            const int at = end & ~15, c = at / (kChunk * kB), p = c / NW - i0;
+            if (c % NW == w && p >= 0 && p < PF && lane < T)
                 *reinterpret_cast<u32x4*>(xs + lane * Sh::kPitch + (p * kChunk - c * kChunk) * kB + at) =
                     cut_unit<kB>(a.x + lane * a.ldx * kB, at, end);
         }
-        if (i0 + PF < mine) load(i0 + PF);
+        load(i0 + PF);
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
-            if (i0 + p >= mine) break;
             const char* xk = xl + p * kChunk * kB;
+            if (i0 + p < mine)
 #pragma unroll
-            for (int f = 0; f < St::kUnits; ++f) {
-                typename M::Acc acc[R] = {};
+                for (int f = 0; f < St::kUnits; ++f) {
+                    typename M::Acc acc[R] = {};
 #pragma unroll
-                for (int j = 0; j < FS; ++j) {
-                    typename M::Op v[M::kPieces];
-                    operand<MATH, W>(xk + (f * FS + j) * kStep * kB, v);
+                    for (int j = 0; j < FS; ++j) {
+                        typename M::Op v[M::kPieces];
+                        operand<MATH, W>(xk + (f * FS + j) * kStep * kB, v);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const typename M::Op b = weights<MATH, W>(st.d[p][r], f * FS + j);
+                        for (int r = 0; r < R; ++r) {
+                            const typename M::Op b = weights<MATH, W>(st.d[p][r], f * FS + j);
 #pragma unroll
-                        for (int q = 0; q < M::kPieces; ++q) acc[r] = M::mma(v[q], b, acc[r]);
+                            for (int q = 0; q < M::kPieces; ++q) acc[r] = M::mma(v[q], b, acc[r]);
+                        }
                     }
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) sum[r][v] = fmaf(st.s[p][r][f], (float)acc[r][v], sum[r][v]);
                 }
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) sum[r][v] = fmaf(st.s[p][r][f], (float)acc[r][v], sum[r][v]);
-            }
-            if (i0 + p + PF < mine) st.fetch(p, w + (int64_t)(i0 + p + PF) * kWaves);
+            st.fetch(p, w + (int64_t)(i0 + p + PF) * NW);
         }
     }
     __syncthreads();
@@ -378,13 +387,13 @@ __global__ __launch_bounds__(kMvThreads) void k_matvec_few(MvArgs a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) red[((w * R + r) * 16 + 4 * (lane >> 4) + v) * 17 + (lane & 15)] = sum[r][v];
     __syncthreads();
-    for (int i = threadIdx.x; i < T * R * 16; i += kMvThreads) {
+    for (int i = threadIdx.x; i < T * R * 16; i += (64 * NW)) {
         const int t = i / (R * 16), r = i / 16 % R;
         const int64_t row = (tile0 + r) * 16 + (i & 15);
         if (row < a.m) {
             float y = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) y += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
+            for (int k = 0; k < NW; ++k) y += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
             y *= unit<MATH, W>();
             if (a.xs) y *= a.xs[t];
             store_elem(a.y, a.ytype, t * a.ldy + row, y);
@@ -514,29 +523,19 @@ void k_matmul(MvArgs a, int token_blocks) {
     const int end = (int)a.n * kB;  // bytes of a row
     const int64_t ldb = a.ldx * kB;
     const char* x0 = a.x + t0 * ldb;
-    const bool full = t0 + 16 * NT <= a.T;
+    const int last_row = (int)min<int64_t>(16 * NT, a.T - t0) - 1;
+    // rows past the last token repeat it, units past the row's end its last one; a row shorter than a unit has no
+    // whole one: the loads, whose values are then not used, go elsewhere
+    const bool some = end >= 16 * kParts;
     const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) {
-        const int at = (it * KC * kChunk + un * kUnitCols) * kB;
-        if (at + 16 * kParts <= end) {
-            if (full) {
-                const char* p = x0 + row0 * ldb + at;
+        const int at = min((it * KC * kChunk + un * kUnitCols) * kB, some ? end - 16 * kParts : 0);
+        const char* p = (some ? x0 : a.codes) + at;
+        const int64_t step = some ? ldb : 0;
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i, p += kRowStep * ldb)
+        for (int i = 0; i < kUnits; ++i) {
+            const int row = min(row0 + i * kRowStep, last_row);
 #pragma unroll
-                    for (int h = 0; h < kParts; ++h) __builtin_memcpy(&to[i][h], p + 16 * h, 16);
-            } else {  // rows past the last token repeat it
-#pragma unroll
-                for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-                    for (int h = 0; h < kParts; ++h)
-                        __builtin_memcpy(&to[i][h], x0 + min<int64_t>(row0 + i * kRowStep, a.T - 1 - t0) * ldb + at + 16 * h,
-                                         16);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-                for (int h = 0; h < kParts; ++h) to[i][h] = u32x4{0, 0, 0, 0};
+            for (int h = 0; h < kParts; ++h) __builtin_memcpy(&to[i][h], p + row * step + 16 * h, 16);
         }
     };
     // unit `ru` of a token row's iteration, into its operands' slots
@@ -572,9 +571,15 @@ void k_matmul(MvArgs a, int token_blocks) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
         const int first = it * KC * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
         const int cut = end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
+        const bool whole = first + (un + 1) * 16 * kParts <= end;
         if (un != cut)
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i * kRowStep, un, from[i]);
+            for (int i = 0; i < kUnits; ++i) {
+                u32x4 v[kParts];
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) v[h] = whole ? from[i][h] : u32x4{0, 0, 0, 0};
+                put(buf, row0 + i * kRowStep, un, v);
+            }
         if (cut >= 0)
             for (int row = threadIdx.x; row < 16 * NT; row += kThreads) {
                 const char* src = a.x + min(t0 + row, a.T - 1) * a.ldx * kB;
@@ -588,19 +593,18 @@ void k_matmul(MvArgs a, int token_blocks) {
     St st(a, tile_b + rg * R, lane);
     const int iters = (int)((a.nc + KC - 1) / KC);
     load(0, raw[0]);
-    if (kg < a.nc) st.fetch(0, kg);
-    if (kAhead == 2 && 1 < iters) load(1, raw[kAhead - 1]);
-    if (kg + KS < a.nc) st.fetch(1, kg + KS);
+    st.fetch(0, kg);
+    if (kAhead == 2) load(1, raw[kAhead - 1]);
+    st.fetch(1, kg + KS);
     store(0, lds, raw[0]);
     __syncthreads();
 
     float sum[R][NT][4] = {};
     const auto body = [&](int it, int parity) {
-        if (it + kAhead < iters) load(it + kAhead, raw[kAhead == 2 ? parity : 0]);
+        load(it + kAhead, raw[kAhead == 2 ? parity : 0]);
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
             const int64_t c = (int64_t)it * KC + ch * KS + kg;
-            if (c >= a.nc) break;
             const char* buf = lds + (it & 1) * Tile::kBytes + (ch * KS + kg) * NT * Tile::kSlabs * 1024 + q * 256;
             const int slot = CH == 2 ? ch : parity;
             using Mm = MmOp<MATH, FS>;
@@ -616,7 +620,8 @@ void k_matmul(MvArgs a, int token_blocks) {
                     for (int j = 0; j < kMfma; ++j)
                         b[f][j][r] = Mm::template weight<W>(st.d[slot][r], f * FS + j * Mm::kSub);
                 }
-            if (c + 2 * KS < a.nc) st.fetch(slot, c + 2 * KS);
+            st.fetch(slot, c + 2 * KS);
+            if (c >= a.nc) continue;
             // token tiles one after the other, each behind the reads of the next one's x and in front of the scaling
             // of the last one's sums, so that neither waits for the matrix core
             constexpr int kSums = NT * St::kUnits;  // sum i: token tile i / kUnits, scale unit i % kUnits
@@ -701,25 +706,29 @@ void launch_mm(const MvArgs& a, hipStream_t stream) {
                        (int)blocks);
 }
 
-template <int MATH, int W, int FS, int R, int PF, int TB>
+template <int MATH, int W, int FS, int R, int PF, int TB, int NW>
 void launch_few(const MvArgs& a, hipStream_t stream) {
-    constexpr size_t red = sizeof(float) * kWaves * R * 16 * 17;
-    constexpr size_t lds = std::max<size_t>((size_t)kWaves * FewShape<MATH, PF, TB>::kBytes, red);
+    constexpr size_t red = sizeof(float) * NW * R * 16 * 17;
+    constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, TB>::kBytes, red);
     const dim3 grid((unsigned)((a.tiles + R - 1) / R));
-    hipLaunchKernelGGL((k_matvec_few<MATH, W, FS, R, PF, TB>), grid, dim3(kMvThreads), lds, stream, a);
+    hipLaunchKernelGGL((k_matvec_few<MATH, W, FS, R, PF, TB, NW>), grid, dim3(64 * NW), lds, stream, a);
+}
+
+template <int MATH, int W, int FS, int TB>
+void launch_tokens(const MvArgs& a, hipStream_t stream) {
+    constexpr int PF = TB <= 4 ? 8 / W : MATH == kF32 ? 1 : 2;  // 2 KB of weights in flight per wave
+    constexpr int R = TB <= 4 ? 1 : 2;                           // tiles that share an operand of x
+    if (a.tiles >= 512) launch_few<MATH, W, FS, R, PF, TB, 8>(a, stream);
+    else launch_few<MATH, W, FS, 1, PF, TB, 8>(a, stream);
 }
 
 template <int MATH, int W, int FS>
 void launch_mv(const MvArgs& a, hipStream_t stream) {
-    if (a.T <= 4) {
-        // 4 KB of weights in flight per wave
-        if (a.tiles >= 1024) launch_few<MATH, W, FS, 2, 8 / W, 4>(a, stream);
-        else launch_few<MATH, W, FS, 1, 16 / W, 4>(a, stream);
-    } else if (a.T <= 16) {
-        constexpr int PF = MATH == kF32 ? 1 : 2;
-        if (a.tiles >= 512) launch_few<MATH, W, FS, 2, PF, 16>(a, stream);
-        else launch_few<MATH, W, FS, 1, PF, 16>(a, stream);
-    } else if (MATH == kF32 || a.T <= 32) {
+    if (a.T == 1) launch_tokens<MATH, W, FS, 1>(a, stream);
+    else if (a.T <= 4) launch_tokens<MATH, W, FS, 4>(a, stream);
+    else if (a.T <= 8) launch_tokens<MATH, W, FS, 8>(a, stream);
+    else if (a.T <= 16) launch_tokens<MATH, W, FS, 16>(a, stream);
+    else if (MATH == kF32 || a.T <= 32) {
         launch_mm<MATH, W, FS, 2, 2, MATH == kF32 ? 2 : 4, 2>(a, stream);
     } else if constexpr (MATH != kF32) {
         constexpr bool kByte = Mt<MATH>::kBytes == 1;
