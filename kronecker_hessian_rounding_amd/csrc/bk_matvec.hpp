@@ -195,13 +195,15 @@ __device__ __forceinline__ u32x2 even_odd(u32x2 x) {
     return u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x06040200u), __builtin_amdgcn_perm(x[1], x[0], 0x07050301u)};
 }
 
-// fp32 as three bf16 pieces, cut by truncation: 8 significant bits each, their sum is x
-// exactly. An infinity or NaN, whose remainder is NaN, stays in the first piece; a NaN is
-// quieted first, so that it does not lose its whole payload to the cut.
-__device__ __forceinline__ void split3(u32x8 x, bf16x8 (&p)[3]) {
-    u32x8 h, m, l;
+// Four fp32 values as three bf16 pieces each, largest first, cut by truncation: 8 significant
+// bits each, their sum is x exactly. An infinity or NaN, whose remainder is NaN, stays in the
+// first piece; a NaN is quieted first, so that it does not lose its whole payload to the cut.
+// (Pieces rounded to nearest take fewer instructions but a branch for what rounds up to
+// infinity: 16 tokens by 8192 x 8192 22.9 us with it, 20.1 so.)
+__device__ __forceinline__ void split4(u32x4 x, u32x2 (&p)[3]) {
+    u32x4 h, m, l;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
         const float v = __uint_as_float(x[e]);
         h[e] = __float_as_uint(__builtin_canonicalizef(v));
         float r = v - __uint_as_float(x[e] & 0xFFFF0000u);
@@ -209,29 +211,22 @@ __device__ __forceinline__ void split3(u32x8 x, bf16x8 (&p)[3]) {
         m[e] = __float_as_uint(r);
         l[e] = __float_as_uint(r - __uint_as_float(m[e] & 0xFFFF0000u));
     }
-    const auto pack = [](u32x8 a) {
-        u32x4 d;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_perm(a[2 * e + 1], a[2 * e], 0x07060302u);
-        return __builtin_bit_cast(bf16x8, d);
+    const auto pack = [](u32x4 a) {
+        return u32x2{__builtin_amdgcn_perm(a[1], a[0], 0x07060302u), __builtin_amdgcn_perm(a[3], a[2], 0x07060302u)};
     };
-    p[0] = pack(l);
+    p[0] = pack(h);
     p[1] = pack(m);
-    p[2] = pack(h);
+    p[2] = pack(l);
 }
 
-// The A operand from 8 elements of x at `src` (in LDS or in registers).
+// The A operand from 8 elements of a staged row of x at `src`, pieces `piece` bytes apart.
 template <int MATH, int W>
-__device__ __forceinline__ void operand(const char* src, typename Mt<MATH>::Op (&p)[Mt<MATH>::kPieces]) {
-    constexpr int kB = Mt<MATH>::kBytes;
-    if constexpr (MATH == kF32) {
-        u32x8 x;
-        __builtin_memcpy(&x, __builtin_assume_aligned(src, 16), sizeof x);
-        split3(x, p);
-    } else {
-        __builtin_memcpy(&p[0], __builtin_assume_aligned(src, 8 * kB), 8 * kB);
-        if constexpr (W == 2 && kB == 1) p[0] = even_odd(p[0]);
-    }
+__device__ __forceinline__ void operand(const char* src, int piece, typename Mt<MATH>::Op (&p)[Mt<MATH>::kPieces]) {
+    using Op = typename Mt<MATH>::Op;
+#pragma unroll
+    for (int i = 0; i < Mt<MATH>::kPieces; ++i)  // the smallest piece first into the sum
+        p[i] = *reinterpret_cast<const Op*>(src + (Mt<MATH>::kPieces - 1 - i) * piece);
+    if constexpr (W == 2 && Mt<MATH>::kBytes == 1) p[0] = even_odd(p[0]);
 }
 
 // The 16 bytes of a row of x from byte `at` on that the row's end, byte `end`, cuts: zeros
@@ -299,7 +294,10 @@ struct FewShape {
     static constexpr int kB = Mt<MATH>::kBytes;
     static constexpr int kRowUnits = PF * kChunk * kB / 16;           // 16-byte units of a token row in a set
     static constexpr int kUnits = (TB * kRowUnits + 63) / 64;         // units of a lane
-    static constexpr int kPitch = kRowUnits * 16 + 16;                // rows 4 banks apart
+    static constexpr int kPieces = Mt<MATH>::kPieces;
+    static constexpr int kL = kB == 4 ? 2 : kB;                       // bytes of an element (or a piece) in LDS
+    static constexpr int kPiece = PF * kChunk * kL;                   // from piece to piece of a token
+    static constexpr int kPitch = kPieces * kPiece + 16;              // from token to token: 4 banks
     static constexpr int kBytes = TB * kPitch;                        // of a wave
 };
 
@@ -328,7 +326,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
     const char* xb = end >= 16 ? a.x : a.codes;
     const int64_t ldb = end >= 16 ? a.ldx * kB : 0;
     const int most = max(end - 16, 0);
-    const auto load = [&](int i0) {
+    const auto load = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < Sh::kUnits; ++i)
             __builtin_memcpy(&x[i], xb + min(token_of(i), T - 1) * ldb + min(byte_of(i, i0), most), 16);
@@ -338,7 +336,18 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
 #pragma unroll
     for (int p = 0; p < PF; ++p) st.fetch(p, w + p * NW);
     float sum[R][4] = {};
-    const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * kB;
+    const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * Sh::kL;
+    const auto put = [&](int token, int place, u32x4 v) __attribute__((always_inline)) {  // unit `place` of a token
+        char* dst = xs + token * Sh::kPitch;
+        if constexpr (kB == 4) {
+            u32x2 p[3];
+            split4(v, p);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x2*>(dst + i * Sh::kPiece + place * 8) = p[i];
+        } else {
+            *reinterpret_cast<u32x4*>(dst + place * 16) = v;
+        }
+    };
     for (int i0 = 0; i0 < mine; i0 += PF) {
         if (((i0 + PF - 1) * NW + w + 1) * kChunk * kB > end)  // the set passes the row's end: zeros from there on
 #pragma unroll
@@ -346,17 +355,16 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
                 if (byte_of(i, i0) + 16 > end) x[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < Sh::kUnits; ++i)
-            if (token_of(i) < TB) *reinterpret_cast<u32x4*>(xs + token_of(i) * Sh::kPitch + place_of(i) * 16) = x[i];
+            if (token_of(i) < TB) put(token_of(i), place_of(i), x[i]);
         if (end % 16 != 0) {  // the unit that the row ends in, if it is in this set
             const int at = end & ~15, c = at / (kChunk * kB), p = c / NW - i0;
             if (c % NW == w && p >= 0 && p < PF && lane < T)
-                *reinterpret_cast<u32x4*>(xs + lane * Sh::kPitch + (p * kChunk - c * kChunk) * kB + at) =
-                    cut_unit<kB>(a.x + lane * a.ldx * kB, at, end);
+                put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + lane * a.ldx * kB, at, end));
         }
         load(i0 + PF);
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
-            const char* xk = xl + p * kChunk * kB;
+            const char* xk = xl + p * kChunk * Sh::kL;
             if (i0 + p < mine)
 #pragma unroll
                 for (int f = 0; f < St::kUnits; ++f) {
@@ -364,7 +372,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
 #pragma unroll
                     for (int j = 0; j < FS; ++j) {
                         typename M::Op v[M::kPieces];
-                        operand<MATH, W>(xk + (f * FS + j) * kStep * kB, v);
+                        operand<MATH, W>(xk + (f * FS + j) * kStep * Sh::kL, Sh::kPiece, v);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const typename M::Op b = weights<MATH, W>(st.d[p][r], f * FS + j);
@@ -379,6 +387,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
                 }
             st.fetch(p, w + (int64_t)(i0 + p + PF) * NW);
         }
+        if constexpr (PF == 1) asm volatile("" ::: "memory");  // or all loads move over the loop's edge, to their use
     }
     __syncthreads();
     float* red = reinterpret_cast<float*>(lds);  // [wave][tile][token][16 rows + 1]
@@ -527,7 +536,7 @@ void k_matmul(MvArgs a, int token_blocks) {
     // rows past the last token repeat it, units past the row's end its last one; a row shorter than a unit has no
     // whole one: the loads, whose values are then not used, go elsewhere
     const bool some = end >= 16 * kParts;
-    const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) {
+    const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) __attribute__((always_inline)) {
         const int at = min((it * KC * kChunk + un * kUnitCols) * kB, some ? end - 16 * kParts : 0);
         const char* p = (some ? x0 : a.codes) + at;
         const int64_t step = some ? ldb : 0;
@@ -539,7 +548,7 @@ void k_matmul(MvArgs a, int token_blocks) {
         }
     };
     // unit `ru` of a token row's iteration, into its operands' slots
-    const auto put = [&](char* buf, int row, int ru, const u32x4 (&v)[kParts]) {
+    const auto put = [&](char* buf, int row, int ru, const u32x4 (&v)[kParts]) __attribute__((always_inline)) {
         const int u = ru % (kChunk / kUnitCols), ck = ru / (kChunk / kUnitCols);
         char* dst = buf + (ck * NT + (row >> 4)) * Tile::kSlabs * 1024;
         if constexpr (kB == 1) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
@@ -555,19 +564,18 @@ void k_matmul(MvArgs a, int token_blocks) {
         } else {  // columns 8 u ..: step u / 4, lanes of q = u % 4
             const int at = (u >> 2) * 1024 + ((u & 3) * 16 + ((row ^ u) & 15)) * 16;
             if constexpr (kB == 4) {
-                u32x8 x;
+                u32x2 lo[3], hi[3];
+                split4(v[0], lo);
+                split4(v[kParts - 1], hi);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = v[e >> 2][e & 3];
-                bf16x8 p[3];
-                split3(x, p);
-#pragma unroll
-                for (int c = 0; c < 3; ++c) *reinterpret_cast<bf16x8*>(dst + c * 4096 + at) = p[c];
+                for (int c = 0; c < 3; ++c)  // the smallest piece first into the sum
+                    *reinterpret_cast<u32x4*>(dst + (2 - c) * 4096 + at) = u32x4{lo[c][0], lo[c][1], hi[c][0], hi[c][1]};
             } else {
                 *reinterpret_cast<u32x4*>(dst + at) = v[0];
             }
         }
     };
-    const auto store = [&](int it, char* buf, const u32x4 (&from)[kUnits][kParts]) {
+    const auto store = [&](int it, char* buf, const u32x4 (&from)[kUnits][kParts]) __attribute__((always_inline)) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
         const int first = it * KC * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
         const int cut = end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
@@ -600,7 +608,7 @@ void k_matmul(MvArgs a, int token_blocks) {
     __syncthreads();
 
     float sum[R][NT][4] = {};
-    const auto body = [&](int it, int parity) {
+    const auto body = [&](int it, int parity) __attribute__((always_inline)) {
         load(it + kAhead, raw[kAhead == 2 ? parity : 0]);
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
@@ -625,12 +633,13 @@ void k_matmul(MvArgs a, int token_blocks) {
             // token tiles one after the other, each behind the reads of the next one's x and in front of the scaling
             // of the last one's sums, so that neither waits for the matrix core
             constexpr int kSums = NT * St::kUnits;  // sum i: token tile i / kUnits, scale unit i % kUnits
-            typename Mm::Op x[2][kMfma][M::kPieces];
+            constexpr int kRead = M::kPieces == 1 ? 2 : 1;  // three pieces leave no registers for the next tile's
+            typename Mm::Op x[kRead][kMfma][M::kPieces];
             typename M::Acc acc[2][R];
             const auto read = [&](int i) {
 #pragma unroll
                 for (int j = 0; j < kMfma; ++j)
-                    Mm::read(x[i & 1][j], buf + i / St::kUnits * Tile::kSlabs * 1024,
+                    Mm::read(x[i % kRead][j], buf + i / St::kUnits * Tile::kSlabs * 1024,
                              i % St::kUnits * FS + j * Mm::kSub, q, t);
             };
             const auto flush = [&](int i) {
@@ -641,10 +650,11 @@ void k_matmul(MvArgs a, int token_blocks) {
                         sum[r][i / St::kUnits][v] =
                             fmaf(s[i % St::kUnits][r], (float)acc[i & 1][r][v], sum[r][i / St::kUnits][v]);
             };
-            read(0);
+            if (kRead == 2) read(0);
 #pragma unroll
             for (int i = 0; i < kSums; ++i) {
-                if (i + 1 < kSums) read(i + 1);
+                if (kRead == 1) read(i);
+                else if (i + 1 < kSums) read(i + 1);
 #pragma unroll
                 for (int r = 0; r < R; ++r) acc[i & 1][r] = typename M::Acc{0, 0, 0, 0};
 #pragma unroll
@@ -653,7 +663,7 @@ void k_matmul(MvArgs a, int token_blocks) {
                     for (int p = 0; p < M::kPieces; ++p)
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            acc[i & 1][r] = Mm::mma(x[i & 1][j][p], b[i % St::kUnits][j][r], acc[i & 1][r]);
+                            acc[i & 1][r] = Mm::mma(x[i % kRead][j][p], b[i % St::kUnits][j][r], acc[i & 1][r]);
                 if (i > 0) flush(i - 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -728,20 +738,23 @@ void launch_mv(const MvArgs& a, hipStream_t stream) {
     else if (a.T <= 4) launch_tokens<MATH, W, FS, 4>(a, stream);
     else if (a.T <= 8) launch_tokens<MATH, W, FS, 8>(a, stream);
     else if (a.T <= 16) launch_tokens<MATH, W, FS, 16>(a, stream);
-    else if (MATH == kF32 || a.T <= 32) {
-        launch_mm<MATH, W, FS, 2, 2, MATH == kF32 ? 2 : 4, 2>(a, stream);
-    } else if constexpr (MATH != kF32) {
+    else if constexpr (MATH == kF32) {
+        // 256 rows x 32 tokens where that makes a workgroup for every compute unit (8192 x 8192 with 512 tokens 215
+        // us, the other 453), else 64 x 32 with split columns (with 64 tokens 58 us, the first 142)
+        if (FS == 4 && (int64_t)((a.tiles + 15) / 16) * ((a.T + 31) / 32) >= 256) {
+            if constexpr (FS == 4) launch_mm<MATH, W, FS, 2, 4, 1, 4>(a, stream);
+        } else {
+            launch_mm<MATH, W, FS, 2, 2, 2, 2>(a, stream);
+        }
+    } else {
         constexpr bool kByte = Mt<MATH>::kBytes == 1;
         const int64_t big = (int64_t)((a.tiles + 7) / 8) * ((a.T + 127) / 128);   // workgroups of 128 x 128
         const int64_t small = (int64_t)((a.tiles + 3) / 4) * ((a.T + 63) / 64);  // and of 64 x 64
-        if (a.T > 64 && big > 256)
-            launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4, kByte ? 2 : 1>(a, stream);
-        else if (a.T <= 48)
-            launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
-        else if (small > 256)
-            launch_mm<MATH, W, FS, 4, 2, 2, 2>(a, stream);
-        else
-            launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
+        if (a.T <= 32) launch_mm<MATH, W, FS, 2, 2, 4, 2>(a, stream);
+        else if (a.T > 64 && big > 256) launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4, kByte ? 2 : 1>(a, stream);
+        else if (a.T <= 48) launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
+        else if (small > 256) launch_mm<MATH, W, FS, 4, 2, 2, 2>(a, stream);
+        else launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
     }
 }
 
