@@ -536,16 +536,16 @@ void k_matmul(MvArgs a, int token_blocks) {
     // rows past the last token repeat it, units past the row's end its last one; a row shorter than a unit has no
     // whole one: the loads, whose values are then not used, go elsewhere
     const bool some = end >= 16 * kParts;
+    const char* rows[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+        rows[i] = some ? x0 + min(row0 + i * kRowStep, last_row) * ldb : a.codes;
     const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) __attribute__((always_inline)) {
         const int at = min((it * KC * kChunk + un * kUnitCols) * kB, some ? end - 16 * kParts : 0);
-        const char* p = (some ? x0 : a.codes) + at;
-        const int64_t step = some ? ldb : 0;
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int row = min(row0 + i * kRowStep, last_row);
+        for (int i = 0; i < kUnits; ++i)
 #pragma unroll
-            for (int h = 0; h < kParts; ++h) __builtin_memcpy(&to[i][h], p + row * step + 16 * h, 16);
-        }
+            for (int h = 0; h < kParts; ++h) __builtin_memcpy(&to[i][h], rows[i] + at + 16 * h, 16);
     };
     // unit `ru` of a token row's iteration, into its operands' slots
     const auto put = [&](char* buf, int row, int ru, const u32x4 (&v)[kParts]) __attribute__((always_inline)) {
@@ -579,15 +579,14 @@ void k_matmul(MvArgs a, int token_blocks) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
         const int first = it * KC * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
         const int cut = end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
-        const bool whole = first + (un + 1) * 16 * kParts <= end;
-        if (un != cut)
+        if (first + (un + 1) * 16 * kParts <= end) {
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-                u32x4 v[kParts];
+            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i * kRowStep, un, from[i]);
+        } else if (un != cut) {  // past the end
+            const u32x4 zero[kParts] = {};
 #pragma unroll
-                for (int h = 0; h < kParts; ++h) v[h] = whole ? from[i][h] : u32x4{0, 0, 0, 0};
-                put(buf, row0 + i * kRowStep, un, v);
-            }
+            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i * kRowStep, un, zero);
+        }
         if (cut >= 0)
             for (int row = threadIdx.x; row < 16 * NT; row += kThreads) {
                 const char* src = a.x + min(t0 + row, a.T - 1) * a.ldx * kB;
@@ -750,7 +749,11 @@ void launch_mv(const MvArgs& a, hipStream_t stream) {
         constexpr bool kByte = Mt<MATH>::kBytes == 1;
         const int64_t big = (int64_t)((a.tiles + 7) / 8) * ((a.T + 127) / 128);   // workgroups of 128 x 128
         const int64_t small = (int64_t)((a.tiles + 3) / 4) * ((a.T + 63) / 64);  // and of 64 x 64
-        if (a.T <= 32) launch_mm<MATH, W, FS, 2, 2, 4, 2>(a, stream);
+        if (a.T <= 64 && a.tiles <= 256) {  // 16 rows a workgroup, or the chip would be idle for the most part
+            if (a.T <= 32) launch_mm<MATH, W, FS, 2, 1, 4, 1>(a, stream);
+            else if (a.T <= 48) launch_mm<MATH, W, FS, 3, 1, 4, 1>(a, stream);
+            else launch_mm<MATH, W, FS, 4, 1, 4, 1>(a, stream);
+        } else if (a.T <= 32) launch_mm<MATH, W, FS, 2, 2, 4, 2>(a, stream);
         else if (a.T > 64 && big > 256) launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4, kByte ? 2 : 1>(a, stream);
         else if (a.T <= 48) launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
         else if (small > 256) launch_mm<MATH, W, FS, 4, 2, 2, 2>(a, stream);
