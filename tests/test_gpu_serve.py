@@ -97,6 +97,44 @@ def test_matvec_against_64_bits(T, m, n, bits, group, dtype):
     check_matvec(T, m, n, bits, group, dtype, F32)
 
 
+# every launch shape: tokens 1, <= 4, 8, 16, 32, 48, 64, more; layers of few and of many row tiles; a row length
+# that ends inside a chunk and inside 16 bytes, and rows shorter than 16 bytes
+SHAPES = [(T, m) for T in (1, 3, 7, 13) for m in (40, 8200)] + \
+         [(T, m) for T in (20, 33, 50, 64) for m in (50, 4200)] + \
+         [(100, 130), (100, 8300), (300, 11100), (260, 8192)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16, I8, E4M3])
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 32), (2, 0), (2, 64)])
+@pytest.mark.parametrize("T,m", SHAPES)
+def test_matvec_launch_shapes(T, m, bits, group, dtype):
+    n = 391
+    codes, scales = layer(m, n, bits, group, T)
+    x = tokens(T, n, dtype, T + 1)
+    w = bk.pack(codes.cuda(), scales.cuda(), bits, group)
+    buf = torch.zeros(T, n + 10, dtype=dtype, device="cuda")
+    buf[:, 1:n + 1] = x.cuda()
+    out = torch.full((T + 1, m + 5), -3.0, device="cuda")
+    y = bk.matvec(buf[:, 1:n + 1], w, out=out[:T, 2:m + 2])
+    # a sample of the rows, the last ones among them, so that the 64-bit product stays small
+    rows = torch.unique(torch.cat([torch.arange(0, m, max(1, m // 150)), torch.arange(max(0, m - 20), m)]))
+    ref, tol = matvec_bound(x, None, dense(codes[rows], scales[rows], bits, group), F32)
+    assert bool(((y[:, rows.cuda()].cpu().double() - ref).abs() <= tol).all())
+    out[:T, 2:m + 2] = -3.0
+    assert bool((out == -3.0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16, I8, E4M3])
+@pytest.mark.parametrize("T", [1, 2, 5, 16, 30, 45, 64, 70, 600])
+@pytest.mark.parametrize("n", [1, 2, 3, 7, 8, 9, 15, 16, 17, 33, 127, 129])
+def test_matvec_short_rows(n, T, dtype):
+    """Rows down to one element, at the end of their buffer."""
+    codes, scales = layer(35, n, 4, 0, n, integer=True)
+    x = tokens(T, n, dtype, T, integer=True)
+    y = bk.matvec(x.cuda(), bk.pack(codes.cuda(), scales.cuda(), 4), out_dtype=F32).cpu().double()
+    assert torch.equal(y, x.double() @ dense(codes, scales, 4, 0).t())
+
+
 @pytest.mark.parametrize("out_dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("T", [1, 9, 40, 200])
 def test_matvec_output_types(T, out_dtype):
