@@ -364,6 +364,8 @@ enum { BAKRON_F32 = 0, BAKRON_F16 = 1, BAKRON_BF16 = 2, BAKRON_I8 = 3, BAKRON_E4
  *   scales: [m x ng] fp32, lds >= ng; scale (i, g) is that of columns group g .. of row i.
  *   packed: device, 16-byte aligned, bakron_packed_bytes(m, n, bits, group) bytes, all
  *     written. It stands for w_ij = s_i,g(j) (c_ij - (2^bits - 1) / 2), the solve's grid.
+ *   Sizes: m < 2^26, n < 2^28, at most 2^25 blocks of 16 rows x 128 columns (6.9e10 weights) and
+ *     2^27 blocks of 16 rows' scales of a group.
  * bakron_packed_bytes returns 0 for sizes or options that bakron_pack refuses.
  *
  * bakron_matvec: for T tokens (rows of X, T x n)
@@ -374,9 +376,9 @@ enum { BAKRON_F32 = 0, BAKRON_F16 = 1, BAKRON_BF16 = 2, BAKRON_I8 = 3, BAKRON_E4
  *   The inner sums have exact products and fp32 accumulation (int32, exact, for _I8), the
  *   outer sum is fp32, and Y is rounded once. Token t's result depends on its own row only.
  *   For given sizes and types it is deterministic. T == 0 does nothing. Needs no workspace.
- * Errors: INVALID_ARG for NULL pointers, m or n <= 0, T < 0, bad types, bits, group or ld,
- *   a packed pointer that is not 16-byte aligned, overlapping Y, or more than 2^31 - 1
- *   workgroups (ceil(m / 16) ceil(T / 16)); WORKSPACE if packed_bytes is too small.
+ * Errors: INVALID_ARG for NULL pointers, m or n <= 0 or too large, T < 0 or > 2^40, bad types,
+ *   bits, group or ld, a packed pointer that is not 16-byte aligned, or a Y that overlaps X,
+ *   xscale or packed; WORKSPACE if packed_bytes is too small.
  */
 size_t bakron_packed_bytes(int64_t m, int64_t n, int32_t bits, int64_t group);
 int bakron_pack(const uint8_t* codes, int64_t m, int64_t n, int64_t ldc, int32_t bits, const float* scales,
@@ -394,7 +396,7 @@ int bakron_matvec(const void* packed, size_t packed_bytes, int64_t m, int64_t n,
  *   rotate != 0 applies U_n of `seed` as bakron_rht does (axis 1, no transpose); n <= 32768.
  *   Y: T x n. ytype _F32, _F16, _BF16: v, rounded once. ytype _I8 or _E4M3: codes q and
  *     yscale [T] (required): yscale = max_j |v_j| / 127 (448), q = v / yscale rounded to
- *     nearest even; v is about yscale * q. A row of zeros gets scale 0 and codes 0; a row
+ *     nearest (from an fp32 quotient); v is about yscale * q. A row of zeros gets scale 0 and codes 0; a row
  *     with a v that is not finite gets scale NaN and codes 0.
  *   The arithmetic is fp32 and uses the unrounded h. No workspace; deterministic.
  *   H may be R or X itself, and Y may be X or R itself (same pointer, type and ld), but

@@ -119,10 +119,12 @@ bool same_rows(const Rows& a, const Rows& b) { return a.p == b.p && a.pitch == b
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 
+// m below 2^26 and n below 2^28 (so 4 n fits 31 bits), and as many chunks and scales as one grid packs
 bool bad_pack_shape(int64_t m, int64_t n, int32_t bits, int64_t group) {
-    if (m <= 0 || n <= 0 || m > kMaxDim || n > kMaxDim / 4 || bits < 1 || bits > 4) return true;  // 4 n fits 31 bits
+    if (m <= 0 || n <= 0 || m >= (int64_t)1 << 26 || n >= (int64_t)1 << 28 || bits < 1 || bits > 4) return true;
     if (group != 0 && (group < 32 || group > kMaxDim || (group & (group - 1)) != 0)) return true;
-    return false;
+    const bk::PackShape p = bk::pack_shape(m, n, bits, group);
+    return p.tiles * p.chunks > (int64_t)1 << 25 || p.tiles * p.groups_padded > (int64_t)1 << 27;
 }
 
 }  // namespace
@@ -295,8 +297,6 @@ int bakron_pack(const uint8_t* codes, int64_t m, int64_t n, int64_t ldc, int32_t
         return BAKRON_E_INVALID_ARG;
     const bk::PackShape p = bk::pack_shape(m, n, bits, group);
     if (bad_ld(lds, p.groups) || ((uintptr_t)packed & 15) != 0) return BAKRON_E_INVALID_ARG;
-    if (p.tiles * p.chunks > (int64_t)0x7fffffff || p.tiles * p.groups_padded > (int64_t)0x7fffffff)
-        return BAKRON_E_INVALID_ARG;
     const Rows out = {packed, 1, (int64_t)p.bytes, (int64_t)p.bytes};
     if (overlap(rows_of(codes, m, n, ldc, BAKRON_I8), out) || overlap(rows_of(scales, m, p.groups, lds, BAKRON_F32), out))
         return BAKRON_E_INVALID_ARG;
@@ -312,7 +312,7 @@ int bakron_matvec(const void* packed, size_t packed_bytes, int64_t m, int64_t n,
     if (elem_size(xtype) == 0 || !wide_type(ytype)) return BAKRON_E_INVALID_ARG;
     if (T == 0) return BAKRON_OK;
     if (!X || !Y || bad_ld(ldx, n) || bad_ld(ldy, m)) return BAKRON_E_INVALID_ARG;
-    if (T > 0x7fffffff || (m + 15) / 16 > 0x7fffffff / ((T + 15) / 16)) return BAKRON_E_INVALID_ARG;
+    if (T > (int64_t)1 << 40) return BAKRON_E_INVALID_ARG;
     const Rows y = rows_of(Y, T, m, ldy, ytype);
     const Rows w = {packed, 1, (int64_t)packed_bytes, (int64_t)packed_bytes};
     const Rows xs = {xscale, 1, 4 * T, 4 * T};

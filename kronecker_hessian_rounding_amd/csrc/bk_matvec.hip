@@ -92,12 +92,8 @@ int launch_matvec(const void* packed, int64_t m, int64_t n, int bits, int64_t gr
     MvArgs a;
     a.codes = (const char*)packed;
     a.scales = (const float*)((const char*)packed + p.scale_offset);
-    a.x = (const char*)x;
-    a.xs = xs;
-    a.y = y;
     a.m = m;
     a.n = n;
-    a.T = T;
     a.ldx = ldx;
     a.ldy = ldy;
     a.tiles = (uint32_t)p.tiles;
@@ -111,12 +107,22 @@ int launch_matvec(const void* packed, int64_t m, int64_t n, int bits, int64_t gr
         a.gshift = 0;
         while (((int64_t)fs * kStep << a.gshift) < group) ++a.gshift;
     }
-    switch (xtype) {
-        case BAKRON_F32: launch_products<kF32>(a, p.W, fs, stream); break;
-        case BAKRON_F16: launch_products<kF16>(a, p.W, fs, stream); break;
-        case BAKRON_BF16: launch_products<kBF16>(a, p.W, fs, stream); break;
-        case BAKRON_I8: launch_products<kI8>(a, p.W, fs, stream); break;
-        default: launch_products<kF8>(a, p.W, fs, stream); break;
+    // a grid has fewer than 2^32 threads: tokens by ranges, whole blocks of 128 (one range for anything usual; at most
+    // 512 threads for 64 rows x 32 tokens, or 16 rows x 16)
+    const int64_t most = std::max<int64_t>(16, ((int64_t)1 << 29) / p.tiles / 128 * 128);
+    const int64_t xb = xtype == BAKRON_F32 ? 4 : xtype == BAKRON_I8 || xtype == BAKRON_E4M3 ? 1 : 2;
+    for (int64_t t0 = 0; t0 < T; t0 += most) {
+        a.x = (const char*)x + t0 * ldx * xb;
+        a.xs = xs ? xs + t0 : nullptr;
+        a.y = (char*)y + t0 * ldy * (ytype == BAKRON_F32 ? 4 : 2);
+        a.T = std::min(most, T - t0);
+        switch (xtype) {
+            case BAKRON_F32: launch_products<kF32>(a, p.W, fs, stream); break;
+            case BAKRON_F16: launch_products<kF16>(a, p.W, fs, stream); break;
+            case BAKRON_BF16: launch_products<kBF16>(a, p.W, fs, stream); break;
+            case BAKRON_I8: launch_products<kI8>(a, p.W, fs, stream); break;
+            default: launch_products<kF8>(a, p.W, fs, stream); break;
+        }
     }
     return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
 }

@@ -337,7 +337,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
             if (c < n) store_row<kWhole>(a, row, c, n, v[i], f, code);
             if (NV > 1) __builtin_amdgcn_sched_barrier(0);
         }
-        if (!kRot) break;
+        if (row + gridDim.x >= a.T) break;
         if (threads > 64) __syncthreads();  // the next row writes red and buf again
     }
 }
@@ -350,64 +350,66 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
     extern __shared__ __align__(16) float buf[];
     __shared__ uint32_t red[2][kLongThreads / 64];
     const int n = (int)a.n, groups = (n + 7) / 8;
-    const int64_t row = blockIdx.x;
-    float ss = 0.0f;
-#pragma unroll 1
-    for (int q = threadIdx.x; q < groups; q += kLongThreads) {
-        float v[8], g[8];
-        load_sum<false, TX>(a, row, 8 * q, n, v);
-        if (a.h) store8f<false, TX>((TX*)a.h + row * a.ldh, 8 * q, n, v);
-        load_gain<false, TX>(a, 8 * q, n, g);
-        const uint32_t neg = a.rotate ? sign_bits(a.seed, 8 * q) : 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            ss = fmaf(v[e], v[e], ss);
-            v[e] *= signed_gain(g[e], neg >> e);
-        }
-        if (a.rotate) butterflies(v, 0, a.kbits);
-        float* p = buf + at(8 * q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = v[e];
-    }
-    ss = block_sum(ss, red[0]);
-    const float f = (a.rotate ? a.rscale : 1.0f) / sqrtf(ss / (float)n + a.eps);
-    if (a.rotate)
-        for (int done = 3; done < a.kbits;) {
-            const int w0 = min(done, a.kbits - 3);
-            __syncthreads();
-#pragma unroll 1
-            for (int q = threadIdx.x; q < groups; q += kLongThreads) {
-                float* p = buf + at((q >> w0 << (w0 + 3)) | (q & ((1 << w0) - 1)));
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = p[at(j << w0)];
-                butterflies(v, done - w0, 3);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[at(j << w0)] = v[j];
-            }
-            done = w0 + 3;
-        }
-    __syncthreads();
-    float mx = 0.0f;
-    if (a.ys) {
-        uint32_t top = 0;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        float ss = 0.0f;
 #pragma unroll 1
         for (int q = threadIdx.x; q < groups; q += kLongThreads) {
+            float v[8], g[8];
+            load_sum<false, TX>(a, row, 8 * q, n, v);
+            if (a.h) store8f<false, TX>((TX*)a.h + row * a.ldh, 8 * q, n, v);
+            load_gain<false, TX>(a, 8 * q, n, g);
+            const uint32_t neg = a.rotate ? sign_bits(a.seed, 8 * q) : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(v[e], v[e], ss);
+                v[e] *= signed_gain(g[e], neg >> e);
+            }
+            if (a.rotate) butterflies(v, 0, a.kbits);
+            float* p = buf + at(8 * q);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = v[e];
+        }
+        ss = block_sum(ss, red[0]);
+        const float f = (a.rotate ? a.rscale : 1.0f) / sqrtf(ss / (float)n + a.eps);
+        if (a.rotate)
+            for (int done = 3; done < a.kbits;) {
+                const int w0 = min(done, a.kbits - 3);
+                __syncthreads();
+#pragma unroll 1
+                for (int q = threadIdx.x; q < groups; q += kLongThreads) {
+                    float* p = buf + at((q >> w0 << (w0 + 3)) | (q & ((1 << w0) - 1)));
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = p[at(j << w0)];
+                    butterflies(v, done - w0, 3);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[at(j << w0)] = v[j];
+                }
+                done = w0 + 3;
+            }
+        __syncthreads();
+        float mx = 0.0f;
+        if (a.ys) {
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int q = threadIdx.x; q < groups; q += kLongThreads) {
+                const float* p = buf + at(8 * q);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, mag(p[e]));  // zeros from column n on
+            }
+            mx = block_max(top, red[1]);
+        }
+        const Coder code(mx, f, a.ytype == BAKRON_I8);
+        if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
+#pragma unroll 1
+        for (int q = threadIdx.x; q < groups; q += kLongThreads) {
+            float v[8];
             const float* p = buf + at(8 * q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, mag(p[e]));  // zeros from column n on
+            for (int e = 0; e < 8; ++e) v[e] = p[e];
+            store_row<false>(a, row, 8 * q, n, v, f, code);
         }
-        mx = block_max(top, red[1]);
-    }
-    const Coder code(mx, f, a.ytype == BAKRON_I8);
-    if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
-#pragma unroll 1
-    for (int q = threadIdx.x; q < groups; q += kLongThreads) {
-        float v[8];
-        const float* p = buf + at(8 * q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = p[e];
-        store_row<false>(a, row, 8 * q, n, v, f, code);
+        __syncthreads();  // the next row writes red and buf again
     }
 }
 
@@ -415,50 +417,55 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_lds(NormArgs a) {
 // element's loads precede its stores in the same thread, so in-place calls hold.
 __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
     __shared__ uint32_t red[2][kLongThreads / 64];
-    const int64_t row = blockIdx.x;
-    const auto h_of = [&](int64_t i) {
-        float h = load_elem(a.x, a.xtype, row * a.ldx + i);
-        if (a.r) h += load_elem(a.r, a.xtype, row * a.ldr + i);
-        return h;
-    };
-    const auto u_of = [&](int64_t i) {
-        const float h = h_of(i);
-        return a.gain ? h * load_elem(a.gain, a.gfloat ? BAKRON_F32 : a.xtype, i) : h;
-    };
-    float ss = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) {
-        const float h = h_of(i);
-        ss = fmaf(h, h, ss);
-    }
-    const float f = 1.0f / sqrtf(block_sum(ss, red[0]) / (float)a.n + a.eps);
-    const bool i8 = a.ytype == BAKRON_I8;
-    float mx = 0.0f;
-    if (a.ys) {
-        uint32_t top = 0;
-        for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) top = max(top, mag(u_of(i)));
-        mx = block_max(top, red[1]);
-    }
-    const Coder code(mx, f, i8);
-    if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
-    for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) {
-        const float h = h_of(i), u = u_of(i);
-        if (a.h) store_elem(a.h, a.xtype, row * a.ldh + i, h);
-        if (!a.ys) {
-            store_elem(a.y, a.ytype, row * a.ldy + i, u * f);
-        } else {
-            const float w[4] = {u * code.up, 0.0f, 0.0f, 0.0f};
-            const uint32_t q = i8 ? int8_4(w, code.inv) : e4m3_4(w, code.inv);
-            ((uint8_t*)a.y)[row * a.ldy + i] = code.inv > 0.0f ? (uint8_t)q : (uint8_t)0;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const auto h_of = [&](int64_t i) {
+            float h = load_elem(a.x, a.xtype, row * a.ldx + i);
+            if (a.r) h += load_elem(a.r, a.xtype, row * a.ldr + i);
+            return h;
+        };
+        const auto u_of = [&](int64_t i) {
+            const float h = h_of(i);
+            return a.gain ? h * load_elem(a.gain, a.gfloat ? BAKRON_F32 : a.xtype, i) : h;
+        };
+        float ss = 0.0f;
+        for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) {
+            const float h = h_of(i);
+            ss = fmaf(h, h, ss);
         }
+        const float f = 1.0f / sqrtf(block_sum(ss, red[0]) / (float)a.n + a.eps);
+        const bool i8 = a.ytype == BAKRON_I8;
+        float mx = 0.0f;
+        if (a.ys) {
+            uint32_t top = 0;
+            for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) top = max(top, mag(u_of(i)));
+            mx = block_max(top, red[1]);
+        }
+        const Coder code(mx, f, i8);
+        if (a.ys && threadIdx.x == 0) a.ys[row] = code.scale;
+        for (int64_t i = threadIdx.x; i < a.n; i += kLongThreads) {
+            const float h = h_of(i), u = u_of(i);
+            if (a.h) store_elem(a.h, a.xtype, row * a.ldh + i, h);
+            if (!a.ys) {
+                store_elem(a.y, a.ytype, row * a.ldy + i, u * f);
+            } else {
+                const float w[4] = {u * code.up, 0.0f, 0.0f, 0.0f};
+                const uint32_t q = i8 ? int8_4(w, code.inv) : e4m3_4(w, code.inv);
+                ((uint8_t*)a.y)[row * a.ldy + i] = code.inv > 0.0f ? (uint8_t)q : (uint8_t)0;
+            }
+        }
+        __syncthreads();  // the next row writes red again
     }
 }
+
+constexpr int64_t kMaxRowGrid = 1 << 21;  // a grid has fewer than 2^32 threads
 
 template <typename TX, int NV, int kbits>
 void launch_rows(const NormArgs& a, hipStream_t stream) {
     const int threads = (int)((a.n + 512 * NV - 1) / (512 * NV)) * 64;
     // enough workgroups to fill the chip; each then keeps its signs and gain over its rows
     const int64_t most = (int64_t)device_info().cus * (2048 / threads);
-    const int64_t per = kbits >= 0 ? (a.T + most - 1) / most : 1;  // rows of a workgroup, as even as possible
+    // rows of a workgroup, as even as possible; without rotation one, but for more rows than a grid has
+    const int64_t per = (a.T + (kbits >= 0 ? most : kMaxRowGrid) - 1) / (kbits >= 0 ? most : kMaxRowGrid);
     const unsigned grid = (unsigned)((a.T + per - 1) / per);
     const size_t lds = kbits > 3 ? sizeof(float) * (a.n + (a.n >> 6 << 3)) : 0;
     hipLaunchKernelGGL((k_norm_rows<TX, NV, kbits>), dim3(grid), dim3(threads), lds, stream, a);
@@ -476,7 +483,7 @@ void launch_type(const NormArgs& a, hipStream_t stream) {
     if (a.n <= 8192) launch_order<TX, 1, 13>(a, stream);
     else if (a.n <= 16384) launch_order<TX, 2, 14>(a, stream);
     else
-        hipLaunchKernelGGL(k_norm_lds<TX>, dim3((unsigned)a.T), dim3(kLongThreads),
+        hipLaunchKernelGGL(k_norm_lds<TX>, dim3((unsigned)std::min(a.T, kMaxRowGrid)), dim3(kLongThreads),
                            sizeof(float) * (a.n + 8 + ((a.n + 7) >> 6 << 3)), stream, a);
 }
 
@@ -508,7 +515,7 @@ int launch_rmsnorm(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, 
     a.seed = seed;
     a.rscale = (float)(1.0 / std::sqrt((double)((int64_t)1 << a.kbits)));
     if (n > kNormMaxBuffered)
-        hipLaunchKernelGGL(k_norm_long, dim3((unsigned)T), dim3(kLongThreads), 0, stream, a);
+        hipLaunchKernelGGL(k_norm_long, dim3((unsigned)std::min(T, kMaxRowGrid)), dim3(kLongThreads), 0, stream, a);
     else if (xtype == BAKRON_F32)
         launch_type<float>(a, stream);
     else if (xtype == BAKRON_F16)

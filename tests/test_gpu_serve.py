@@ -275,6 +275,19 @@ def test_matvec_packed_layer_past_4_gib(T):
         assert bool(((y[:, r].cpu().double() - ref).abs() <= tol).all())
 
 
+def test_matvec_tokens_in_ranges():
+    """So many rows that 2060 tokens take two grids: whole numbers, each token against its own value."""
+    m, T = 1 << 22, 2060
+    codes = (torch.arange(m, device="cuda") % 16).to(torch.uint8).reshape(m, 1)
+    w = bk.pack(codes, torch.full((m,), 2.0, device="cuda"), 4)
+    x = (torch.arange(T, device="cuda") % 16).to(BF16).reshape(T, 1)
+    xs = torch.where(torch.arange(T, device="cuda") % 3 == 0, 2.0, 1.0)
+    y = bk.matvec(x, w, x_scale=xs)
+    for t in (0, 1, 2045, 2046, 2047, 2048, 2049, 2059):
+        ref = x[t, 0].float() * xs[t] * (codes[:, 0].float() * 2 - 15)
+        assert torch.equal(y[t].float(), ref.to(BF16).float())
+
+
 def test_pack_clamps_and_overwrites_all_of_it():
     """Codes past the grid count as the largest; every byte of the packed buffer is written."""
     codes, scales = layer(19, 140, 4, 32, 1)
@@ -394,7 +407,7 @@ def test_rmsnorm_output_types(T, n, dtype, out_dtype):
 @pytest.mark.parametrize("out_dtype", [F32, BF16, I8, E4M3])
 @pytest.mark.parametrize("T,n", [(1, 1), (2, 2), (3, 7), (2, 24), (1, 64), (3, 512), (2, 640), (5, 1024), (1, 2048),
                                  (4, 4096), (2, 5120), (3, 8192), (2, 14336), (1, 16384), (2, 28672), (1, 32768),
-                                 (2, 32764)])
+                                 (2, 32764), (2, 12300), (2, 10001), (3, 9984), (2, 16352), (1500, 8448)])
 def test_rmsnorm_rotated(T, n, out_dtype):
     check_norm(T, n, BF16, out_dtype, seed=n * 12345 + 7)
 
@@ -484,6 +497,15 @@ def test_rmsnorm_rows_of_wider_buffers():
 def test_rmsnorm_empty():
     r = bk.rmsnorm(torch.empty(0, 64, device="cuda", dtype=BF16), out_dtype=I8)
     assert r.y.shape == (0, 64) and r.scale.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rmsnorm_more_rows_than_a_grid(dtype):
+    """2^21 + 5 rows of one column: workgroups take a second row."""
+    x = tokens((1 << 21) + 5, 1, dtype, 1).cuda()
+    y = bk.rmsnorm(x, eps=1e-5).y
+    ref = x.double() / (x.double().square() + 1e-5).sqrt()
+    assert float((y.double() - ref).abs().max()) <= torch.finfo(dtype).eps / 2 + 10 * U
 
 
 def test_rmsnorm_offsets_past_2_31():

@@ -28,7 +28,8 @@ def test_packed_bytes():
     # 2-bit: 512 bytes
     assert f(16, 256, 2, 128) == 1024 + 2 * 64
     assert f(16, 257, 1, 0) == 3 * 512 + 64
-    for bad in ((0, 4, 4, 0), (4, 0, 4, 0), (4, 4, 0, 0), (4, 4, 5, 0), (4, 4, 4, 16), (4, 4, 4, 48), (4, 4, 4, -32)):
+    for bad in ((0, 4, 4, 0), (4, 0, 4, 0), (4, 4, 0, 0), (4, 4, 5, 0), (4, 4, 4, 16), (4, 4, 4, 48), (4, 4, 4, -32),
+                (1 << 26, 4, 4, 0), (4, 1 << 28, 4, 0), (1 << 20, 1 << 17, 4, 0)):
         assert f(*bad) == 0, bad
 
 
@@ -58,7 +59,7 @@ def test_matvec_refuses():
 
     for kw in (dict(packed=None), dict(packed=at((1 << 32) + 4)), dict(m=0), dict(n=0), dict(bits=6), dict(group=31),
                dict(X=None), dict(Y=None), dict(xtype=5), dict(xtype=-1), dict(ytype=I8), dict(ytype=E4M3),
-               dict(T=-1), dict(ldx=255), dict(ldy=63), dict(Y=B), dict(Y=A), dict(T=1 << 40),
+               dict(T=-1), dict(ldx=255), dict(ldy=63), dict(Y=B), dict(Y=A), dict(T=(1 << 40) + 1),
                dict(xs=C), dict(Y=at((2 << 32) + 2 * 256 * 3 - 2))):
         assert call(**kw) == INVALID, kw
     assert call(nb=nb - 1) == WORKSPACE
