@@ -184,11 +184,19 @@ __device__ __forceinline__ void load_gain(const NormArgs& a, int c, int n, float
         for (int e = 0; e < 8; ++e) g[e] = (float)w[e];
     }
 }
-// The signs of columns c .. c + 7, a bit each.
+// The signs of columns c .. c + 7, a bit each: bit 63 of SplitMix64's outputs c .. c + 7
+// (splitmix64_out; its last step, z ^ z >> 31, leaves that bit as it is).
 __device__ __forceinline__ uint32_t sign_bits(uint64_t seed, int c) {
+    constexpr uint64_t kStep = 0x9E3779B97F4A7C15ull;
+    const uint64_t first = seed + (uint64_t)(c + 1) * kStep;
     uint32_t neg = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) neg |= (uint32_t)(splitmix64_out(seed, (uint64_t)(c + e)) >> 63) << e;
+    for (int e = 0; e < 8; ++e) {
+        uint64_t z = first + e * kStep;
+        z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+        z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+        neg |= (uint32_t)(z >> 63) << e;
+    }
     return neg;
 }
 __device__ __forceinline__ float signed_gain(float g, uint32_t bit) {
@@ -235,6 +243,18 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
     __shared__ uint32_t red[2][16];
     const int n = (int)a.n, threads = blockDim.x;
     uint32_t neg = 0;  // 8 bits a group
+    // the first row's loads, before the signs are drawn (about 1 us of multiplications): 16-bit types, whose
+    // registers allow it
+    using V = typename Vec<TX>::type;
+    constexpr bool kFirst = kRot && kWhole && sizeof(TX) == 2;
+    V fx[NV], fr[NV];
+    if (kFirst)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = min(8 * ((int)threadIdx.x + i * threads), n - 8);
+            fx[i] = load8<kWhole>((const TX*)a.x + blockIdx.x * a.ldx, c, n);
+            fr[i] = load8<kWhole>((const TX*)(a.r ? a.r : a.x) + blockIdx.x * (a.r ? a.ldr : a.ldx), c, n);
+        }
     if (kRot)
 #pragma unroll 1
         for (int i = 0; i < NV; ++i) neg |= sign_bits(a.seed, 8 * ((int)threadIdx.x + i * threads)) << (8 * i);
@@ -258,7 +278,12 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
             const int c = 8 * (tid() + i * threads);
             if (c < n) {
                 float g[8];
-                load_sum<kWhole, TX>(a, row, c, n, v[i]);
+                if (kFirst && row == blockIdx.x) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] = a.r ? (float)fx[i][e] + (float)fr[i][e] : (float)fx[i][e];
+                } else {
+                    load_sum<kWhole, TX>(a, row, c, n, v[i]);
+                }
                 if (!kKeep) load_gain<kWhole, TX>(a, c, n, g);
                 if (a.h) store8f<kWhole, TX>((TX*)a.h + row * a.ldh, c, n, v[i]);
 #pragma unroll
