@@ -14,7 +14,8 @@ extern template void launch_products<kF8>(const MvArgs&, int, int, hipStream_t);
 namespace {
 
 // ---------------------------------------------------------------- pack
-// One thread per lane's share of a chunk: it gathers its 32 codes. Bound by HBM (reads m n bytes).
+// One thread per lane's share of a chunk: it gathers its 32 codes. Done once a layer; bound by the 8-byte pieces in
+// which it reads its m n bytes.
 template <int W>
 __global__ __launch_bounds__(256) void k_pack(const uint8_t* __restrict__ codes, int64_t m, int64_t n,
                                               int64_t ldc, int shift, int64_t nc, int64_t units,

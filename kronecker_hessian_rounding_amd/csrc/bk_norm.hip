@@ -11,8 +11,10 @@
 // applied last, so a value is rounded once for the gain, once a butterfly and once for f;
 // the codes are u * (127 / max|u|), which f does not enter.
 //
-// Bound by HBM for many rows (x, r, h and y are touched once: the row stays in registers),
-// by latency for few.
+// Bound by HBM for many rows (x, r, h and y are touched once: the row stays in registers):
+// 4096 bf16 rows of 8192 with residual 50 us, 5.3 TB/s. With the rotation its vector
+// instructions and LDS passes come close (e4m3 out: 62 us, 3.8 TB/s). By latency for few: one
+// row of 4096 3.2 us, rotated to int8 4.4 (an empty kernel 2.4).
 #include <cmath>
 
 #include "bk_common.hpp"
