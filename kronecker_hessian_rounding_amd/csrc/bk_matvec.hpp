@@ -260,24 +260,25 @@ struct Stream {
     const Sh* wp[R];
     const float* sp[R];
     int64_t nc;
-    int gshift;
+    int gshift, lane;
     Sh d[PF][R];
     float s[PF][R][kUnits];
-    __device__ __forceinline__ Stream(const MvArgs& a, int64_t tile0, int lane) : nc(a.nc), gshift(a.gshift) {
+    // tile0 and c are uniform over the wave (and known to be): addresses but for the lane's part are scalar
+    __device__ __forceinline__ Stream(const MvArgs& a, int64_t tile0, int lane_) : nc(a.nc), gshift(a.gshift), lane(lane_) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t tile = min(tile0 + r, (int64_t)a.tiles - 1);
-            wp[r] = reinterpret_cast<const Sh*>(a.codes) + tile * a.nc * 64 + lane;
-            sp[r] = a.scales + tile * a.ngp * 16 + (lane & 15);
+            wp[r] = reinterpret_cast<const Sh*>(a.codes) + tile * a.nc * 64;
+            sp[r] = a.scales + tile * a.ngp * 16;
         }
     }
     __device__ __forceinline__ void fetch(int slot, int64_t c) {
         c = min(c, nc - 1);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            d[slot][r] = wp[r][c * 64];
+            d[slot][r] = (wp[r] + c * 64)[lane];
 #pragma unroll
-            for (int f = 0; f < kUnits; ++f) s[slot][r][f] = sp[r][((c * kUnits + f) >> gshift) * 16];
+            for (int f = 0; f < kUnits; ++f) s[slot][r][f] = (sp[r] + ((c * kUnits + f) >> gshift) * 16)[lane & 15];
         }
     }
 };
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
     using Sh = FewShape<MATH, PF, TB>;
     constexpr int kB = M::kBytes;
     extern __shared__ __align__(16) char lds[];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     char* xs = lds + w * Sh::kBytes;
     const int64_t tile0 = (int64_t)blockIdx.x * R;
     const int T = (int)a.T, end = (int)a.n * kB;  // bytes of a row
@@ -527,7 +528,8 @@ void k_matmul(MvArgs a, int token_blocks) {
     const uint32_t total = gridDim.x, per = total / 8, extra = total % 8;
     const uint32_t xcd = blockIdx.x % 8, id = xcd * per + min(xcd, extra) + blockIdx.x / 8;
     const int64_t tile_b = (int64_t)(id / token_blocks) * R * RW, t0 = (int64_t)(id % token_blocks) * 16 * NT;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kg = wave / RW, rg = wave % RW;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave / RW, rg = wave % RW;
     const int q = lane >> 4, t = lane & 15;
 
     constexpr int kParts = kB == 4 ? 2 : 1;  // 16-byte parts of a unit
