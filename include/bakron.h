@@ -398,7 +398,8 @@ int bakron_matvec(const void* packed, size_t packed_bytes, int64_t m, int64_t n,
  *     yscale [T] (required): yscale = max_j |v_j| / 127 (448), q = v / yscale rounded to
  *     nearest (from an fp32 quotient); v is about yscale * q. A row of zeros gets scale 0 and codes 0; a row
  *     with a v that is not finite gets scale NaN and codes 0.
- *   The arithmetic is fp32 and uses the unrounded h. No workspace; deterministic.
+ *   The arithmetic is fp32 and uses the unrounded h: a row whose sum of squares passes fp32's largest value
+ *   (3.4e38) gives zeros, as one with an infinity does in its finite places. No workspace; deterministic.
  *   H may be R or X itself, and Y may be X or R itself (same pointer, type and ld), but
  *   no other overlap of H or Y with a buffer of the call is allowed.
  * Errors: INVALID_ARG for NULL X or Y (T > 0), n <= 0, T < 0 or > 2^31 - 1, bad types or

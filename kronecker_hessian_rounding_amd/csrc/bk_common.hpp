@@ -354,6 +354,9 @@ __device__ __forceinline__ void st_coherent16(f16x8* q, const uint32_t (&v)[4]) 
                        __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void acquire_agent() { __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent"); }
+// Between LDS writes and reads by different lanes of one wave: the hardware keeps a wave's LDS operations in order,
+// so this costs no instruction and only holds the compiler to that order.
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 // keeps the compiler from moving the data loads above the counter check
 __device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }
 // the wave's own memory operations, cache maintenance included, have completed

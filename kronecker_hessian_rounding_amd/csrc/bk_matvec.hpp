@@ -290,7 +290,7 @@ struct Stream {
 // a read: loads of a set are in flight while the set before is multiplied, and no wave
 // waits for another. The 8 waves split the columns (wave w takes chunks w, w + 8, ...);
 // their sums meet in LDS at the end and are added in a fixed order. Bound by HBM for large
-// layers (28672 x 8192, one bf16 token: 4 bits 25 us, 4.9 TB/s; 2 bits 15.6 us, where the
+// layers (28672 x 8192, one bf16 token: 4 bits 25 us, 4.9 TB/s; 2 bits 14.5 us, where the
 // LDS reads of x weigh as much), by latency for small ones (4096 x 4096 4.3 us, an empty
 // kernel 2.4), by the pieces' instructions for fp32 (16 tokens by 8192 x 8192 20 us; 16 bf16
 // tokens by 14336 x 4096 10).
@@ -366,6 +366,9 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
             if (c % NW == w && p >= 0 && p < PF && lane < T)
                 put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + lane * a.ldx * kB, at, end));
         }
+        // this wave alone reads what it staged. (A fence behind the reads too would keep the next set's weights from
+        // moving up: 4096 x 14336 int8 8.8 -> 10.0 us. Their addresses are not known apart from the next writes'.)
+        wave_fence();
         load(i0 + PF);
 #pragma unroll
         for (int p = 0; p < PF; ++p) {

@@ -316,6 +316,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
                 }
                 const auto pass = [&](int w0, int skip) {
                     if (w0 + 3 > 9) __syncthreads();
+                    else wave_fence();
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         const int q = tid() + i * threads;
@@ -336,6 +337,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
                 if (kbits >= 12) pass(9, 0);
                 if (kbits % 3 != 0) pass(kbits - 3, 3 - kbits % 3);
                 if (kbits > 9) __syncthreads();
+                else wave_fence();
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int q = tid() + i * threads;
@@ -366,6 +368,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NV == 1 ? 
         }
         if (row + gridDim.x >= a.T) break;
         if (threads > 64) __syncthreads();  // the next row writes red and buf again
+        else wave_fence();
     }
 }
 
