@@ -461,6 +461,18 @@ def test_rmsnorm_special_rows(n, out_dtype):
         assert bool(((y[3:] - v[3:]).abs() <= half * v[3:].abs().amax(1, keepdim=True) * (1 + 1e-4)).all())
 
 
+@pytest.mark.parametrize("n", [100, 4096, 40000])
+def test_rmsnorm_sum_of_squares_past_fp32(n):
+    """(1e20)^2 passes fp32's largest value: the row's values are zeros; the next row's are its own."""
+    x = tokens(2, n, BF16, 3).cuda()
+    ref = bk.rmsnorm(x)
+    x[0] *= 1e20
+    y = bk.rmsnorm(x).y
+    assert bool((y[0] == 0).all()) and torch.equal(y[1], ref.y[1])
+    q = bk.rmsnorm(x, out_dtype=I8)
+    assert bool(torch.equal(q.scale[0] * q.y[0].float(), torch.zeros(n, device="cuda"))) and q.scale[1] > 0
+
+
 @pytest.mark.parametrize("n", [200, 33000])
 def test_rmsnorm_in_place(n):
     """sum_out = residual, out = x: the values are those of a call with buffers of its own."""
