@@ -4,10 +4,13 @@
 // The solve leaves a layer as codes c_ij in {0..Lq}, Lq = 2^bits - 1, and scales; the
 // weight it stands for is w_ij = s_i,g(j) v_ij with v_ij = c_ij - Lq/2. For T tokens
 //   y_ti = a_t sum_g s_ig sum_{j in group g} x_tj v_ij.
-// v is a half-integer of at most 4 bits, so it is exact in bf16, fp16, e4m3 and (times a
-// power of two) int8: the inner sums run on the matrix cores with exact products and
-// fp32 (int8: exact int32) accumulation, and only the group's scale is applied to the
-// sum, in fp32. Nothing is rounded below 32 bits before the output.
+// v is a half-integer of at most 4 bits, so it is exact in bf16, fp16 and (times a power
+// of two) int8: the inner sums run on the matrix cores with exact products and fp32
+// (int8: exact int32) accumulation, and only the group's scale is applied to the sum, in
+// fp32. Nothing is rounded below 32 bits before the output. e4m3 tokens are converted to
+// fp16, which holds them all, on their way into LDS: the matrix cores' e4m3 operations do
+// not keep 32 bits (448 and 127 times 2^-9 lose most of the small ones; activations with a
+// few large channels came out 2e-5 to 2e-4 off in the 2-norm, in fp16 1e-7).
 //
 // Packed layout (k_pack). Storage width W = 2 for bits <= 2, else 4; a code of fewer bits
 // is moved to the middle of the wider grid, c' = c + (2^W - 2^bits) / 2, which leaves v
@@ -38,7 +41,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRowTile = 16;
@@ -64,11 +66,12 @@ struct MvArgs {
 // ---------------------------------------------------------------- operands
 enum Math { kBF16, kF16, kF8, kI8, kF32 };
 
+// kBytes: of an element of x in memory; kLds: of one (fp32: of a piece of one) in LDS.
 template <int MATH> struct Mt;
 template <> struct Mt<kBF16> {
     using Op = bf16x8;
     using Acc = f32x4;
-    static constexpr int kBytes = 2, kPieces = 1;
+    static constexpr int kBytes = 2, kLds = 2, kPieces = 1;
     static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -79,40 +82,34 @@ template <> struct Mt<kF32> : Mt<kBF16> {
 template <> struct Mt<kF16> {
     using Op = f16x8;
     using Acc = f32x4;
-    static constexpr int kBytes = 2, kPieces = 1;
+    static constexpr int kBytes = 2, kLds = 2, kPieces = 1;
     static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
 };
-template <> struct Mt<kF8> {
-    using Op = u32x2;
-    using Acc = f32x4;
-    static constexpr int kBytes = 1, kPieces = 1;
-    static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c,
-                                                          0, 0, 0);
-    }
+template <> struct Mt<kF8> : Mt<kF16> {
+    static constexpr int kBytes = 1;
 };
 template <> struct Mt<kI8> {
     using Op = u32x2;
     using Acc = i32x4;
-    static constexpr int kBytes = 1, kPieces = 1;
+    static constexpr int kBytes = 1, kLds = 1, kPieces = 1;
     static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
         return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0,
                                                      0);
     }
 };
 
-// What the weight operand holds, as a multiple of v: e4m3 bytes hold 2 |v| in the three
-// low mantissa bits of the subnormal range and the first binade, where e4m3 is linear
-// (value = bits * 2^-9, so v 2^-8); int8 holds 16 v (W = 4) or 64 v (W = 2); bf16 and
+// What the weight operand holds, as a multiple of v: int8 holds 16 v (W = 4) or 64 v (W = 2); bf16 and
 // fp16 hold v. `unit` undoes it on the finished sum; powers of two, exact.
 template <int MATH, int W>
 constexpr float unit() {
-    return MATH == kF8 ? 256.0f : MATH == kI8 ? (W == 4 ? 1.0f / 16 : 1.0f / 64) : 1.0f;
+    return MATH == kI8 ? (W == 4 ? 1.0f / 16 : 1.0f / 64) : 1.0f;
 }
 
-// 4 weights of W = 4 as e4m3 bytes: sign to bit 7, k to bits 3..1, bit 0 set.
+// 4 weights of W = 4 as e4m3 bytes, on their way to bf16 or fp16: sign to bit 7, k to bits 3..1, bit 0 set.
+// That is 2 |v| in the low bits of the subnormal range and the first binade, where e4m3 is linear (value =
+// bits * 2^-9, so v 2^-8), and the conversions' scale undoes the 2^-8.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
     return ((w << 1) & 0x0E0E0E0Eu) | 0x01010101u | ((w << 4) & 0x80808080u);
 }
@@ -161,9 +158,7 @@ __device__ __forceinline__ typename Mt<MATH>::Op weights(typename Share<W>::T d,
     using Op = typename Mt<MATH>::Op;
     if constexpr (W == 4) {
         uint32_t w = d[st];
-        if constexpr (MATH == kF8) {
-            return Op{e4m3_lo(w), e4m3_hi(w)};
-        } else if constexpr (MATH == kI8) {
+        if constexpr (MATH == kI8) {
             // to two's complement: k -> 7 - k under a sign, then 16 (-8 s + k) + 8 = 16 v
             const uint32_t n = w & 0x88888888u;
             w ^= n - (n >> 3);
@@ -173,16 +168,12 @@ __device__ __forceinline__ typename Mt<MATH>::Op weights(typename Share<W>::T d,
         }
     } else {
         uint32_t w = d[st >> 1];
-        if constexpr (MATH == kF8 || MATH == kI8) {
+        if constexpr (MATH == kI8) {
             // even nibbles give columns 0 2 4 6, odd ones 1 3 5 7 (even_odd does the same to x)
-            if constexpr (MATH == kI8) w ^= (w >> 2) & 0x33333333u;
+            w ^= (w >> 2) & 0x33333333u;
             if (st & 1) w <<= 1;  // step b into the places of step a: sign at bit 3, k at bit 1
-            if constexpr (MATH == kF8)
-                return Op{((w << 4) & 0x80808080u) | (w & 0x02020202u) | 0x01010101u,
-                          (w & 0x80808080u) | ((w >> 4) & 0x02020202u) | 0x01010101u};
-            else
-                return Op{((w << 4) & 0x80808080u) | ((w << 5) & 0x40404040u) | 0x20202020u,
-                          (w & 0x80808080u) | ((w << 1) & 0x40404040u) | 0x20202020u};
+            return Op{((w << 4) & 0x80808080u) | ((w << 5) & 0x40404040u) | 0x20202020u,
+                      (w & 0x80808080u) | ((w << 1) & 0x40404040u) | 0x20202020u};
         } else {
             if (st & 1) w <<= 1;
             return from_e2m1((w & 0xAAAAAAAAu) | 0x11111111u, Op{});
@@ -190,9 +181,18 @@ __device__ __forceinline__ typename Mt<MATH>::Op weights(typename Share<W>::T d,
     }
 }
 
-// 8 bytes of x in the order of the 8-bit operands of W = 2.
+// 8 bytes of x in the order of the int8 operands of W = 2.
 __device__ __forceinline__ u32x2 even_odd(u32x2 x) {
     return u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x06040200u), __builtin_amdgcn_perm(x[1], x[0], 0x07050301u)};
+}
+
+// 8 e4m3 values as fp16 (NaN stays NaN).
+__device__ __forceinline__ u32x4 f16_of_e4m3(uint32_t lo, uint32_t hi) {
+    const f16x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false),
+                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true),
+                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false),
+                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true)};
+    return __builtin_bit_cast(u32x4, p);
 }
 
 // Four fp32 values as three bf16 pieces each, largest first, cut by truncation: 8 significant
@@ -226,7 +226,7 @@ __device__ __forceinline__ void operand(const char* src, int piece, typename Mt<
 #pragma unroll
     for (int i = 0; i < Mt<MATH>::kPieces; ++i)  // the smallest piece first into the sum
         p[i] = *reinterpret_cast<const Op*>(src + (Mt<MATH>::kPieces - 1 - i) * piece);
-    if constexpr (W == 2 && Mt<MATH>::kBytes == 1) p[0] = even_odd(p[0]);
+    if constexpr (W == 2 && MATH == kI8) p[0] = even_odd(p[0]);
 }
 
 // The 16 bytes of a row of x from byte `at` on that the row's end, byte `end`, cuts: zeros
@@ -300,7 +300,7 @@ struct FewShape {
     static constexpr int kRowUnits = PF * kChunk * kB / 16;           // 16-byte units of a token row in a set
     static constexpr int kUnits = (TB * kRowUnits + 63) / 64;         // units of a lane
     static constexpr int kPieces = Mt<MATH>::kPieces;
-    static constexpr int kL = kB == 4 ? 2 : kB;                       // bytes of an element (or a piece) in LDS
+    static constexpr int kL = Mt<MATH>::kLds;
     static constexpr int kPiece = PF * kChunk * kL;                   // from piece to piece of a token
     static constexpr int kPitch = kPieces * kPiece + 16;              // from token to token: 4 banks
     static constexpr int kBytes = TB * kPitch;                        // of a wave
@@ -349,6 +349,9 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
             split4(v, p);
 #pragma unroll
             for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x2*>(dst + i * Sh::kPiece + place * 8) = p[i];
+        } else if constexpr (MATH == kF8) {
+            *reinterpret_cast<u32x4*>(dst + place * 32) = f16_of_e4m3(v[0], v[1]);
+            *reinterpret_cast<u32x4*>(dst + place * 32 + 16) = f16_of_e4m3(v[2], v[3]);
         } else {
             *reinterpret_cast<u32x4*>(dst + place * 16) = v;
         }
@@ -429,22 +432,21 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
 // x lies in LDS in operand form, 1 KB for 64 lanes of 16 bytes, so an operand is one
 // conflict-free read. A thread stages 16 bytes of a row (u-th of the row's chunk); the
 // lane slot is (q, t ^ u) for token t, which spreads a row's units over the banks. fp32 is
-// cut into its three pieces on the way in. Of 8-bit types, 16 bytes of a lane are its
-// columns of two steps.
+// cut into its three pieces on the way in, e4m3 becomes fp16. Of int8, 16 bytes of a lane
+// are its columns of two steps.
 //
 // Bound by vector instructions beside the MFMAs: dequantisation (11 for 8 bf16 weights, 7 for
 // int8), spread over the NT tiles that use a weight, and scaling (for int8 two a sum and chunk).
-// 14336 x 4096, groups of 128, 2048 tokens: int8 182 us (1.32 PFLOP/s), e4m3 160, bf16 257;
+// 14336 x 4096, groups of 128, 2048 tokens: int8 182 us (1.32 PFLOP/s), e4m3 244, bf16 263;
 // 48 bf16 tokens 17 us.
 //
 // MmOp: the MFMA of kSub steps, its operands from a share of weights and from LDS. Whole
-// chunks (FS = 4) take int8 two steps and e4m3 four steps at a time, at twice the rate.
+// chunks (FS = 4) take int8 two steps at a time, at twice the rate.
 template <int MATH, int FS>
 struct MmOp {
     using M = Mt<MATH>;
-    static constexpr bool kByte = M::kBytes == 1;
-    static constexpr int kSub = FS == 4 ? (MATH == kI8 ? 2 : MATH == kF8 ? 4 : 1) : 1;
-    using Op = std::conditional_t<kSub == 2, u32x4, std::conditional_t<kSub == 4, u32x8, typename M::Op>>;
+    static constexpr int kSub = FS == 4 && MATH == kI8 ? 2 : 1;
+    using Op = std::conditional_t<kSub == 2, u32x4, typename M::Op>;
     template <int W>
     static __device__ __forceinline__ Op weight(typename Share<W>::T d, int step) {
         if constexpr (kSub == 1) {
@@ -461,21 +463,10 @@ struct MmOp {
         }
     }
     static __device__ __forceinline__ void read(Op (&x)[M::kPieces], const char* buf, int step, int q, int t) {
-        if constexpr (kByte) {
-            Op v;
-#pragma unroll
-            for (int h = 0; h < (kSub + 1) / 2; ++h) {
-                const int pair = (step >> 1) + h;
-                const char* p = buf + pair * 1024 + ((t ^ (4 * pair + q)) & 15) * 16;
-                if constexpr (kSub == 1) {
-                    v = *reinterpret_cast<const u32x2*>(p + (step & 1) * 8);
-                } else {
-                    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[4 * h + e] = w[e];
-                }
-            }
-            x[0] = v;
+        if constexpr (MATH == kI8) {
+            const int pair = step >> 1;
+            const char* p = buf + pair * 1024 + ((t ^ (4 * pair + q)) & 15) * 16;
+            x[0] = *reinterpret_cast<const Op*>(kSub == 1 ? p + (step & 1) * 8 : p);
         } else {
 #pragma unroll
             for (int p = 0; p < M::kPieces; ++p)
@@ -485,14 +476,9 @@ struct MmOp {
     static __device__ __forceinline__ typename M::Acc mma(Op a, Op b, typename M::Acc c) {
         if constexpr (kSub == 1) {
             return M::mma(a, b, c);
-        } else if constexpr (kSub == 2) {
+        } else {
             return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
                                                          0, 0, 0);
-        } else {  // both operands e4m3, block scales 2^0
-            typedef int i32x8 __attribute__((ext_vector_type(8)));
-            return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a),
-                                                                    __builtin_bit_cast(i32x8, b), c, 0, 0, 0, 127, 0,
-                                                                    127);
         }
     }
 };
@@ -500,7 +486,7 @@ struct MmOp {
 template <int MATH, int NT, int KC>
 struct MmTile {
     // bytes of x in LDS a buffer: [chunk][token tile][piece or not][4 steps or 2 pairs][64 lanes][16 bytes]
-    static constexpr int kSlabs = MATH == kF32 ? 12 : Mt<MATH>::kBytes == 2 ? 4 : 2;  // of 1 KB a chunk and tile
+    static constexpr int kSlabs = 2 * Mt<MATH>::kLds * Mt<MATH>::kPieces;  // of 1 KB a chunk and tile
     static constexpr int kBytes = KC * NT * kSlabs * 1024;
 };
 
@@ -519,7 +505,7 @@ void k_matmul(MvArgs a, int token_blocks) {
     constexpr int KC = KS * CH;  // chunks of an iteration
     using Tile = MmTile<MATH, NT, KC>;
     constexpr int kB = M::kBytes, kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
-    constexpr int kUnitCols = 16 / (kB == 4 ? 2 : kB);        // columns of a staged unit: 16 bytes, fp32 32
+    constexpr int kUnitCols = 16 / (kB == 4 ? 2 : kB);        // columns of a staged unit: 16 bytes of x, fp32 32
     constexpr int kRowUnits = KC * kChunk / kUnitCols;        // units of a token row in an iteration
     constexpr int kUnits = 16 * NT * kRowUnits / kThreads;    // units a thread stages
     static_assert(16 * NT * kRowUnits % kThreads == 0, "units divide over the threads");
@@ -565,7 +551,7 @@ void k_matmul(MvArgs a, int token_blocks) {
     const auto put = [&](char* buf, int row, int ru, const u32x4 (&v)[kParts]) __attribute__((always_inline)) {
         const int u = ru % (kChunk / kUnitCols), ck = ru / (kChunk / kUnitCols);
         char* dst = buf + (ck * NT + (row >> 4)) * Tile::kSlabs * 1024;
-        if constexpr (kB == 1) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
+        if constexpr (MATH == kI8) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
             const u32x2 lo = {v[0][0], v[0][1]}, hi = {v[0][2], v[0][3]};
             const int step = u >> 1, pair = step >> 1;
 #pragma unroll
@@ -574,6 +560,13 @@ void k_matmul(MvArgs a, int token_blocks) {
                 const u32x2 w = h ? hi : lo;
                 *reinterpret_cast<u32x2*>(dst + pair * 1024 + (qq * 16 + ((row ^ (4 * pair + qq)) & 15)) * 16 +
                                           (step & 1) * 8) = W == 2 ? even_odd(w) : w;
+            }
+        } else if constexpr (MATH == kF8) {  // columns 16 u ..: 8 of them as below, and the next 8
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int o = 2 * u + h;
+                *reinterpret_cast<u32x4*>(dst + (o >> 2) * 1024 + ((o & 3) * 16 + ((row ^ o) & 15)) * 16) =
+                    f16_of_e4m3(v[0][2 * h], v[0][2 * h + 1]);
             }
         } else {  // columns 8 u ..: step u / 4, lanes of q = u % 4
             const int at = (u >> 2) * 1024 + ((u & 3) * 16 + ((row ^ u) & 15)) * 16;
@@ -760,7 +753,7 @@ void launch_mv(const MvArgs& a, hipStream_t stream) {
             launch_mm<MATH, W, FS, 2, 2, 2, 2>(a, stream);
         }
     } else {
-        constexpr bool kByte = Mt<MATH>::kBytes == 1;
+        constexpr bool kByte = MATH == kI8;
         const int64_t big = (int64_t)((a.tiles + 7) / 8) * ((a.T + 127) / 128);   // workgroups of 128 x 128
         const int64_t small = (int64_t)((a.tiles + 3) / 4) * ((a.T + 63) / 64);  // and of 64 x 64
         if (a.T <= 64 && a.tiles <= 256) {  // 16 rows a workgroup, or the chip would be idle for the most part

@@ -1,0 +1,88 @@
+"""What the serving operators hold, on the GPU: fp32 sums for every type of tokens, against 64 bits.
+
+The tolerances are bounds of the 2-norm of all results' errors. Roundings of a sum whose partial sums have random
+signs add in squares, so these are far below the worst case of every element, and a type that is summed in fewer
+bits, or a part of it left out, shows.
+"""
+import math
+
+import pytest
+import torch
+
+import kronecker_hessian_rounding_amd as bk
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24  # half a step of fp32
+F32, F16, BF16, I8, E4M3 = torch.float32, torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def layer(m, n, bits, group, seed):
+    g = gen(seed)
+    codes = torch.randint(0, 2 ** bits, (m, n), generator=g, dtype=torch.uint8)
+    return codes, torch.rand(m, -(-n // group) if group else 1, generator=g) + 0.25
+
+
+def dense(codes, scales, bits, group):
+    v = codes.double() - (2 ** bits - 1) / 2
+    s = scales.double()
+    return v * (s.repeat_interleave(group, 1)[:, :codes.shape[1]] if group else s)
+
+
+def activations(T, n, dtype, seed):
+    """Values with a few large channels; in 8 bits each token's largest magnitude takes the top value."""
+    g = gen(seed)
+    x = torch.randn(T, n, generator=g) * (0.5 + torch.randn(n, generator=g).square())
+    if dtype == I8:
+        return (x / (x.abs().amax(1, keepdim=True) / 127)).round().clamp(-127, 127).to(I8)
+    return (x / (x.abs().amax(1, keepdim=True) / 448)).to(E4M3) if dtype == E4M3 else x.to(dtype)
+
+
+def wide_rows(T, n, dtype, seed):
+    """Magnitudes spread evenly over the type's octaves (bf16 and fp32: over 60 of them), both signs."""
+    g = gen(seed)
+    lo, hi = {E4M3: (-9.0, 8.8), F16: (-24.0, 15.0), BF16: (-40.0, 20.0), F32: (-40.0, 20.0)}[dtype]
+    x = torch.exp2(torch.rand(T, n, generator=g) * (hi - lo) + lo)
+    return torch.where(torch.rand(T, n, generator=g) < 0.5, x, -x).to(dtype)
+
+
+def norm_bound(n, dtype, group):
+    """The relative 2-norm of the error. The products are exact. A scale's unit (a chunk of 128 columns, or 32 where
+    groups are shorter) takes k matrix operations, each off by at most 2 U of its sum, so 2 U / sqrt(3) in the mean
+    square: 2 U sqrt(k / 3) (int8: exact integers, 0). The N units' sums meet in N additions, each rounded to nearest
+    (U / sqrt(3)) and none of a larger partial sum than the result's norm: U sqrt(N / 3). Adding the waves' sums: 2 U."""
+    steps = 1 if group and group < 128 else 4
+    k = 0 if dtype == I8 else steps * (3 if dtype == F32 else 1)
+    return U * (2 * math.sqrt(k / 3) + math.sqrt(n / (32 * steps) / 3) + 2)
+
+
+@pytest.mark.parametrize("rows", [activations, wide_rows])
+@pytest.mark.parametrize("bits,group", [(4, 32), (4, 128), (4, 0), (3, 64), (2, 64), (2, 0), (1, 0)])
+@pytest.mark.parametrize("T", [1, 4, 7, 16, 40, 100])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16, I8, E4M3])
+def test_matvec_holds_fp32_sums(dtype, T, bits, group, rows):
+    if rows is wide_rows and dtype == I8:
+        rows = activations
+    m, n = 300, 4096
+    codes, scales = layer(m, n, bits, group, T)
+    x = rows(T, n, dtype, T + 1)
+    y = bk.matvec(x.cuda(), bk.pack(codes.cuda(), scales.cuda(), bits, group), out_dtype=F32).cpu().double()
+    ref = x.double() @ dense(codes, scales, bits, group).t()
+    assert float((y - ref).norm() / ref.norm()) <= norm_bound(n, dtype, group)
+
+
+@pytest.mark.parametrize("bits,group", [(4, 0), (4, 32), (2, 0), (2, 64)])
+@pytest.mark.parametrize("T", [1, 5, 20, 100])
+def test_matvec_e4m3_smallest_beside_largest(T, bits, group):
+    """448 and 127 of the smallest value, 2^-9, in a chunk: their sum takes 25 bits below which nothing is left, and
+    every partial sum of it is a multiple of 2^-10 below 2^14, so the result is exact."""
+    x = torch.full((T, 128), 2.0 ** -9)
+    x[torch.arange(T), (torch.arange(T) * 37) % 128] = 448.0
+    codes = torch.full((16, 128), 2 ** bits - 1, dtype=torch.uint8)
+    scales = torch.ones(16, 128 // group if group else 1)
+    y = bk.matvec(x.to(E4M3).cuda(), bk.pack(codes.cuda(), scales.cuda(), bits, group), out_dtype=F32).cpu().double()
+    assert torch.equal(y, torch.full((T, 16), (448 + 127 * 2.0 ** -9) * (2 ** bits - 1) / 2, dtype=torch.float64))
