@@ -18,14 +18,14 @@ namespace {
 // which it reads its m n bytes.
 template <int W>
 __global__ __launch_bounds__(256) void k_pack(const uint8_t* __restrict__ codes, int64_t m, int64_t n,
-                                              int64_t ldc, int shift, int64_t nc, int64_t units,
+                                              int64_t ldc, int top, int shift, int64_t nc, int64_t units,
                                               typename Share<W>::T* __restrict__ out) {
     const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (u >= units) return;
     const int lane = (int)(u & 63);
     const int64_t chunk = (u >> 6) % nc, tile = (u >> 6) / nc;
     const int64_t row = tile * kRowTile + (lane & 15);
-    constexpr int kTop = (1 << W) - 1, kHalf = 1 << (W - 1);
+    constexpr int kHalf = 1 << (W - 1);
     typename Share<W>::T d;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
@@ -35,8 +35,8 @@ __global__ __launch_bounds__(256) void k_pack(const uint8_t* __restrict__ codes,
             // W = 4: e is the column; W = 2: e >> 3 picks step a or b
             const int step = W == 4 ? j : 2 * j + (e >> 3);
             const int64_t col = chunk * kChunk + step * kStep + 8 * (lane >> 4) + (e & 7);
-            int c = row < m && col < n ? codes[row * ldc + col] + shift : kHalf;
-            c = min(c, kTop);
+            // cut to the layer's own grid, then moved to the middle of the stored one
+            const int c = row < m && col < n ? min((int)codes[row * ldc + col], top) + shift : kHalf;
             const uint32_t s = c < kHalf, k = s ? kHalf - 1 - c : c - kHalf;
             if (W == 4)
                 w |= (s << 3 | k) << (8 * (e & 3) + 4 * (e >> 2));
@@ -74,13 +74,13 @@ int launch_pack(const uint8_t* codes, int64_t m, int64_t n, int64_t ldc, int bit
                 int64_t group, void* packed, hipStream_t stream) {
     const PackShape p = pack_shape(m, n, bits, group);
     const int64_t units = p.tiles * p.chunks * 64, total = p.tiles * p.groups_padded * kRowTile;
-    const int shift = ((1 << p.W) - (1 << bits)) / 2;
+    const int top = (1 << bits) - 1, shift = ((1 << p.W) - (1 << bits)) / 2;
     const dim3 grid((unsigned)((units + 255) / 256)), sgrid((unsigned)((total + 255) / 256));
     if (p.W == 4)
-        hipLaunchKernelGGL(k_pack<4>, grid, dim3(256), 0, stream, codes, m, n, ldc, shift, p.chunks, units,
+        hipLaunchKernelGGL(k_pack<4>, grid, dim3(256), 0, stream, codes, m, n, ldc, top, shift, p.chunks, units,
                            (u32x4*)packed);
     else
-        hipLaunchKernelGGL(k_pack<2>, grid, dim3(256), 0, stream, codes, m, n, ldc, shift, p.chunks, units,
+        hipLaunchKernelGGL(k_pack<2>, grid, dim3(256), 0, stream, codes, m, n, ldc, top, shift, p.chunks, units,
                            (u32x2*)packed);
     hipLaunchKernelGGL(k_pack_scales, sgrid, dim3(256), 0, stream, scales, m, lds, p.groups, p.groups_padded, total,
                        (float*)((char*)packed + p.scale_offset));

@@ -304,6 +304,21 @@ def test_pack_clamps_and_overwrites_all_of_it():
     assert st == 0 and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("bits", [1, 2, 3, 4])
+def test_pack_clamps_to_the_layers_own_grid(bits):
+    """A code past 2^bits - 1 counts as that, also where codes are stored in more bits than they have."""
+    top = 2 ** bits - 1
+    codes, scales = layer(21, 150, bits, 32, 1)
+    big = codes.clone()
+    at = codes == top
+    big[at] = torch.tensor([top + 1, top + 2, 200, 255], dtype=torch.uint8)[torch.arange(int(at.sum())) % 4]
+    a = bk.pack(codes.cuda(), scales.cuda(), bits, 32)
+    b = bk.pack(big.cuda(), scales.cuda(), bits, 32)
+    assert torch.equal(a.data, b.data)
+    y = bk.matvec(torch.eye(150, device="cuda"), b).cpu()  # w itself: exact in fp32
+    assert torch.equal(y, dense(codes, scales, bits, 32).float().t())
+
+
 def test_pack_strided_codes():
     codes, scales = layer(30, 100, 2, 64, 1)
     wide = torch.zeros(30, 131, dtype=torch.uint8)
