@@ -366,6 +366,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
             if (token_of(i) < TB) put(token_of(i), place_of(i), x[i]);
         if (end % 16 != 0) {  // the unit that the row ends in, if it is in this set
             const int at = end & ~15, c = at / (kChunk * kB), p = c / NW - i0;
+            wave_fence();  // behind the zeros that another lane wrote there
             if (c % NW == w && p >= 0 && p < PF && lane < T)
                 put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + lane * a.ldx * kB, at, end));
         }

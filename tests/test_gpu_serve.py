@@ -135,6 +135,18 @@ def test_matvec_short_rows(n, T, dtype):
     assert torch.equal(y, x.double() @ dense(codes, scales, 4, 0).t())
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16, I8, E4M3])
+@pytest.mark.parametrize("T", [1, 3, 16])
+@pytest.mark.parametrize("n", [1025, 2051, 3077, 6151])
+def test_matvec_unit_that_the_rows_end_cuts(n, T, dtype):
+    """The last elements of a row weigh most: what another lane leaves in their place would show."""
+    codes, scales = layer(18, n, 4, 0, n, integer=True)
+    x = torch.ones(T, n)
+    x[:, n - n % 4:] = 8.0
+    y = bk.matvec(x.to(dtype).cuda(), bk.pack(codes.cuda(), scales.cuda(), 4), out_dtype=F32).cpu().double()
+    assert torch.equal(y, x.double() @ dense(codes, scales, 4, 0).t())
+
+
 @pytest.mark.parametrize("out_dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("T", [1, 9, 40, 200])
 def test_matvec_output_types(T, out_dtype):
