@@ -342,8 +342,12 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
     for (int p = 0; p < PF; ++p) st.fetch(p, w + p * NW);
     float sum[R][4] = {};
     const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * Sh::kL;
+    // 0, but known to the compiler only as made from every operand read so far: a set's writes, whose addresses it is
+    // part of, cannot move in front of other lanes' reads of the set before. (A fence there would keep global loads
+    // in place too: 4096 x 14336 int8 8.8 -> 10.0 us. This costs nothing.)
+    int after = 0;
     const auto put = [&](int token, int place, u32x4 v) __attribute__((always_inline)) {  // unit `place` of a token
-        char* dst = xs + token * Sh::kPitch;
+        char* dst = xs + token * Sh::kPitch + after;
         if constexpr (kB == 4) {
             u32x2 p[3];
             split4(v, p);
@@ -370,8 +374,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
             if (c % NW == w && p >= 0 && p < PF && lane < T)
                 put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + lane * a.ldx * kB, at, end));
         }
-        // this wave alone reads what it staged. (A fence behind the reads too would keep the next set's weights from
-        // moving up: 4096 x 14336 int8 8.8 -> 10.0 us. Their addresses are not known apart from the next writes'.)
+        // this wave alone reads what it staged
         wave_fence();
         load(i0 + PF);
 #pragma unroll
@@ -385,6 +388,8 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
                     for (int j = 0; j < FS; ++j) {
                         typename M::Op v[M::kPieces];
                         operand<MATH, W>(xk + (f * FS + j) * kStep * Sh::kL, Sh::kPiece, v);
+#pragma unroll
+                        for (int q = 0; q < M::kPieces; ++q) asm("" : "+v"(after) : "v"(v[q]));
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const typename M::Op b = weights<MATH, W>(st.d[p][r], f * FS + j);
