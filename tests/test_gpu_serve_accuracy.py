@@ -86,3 +86,22 @@ def test_matvec_e4m3_smallest_beside_largest(T, bits, group):
     scales = torch.ones(16, 128 // group if group else 1)
     y = bk.matvec(x.to(E4M3).cuda(), bk.pack(codes.cuda(), scales.cuda(), bits, group), out_dtype=F32).cpu().double()
     assert torch.equal(y, torch.full((T, 16), (448 + 127 * 2.0 ** -9) * (2 ** bits - 1) / 2, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("bits,group", [(4, 0), (4, 32), (2, 0), (2, 32)])
+@pytest.mark.parametrize("T", [1, 5, 16, 20, 50, 100, 300])
+def test_matvec_every_bit_of_an_fp32_token(T, bits, group):
+    """One value of 24 bits a row, in every column in turn, against weights of -1/2 and 1/2: the results are halves of
+    the values, exact, whatever the launch; a piece of x that is lost or misplaced shows."""
+    m, n = 40, 141
+    g = gen(T)
+    codes = torch.randint(2 ** (bits - 1) - 1, 2 ** (bits - 1) + 1, (m, n), generator=g, dtype=torch.uint8)
+    ones = torch.ones(m, -(-n // group) if group else 1)
+    w, v = bk.pack(codes.cuda(), ones.cuda(), bits, group), dense(codes, ones, bits, group)
+    for first in range(0, n, T):
+        value = (torch.randint(2 ** 23, 2 ** 24, (T,), generator=g) | 1).float() * 2.0 ** -20
+        col = (first + torch.arange(T)) % n
+        x = torch.zeros(T, n)
+        x[torch.arange(T), col] = value
+        y = bk.matvec(x.cuda(), w).cpu().double()
+        assert torch.equal(y, value.double()[:, None] * v[:, col].t())
