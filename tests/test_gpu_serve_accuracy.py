@@ -105,3 +105,69 @@ def test_matvec_every_bit_of_an_fp32_token(T, bits, group):
         x[torch.arange(T), col] = value
         y = bk.matvec(x.cuda(), w).cpu().double()
         assert torch.equal(y, value.double()[:, None] * v[:, col].t())
+
+
+def hadamard(b):
+    h = torch.ones(1, 1, dtype=torch.float64)
+    while len(h) < b:
+        h = torch.cat([torch.cat([h, h], 1), torch.cat([h, -h], 1)])
+    return h
+
+
+def signs(seed, n):
+    out = []
+    for i in range(1, n + 1):
+        z = (seed + i * 0x9E3779B97F4A7C15) % 2 ** 64
+        z = (z ^ z >> 30) * 0xBF58476D1CE4E5B9 % 2 ** 64
+        z = (z ^ z >> 27) * 0x94D049BB133111EB % 2 ** 64
+        out.append(-1.0 if (z ^ z >> 31) >> 63 else 1.0)
+    return torch.tensor(out, dtype=torch.float64)
+
+
+def rotation(seed, n):
+    """U = (I (x) H_b / sqrt(b)) diag(signs), b the largest power of two that divides n."""
+    b = n & -n
+    return torch.block_diag(*[hadamard(b)] * (n // b)) / math.sqrt(b) * signs(seed, n)
+
+
+@pytest.mark.parametrize("bits,q", [(4, I8), (4, E4M3), (4, BF16), (3, F32), (2, I8), (2, E4M3), (1, F16)])
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_rotated_layer_chain(T, bits, q):
+    """A layer rotated, rounded by the solve, packed and used: norm with rotation, product, rotation back, in 64 bits.
+
+    First from the norm's own output, with fp32 tolerances: the product's (norm_bound, and U for the token's scale),
+    and a rounding a stage and for the scale of the rotation back, which is orthogonal. Then from the layer's inputs:
+    the rotation keeps 2-norms, so what the rounding of the activations does is at most ||W'|| times its 2-norm."""
+    m, n = 192, 320
+    g = gen(bits)
+    W = torch.randn(m, n, generator=g).cuda()
+    HI = bk.hessian_accum(torch.randn(900, n, generator=g).cuda())
+    HO = bk.hessian_accum(torch.randn(700, m, generator=g).cuda())
+    bk.rotate_layer(W, HI, HO, seed_O=11, seed_I=22)
+    (LO, DO), (LI, DI) = bk.ldl_pair(HO, HI)
+    res = bk.solve(W, LO, LI, bits, D_O=DO, D_I=DI)
+    w = bk.pack(res.codes, res.scales, bits)
+    x, r = torch.randn(T, n, generator=g).to(BF16), torch.randn(T, n, generator=g).to(BF16)
+    gain = 1 + 0.1 * torch.randn(n, generator=g)
+    nr = bk.rmsnorm(x.cuda(), gain.cuda(), residual=r.cuda(), rotate_seed=22, out_dtype=q)
+    y = bk.rht(bk.matvec(nr.y, w, x_scale=nr.scale, out_dtype=F32), 1, 11, transpose=True).cpu().double()
+
+    wq = dense(res.codes.cpu(), res.scales.cpu().reshape(-1, 1), bits, 0)
+    back = rotation(11, m)
+    held = nr.y.cpu().double() * (1.0 if nr.scale is None else nr.scale.cpu().double()[:, None])
+    own = held @ wq.t() @ back  # rows times U_O: U_O^T y
+    fp32 = norm_bound(n, q, 0) + U + U * (math.log2(m & -m) + 1)
+    assert float((y - own).norm()) <= fp32 * float(own.norm())
+
+    h = x.double() + r.double()
+    v = h / (h.square().mean(1, keepdim=True) + 1e-6).sqrt() * gain.double() @ rotation(22, n).t()
+    full = v @ wq.t() @ back
+    lost = (v - held).norm(dim=1)
+    half = {I8: 0.5 / 127, E4M3: 2.0 ** -4, BF16: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}[q]
+    # the norm's own fp32 error: n / 64 + 16 roundings of the sum, halved by the root, 8 more, one a stage
+    norm = U * (n / 128 + 16 + math.log2(n & -n) + 3)
+    top = v.abs().amax(1, keepdim=True) if q == I8 else torch.maximum(v.abs(), v.abs().amax(1, keepdim=True) / 448 / 8)
+    assert bool((lost <= half * top.expand_as(v).norm(dim=1) * (1 + 2.0 ** -10) + norm * v.norm(dim=1)).all())
+    limit = torch.linalg.matrix_norm(wq, 2) * lost + fp32 * own.norm(dim=1)
+    assert bool(((y - full).norm(dim=1) <= limit).all())
+    assert bool((limit <= 0.25 * full.norm(dim=1)).all())  # and that is small beside the result
