@@ -608,7 +608,7 @@ def _token_scales(t: torch.Tensor, name: str, T: int, dev: int) -> int:
 
 @dataclass
 class PackedWeight:
-    """A layer's codes and scales in bakron_matvec's layout (device bytes)."""
+    """A layer's codes and scales in bakron_matvec's layout (device bytes, as pack() returns them)."""
     data: torch.Tensor
     m: int
     n: int
@@ -616,7 +616,14 @@ class PackedWeight:
     group: int
 
     def __post_init__(self):
-        self.nbytes = self.data.numel()
+        nb = LIB.bakron_packed_bytes(self.m, self.n, self.bits, self.group)
+        d = self.data
+        if nb == 0 or d.dtype != torch.uint8 or not d.is_contiguous() or d.numel() != nb:
+            raise ValueError("data must hold the %d contiguous bytes of a packed %d x %d layer" % (nb, self.m, self.n))
+
+    @property
+    def nbytes(self) -> int:
+        return self.data.numel()
 
 
 def pack(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -> PackedWeight:
@@ -659,8 +666,9 @@ def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = N
     m = w.m
     if n != w.n:
         raise ValueError("x must have %d columns" % w.n)
-    if w.data.get_device() != dev:
-        raise ValueError("the packed layer must be on x's device")
+    packed = w.data
+    if packed.get_device() != dev or not packed.is_contiguous():
+        raise ValueError("the packed layer must be contiguous and on x's device")
     xtype = x.dtype
     if out is None:
         if out_dtype is None:
@@ -674,7 +682,7 @@ def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = N
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out must be a tensor of %s" % out_dtype)
         out_dtype = out.dtype
-    st = LIB.bakron_matvec(w.data.data_ptr(), w.nbytes, m, n, w.bits, w.group, x.data_ptr(), ROW_TYPES[xtype], T, ldx,
+    st = LIB.bakron_matvec(packed.data_ptr(), packed.numel(), m, n, w.bits, w.group, x.data_ptr(), ROW_TYPES[xtype], T, ldx,
                            None if x_scale is None else _token_scales(x_scale, "x_scale", T, dev), out.data_ptr(),
                            ROW_TYPES[out_dtype], ldy, torch._C._cuda_getCurrentRawStream(dev))
     if st:

@@ -605,6 +605,22 @@ def test_binding_refusals():
             f()
 
 
+def test_binding_refuses_a_layer_whose_bytes_were_replaced():
+    codes, scales = layer(32, 128, 4, 32, 1)
+    w = bk.pack(codes.cuda(), scales.cuda(), 4, 32)
+    x = tokens(2, 128, BF16, 2).cuda()
+    data = w.data
+    w.data = data[:-16]
+    with pytest.raises(bk.BakronError):
+        bk.matvec(x, w)
+    for bad in (data[:1].expand(data.numel()), data.cpu()):
+        w.data = bad
+        with pytest.raises(ValueError):
+            bk.matvec(x, w)
+    w.data = data.clone()
+    assert bk.matvec(x, w).shape == (2, 32)
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("bits,q", [(4, I8), (4, E4M3), (2, I8), (3, BF16)])
 @pytest.mark.parametrize("T", [1, 5, 70])

@@ -108,3 +108,20 @@ def test_binding_refuses_host_tensors():
         bk.pack(torch.zeros(4, 64, dtype=torch.uint8), torch.ones(4), 4)
     with pytest.raises(ValueError):
         bk.matvec(x, bk.PackedWeight(torch.zeros(1, dtype=torch.uint8), 4, 64, 4, 0))
+
+
+def test_packed_weight_refuses_other_bytes():
+    """A layer made or changed by hand holds exactly the bytes that the products read."""
+    nb = bk.LIB.bakron_packed_bytes(64, 256, 4, 128)
+    data = torch.zeros(nb, dtype=torch.uint8)
+    w = bk.PackedWeight(data, 64, 256, 4, 128)
+    assert w.nbytes == nb
+    w.data = data[:-1]
+    assert w.nbytes == nb - 1  # what a product is told, and refuses
+    one = torch.zeros(1, dtype=torch.uint8)
+    for bad in (data[:-1], torch.zeros(nb + 1, dtype=torch.uint8), data.int(), one.expand(nb),
+                torch.zeros(2 * nb, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            bk.PackedWeight(bad, 64, 256, 4, 128)
+    with pytest.raises(ValueError):
+        bk.PackedWeight(data, 64, 256, 5, 128)
