@@ -374,7 +374,9 @@ enum { BAKRON_F32 = 0, BAKRON_F16 = 1, BAKRON_BF16 = 2, BAKRON_I8 = 3, BAKRON_E4
  *   X: BAKRON_F32, _F16, _BF16, _I8 or _E4M3, ldx >= n. xscale: [T] fp32 factors a_t, or
  *     NULL for 1. Y: T x m, BAKRON_F32, _F16 or _BF16, ldy >= m; it must not overlap X.
  *   The inner sums have exact products and fp32 accumulation (int32, exact, for _I8), the
- *   outer sum is fp32, and Y is rounded once. Token t's result depends on its own row only.
+ *   outer sum is fp32, and Y is rounded once. (An fp32 x is taken to a multiple of 2^-133, towards
+ *   zero, which leaves a value of 2^-110 or more as it is; an inner sum is of X times up to 2^bits / 2,
+ *   before its scale, and overflows as fp32 does.) Token t's result depends on its own row only.
  *   For given sizes and types it is deterministic. T == 0 does nothing. Needs no workspace.
  * Errors: INVALID_ARG for NULL pointers, m or n <= 0 or too large, T < 0 or > 2^40, bad types,
  *   bits, group or ld, a packed pointer that is not 16-byte aligned, or a Y that overlaps X,
@@ -399,7 +401,9 @@ int bakron_matvec(const void* packed, size_t packed_bytes, int64_t m, int64_t n,
  *     nearest (from an fp32 quotient); v is about yscale * q. A row of zeros gets scale 0 and codes 0; a row
  *     with a v that is not finite gets scale NaN and codes 0.
  *   The arithmetic is fp32 and uses the unrounded h: a row whose sum of squares passes fp32's largest value
- *   (3.4e38) gives zeros, as one with an infinity does in its finite places. No workspace; deterministic.
+ *   (3.4e38) gives zeros, as one with an infinity does in its finite places. With eps = 0 a row below about 1e-19
+ *   loses accuracy with its squares, and one whose sum of squares is 0 in fp32 (zeros, or nothing above about 1e-23)
+ *   has no finite v. No workspace; deterministic.
  *   H may be R or X itself, and Y may be X or R itself (same pointer, type and ld), but
  *   no other overlap of H or Y with a buffer of the call is allowed.
  * Errors: INVALID_ARG for NULL X or Y (T > 0), n <= 0, T < 0 or > 2^31 - 1, bad types or

@@ -654,7 +654,7 @@ def matvec(x: torch.Tensor, w: PackedWeight, x_scale: Optional[torch.Tensor] = N
 
     x: float32, float16, bfloat16, or int8 / float8_e4m3fn; x_scale (T,) float32 multiplies
     each token's result. The result is T x m (or (m,)) in out_dtype (default: x's type, or
-    bfloat16 for an 8-bit x).
+    bfloat16 for an 8-bit x). No gradient is formed.
     """
     one = isinstance(x, torch.Tensor) and x.dim() == 1
     if one:
@@ -706,7 +706,7 @@ def rmsnorm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Opti
     rotate_seed applies the rotation that rht(..., axis=1, seed) applies to a layer's inputs.
     out_dtype: float32, float16, bfloat16 (default: x's type), or int8 / float8_e4m3fn, which
     come with one scale per token: the values are scale[:, None] * y. sum receives h in x's
-    type when a residual is given (sum_out=residual updates it in place).
+    type when a residual is given (sum_out=residual updates it in place). No gradient is formed.
     """
     dev = _device_of(x, "x")
     ldx = _rows(x, "x", _WIDE, dev)

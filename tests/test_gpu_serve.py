@@ -515,6 +515,23 @@ def test_rmsnorm_sum_of_squares_past_fp32(n):
     assert bool(torch.equal(q.scale[0] * q.y[0].float(), torch.zeros(n, device="cuda"))) and q.scale[1] > 0
 
 
+@pytest.mark.parametrize("n", [100, 4096, 20000, 40000])
+def test_rmsnorm_without_eps(n):
+    """eps = 0: a row of zeros, or of values whose squares are 0 in fp32, has no finite values; others are right."""
+    x = tokens(4, n, F32, 3)
+    x[1] = 0.0
+    x[2] *= 1e-30
+    x[3] *= 1e-15
+    y = bk.rmsnorm(x.cuda(), eps=0.0).y.cpu().double()
+    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[2]).any())
+    v, tol = norm64(x, None, None, 0.0, None)
+    assert bool(((y - v).abs() <= tol + v.abs() * U)[[0, 3]].all())
+    for out_dtype in (I8, E4M3):
+        q = bk.rmsnorm(x.cuda(), eps=0.0, out_dtype=out_dtype)
+        assert bool(torch.isnan(q.scale[1:3]).all()) and bool((q.y[1:3].float() == 0).all())
+        assert bool(torch.isfinite(q.scale[[0, 3]]).all())
+
+
 @pytest.mark.parametrize("n", [200, 33000])
 def test_rmsnorm_in_place(n):
     """sum_out = residual, out = x: the values are those of a call with buffers of its own."""

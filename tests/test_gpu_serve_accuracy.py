@@ -107,6 +107,22 @@ def test_matvec_every_bit_of_an_fp32_token(T, bits, group):
         assert torch.equal(y, value.double()[:, None] * v[:, col].t())
 
 
+@pytest.mark.parametrize("T", [1, 12, 40])
+def test_matvec_fp32_tokens_near_the_smallest(T):
+    """An fp32 value is taken to a multiple of 2^-133 towards zero: itself from 2^-110 on, and never more than 2^-133
+    off. Weights of 1/2 and scales of 2^20 keep the results normal, so they are exact."""
+    w = bk.pack(torch.full((16, 32), 8, dtype=torch.uint8).cuda(), torch.full((16,), 2.0 ** 20).cuda(), 4)
+    g = gen(T)
+    for e in (-149, -140, -133, -126, -120, -111, -110, -100):
+        x = torch.zeros(T, 32, dtype=torch.float64)
+        x[:, 5] = (1 + torch.rand(T, generator=g, dtype=torch.float64)) * 2.0 ** e
+        x = x.float()
+        y = bk.matvec(x.cuda(), w).cpu().double() / 2.0 ** 19
+        held = (x.double() * 2.0 ** 133).trunc() / 2.0 ** 133
+        assert torch.equal(y, held[:, 5:6].expand(T, 16)), e
+        assert e < -110 or torch.equal(held, x.double())
+
+
 def hadamard(b):
     h = torch.ones(1, 1, dtype=torch.float64)
     while len(h) < b:
