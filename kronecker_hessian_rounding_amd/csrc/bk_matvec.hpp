@@ -737,41 +737,60 @@ void launch_few(const MvArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((k_matvec_few<MATH, W, FS, R, PF, TB, NW>), grid, dim3(64 * NW), lds, stream, a);
 }
 
+// Chunks ahead of their use (PF): 2 KB of weights in flight per wave, 1 KB for fp32 from 5 tokens on, whose pieces fill
+// LDS. 14336 x 4096, 16 bf16 tokens 10.6 us, with half 10.6, with twice as many 15.0; one token 8.5, 8.7 and 9.2.
+// Tiles that share an operand of x (R): two, from 5 tokens on, where that still makes a workgroup for every compute
+// unit: 16 tokens by 8176 x 4096 (256 workgroups of two tiles) bf16 7.4 us, one tile 8.2, fp32 11.7 and 17.5; by 4096 x
+// 4096 (128) 6.7 and 5.5. Up to 4 tokens two tiles gain nothing but for fp32 (14336 x 4096: bf16 9.1 and 9.1, int8 8.1
+// and 8.2, fp32 12.0 and 14.3).
 template <int MATH, int W, int FS, int TB>
 void launch_tokens(const MvArgs& a, hipStream_t stream) {
-    constexpr int PF = TB <= 4 ? 8 / W : MATH == kF32 ? 1 : 2;  // 2 KB of weights in flight per wave
-    constexpr int R = TB <= 4 ? 1 : 2;                           // tiles that share an operand of x
-    if (a.tiles >= 512) launch_few<MATH, W, FS, R, PF, TB, 8>(a, stream);
+    constexpr int PF = TB <= 4 ? 8 / W : MATH == kF32 ? 1 : 2;
+    constexpr int R = TB <= 4 ? 1 : 2;
+    if ((int)a.tiles >= 2 * device_info().cus) launch_few<MATH, W, FS, R, PF, TB, 8>(a, stream);
     else launch_few<MATH, W, FS, 1, PF, TB, 8>(a, stream);
 }
 
+// Up to 16 tokens k_matvec_few, by the tokens that its LDS holds (fp32, 4096 x 4096, one token 5.0 us, with room for 4
+// 6.1, 8 7.5, 16 9.6; bf16 4.45, 4.5, 4.7, 5.3): 16 bf16 tokens by 14336 x 4096 10.9 us, the smallest k_matmul 14.7.
+// More than 16 tokens: k_matmul with the first of these tiles whose workgroups all run at once (two of the first on a
+// compute unit, one of the others), so that a call is one round of them; us of each side by the number of workgroups:
+//   rows x tokens  (16-bit types and int8)
+//   16 x 32  64 bf16 tokens by 4096 x 4096 (512 workgroups) 12.7, 64 x 32 13.8; 80 tokens (768) 19.2 and 13.9
+//   64 x 32  64 tokens by 8192 x 8192 (256) 24.1, 64 x 48 30.3; 80 tokens (384) 44.2 and 30.7
+//   64 x 48  80 tokens by 8192 x 8192 (256) 30.7, 64 x 64 34.9; 100 tokens (384) 55.8 and 34.5
+//   64 x 64  columns split over 4 waves: 128 tokens by 8192 x 8192 (256) 34.5, over 2 40.7; 200 tokens (512) 64.3, 54.9
+// else, up to 32 tokens, 64 x 32 in rounds (32 tokens by 28672 x 4096 26.9, 64 x 64 29.1); 128 x 128 with a workgroup
+// for every unit (512 tokens by 8192 x 8192 (256): bf16 98.7, 64 x 64 108, int8 73 and 79; 512 tokens by 4096 x 14336
+// (128) 164 and 95), for which 64 tokens are too few; 64 x 64 over 2 waves for the rest.
+// 128 x 128 takes two chunks an iteration for int8 (2048 tokens by 14336 x 4096 209, one 217), and half the tokens
+// where 16-bit types scale every step, for the registers (with whole chunks half the tokens cost 303 -> 354).
+// fp32: 64 x 32 while its workgroups make two rounds at most, else 256 x 32 (n = 8192, 128 tokens by 8192 rows (512
+// workgroups) 125, 256 x 32 131; 200 tokens (896) 239 and 128; n = 4096, 64 tokens by 14336 rows (448) 66 and 68).
 template <int MATH, int W, int FS>
 void launch_mv(const MvArgs& a, hipStream_t stream) {
+    const int64_t cus = device_info().cus;
+    const auto blocks = [&](int tiles, int tokens) {
+        return (int64_t)((a.tiles + tiles - 1) / tiles) * ((a.T + tokens - 1) / tokens);
+    };
     if (a.T == 1) launch_tokens<MATH, W, FS, 1>(a, stream);
     else if (a.T <= 4) launch_tokens<MATH, W, FS, 4>(a, stream);
     else if (a.T <= 8) launch_tokens<MATH, W, FS, 8>(a, stream);
     else if (a.T <= 16) launch_tokens<MATH, W, FS, 16>(a, stream);
     else if constexpr (MATH == kF32) {
-        // 256 rows x 32 tokens where that makes a workgroup for every compute unit (8192 x 8192 with 512 tokens 215
-        // us, the other 453), else 64 x 32 with split columns (with 64 tokens 58 us, the first 142)
-        if (FS == 4 && (int64_t)((a.tiles + 15) / 16) * ((a.T + 31) / 32) >= 256) {
-            if constexpr (FS == 4) launch_mm<MATH, W, FS, 2, 4, 1, 4>(a, stream);
-        } else {
-            launch_mm<MATH, W, FS, 2, 2, 2, 2>(a, stream);
+        if constexpr (FS == 4) {
+            if (blocks(4, 32) > 2 * cus) return launch_mm<MATH, W, FS, 2, 4, 1, 4>(a, stream);
         }
+        launch_mm<MATH, W, FS, 2, 2, 2, 2>(a, stream);
     } else {
         constexpr bool kByte = MATH == kI8;
-        const int64_t big = (int64_t)((a.tiles + 7) / 8) * ((a.T + 127) / 128);   // workgroups of 128 x 128
-        const int64_t small = (int64_t)((a.tiles + 3) / 4) * ((a.T + 63) / 64);  // and of 64 x 64
-        if (a.T <= 64 && a.tiles <= 256) {  // 16 rows a workgroup, or the chip would be idle for the most part
-            if (a.T <= 32) launch_mm<MATH, W, FS, 2, 1, 4, 1>(a, stream);
-            else if (a.T <= 48) launch_mm<MATH, W, FS, 3, 1, 4, 1>(a, stream);
-            else launch_mm<MATH, W, FS, 4, 1, 4, 1>(a, stream);
-        } else if (a.T <= 32) launch_mm<MATH, W, FS, 2, 2, 4, 2>(a, stream);
-        else if (a.T > 64 && big > 256) launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4, kByte ? 2 : 1>(a, stream);
-        else if (a.T <= 48) launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
-        else if (small > 256) launch_mm<MATH, W, FS, 4, 2, 2, 2>(a, stream);
-        else launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
+        if (blocks(1, 32) <= 2 * cus) launch_mm<MATH, W, FS, 2, 1, 4, 1>(a, stream);
+        else if (a.T <= 32 || blocks(4, 32) <= cus) launch_mm<MATH, W, FS, 2, 2, 4, 2>(a, stream);
+        else if (blocks(4, 48) <= cus) launch_mm<MATH, W, FS, 3, 2, 4, 2>(a, stream);
+        else if (blocks(4, 64) <= cus) launch_mm<MATH, W, FS, 4, 2, 4, 2>(a, stream);
+        else if (a.T > 64 && blocks(8, 128) >= cus)
+            launch_mm<MATH, W, FS, kByte || FS == 4 ? 8 : 4, 2, 1, 4, kByte ? 2 : 1>(a, stream);
+        else launch_mm<MATH, W, FS, 4, 2, 2, 2>(a, stream);
     }
 }
 

@@ -124,6 +124,15 @@ def test_matvec_launch_shapes(T, m, bits, group, dtype):
     assert bool((out == -3.0).all())
 
 
+# workgroups of 64 rows x 32 tokens in one round and in several, of 64 x 48, 64 x 64 with columns split over 4 waves,
+# 128 x 128 at exactly one a compute unit, and fp32 on both sides of two rounds
+@pytest.mark.parametrize("dtype", [F32, F16, BF16, I8, E4M3])
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 32), (2, 0)])
+@pytest.mark.parametrize("T,m", [(40, 4200), (32, 16400), (80, 8190), (100, 8190), (512, 8190), (129, 8190), (128, 8190)])
+def test_matvec_launch_shapes_by_workgroups(T, m, bits, group, dtype):
+    test_matvec_launch_shapes(T, m, bits, group, dtype)
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16, I8, E4M3])
 @pytest.mark.parametrize("T", [1, 2, 5, 16, 30, 45, 64, 70, 600])
 @pytest.mark.parametrize("n", [1, 2, 3, 7, 8, 9, 15, 16, 17, 33, 127, 129])
