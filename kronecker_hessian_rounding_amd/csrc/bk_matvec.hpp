@@ -291,7 +291,7 @@ struct Stream {
 // a read: loads of a set are in flight while the set before is multiplied, and no wave
 // waits for another. The 8 waves split the columns (wave w takes chunks w, w + 8, ...);
 // their sums meet in LDS at the end and are added in a fixed order. Bound by HBM for large
-// layers (28672 x 8192, one bf16 token: 4 bits 25 us, 4.9 TB/s; 2 bits 14.5 us, where the
+// layers (28672 x 8192, one bf16 token: 4 bits 25 to 28 us, 4.4 to 4.9 TB/s; 2 bits 14.5 us, where the
 // LDS reads of x weigh as much), by latency for small ones (4096 x 4096 4.3 us, an empty
 // kernel 2.4), by the pieces' instructions for fp32 (16 tokens by 8192 x 8192 20 us; 16 bf16
 // tokens by 14336 x 4096 10).
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
     const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * Sh::kL;
     // 0, but known to the compiler only as made from every operand read so far: a set's writes, whose addresses it is
     // part of, cannot move in front of other lanes' reads of the set before. (A fence there would keep global loads
-    // in place too: 4096 x 14336 int8 8.8 -> 10.0 us. This costs nothing.)
+    // in place too: 4096 x 14336 int8 8.8 -> 9.9 us. This costs nothing.)
     int after = 0;
     const auto put = [&](int token, int place, u32x4 v) __attribute__((always_inline)) {  // unit `place` of a token
         char* dst = xs + token * Sh::kPitch + after;
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
 //
 // Bound by vector instructions beside the MFMAs: dequantisation (11 for 8 bf16 weights, 7 for
 // int8), spread over the NT tiles that use a weight, and scaling (for int8 two a sum and chunk).
-// 14336 x 4096, groups of 128, 2048 tokens: int8 182 us (1.32 PFLOP/s), e4m3 244, bf16 263;
+// 14336 x 4096, groups of 128, 2048 tokens: int8 182 us (1.32 PFLOP/s), e4m3 240, bf16 261;
 // 48 bf16 tokens 17 us.
 //
 // MmOp: the MFMA of kSub steps, its operands from a share of weights and from LDS. Whole
