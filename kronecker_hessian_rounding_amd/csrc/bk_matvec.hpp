@@ -747,7 +747,7 @@ template <int MATH, int W, int FS, int TB>
 void launch_tokens(const MvArgs& a, hipStream_t stream) {
     constexpr int PF = TB <= 4 ? 8 / W : MATH == kF32 ? 1 : 2;
     constexpr int R = TB <= 4 ? 1 : 2;
-    if ((int)a.tiles >= 2 * device_info().cus) launch_few<MATH, W, FS, R, PF, TB, 8>(a, stream);
+    if (R > 1 && (int)a.tiles >= 2 * device_info().cus) launch_few<MATH, W, FS, R, PF, TB, 8>(a, stream);
     else launch_few<MATH, W, FS, 1, PF, TB, 8>(a, stream);
 }
 
@@ -769,15 +769,15 @@ void launch_tokens(const MvArgs& a, hipStream_t stream) {
 // workgroups) 125, 256 x 32 131; 200 tokens (896) 239 and 128; n = 4096, 64 tokens by 14336 rows (448) 66 and 68).
 template <int MATH, int W, int FS>
 void launch_mv(const MvArgs& a, hipStream_t stream) {
+    if (a.T == 1) return launch_tokens<MATH, W, FS, 1>(a, stream);
+    if (a.T <= 4) return launch_tokens<MATH, W, FS, 4>(a, stream);
+    if (a.T <= 8) return launch_tokens<MATH, W, FS, 8>(a, stream);
+    if (a.T <= 16) return launch_tokens<MATH, W, FS, 16>(a, stream);
     const int64_t cus = device_info().cus;
     const auto blocks = [&](int tiles, int tokens) {
         return (int64_t)((a.tiles + tiles - 1) / tiles) * ((a.T + tokens - 1) / tokens);
     };
-    if (a.T == 1) launch_tokens<MATH, W, FS, 1>(a, stream);
-    else if (a.T <= 4) launch_tokens<MATH, W, FS, 4>(a, stream);
-    else if (a.T <= 8) launch_tokens<MATH, W, FS, 8>(a, stream);
-    else if (a.T <= 16) launch_tokens<MATH, W, FS, 16>(a, stream);
-    else if constexpr (MATH == kF32) {
+    if constexpr (MATH == kF32) {
         if constexpr (FS == 4) {
             if (blocks(4, 32) > 2 * cus) return launch_mm<MATH, W, FS, 2, 4, 1, 4>(a, stream);
         }
