@@ -413,6 +413,49 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
                    void* H, int64_t ldh, const void* gain, int32_t gtype, float eps, int rotate, uint64_t seed,
                    void* Y, int32_t ytype, int64_t ldy, float* yscale, void* stream);
 
+/*
+ * Root-mean-square norm of each query and key head, with the position rotation, in one pass over the rows that a
+ * query-key-value product leaves. For token t and head h, x its d elements:
+ *     v = gain * x / sqrt(mean(x^2) + eps), or x where norm == 0,
+ *   then, for i < rot / 2 and the angle a = pos[t] * freq[i], pair i = (p, q) of v's first rot elements becomes
+ *     (p cos a - q sin a, q cos a + p sin a);
+ *   pair i is (v[i], v[i + rot / 2]), or with interleaved != 0 (v[2 i], v[2 i + 1]). The other elements stay.
+ *   Q: T tokens of hq heads, K: T tokens of hk heads (hk = 0: no keys), type BAKRON_F32, F16 or BF16. Element e of
+ *     head h of token t is at t * qt + h * qh + e (keys kt, kh); heads lie inside a token's row (qt >= (hq - 1) qh + d)
+ *     or tokens inside a head's (qh >= (T - 1) qt + d). YQ, YK: the results, of the same type, strides yqt, ...
+ *   qgain, kgain: [d], type gtype = Q's or BAKRON_F32, or NULL (1). norm == 0 takes none.
+ *   pos: [T] int64, or int32 with pos32 != 0, any values. freq: [rot / 2] fp32. rot even, 0 to d; 0 needs neither.
+ *   The arithmetic is fp32, rounded once at the end; angles are formed and reduced in 64 bits (the product is exact
+ *   for positions below 2^29; sine and cosine within 3e-7). A head of zeros with eps = 0, or one whose sum of squares passes
+ *   fp32's range, is as for bakron_rmsnorm. No workspace; deterministic; a head's result depends on its own row only.
+ *   YQ may be Q itself and YK K itself (same pointer and strides); no other overlap with an output is allowed.
+ * Errors: INVALID_ARG for NULL Q or YQ (with T > 0; K and YK with hk > 0), T < 0 or > 2^31 - 1, hq < 1, hk < 0, either
+ *   above 65535, d < 1 or > 512, rot odd, negative or > d, missing pos or freq with rot > 0, bad types or strides, eps
+ *   negative or not finite, a gain without the norm, or overlap.
+ */
+int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const void* K, int64_t hk, int64_t kt, int64_t kh,
+                     int32_t type, int64_t T, int64_t d, const void* qgain, const void* kgain, int32_t gtype, float eps,
+                     int norm, const void* pos, int pos32, const float* freq, int64_t rot, int interleaved, void* YQ,
+                     int64_t yqt, int64_t yqh, void* YK, int64_t ykt, int64_t ykh, void* stream);
+
+/*
+ * A router's choice: for each of T rows of E logits l, k experts and their weights.
+ *   BAKRON_SCORE_SOFTMAX: score_e = exp(l_e) / sum over all experts of exp(l), chosen by l_e (bias NULL).
+ *   BAKRON_SCORE_SIGMOID: score_e = 1 / (1 + exp(-l_e)), chosen by score_e + bias_e (bias: [E] fp32, or NULL), formed in
+ *     64 bits.
+ *   logits: BAKRON_F32, F16 or BF16, ldl >= E. ids: T x k int32, contiguous, the experts in falling order of what they
+ *     are chosen by, the lowest index first among equals. weights: T x k fp32: the scores of the chosen; with
+ *     renorm != 0 divided by their sum (0 if that is 0); times scale.
+ *   An expert whose logit or bias is -infinity or NaN is never chosen (and not in softmax's sum): slots that find none
+ *     hold id -1 and weight 0. Logits of +infinity share softmax's whole weight equally.
+ *   No workspace; deterministic.
+ * Errors: INVALID_ARG for NULL logits, ids or weights (T > 0), T < 0 or > 2^40, E < 1 or > 1024, k < 1, > 64 or > E, bad
+ *   types, ldl or scoring, a bias with softmax, a scale that is not finite, or outputs that overlap each other or an input.
+ */
+enum { BAKRON_SCORE_SOFTMAX = 0, BAKRON_SCORE_SIGMOID = 1 };
+int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t ldl, int64_t k, int scoring,
+                 const float* bias, int renorm, float scale, int32_t* ids, float* weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

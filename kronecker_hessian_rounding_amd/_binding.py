@@ -93,6 +93,12 @@ def _load() -> ctypes.CDLL:
     lib.bakron_rmsnorm.restype = ctypes.c_int
     lib.bakron_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i32, f32, ctypes.c_int,
                                    ctypes.c_uint64, vp, i32, i64, vp, vp]
+    ci = ctypes.c_int
+    lib.bakron_head_norm.restype = ci
+    lib.bakron_head_norm.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, i32, i64, i64, vp, vp, i32, f32, ci, vp, ci,
+                                     vp, i64, ci, vp, i64, i64, vp, i64, i64, vp]
+    lib.bakron_route.restype = ci
+    lib.bakron_route.argtypes = [vp, i32, i64, i64, i64, i64, ci, vp, ci, f32, vp, vp, vp]
     return lib
 
 
@@ -107,7 +113,8 @@ EXPORTS = ("bakron_abi_version", "bakron_status_str", "bakron_hessian_accum_work
            "bakron_token_weights_workspace_bytes", "bakron_token_weights", "bakron_ldl_workspace_bytes", "bakron_ldl", "bakron_ldl_async",
            "bakron_ldl_pair_async",
            "bakron_solve_workspace_bytes", "bakron_solve", "bakron_solve_noalloc", "bakron_rht",
-           "bakron_layer_report", "bakron_packed_bytes", "bakron_pack", "bakron_matvec", "bakron_rmsnorm")
+           "bakron_layer_report", "bakron_packed_bytes", "bakron_pack", "bakron_matvec", "bakron_rmsnorm",
+           "bakron_head_norm", "bakron_route")
 
 
 def abi_version() -> int:
@@ -755,3 +762,126 @@ def rmsnorm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Opti
     if st:
         _check("bakron_rmsnorm", st)
     return NormResult(out, scale_out, sum_out)
+
+
+def _heads(t: torch.Tensor, name: str, dtypes, dev: int, shape=None):
+    """Validate heads (T x heads x d) on the current device; returns the strides of tokens and heads."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError("%s must be a CUDA/ROCm tensor on the current device" % name)
+    size = t.shape
+    if t.dtype not in dtypes or len(size) != 3 or size[1] == 0 or size[2] == 0:
+        raise ValueError("%s must be tokens x heads x elements of %s" % (name, ", ".join(str(d) for d in dtypes)))
+    if shape is not None and size != shape:
+        raise ValueError("%s must be %d x %d x %d" % ((name,) + tuple(shape)))
+    st, sh, step = t.stride()
+    if step != 1 and size[2] > 1:
+        raise ValueError("%s must have unit stride inside a head" % name)
+    return st, sh
+
+
+def _gain(g: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype, dev: int):
+    """The address of a gain vector in float32 or `dtype`, or None."""
+    if g is None:
+        return None
+    if (not isinstance(g, torch.Tensor) or g.get_device() != dev or g.numel() != n or not g.is_contiguous()
+            or (g.dtype != dtype and g.dtype != torch.float32)):
+        raise ValueError("%s must be a contiguous vector of length %d, float32 or x's type" % (name, n))
+    return g.data_ptr()
+
+
+def head_norm(q: torch.Tensor, k: Optional[torch.Tensor] = None, q_gain: Optional[torch.Tensor] = None,
+              k_gain: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              freq: Optional[torch.Tensor] = None, eps: float = 1e-6, norm: bool = True, pairs: str = "half",
+              out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None):
+    """The norm of each head of q (T x heads x d) and k, and the position rotation, in one pass; returns (q, k).
+
+    v = gain * x / sqrt(mean(x^2) + eps) over a head (norm=False: v = x). positions (T,) int64 or int32 and freq
+    (r,) float32 rotate r pairs of v by the angles positions[t] * freq[i]: pairs="half" takes (v[i], v[i + r]),
+    "interleaved" (v[2 i], v[2 i + 1]); elements from 2 r on stay. Views of the rows that a product left are taken as
+    they are; out_q=q, out_k=k work in place. d up to 512. No gradient is formed.
+    """
+    dev = _device_of(q, "q")
+    qt, qh = _heads(q, "q", _WIDE, dev)
+    T, hq, d = q.shape
+    dtype = q.dtype
+    hk = kt = kh = ykt = ykh = 0
+    pk = yk = pp = pf = None
+    if out_q is None:
+        out_q = q.new_empty((T, hq, d))
+        yqt, yqh = hq * d, d
+    else:
+        yqt, yqh = _heads(out_q, "out_q", (dtype,), dev, q.shape)
+    if k is not None:
+        kt, kh = _heads(k, "k", (dtype,), dev)
+        hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("k must hold %d tokens' heads of %d elements" % (T, d))
+        if out_k is None:
+            out_k = k.new_empty((T, hk, d))
+            ykt, ykh = hk * d, d
+        else:
+            ykt, ykh = _heads(out_k, "out_k", (dtype,), dev, k.shape)
+        pk, yk = k.data_ptr(), out_k.data_ptr()
+    elif out_k is not None or k_gain is not None:
+        raise ValueError("out_k and k_gain go with k")
+    if not norm and (q_gain is not None or k_gain is not None):
+        raise ValueError("a gain goes with the norm")
+    if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
+        raise ValueError("q_gain and k_gain must have one type")
+    gq, gk = _gain(q_gain, "q_gain", d, dtype, dev), _gain(k_gain, "k_gain", d, dtype, dev)
+    gtype = ROW_TYPES[q_gain.dtype if gq is not None else k_gain.dtype if gk is not None else dtype]
+    rot = pos32 = 0
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq go together")
+    if freq is not None:
+        if (not isinstance(freq, torch.Tensor) or freq.get_device() != dev or freq.dtype != torch.float32
+                or freq.dim() != 1 or not freq.is_contiguous() or 2 * freq.numel() > d):
+            raise ValueError("freq must be a contiguous float32 vector of at most d / 2 = %d on the current device" % (d // 2))
+        if (not isinstance(positions, torch.Tensor) or positions.get_device() != dev or positions.numel() != T
+                or positions.dtype not in (torch.int64, torch.int32) or not positions.is_contiguous()):
+            raise ValueError("positions must be a contiguous int64 or int32 vector of length %d on the current device" % T)
+        rot, pos32 = 2 * freq.numel(), int(positions.dtype == torch.int32)
+        pp, pf = positions.data_ptr(), freq.data_ptr()
+    if pairs != "half" and pairs != "interleaved":
+        raise ValueError("pairs must be 'half' or 'interleaved'")
+    st = LIB.bakron_head_norm(q.data_ptr(), hq, qt, qh, pk, hk, kt, kh, ROW_TYPES[dtype], T, d, gq, gk, gtype, eps,
+                              int(norm), pp, pos32, pf, rot, int(pairs == "interleaved"), out_q.data_ptr(), yqt, yqh,
+                              yk, ykt, ykh, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("bakron_head_norm", st)
+    return out_q, out_k
+
+
+SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def route(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
+          renormalize: bool = True, scale: float = 1.0):
+    """The k experts of each row of a router's logits (T x E), and their weights: (ids int32, weights float32), T x k.
+
+    scoring "softmax" chooses by the logits; "sigmoid" by sigmoid(logit) + bias, where the bias (E,) float32 acts on the
+    choice alone. The weights are the scores of the chosen, divided by their sum with renormalize, times scale. Experts
+    come in falling order, the lowest index first among equals; a logit of -inf or NaN is never chosen, and slots left
+    over hold id -1 and weight 0, which experts() skips. E up to 1024, k up to 64.
+    """
+    dev = _device_of(logits, "logits")
+    ldl = _rows(logits, "logits", _WIDE, dev)
+    T, E = logits.shape
+    k = int(k)
+    if scoring not in SCORING:
+        raise ValueError("scoring must be 'softmax' or 'sigmoid'")
+    if not 1 <= k <= min(E, 64) or E > 1024:
+        raise ValueError("route takes 1 <= k <= 64, k <= E <= 1024")
+    b = None
+    if bias is not None:
+        if scoring != "sigmoid":
+            raise ValueError("a bias goes with sigmoid scores")
+        b = _token_scales(bias, "bias", E, dev)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    st = LIB.bakron_route(logits.data_ptr(), ROW_TYPES[logits.dtype], T, E, ldl, k, SCORING[scoring], b,
+                          int(bool(renormalize)), scale, ids.data_ptr(), weights.data_ptr(),
+                          torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("bakron_route", st)
+    return ids, weights

@@ -127,6 +127,20 @@ bool bad_pack_shape(int64_t m, int64_t n, int32_t bits, int64_t group) {
     return p.tiles * p.chunks > (int64_t)1 << 25 || p.tiles * p.groups_padded > (int64_t)1 << 27;
 }
 
+// Heads of T tokens as rows: tokens that hold heads, or heads that hold tokens (see bakron_head_norm).
+bool bad_heads(int64_t T, int64_t H, int64_t d, int64_t st, int64_t sh) {
+    if ((H > 1 && sh < d) || (T > 1 && st < d)) return true;
+    if (H <= 1 || T <= 1) return false;
+    return st < (__int128)(H - 1) * sh + d && sh < (__int128)(T - 1) * st + d;
+}
+Rows rows_of_heads(const void* p, int64_t T, int64_t H, int64_t d, int64_t st, int64_t sh, int type) {
+    const int64_t e = (int64_t)elem_size(type);
+    if (H <= 1) return {p, T, d * e, T > 1 ? st * e : d * e};
+    if (T <= 1) return {p, H, d * e, sh * e};
+    if (st >= sh) return {p, T, ((H - 1) * sh + d) * e, st * e};
+    return {p, H, ((T - 1) * st + d) * e, sh * e};
+}
+
 }  // namespace
 
 extern "C" {
@@ -347,6 +361,56 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
         return BAKRON_E_INVALID_ARG;
     return bk::launch_rmsnorm(X, xtype, T, n, ldx, R, ldr, H, ldh, gain, gtype, eps, rotate != 0, seed, Y, ytype, ldy,
                               yscale, (hipStream_t)stream);
+}
+
+int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const void* K, int64_t hk, int64_t kt, int64_t kh,
+                     int32_t type, int64_t T, int64_t d, const void* qgain, const void* kgain, int32_t gtype, float eps,
+                     int norm, const void* pos, int pos32, const float* freq, int64_t rot, int interleaved, void* YQ,
+                     int64_t yqt, int64_t yqh, void* YK, int64_t ykt, int64_t ykh, void* stream) {
+    if (!wide_type(type) || T < 0 || T > 0x7fffffff || hq < 1 || hk < 0 || hq > 65535 || hk > 65535 || d < 1 ||
+        d > bk::kMaxHeadDim || rot < 0 || rot > d || (rot & 1))
+        return BAKRON_E_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(eps < INFINITY)) return BAKRON_E_INVALID_ARG;
+    if ((qgain || kgain) && (!norm || (gtype != type && gtype != BAKRON_F32))) return BAKRON_E_INVALID_ARG;
+    if (T == 0) return BAKRON_OK;
+    if (!Q || !YQ || (hk && (!K || !YK)) || (rot && (!pos || !freq))) return BAKRON_E_INVALID_ARG;
+    if (bad_heads(T, hq, d, qt, qh) || bad_heads(T, hq, d, yqt, yqh)) return BAKRON_E_INVALID_ARG;
+    if (hk && (bad_heads(T, hk, d, kt, kh) || bad_heads(T, hk, d, ykt, ykh))) return BAKRON_E_INVALID_ARG;
+    const Rows in[2] = {rows_of_heads(Q, T, hq, d, qt, qh, type), rows_of_heads(hk ? K : nullptr, T, hk, d, kt, kh, type)};
+    const Rows out[2] = {rows_of_heads(YQ, T, hq, d, yqt, yqh, type),
+                         rows_of_heads(hk ? YK : nullptr, T, hk, d, ykt, ykh, type)};
+    const bool same[2] = {Q == YQ && (T == 1 || qt == yqt) && (hq == 1 || qh == yqh),
+                          K == YK && (T == 1 || kt == ykt) && (hk <= 1 || kh == ykh)};
+    const Rows small[4] = {rows_of(qgain, 1, d, d, gtype), rows_of(kgain, 1, d, d, gtype),
+                           {rot ? pos : nullptr, 1, (pos32 ? 4 : 8) * T, (pos32 ? 4 : 8) * T},
+                           {rot ? freq : nullptr, 1, 2 * rot, 2 * rot}};
+    if (overlap(out[0], out[1])) return BAKRON_E_INVALID_ARG;
+    for (int o = 0; o < 2; ++o) {
+        for (int i = 0; i < 2; ++i)
+            if (overlap(in[i], out[o]) && !(i == o && same[i])) return BAKRON_E_INVALID_ARG;
+        for (const Rows& r : small)
+            if (overlap(r, out[o])) return BAKRON_E_INVALID_ARG;
+    }
+    const bk::HeadRows q = {Q, YQ, qgain, hq, qt, qh, yqt, yqh}, k = {K, YK, kgain, hk, kt, kh, ykt, ykh};
+    return bk::launch_head_norm(q, k, type, T, d, gtype, eps, norm != 0, pos, pos32 != 0, freq, rot, interleaved != 0,
+                                (hipStream_t)stream);
+}
+
+int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t ldl, int64_t k, int scoring,
+                 const float* bias, int renorm, float scale, int32_t* ids, float* weights, void* stream) {
+    if (!wide_type(type) || T < 0 || T > (int64_t)1 << 40 || E < 1 || E > bk::kMaxExperts || k < 1 ||
+        k > bk::kMaxChosen || k > E)
+        return BAKRON_E_INVALID_ARG;
+    if ((scoring != BAKRON_SCORE_SOFTMAX && scoring != BAKRON_SCORE_SIGMOID) || (bias && scoring == BAKRON_SCORE_SOFTMAX) ||
+        !(scale - scale == 0.0f))
+        return BAKRON_E_INVALID_ARG;
+    if (T == 0) return BAKRON_OK;
+    if (!logits || !ids || !weights || bad_ld(ldl, E)) return BAKRON_E_INVALID_ARG;
+    const Rows l = rows_of(logits, T, E, ldl, type), b = rows_of(bias, 1, E, E, BAKRON_F32);
+    const Rows i = {ids, 1, 4 * T * k, 4 * T * k}, w = {weights, 1, 4 * T * k, 4 * T * k};
+    if (overlap(i, w) || overlap(l, i) || overlap(l, w) || overlap(b, i) || overlap(b, w)) return BAKRON_E_INVALID_ARG;
+    return bk::launch_route(logits, type, T, E, ldl, k, scoring == BAKRON_SCORE_SIGMOID, bias, renorm != 0, scale, ids,
+                            weights, (hipStream_t)stream);
 }
 
 }  // extern "C"

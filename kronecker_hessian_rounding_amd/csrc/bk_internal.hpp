@@ -86,6 +86,22 @@ int launch_rmsnorm(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, 
                    int64_t ldh, const void* gain, int gtype, float eps, int rotate, uint64_t seed, void* y, int ytype,
                    int64_t ldy, float* ys, hipStream_t stream);
 
+// --- norm and position rotation of heads (bk_heads.hip) ---
+constexpr int64_t kMaxHeadDim = 512;
+struct HeadRows {
+    const void* x;
+    void* y;
+    const void* gain;
+    int64_t heads, xt, xh, yt, yh;  // strides of tokens and heads, in elements
+};
+int launch_head_norm(const HeadRows& q, const HeadRows& k, int type, int64_t T, int64_t d, int gtype, float eps, int norm,
+                     const void* pos, int pos32, const float* freq, int64_t rot, int interleaved, hipStream_t stream);
+
+// --- a router's choice of experts (bk_route.hip) ---
+constexpr int64_t kMaxExperts = 1024, kMaxChosen = 64;
+int launch_route(const void* logits, int type, int64_t T, int64_t E, int64_t ldl, int64_t k, int sigmoid,
+                 const float* bias, int renorm, float scale, int32_t* ids, float* weights, hipStream_t stream);
+
 // --- bound and sensitivity report (bk_report.hip) ---
 int launch_layer_report(int64_t m, int64_t n, const float* DO, const float* DI, const float* scales,
                         const float* HI, int64_t ldhi, const float* HO, int64_t ldho, double* out,

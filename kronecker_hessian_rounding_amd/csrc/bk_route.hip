@@ -1,0 +1,168 @@
+// bk_route.hip -- a router's logits to the experts of each token and their weights.
+//
+//   softmax: score_e = exp(l_e - max) / sum over all experts, chosen by l_e
+//   sigmoid: score_e = 1 / (1 + exp(-l_e)), chosen by score_e + bias_e
+// The k largest are taken one after the other, the lowest index first among equals, which softmax's order
+// decides on the logits themselves and sigmoid's on 64-bit scores: sigmoids crowd below 1, where 32 bits
+// would make many of them equal.
+//
+// One wave a row, expert 64 i + lane in register i of a lane. A round is a maximum over the wave of (value,
+// index); the lane that owned it looks for its next one.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "bk_common.hpp"
+#include "bk_internal.hpp"
+#include "bk_rows.hpp"
+
+namespace bk {
+
+namespace {
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int64_t T, ldl;
+    int type, E, k, renorm;
+    float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ T wave_add(T v) {
+#pragma unroll
+    for (int w = 1; w < 64; w *= 2) v += __shfl_xor(v, w);
+    return v;
+}
+
+template <int NV, bool kSigmoid>
+__global__ __launch_bounds__(256) void k_route(RouteArgs a) {
+    using Key = std::conditional_t<kSigmoid, double, float>;
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * 4;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += waves) {
+        Key key[NV];
+        float l[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = 64 * i + lane;
+            l[i] = e < a.E ? load_elem(a.logits, a.type, t * a.ldl + e) : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = 64 * i + lane;
+            if constexpr (kSigmoid) {
+                key[i] = 1.0 / (1.0 + exp(-(double)l[i])) + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
+            } else {
+                key[i] = l[i];
+            }
+            if (!(l[i] > -INFINITY) || !(key[i] > -INFINITY)) key[i] = -INFINITY;  // masked, or NaN: never chosen
+        }
+        // the lane's own best, the lowest index among equals
+        Key best;
+        int at;
+        const auto look = [&]() __attribute__((always_inline)) {
+            best = key[0];
+            at = lane;
+#pragma unroll
+            for (int i = 1; i < NV; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = 64 * i + lane;
+                }
+        };
+        look();
+        float mx = -INFINITY, chosen_l = 0.0f;
+        int chosen = -1;
+        for (int j = 0; j < a.k; ++j) {
+            Key b = best;
+            int e = at;
+#pragma unroll
+            for (int w = 1; w < 64; w *= 2) {
+                const Key ob = __shfl_xor(b, w);
+                const int oe = __shfl_xor(e, w);
+                if (ob > b || (ob == b && oe < e)) {
+                    b = ob;
+                    e = oe;
+                }
+            }
+            if (!(b > -INFINITY)) break;  // nothing left to choose
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (64 * i + lane == e) {
+                    v = l[i];
+                    key[i] = -INFINITY;
+                }
+            v = __shfl(v, e & 63);
+            if (j == 0) mx = v;
+            if (lane == j) {
+                chosen = e;
+                chosen_l = v;
+            }
+            if (at == e) look();
+        }
+        float w = 0.0f;
+        if constexpr (kSigmoid) {
+            double p = chosen >= 0 ? 1.0 / (1.0 + exp(-(double)chosen_l)) : 0.0;
+            if (a.renorm) {
+                const double s = wave_add(p);
+                p = s > 0.0 ? p / s : 0.0;
+            }
+            w = (float)p;
+        } else {
+            // l - mx, 0 where both are infinite
+            const auto term = [&](float v) { return v == mx ? 1.0f : expf(v - mx); };
+            w = chosen >= 0 ? term(chosen_l) : 0.0f;
+            float s;
+            if (a.renorm) {
+                s = w;
+            } else {
+                s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) s += l[i] > -INFINITY ? term(l[i]) : 0.0f;
+            }
+            s = wave_add(s);
+            w = s > 0.0f ? w / s : 0.0f;
+        }
+        if (lane < a.k) {
+            a.ids[t * a.k + lane] = chosen;
+            a.weights[t * a.k + lane] = w * a.scale;
+        }
+    }
+}
+
+template <int NV>
+void launch_nv(const RouteArgs& a, int sigmoid, unsigned grid, hipStream_t stream) {
+    if (sigmoid) hipLaunchKernelGGL((k_route<NV, true>), dim3(grid), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_route<NV, false>), dim3(grid), dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+int launch_route(const void* logits, int type, int64_t T, int64_t E, int64_t ldl, int64_t k, int sigmoid,
+                 const float* bias, int renorm, float scale, int32_t* ids, float* weights, hipStream_t stream) {
+    RouteArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.T = T;
+    a.ldl = ldl;
+    a.type = type;
+    a.E = (int)E;
+    a.k = (int)k;
+    a.renorm = renorm;
+    a.scale = scale;
+    const unsigned grid = (unsigned)std::min<int64_t>((T + 3) / 4, (int64_t)1 << 22);
+    if (E <= 64) launch_nv<1>(a, sigmoid, grid, stream);
+    else if (E <= 128) launch_nv<2>(a, sigmoid, grid, stream);
+    else if (E <= 256) launch_nv<4>(a, sigmoid, grid, stream);
+    else if (E <= 512) launch_nv<8>(a, sigmoid, grid, stream);
+    else launch_nv<16>(a, sigmoid, grid, stream);
+    return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
+}
+
+}  // namespace bk

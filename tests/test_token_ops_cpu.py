@@ -1,0 +1,70 @@
+"""Argument checks of the operators in which tokens name their own weights, and of the heads' norm; no GPU is needed."""
+import ctypes
+
+import pytest
+import torch
+
+import kronecker_hessian_rounding_amd as bk
+
+F32, F16, BF16, I8, E4M3 = range(5)
+INVALID, WORKSPACE, OK = 1, 3, 0
+
+
+def at(addr):
+    return ctypes.c_void_p(addr)  # never dereferenced: validation fails first
+
+
+A, B, C, D, E, F, G = (at(i << 36) for i in range(1, 8))
+
+
+def test_head_norm_refuses():
+    f = bk.LIB.bakron_head_norm
+    ok = dict(Q=A, hq=4, qt=512, qh=64, K=B, hk=2, kt=128, kh=64, type=BF16, T=3, d=64, qg=C, kg=C, gtype=BF16, eps=1e-6,
+              norm=1, pos=D, pos32=0, freq=E, rot=64, inter=0, YQ=F, yqt=256, yqh=64, YK=G, ykt=128, ykh=64, stream=None)
+
+    def call(**kw):
+        return f(*{**ok, **kw}.values())
+
+    for kw in (dict(Q=None), dict(YQ=None), dict(K=None), dict(YK=None), dict(pos=None), dict(freq=None), dict(T=-1),
+               dict(T=1 << 31), dict(hq=0), dict(hk=-1), dict(hq=65536), dict(d=0), dict(d=513), dict(rot=63), dict(rot=66),
+               dict(rot=-2), dict(type=I8), dict(type=5), dict(gtype=F16), dict(norm=0), dict(eps=-1.0),
+               dict(eps=float("nan")), dict(eps=float("inf")), dict(qh=63), dict(qt=255), dict(qt=63, qh=190),
+               dict(yqt=255), dict(kt=127), dict(ykh=10),
+               # outputs over inputs, shifted, or on each other
+               dict(YQ=A), dict(YQ=at((1 << 36) + 2)), dict(YK=A), dict(YQ=B), dict(YQ=G), dict(YQ=C), dict(YQ=D),
+               dict(YK=E), dict(YQ=at((4 << 36) + 23))):
+        assert call(**kw) == INVALID, kw
+    assert call(T=0) == OK
+    assert call(T=0, Q=None, K=None, YQ=None, YK=None, pos=None, freq=None) == OK
+    # in place is allowed: such a call passes every check but the last one looked at here
+    assert call(YQ=A, yqt=512, YK=B, rot=65) == INVALID
+
+
+def test_head_norm_strides_do_not_wrap():
+    f = bk.LIB.bakron_head_norm
+    big = 1 << 61
+    args = [A, 16, big, 64, None, 0, 0, 0, BF16, 3, 64, None, None, BF16, 1e-6, 1, None, 0, None, 0, 0, B, 64, 63, None, 0, 0, None]
+    assert f(*args) == INVALID  # the output's heads overlap, whatever the input's strides
+
+
+def test_route_refuses():
+    f = bk.LIB.bakron_route
+    ok = dict(l=A, type=F32, T=4, E=64, ldl=64, k=8, scoring=1, bias=B, renorm=1, scale=1.0, ids=C, w=D, stream=None)
+
+    def call(**kw):
+        return f(*{**ok, **kw}.values())
+
+    for kw in (dict(l=None), dict(ids=None), dict(w=None), dict(type=I8), dict(type=-1), dict(T=-1), dict(T=(1 << 40) + 1),
+               dict(E=0), dict(E=1025, ldl=1025), dict(ldl=63), dict(k=0), dict(k=65, E=100, ldl=100), dict(k=9, E=8),
+               dict(scoring=2), dict(scoring=0), dict(scale=float("inf")), dict(scale=float("nan")), dict(ids=D), dict(ids=A),
+               dict(w=A), dict(w=B), dict(ids=B), dict(w=at((3 << 36) + 4 * 4 * 8 - 4))):
+        assert call(**kw) == INVALID, kw
+    assert call(T=0) == OK
+    assert call(T=0, l=None, ids=None, w=None) == OK
+
+
+def test_binding_refuses_host_tensors():
+    with pytest.raises(ValueError):
+        bk.head_norm(torch.zeros(2, 4, 64))
+    with pytest.raises(ValueError):
+        bk.route(torch.zeros(2, 8), 2)
