@@ -414,6 +414,25 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
                    void* Y, int32_t ytype, int64_t ldy, float* yscale, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection (a packed layer's product, or any other): token t names
+ * an adapter a = ids[t] of R, and
+ *     u_k = xscale_t sum_j X[t][j] A[a][k][j],   Y[t][i] = base[t][i] + scales_a sum_k u_k B[a][i][k].
+ *   X: T x n, BAKRON_F32, F16, BF16, I8 or E4M3, ldx >= n. xscale: [T] fp32 factors, or NULL for 1.
+ *   A: [R][r][n], B: [R][m][r], contiguous, of wtype: X's type, or for an 8-bit X BAKRON_F16 or BF16. Adapters of a
+ *     smaller rank are padded with zeros.
+ *   scales: [R] fp32, or NULL for 1. ids: [T] int32; an id outside 0 .. R - 1 means no adapter: Y[t] = base[t].
+ *   base: T x m of btype (F32, F16 or BF16), ldb >= m, or NULL for 0. Y: T x m of ytype, ldy >= m.
+ *   Products are exact (8 and 16 bits) or fp32, u and all sums are fp32, and Y is rounded once. Token t's result depends on
+ *   its own row and adapter only. For given sizes, types and ids it is deterministic. No workspace.
+ *   Y may be base itself (same pointer, type and ld); no other overlap of Y with a buffer of the call is allowed.
+ * Errors: INVALID_ARG for NULL X, A, B, ids or Y (T > 0), T < 0 or > 2^40, n, m < 1 or >= 2^28, r < 1 or > 512, R < 1 or
+ *   > 2^31 - 1, bad types or ld, or overlap.
+ */
+int bakron_lora(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx, const float* xscale, const void* A,
+                const void* B, int32_t wtype, int64_t R, int64_t r, int64_t m, const float* scales, const int32_t* ids,
+                const void* base, int32_t btype, int64_t ldb, void* Y, int32_t ytype, int64_t ldy, void* stream);
+
+/*
  * Root-mean-square norm of each query and key head, with the position rotation, in one pass over the rows that a
  * query-key-value product leaves. For token t and head h, x its d elements:
  *     v = gain * x / sqrt(mean(x^2) + eps), or x where norm == 0,

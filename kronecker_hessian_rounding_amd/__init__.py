@@ -17,12 +17,13 @@ tensors for device memory and uses the current stream.
   pack(codes, scales, bits)   a rounded layer laid out for matvec (2 or 4 bits a weight, row or group scales)
   matvec(x, packed)           x W^T for tokens x in fp32, fp16, bf16, int8 or e4m3
   rmsnorm(x, gain, residual)  norm with the residual's addition, the layer's rotation and an 8-bit output
+  lora(x, a, b, ids, base)    low-rank adapters of many requests beside a shared projection
   head_norm(q, k, ...)        norm of each query and key head with the position rotation
   route(logits, k)            a router's choice of experts and their weights
 """
 from ._binding import (  # noqa: F401
     BAKRON_E_DEVICE, BAKRON_E_INVALID_ARG, BAKRON_E_NOT_SPD, BAKRON_E_WORKSPACE, BAKRON_OK,
     EXPORTS, LIB, LIB_PATH, NOALLOC_SCRATCH_BYTES, ROW_TYPES, BakronError, NormResult, PackedWeight, SolveResult,
-    abi_version, check_ldl_pair, head_norm, hessian_accum, ldl, ldl_pair, layer_report, matvec, pack, quantize_layer,
+    abi_version, check_ldl_pair, head_norm, hessian_accum, ldl, ldl_pair, layer_report, lora, matvec, pack, quantize_layer,
     release_workspace, rht, rmsnorm, rotate_layer, route, sketch_a, sketch_b, solve, solve_noalloc, token_weights,
 )

@@ -94,6 +94,9 @@ def _load() -> ctypes.CDLL:
     lib.bakron_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i32, f32, ctypes.c_int,
                                    ctypes.c_uint64, vp, i32, i64, vp, vp]
     ci = ctypes.c_int
+    lib.bakron_lora.restype = ci
+    lib.bakron_lora.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i32, i64, i64, i64, vp, vp, vp, i32, i64, vp, i32, i64,
+                                vp]
     lib.bakron_head_norm.restype = ci
     lib.bakron_head_norm.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, i32, i64, i64, vp, vp, i32, f32, ci, vp, ci,
                                      vp, i64, ci, vp, i64, i64, vp, i64, i64, vp]
@@ -114,7 +117,7 @@ EXPORTS = ("bakron_abi_version", "bakron_status_str", "bakron_hessian_accum_work
            "bakron_ldl_pair_async",
            "bakron_solve_workspace_bytes", "bakron_solve", "bakron_solve_noalloc", "bakron_rht",
            "bakron_layer_report", "bakron_packed_bytes", "bakron_pack", "bakron_matvec", "bakron_rmsnorm",
-           "bakron_head_norm", "bakron_route")
+           "bakron_lora", "bakron_head_norm", "bakron_route")
 
 
 def abi_version() -> int:
@@ -762,6 +765,59 @@ def rmsnorm(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Opti
     if st:
         _check("bakron_rmsnorm", st)
     return NormResult(out, scale_out, sum_out)
+
+
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None,
+         scales: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
+         out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """base + scales[i] * (x A_i^T) B_i^T for tokens x (T x n), token t with the adapter i = ids[t] (T,) int32.
+
+    a (R, r, n) and b (R, m, r), contiguous, in x's type (float16 or bfloat16 beside an int8 / float8_e4m3fn x, whose
+    x_scale (T,) float32 multiplies each token's product). An id outside 0..R-1 means no adapter: the token's row is
+    base's. base (T x m): what the shared projection gave, as matvec() returns it; None: 0. scales (R,) float32. The result
+    is T x m in out_dtype (default: base's type, else x's, or bfloat16 for an 8-bit x), rounded once; out=base works in
+    place. r up to 512. No gradient is formed.
+    """
+    dev = _device_of(x, "x")
+    ldx = _rows(x, "x", ROW_TYPES, dev)
+    T, n = x.shape
+    xtype = x.dtype
+    wtypes = (xtype,) if xtype in _WIDE else (torch.float16, torch.bfloat16)
+    for t, name in ((a, "a"), (b, "b")):
+        if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in wtypes or t.dim() != 3
+                or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous adapters in three dimensions of %s" % (name, ", ".join(map(str, wtypes))))
+    R, r, na = a.shape
+    rb, m, rr = b.shape
+    if na != n or rb != R or rr != r or a.dtype != b.dtype or a.numel() == 0 or m == 0 or r > 512:
+        raise ValueError("adapters are a (R, r, %d) and b (R, m, r) of one type, r up to 512" % n)
+    if (not isinstance(ids, torch.Tensor) or ids.get_device() != dev or ids.dtype != torch.int32 or ids.numel() != T
+            or not ids.is_contiguous()):
+        raise ValueError("ids must be a contiguous int32 vector of length %d on the current device" % T)
+    pb = btype = ldb = 0
+    if base is not None:
+        ldb = _rows(base, "base", _WIDE, dev, (T, m))
+        pb, btype = base.data_ptr(), ROW_TYPES[base.dtype]
+    if out is None:
+        if out_dtype is None:
+            out_dtype = base.dtype if base is not None else xtype if xtype in _WIDE else torch.bfloat16
+        elif out_dtype not in _WIDE:
+            raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in _WIDE))
+        out = x.new_empty((T, m), dtype=out_dtype)
+        ldy = m
+    else:
+        ldy = _rows(out, "out", _WIDE, dev, (T, m))
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must be a tensor of %s" % out_dtype)
+        out_dtype = out.dtype
+    st = LIB.bakron_lora(x.data_ptr(), ROW_TYPES[xtype], T, n, ldx,
+                         None if x_scale is None else _token_scales(x_scale, "x_scale", T, dev), a.data_ptr(), b.data_ptr(),
+                         ROW_TYPES[a.dtype], R, r, m, None if scales is None else _token_scales(scales, "scales", R, dev),
+                         ids.data_ptr(), pb or None, btype, ldb, out.data_ptr(), ROW_TYPES[out_dtype], ldy,
+                         torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("bakron_lora", st)
+    return out
 
 
 def _heads(t: torch.Tensor, name: str, dtypes, dev: int, shape=None):

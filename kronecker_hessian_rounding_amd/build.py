@@ -25,7 +25,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libbakron.so")
 SOURCES = ["bk_api.hip", "bk_accum.hip", "bk_ldl.hip", "bk_solve.hip", "bk_rotate.hip", "bk_report.hip", "bk_sketch.hip",
            "bk_matvec.hip", "bk_matvec_f32.hip", "bk_matvec_f16.hip", "bk_matvec_bf16.hip", "bk_matvec_i8.hip",
-           "bk_matvec_e4m3.hip", "bk_norm.hip", "bk_heads.hip", "bk_route.hip"]
+           "bk_matvec_e4m3.hip", "bk_norm.hip", "bk_lora.hip",
+           "bk_heads.hip", "bk_route.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -363,6 +363,29 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
                               yscale, (hipStream_t)stream);
 }
 
+int bakron_lora(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx, const float* xscale, const void* A,
+                const void* B, int32_t wtype, int64_t R, int64_t r, int64_t m, const float* scales, const int32_t* ids,
+                const void* base, int32_t btype, int64_t ldb, void* Y, int32_t ytype, int64_t ldy, void* stream) {
+    constexpr int64_t kMax = (int64_t)1 << 28;
+    if (T < 0 || T > (int64_t)1 << 40 || n < 1 || m < 1 || n >= kMax || m >= kMax || r < 1 || r > bk::kMaxRank || R < 1 ||
+        R > 0x7fffffff)
+        return BAKRON_E_INVALID_ARG;
+    if (elem_size(xtype) == 0 || !wide_type(wtype) || !wide_type(ytype) || (base && !wide_type(btype)))
+        return BAKRON_E_INVALID_ARG;
+    if (wide_type(xtype) ? wtype != xtype : wtype == BAKRON_F32) return BAKRON_E_INVALID_ARG;
+    if (T == 0) return BAKRON_OK;
+    if (!X || !A || !B || !ids || !Y || bad_ld(ldx, n) || bad_ld(ldy, m) || (base && bad_ld(ldb, m)))
+        return BAKRON_E_INVALID_ARG;
+    const Rows y = rows_of(Y, T, m, ldy, ytype), b = rows_of(base, T, m, ldb, btype);
+    const Rows in[6] = {rows_of(X, T, n, ldx, xtype), rows_of(A, R, r * n, r * n, wtype), rows_of(B, R, m * r, m * r, wtype),
+                        {xscale, 1, 4 * T, 4 * T}, {scales, 1, 4 * R, 4 * R}, {ids, 1, 4 * T, 4 * T}};
+    for (const Rows& i : in)
+        if (overlap(i, y)) return BAKRON_E_INVALID_ARG;
+    if (overlap(b, y) && !(same_rows(b, y) && btype == ytype)) return BAKRON_E_INVALID_ARG;
+    return bk::launch_lora(X, xtype, T, n, ldx, xscale, A, B, wtype, R, r, m, scales, ids, base, btype, ldb, Y, ytype, ldy,
+                           (hipStream_t)stream);
+}
+
 int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const void* K, int64_t hk, int64_t kt, int64_t kh,
                      int32_t type, int64_t T, int64_t d, const void* qgain, const void* kgain, int32_t gtype, float eps,
                      int norm, const void* pos, int pos32, const float* freq, int64_t rot, int interleaved, void* YQ,

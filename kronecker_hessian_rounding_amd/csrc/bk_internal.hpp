@@ -86,6 +86,12 @@ int launch_rmsnorm(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, 
                    int64_t ldh, const void* gain, int gtype, float eps, int rotate, uint64_t seed, void* y, int ytype,
                    int64_t ldy, float* ys, hipStream_t stream);
 
+// --- low-rank adapters (bk_lora.hip) ---
+constexpr int64_t kMaxRank = 512;
+int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, const float* xs, const void* A, const void* B,
+                int wtype, int64_t R, int64_t r, int64_t m, const float* scales, const int32_t* ids, const void* base,
+                int btype, int64_t ldb, void* y, int ytype, int64_t ldy, hipStream_t stream);
+
 // --- norm and position rotation of heads (bk_heads.hip) ---
 constexpr int64_t kMaxHeadDim = 512;
 struct HeadRows {

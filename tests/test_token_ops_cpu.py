@@ -68,3 +68,28 @@ def test_binding_refuses_host_tensors():
         bk.head_norm(torch.zeros(2, 4, 64))
     with pytest.raises(ValueError):
         bk.route(torch.zeros(2, 8), 2)
+
+
+def test_lora_refuses():
+    f = bk.LIB.bakron_lora
+    ok = dict(X=A, xtype=BF16, T=3, n=64, ldx=64, xs=None, A=B, B=C, wtype=BF16, R=4, r=8, m=32, scales=D, ids=E, base=F,
+              btype=F32, ldb=32, Y=G, ytype=F16, ldy=32, stream=None)
+
+    def call(**kw):
+        return f(*{**ok, **kw}.values())
+
+    for kw in (dict(X=None), dict(A=None), dict(B=None), dict(ids=None), dict(Y=None), dict(T=-1), dict(T=(1 << 40) + 1),
+               dict(n=0), dict(m=0), dict(n=1 << 28, ldx=1 << 28), dict(m=1 << 28, ldb=1 << 28, ldy=1 << 28), dict(r=0),
+               dict(r=513), dict(R=0), dict(R=1 << 31), dict(xtype=9), dict(wtype=F16), dict(wtype=I8),
+               dict(xtype=I8, wtype=F32), dict(xtype=F32), dict(ytype=I8), dict(btype=E4M3), dict(ldx=63), dict(ldb=31), dict(ldy=31),
+               dict(Y=A), dict(Y=B), dict(Y=C), dict(Y=D), dict(Y=E), dict(Y=F), dict(Y=F, ytype=F32, ldy=33),
+               dict(Y=at((6 << 36) + 4), ytype=F32), dict(xs=G)):
+        assert call(**kw) == INVALID, kw
+    assert call(T=0) == OK
+    assert call(T=0, X=None, A=None, B=None, ids=None, base=None, Y=None) == OK
+
+
+def test_lora_binding_refuses_host_tensors():
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        bk.lora(z(2, 8), z(1, 4, 8), z(1, 6, 4), z(2, dtype=torch.int32))
