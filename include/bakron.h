@@ -475,6 +475,33 @@ enum { BAKRON_SCORE_SOFTMAX = 0, BAKRON_SCORE_SIGMOID = 1 };
 int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t ldl, int64_t k, int scoring,
                  const float* bias, int renorm, float scale, int32_t* ids, float* weights, void* stream);
 
+/*
+ * The products of a mixture of rounded experts. For each of T tokens x (rows of X), k experts e = ids[t][j] of E and
+ * their weights, as bakron_route leaves them:
+ *     Y[t] = sum_j weights[t][j] Down_e (act(Gate_e x) * (Up_e x)),  x = xscale_t X[t].
+ *   gate, up: E packed layers of I rows and n columns, one behind the other, bakron_packed_bytes(I, n, bits, group) bytes
+ *     each, as bakron_pack leaves them; gate_bytes is the size of each of the two buffers. down: E packed layers of n rows
+ *     and I columns (dbits, dgroup), down_bytes. All 16-byte aligned.
+ *   X: T x n, BAKRON_F32, F16, BF16, I8 or E4M3, ldx >= n. xscale: [T] fp32 factors, or NULL for 1.
+ *   ids: T x k int32, contiguous. An id outside 0 .. E - 1 adds nothing (a token without any gets zeros); one that comes
+ *     twice in a row counts with both weights. weights: T x k fp32, contiguous.
+ *   act: BAKRON_ACT_SILU, v / (1 + exp(-v)), or BAKRON_ACT_GELU, gelu's tanh form.
+ *   Y: T x n, BAKRON_F32, F16 or BF16, ldy >= n.
+ *   The products are exact with fp32 accumulation as bakron_matvec's; the values between the two products and all
+ *   sums are fp32, and Y is rounded once. Token t's result depends on its own row only. Deterministic.
+ *   ws: at least bakron_experts_workspace_bytes(T, k, E, n, I) bytes (0 for sizes that bakron_experts refuses, and T = 0),
+ *     16-byte aligned. Calls that overlap need one each.
+ * Errors: INVALID_ARG for NULL pointers (T > 0), T < 0 or > 2^40, n or I < 1 or > 2^18, E < 1 or > 1024, k < 1 or > 64,
+ *   bad types, act, bits, groups, ld or alignment, or outputs that overlap an input or the workspace; WORKSPACE if the
+ *   workspace or a packed buffer is too small.
+ */
+enum { BAKRON_ACT_SILU = 0, BAKRON_ACT_GELU = 1 };
+size_t bakron_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I);
+int bakron_experts(const void* gate, const void* up, size_t gate_bytes, int32_t bits, int64_t group, const void* down,
+                   size_t down_bytes, int32_t dbits, int64_t dgroup, int64_t E, int64_t n, int64_t I, const void* X,
+                   int32_t xtype, int64_t T, int64_t ldx, const float* xscale, const int32_t* ids, const float* weights,
+                   int64_t k, int act, void* Y, int32_t ytype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,10 +20,13 @@ tensors for device memory and uses the current stream.
   lora(x, a, b, ids, base)    low-rank adapters of many requests beside a shared projection
   head_norm(q, k, ...)        norm of each query and key head with the position rotation
   route(logits, k)            a router's choice of experts and their weights
+  pack_experts(codes, scales, bits)  the layers of a mixture of experts laid out for experts
+  experts(x, gate, up, down, ids, weights)  the products of a mixture of rounded experts
 """
 from ._binding import (  # noqa: F401
     BAKRON_E_DEVICE, BAKRON_E_INVALID_ARG, BAKRON_E_NOT_SPD, BAKRON_E_WORKSPACE, BAKRON_OK,
-    EXPORTS, LIB, LIB_PATH, NOALLOC_SCRATCH_BYTES, ROW_TYPES, BakronError, NormResult, PackedWeight, SolveResult,
-    abi_version, check_ldl_pair, head_norm, hessian_accum, ldl, ldl_pair, layer_report, lora, matvec, pack, quantize_layer,
+    EXPORTS, LIB, LIB_PATH, NOALLOC_SCRATCH_BYTES, ROW_TYPES, BakronError, NormResult, PackedExperts, PackedWeight,
+    SolveResult,
+    abi_version, check_ldl_pair, experts, head_norm, hessian_accum, ldl, ldl_pair, layer_report, lora, matvec, pack, pack_experts, quantize_layer,
     release_workspace, rht, rmsnorm, rotate_layer, route, sketch_a, sketch_b, solve, solve_noalloc, token_weights,
 )

@@ -102,6 +102,11 @@ def _load() -> ctypes.CDLL:
                                      vp, i64, ci, vp, i64, i64, vp, i64, i64, vp]
     lib.bakron_route.restype = ci
     lib.bakron_route.argtypes = [vp, i32, i64, i64, i64, i64, ci, vp, ci, f32, vp, vp, vp]
+    lib.bakron_experts_workspace_bytes.restype = sz
+    lib.bakron_experts_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.bakron_experts.restype = ci
+    lib.bakron_experts.argtypes = [vp, vp, sz, i32, i64, vp, sz, i32, i64, i64, i64, i64, vp, i32, i64, i64, vp, vp, vp, i64,
+                                   ci, vp, i32, i64, vp, sz, vp]
     return lib
 
 
@@ -117,7 +122,8 @@ EXPORTS = ("bakron_abi_version", "bakron_status_str", "bakron_hessian_accum_work
            "bakron_ldl_pair_async",
            "bakron_solve_workspace_bytes", "bakron_solve", "bakron_solve_noalloc", "bakron_rht",
            "bakron_layer_report", "bakron_packed_bytes", "bakron_pack", "bakron_matvec", "bakron_rmsnorm",
-           "bakron_lora", "bakron_head_norm", "bakron_route")
+           "bakron_lora", "bakron_head_norm", "bakron_route",
+           "bakron_experts_workspace_bytes", "bakron_experts")
 
 
 def abi_version() -> int:
@@ -941,3 +947,113 @@ def route(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: Optional
     if st:
         _check("bakron_route", st)
     return ids, weights
+
+
+@dataclass
+class PackedExperts:
+    """E layers of one shape in bakron_pack's layout, one behind the other (device bytes, as pack_experts() returns them)."""
+    data: torch.Tensor
+    E: int
+    m: int
+    n: int
+    bits: int
+    group: int
+
+    def __post_init__(self):
+        nb = LIB.bakron_packed_bytes(self.m, self.n, self.bits, self.group)
+        d = self.data
+        if nb == 0 or self.E < 1 or d.dtype != torch.uint8 or not d.is_contiguous() or d.numel() != self.E * nb:
+            raise ValueError("data must hold the %d contiguous bytes of each of %d packed %d x %d layers"
+                             % (nb, self.E, self.m, self.n))
+
+    @property
+    def nbytes(self) -> int:
+        return self.data.numel()
+
+
+def pack_experts(codes: torch.Tensor, scales: torch.Tensor, bits: int, group: int = 0) -> PackedExperts:
+    """Lay out the codes (E x m x n uint8) of E layers and their scales for experts(), each as pack() does.
+
+    scales: (E, m) or (E, m, 1) with group = 0, else (E, m, ceil(n / group)).
+    """
+    dev = _device_of(codes, "codes")
+    if codes.dim() != 3 or codes.shape[0] < 1 or not isinstance(scales, torch.Tensor) or scales.shape[:1] != codes.shape[:1]:
+        raise ValueError("codes must be experts x rows x columns, with scales for as many experts")
+    E, m, n = codes.shape
+    bits, group = int(bits), int(group)
+    if scales.dim() == 2 and group == 0:
+        scales = scales.unsqueeze(2)
+    nb = LIB.bakron_packed_bytes(m, n, bits, group)
+    if nb == 0:
+        raise ValueError("pack takes m, n >= 1, bits 1..4 and group 0 or a power of two >= 32")
+    if scales.dim() != 3:
+        raise ValueError("scales must be experts x rows x groups")
+    ldc = _rows(codes[0], "codes", (torch.uint8,), dev)
+    lds = _rows(scales[0], "scales", (torch.float32,), dev, (m, -(-n // group) if group else 1))
+    data = torch.empty(E * nb, dtype=torch.uint8, device=codes.device)
+    pc, ps, pd = codes.data_ptr(), scales.data_ptr(), data.data_ptr()
+    for e in range(E):
+        _check("bakron_pack", LIB.bakron_pack(pc + e * codes.stride(0), m, n, ldc, bits, ps + 4 * e * scales.stride(0), lds,
+                                              group, pd + e * nb, nb, _stream()))
+    return PackedExperts(data, E, m, n, bits, group)
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def experts(x: torch.Tensor, gate: PackedExperts, up: PackedExperts, down: PackedExperts, ids: torch.Tensor,
+            weights: torch.Tensor, x_scale: Optional[torch.Tensor] = None, act: str = "silu",
+            out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """sum_j weights[t, j] D_e(act(G_e x_t) * (U_e x_t)), e = ids[t, j], for tokens x (T x n) and rounded experts.
+
+    gate, up: packed I x n layers of one shape, bits and group; down: packed n x I. ids (T, k) int32 and weights (T, k)
+    float32 as route() returns them: an id outside 0..E-1 adds nothing, one that comes twice in a row counts with both
+    weights. x: float32, float16, bfloat16, or int8 / float8_e4m3fn with x_scale (T,) float32. act: "silu" or "gelu" (its
+    tanh form). The result is T x n in out_dtype (default: x's type, or bfloat16 for an 8-bit x), rounded once. E up to
+    1024, k up to 64, n and I up to 2^18. No gradient is formed.
+    """
+    dev = _device_of(x, "x")
+    ldx = _rows(x, "x", ROW_TYPES, dev)
+    T, n = x.shape
+    E, inner = gate.E, gate.m
+    if (gate.n != n or up.E != E or up.m != inner or up.n != n or up.bits != gate.bits or up.group != gate.group
+            or down.E != E or down.m != n or down.n != inner):
+        raise ValueError("gate and up must be %d x I layers' experts of one shape, bits and group, down I x %d ones" % (n, n))
+    for w, name in ((gate, "gate"), (up, "up"), (down, "down")):
+        if w.data.get_device() != dev or not w.data.is_contiguous():
+            raise ValueError("%s must be contiguous and on x's device" % name)
+    if up.data.numel() != gate.data.numel():
+        raise ValueError("gate and up must hold as many bytes")
+    if (not isinstance(ids, torch.Tensor) or ids.get_device() != dev or ids.dtype != torch.int32 or ids.dim() != 2
+            or ids.shape[0] != T or not ids.is_contiguous()):
+        raise ValueError("ids must be contiguous int32, %d x k, on the current device" % T)
+    if (not isinstance(weights, torch.Tensor) or weights.get_device() != dev or weights.dtype != torch.float32
+            or weights.shape != ids.shape or not weights.is_contiguous()):
+        raise ValueError("weights must be contiguous float32 of ids' shape on the current device")
+    k = ids.shape[1]
+    if act not in ACTIVATIONS:
+        raise ValueError("act must be 'silu' or 'gelu'")
+    xtype = x.dtype
+    if out is None:
+        if out_dtype is None:
+            out_dtype = xtype if xtype in _WIDE else torch.bfloat16
+        elif out_dtype not in _WIDE:
+            raise ValueError("out_dtype must be one of %s" % ", ".join(str(d) for d in _WIDE))
+        out = x.new_empty((T, n), dtype=out_dtype)
+        ldy = n
+    else:
+        ldy = _rows(out, "out", _WIDE, dev, (T, n))
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must be a tensor of %s" % out_dtype)
+        out_dtype = out.dtype
+    # of this call alone: calls on two streams, or two captured graphs, share nothing
+    nb = LIB.bakron_experts_workspace_bytes(T, k, E, n, inner)
+    ws = x.new_empty((nb,), dtype=torch.uint8)
+    st = LIB.bakron_experts(gate.data.data_ptr(), up.data.data_ptr(), gate.data.numel(), gate.bits, gate.group,
+                            down.data.data_ptr(), down.data.numel(), down.bits, down.group, E, n, inner, x.data_ptr(),
+                            ROW_TYPES[xtype], T, ldx, None if x_scale is None else _token_scales(x_scale, "x_scale", T, dev),
+                            ids.data_ptr(), weights.data_ptr(), k, ACTIVATIONS[act], out.data_ptr(), ROW_TYPES[out_dtype], ldy,
+                            ws.data_ptr(), nb, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check("bakron_experts", st)
+    return out

@@ -141,6 +141,11 @@ Rows rows_of_heads(const void* p, int64_t T, int64_t H, int64_t d, int64_t st, i
     return {p, H, ((T - 1) * st + d) * e, sh * e};
 }
 
+bool bad_experts(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
+    return T < 0 || T > (int64_t)1 << 40 || k < 1 || k > bk::kMaxChosen || E < 1 || E > bk::kMaxExperts || n < 1 ||
+           n > bk::kMaxExpertDim || I < 1 || I > bk::kMaxExpertDim;
+}
+
 }  // namespace
 
 extern "C" {
@@ -434,6 +439,37 @@ int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t
     if (overlap(i, w) || overlap(l, i) || overlap(l, w) || overlap(b, i) || overlap(b, w)) return BAKRON_E_INVALID_ARG;
     return bk::launch_route(logits, type, T, E, ldl, k, scoring == BAKRON_SCORE_SIGMOID, bias, renorm != 0, scale, ids,
                             weights, (hipStream_t)stream);
+}
+
+size_t bakron_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
+    if (bad_experts(T, k, E, n, I) || T == 0) return 0;
+    return bk::experts_workspace_bytes(T, k, E, n, I);
+}
+
+int bakron_experts(const void* gate, const void* up, size_t gate_bytes, int32_t bits, int64_t group, const void* down,
+                   size_t down_bytes, int32_t dbits, int64_t dgroup, int64_t E, int64_t n, int64_t I, const void* X,
+                   int32_t xtype, int64_t T, int64_t ldx, const float* xscale, const int32_t* ids, const float* weights,
+                   int64_t k, int act, void* Y, int32_t ytype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    if (bad_experts(T, k, E, n, I) || bad_pack_shape(I, n, bits, group) || bad_pack_shape(n, I, dbits, dgroup))
+        return BAKRON_E_INVALID_ARG;
+    if (elem_size(xtype) == 0 || !wide_type(ytype) || (act != BAKRON_ACT_SILU && act != BAKRON_ACT_GELU))
+        return BAKRON_E_INVALID_ARG;
+    if (T == 0) return BAKRON_OK;
+    if (!gate || !up || !down || !X || !ids || !weights || !Y || bad_ld(ldx, n) || bad_ld(ldy, n))
+        return BAKRON_E_INVALID_ARG;
+    if ((((uintptr_t)gate | (uintptr_t)up | (uintptr_t)down | (uintptr_t)ws) & 15) != 0) return BAKRON_E_INVALID_ARG;
+    const int64_t gb = (int64_t)gate_bytes, db = (int64_t)down_bytes, wb = (int64_t)ws_bytes;
+    const Rows y = rows_of(Y, T, n, ldy, ytype), w = {ws, 1, wb, wb};
+    const Rows in[7] = {{gate, 1, gb, gb}, {up, 1, gb, gb}, {down, 1, db, db}, rows_of(X, T, n, ldx, xtype),
+                        {xscale, 1, 4 * T, 4 * T}, {ids, 1, 4 * T * k, 4 * T * k}, {weights, 1, 4 * T * k, 4 * T * k}};
+    if (overlap(y, w)) return BAKRON_E_INVALID_ARG;
+    for (const Rows& i : in)
+        if (overlap(i, y) || overlap(i, w)) return BAKRON_E_INVALID_ARG;
+    if (gate_bytes / E < bk::pack_shape(I, n, bits, group).bytes || down_bytes / E < bk::pack_shape(n, I, dbits, dgroup).bytes)
+        return BAKRON_E_WORKSPACE;
+    if (!ws || ws_bytes < bk::experts_workspace_bytes(T, k, E, n, I)) return BAKRON_E_WORKSPACE;
+    return bk::launch_experts(gate, up, bits, group, down, dbits, dgroup, E, n, I, X, xtype, T, ldx, xscale, ids, weights, k,
+                              act, Y, ytype, ldy, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

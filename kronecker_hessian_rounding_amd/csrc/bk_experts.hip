@@ -1,0 +1,214 @@
+// bk_experts.hip -- plan, sum and dispatch of the experts' products (bk_experts.hpp has the rest).
+#include "bk_experts.hpp"
+
+namespace bk {
+
+// compiled in bk_experts_*.hip, one file for each type of x
+extern template void launch_experts_first<kF32>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kF16>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kBF16>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_second<kF32>(const ExpertArgs&, int, int, hipStream_t);
+
+namespace {
+
+// Whether pair p = t k + j leads: its id is an expert and no earlier slot of its token has it.
+__device__ __forceinline__ bool leads(const int32_t* ids, int64_t p, int k, int E) {
+    const int e = ids[p];
+    if (e < 0 || e >= E) return false;
+    for (int64_t i = p / k * k; i < p; ++i)
+        if (ids[i] == e) return false;
+    return true;
+}
+
+struct PlanArgs {
+    const int32_t* ids;
+    const float* weights;
+    int64_t pairs;
+    int k, E, tile;
+    int32_t* tiles_used;
+    ExpertTile* list;
+    int32_t* tokens;
+    int32_t* pair;
+    float* weight;
+};
+
+// One workgroup: leaders counted by expert, the counts' running sums, then each leader to its place (the order
+// within an expert's list is that in which they come, and nothing depends on it).
+__global__ __launch_bounds__(1024) void k_experts_plan(PlanArgs a) {
+    __shared__ int count[1024], begin[1024], tiles[1024], next[1024];
+    const int e = threadIdx.x;
+    count[e] = 0;
+    __syncthreads();
+    for (int64_t p = threadIdx.x; p < a.pairs; p += 1024)
+        if (leads(a.ids, p, a.k, a.E)) atomicAdd(&count[a.ids[p]], 1);
+    __syncthreads();
+    const int mine = count[e], mine_tiles = (mine + a.tile - 1) / a.tile;
+    begin[e] = mine;
+    tiles[e] = mine_tiles;
+    for (int d = 1; d < 1024; d *= 2) {
+        __syncthreads();
+        const int b = e >= d ? begin[e - d] : 0, t = e >= d ? tiles[e - d] : 0;
+        __syncthreads();
+        begin[e] += b;
+        tiles[e] += t;
+    }
+    __syncthreads();
+    const int first = begin[e] - mine, first_tile = tiles[e] - mine_tiles;
+    next[e] = first;
+    for (int i = 0; i < mine_tiles; ++i)
+        a.list[first_tile + i] = ExpertTile{e, first + i * a.tile, min(a.tile, mine - i * a.tile), 0};
+    if (e == 1023) *a.tiles_used = tiles[e];
+    __syncthreads();
+    for (int64_t p = threadIdx.x; p < a.pairs; p += 1024)
+        if (leads(a.ids, p, a.k, a.E)) {
+            const int x = a.ids[p], at = atomicAdd(&next[x], 1);
+            float w = a.weights[p];
+            for (int64_t i = p + 1; i < (p / a.k + 1) * a.k; ++i)
+                if (a.ids[i] == x) w += a.weights[i];
+            a.tokens[at] = (int32_t)(p / a.k);
+            a.pair[at] = (int32_t)p;
+            a.weight[at] = w;
+        }
+}
+
+struct SumArgs {
+    const int32_t* ids;
+    const float* part;
+    void* y;
+    int64_t T, n, ldy;
+    int k, E, ytype;
+};
+
+// y_t: the rows of a token's leaders, in the order of its slots. 4 columns a thread.
+__global__ __launch_bounds__(256) void k_experts_sum(SumArgs a) {
+    const int64_t per = (a.n + 1023) / 1024, t = blockIdx.x / per;
+    const int64_t i = (blockIdx.x % per) * 1024 + threadIdx.x * 4;
+    const int lane = threadIdx.x & 63;
+    const uint64_t lead = __ballot(lane < a.k && leads(a.ids, t * a.k + min(lane, a.k - 1), a.k, a.E));
+    if (i >= a.n) return;
+    const int count = (int)min<int64_t>(4, a.n - i);
+    f4 y = {};
+    for (uint64_t m = lead; m; m &= m - 1) {
+        const float* p = a.part + (t * a.k + __builtin_ctzll(m)) * a.n + i;
+        f4 v = {};
+        if (count == 4) __builtin_memcpy(&v, p, 16);
+        else
+            for (int e = 0; e < 4; ++e) v[e] = e < count ? p[e] : 0.0f;
+        y += v;
+    }
+    store4(a.y, a.ytype, t * a.ldy + i, y, count);
+}
+
+// Tokens of one round of launches: the workspace holds 2^14 pairs at most, and a grid fewer than 2^32 threads.
+int64_t round_tokens(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
+    int64_t t = std::max<int64_t>(1, std::min(T, ((int64_t)1 << 14) / k));
+    const int64_t tiles = (std::max(n, I) + kRowTile - 1) / kRowTile;
+    while (t > 1 && tiles * (std::min(E, t * k) + t * k / kExpertTokens) * kMvThreads >= (int64_t)1 << 32) t /= 2;
+    return t;
+}
+
+struct Layout {
+    size_t used, list, tokens, pair, weight, h, part, bytes;
+    int64_t ldh, most;
+};
+Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
+    const int64_t t = round_tokens(T, k, E, n, I), p = t * k;
+    Layout l;
+    l.most = std::min(E, p) + p / kExpertTokens;
+    l.ldh = (I + 3) / 4 * 4;
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    l.used = take(4);
+    l.list = take(sizeof(ExpertTile) * l.most);
+    l.tokens = take(4 * p);
+    l.pair = take(4 * p);
+    l.weight = take(4 * p);
+    l.h = take(4 * p * l.ldh);
+    l.part = take(4 * p * n);
+    l.bytes = at;
+    return l;
+}
+
+MvArgs product(const void* packed, const PackShape& p, int64_t m, int64_t n, int64_t group, int* fs) {
+    MvArgs a = {};
+    a.codes = (const char*)packed;
+    a.scales = (const float*)((const char*)packed + p.scale_offset);
+    a.m = m;
+    a.n = n;
+    a.tiles = (uint32_t)p.tiles;
+    a.nc = p.chunks;
+    a.ngp = p.groups_padded;
+    // units of scaling: steps where groups are shorter than a chunk, else chunks
+    *fs = group && group < kChunk ? 1 : kSteps;
+    a.gshift = 62;  // one group
+    if (group) {
+        a.gshift = 0;
+        while (((int64_t)*fs * kStep << a.gshift) < group) ++a.gshift;
+    }
+    return a;
+}
+
+}  // namespace
+
+size_t experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) { return layout(T, k, E, n, I).bytes; }
+
+int launch_experts(const void* gate, const void* up, int bits, int64_t group, const void* down, int dbits, int64_t dgroup,
+                   int64_t E, int64_t n, int64_t I, const void* x, int xtype, int64_t T, int64_t ldx, const float* xs,
+                   const int32_t* ids, const float* weights, int64_t k, int act, void* y, int ytype, int64_t ldy, void* ws,
+                   hipStream_t stream) {
+    const PackShape p1 = pack_shape(I, n, bits, group), p2 = pack_shape(n, I, dbits, dgroup);
+    const Layout l = layout(T, k, E, n, I);
+    char* w = (char*)ws;
+    ExpertArgs e = {};
+    int fs1, fs2;
+    e.first = product(gate, p1, I, n, group, &fs1);
+    e.second = product(down, p2, n, I, dgroup, &fs2);
+    e.up_codes = (const char*)up;
+    e.up_scales = (const float*)((const char*)up + p1.scale_offset);
+    e.first_stride = (int64_t)p1.bytes;
+    e.second_stride = (int64_t)p2.bytes;
+    e.tiles_used = (const int32_t*)(w + l.used);
+    e.list = (const ExpertTile*)(w + l.list);
+    e.tokens = (const int32_t*)(w + l.tokens);
+    e.pairs = (const int32_t*)(w + l.pair);
+    e.weights = (const float*)(w + l.weight);
+    e.h = (float*)(w + l.h);
+    e.ldh = l.ldh;
+    e.part = (float*)(w + l.part);
+    e.n = n;
+    e.I = I;
+    e.act = act;
+    e.first.ldx = ldx;
+    e.second.x = (const char*)e.h;
+    e.second.ldx = l.ldh;
+    const int64_t xb = xtype == BAKRON_F32 ? 4 : xtype == BAKRON_I8 || xtype == BAKRON_E4M3 ? 1 : 2;
+    const int64_t round = round_tokens(T, k, E, n, I);
+    for (int64_t t0 = 0; t0 < T; t0 += round) {
+        const int64_t tokens = std::min(round, T - t0), pairs = tokens * k;
+        e.first.x = (const char*)x + t0 * ldx * xb;
+        e.first.xs = xs ? xs + t0 : nullptr;
+        e.most_tiles = (int)(std::min(E, pairs) + pairs / kExpertTokens);
+        PlanArgs p = {ids + t0 * k, weights + t0 * k, pairs, (int)k, (int)E, kExpertTokens, (int32_t*)(w + l.used),
+                      (ExpertTile*)(w + l.list), (int32_t*)(w + l.tokens), (int32_t*)(w + l.pair), (float*)(w + l.weight)};
+        hipLaunchKernelGGL(k_experts_plan, dim3(1), dim3(1024), 0, stream, p);
+        switch (xtype) {
+            case BAKRON_F32: launch_experts_first<kF32>(e, p1.W, fs1, stream); break;
+            case BAKRON_F16: launch_experts_first<kF16>(e, p1.W, fs1, stream); break;
+            case BAKRON_BF16: launch_experts_first<kBF16>(e, p1.W, fs1, stream); break;
+            case BAKRON_I8: launch_experts_first<kI8>(e, p1.W, fs1, stream); break;
+            default: launch_experts_first<kF8>(e, p1.W, fs1, stream); break;
+        }
+        launch_experts_second<kF32>(e, p2.W, fs2, stream);
+        SumArgs s = {ids + t0 * k, e.part, (char*)y + t0 * ldy * (ytype == BAKRON_F32 ? 4 : 2), tokens, n, ldy, (int)k, (int)E, ytype};
+        hipLaunchKernelGGL(k_experts_sum, dim3((unsigned)(tokens * ((n + 1023) / 1024))), dim3(256), 0, stream, s);
+    }
+    return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
+}
+
+}  // namespace bk

@@ -1,0 +1,6 @@
+// bk_experts_f16.hip -- the experts' first product of f16 token rows (kernels in bk_experts.hpp).
+#include "bk_experts.hpp"
+
+namespace bk {
+template void launch_experts_first<kF16>(const ExpertArgs&, int, int, hipStream_t);
+}  // namespace bk

@@ -1,0 +1,6 @@
+// bk_experts_f32.hip -- the experts' first product of f32 token rows (kernels in bk_experts.hpp).
+#include "bk_experts.hpp"
+
+namespace bk {
+template void launch_experts_first<kF32>(const ExpertArgs&, int, int, hipStream_t);
+}  // namespace bk

@@ -108,6 +108,14 @@ constexpr int64_t kMaxExperts = 1024, kMaxChosen = 64;
 int launch_route(const void* logits, int type, int64_t T, int64_t E, int64_t ldl, int64_t k, int sigmoid,
                  const float* bias, int renorm, float scale, int32_t* ids, float* weights, hipStream_t stream);
 
+// --- a mixture of rounded experts (bk_experts.hip) ---
+constexpr int64_t kMaxExpertDim = (int64_t)1 << 18;
+size_t experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I);
+int launch_experts(const void* gate, const void* up, int bits, int64_t group, const void* down, int dbits, int64_t dgroup,
+                   int64_t E, int64_t n, int64_t I, const void* x, int xtype, int64_t T, int64_t ldx, const float* xs,
+                   const int32_t* ids, const float* weights, int64_t k, int act, void* y, int ytype, int64_t ldy, void* ws,
+                   hipStream_t stream);
+
 // --- bound and sensitivity report (bk_report.hip) ---
 int launch_layer_report(int64_t m, int64_t n, const float* DO, const float* DI, const float* scales,
                         const float* HI, int64_t ldhi, const float* HO, int64_t ldho, double* out,

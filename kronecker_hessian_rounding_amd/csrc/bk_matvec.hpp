@@ -273,6 +273,16 @@ struct Stream {
             sp[r] = a.scales + tile * a.ngp * 16;
         }
     }
+    // one tile each of two layers of one shape
+    __device__ __forceinline__ Stream(const MvArgs& a, const MvArgs& b, int64_t tile0, int lane_)
+        : nc(a.nc), gshift(a.gshift), lane(lane_) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t tile = min(tile0 + r / 2, (int64_t)a.tiles - 1);
+            wp[r] = reinterpret_cast<const Sh*>(r % 2 ? b.codes : a.codes) + tile * a.nc * 64;
+            sp[r] = (r % 2 ? b.scales : a.scales) + tile * a.ngp * 16;
+        }
+    }
     __device__ __forceinline__ void fetch(int slot, int64_t c) {
         c = min(c, nc - 1);
 #pragma unroll
@@ -307,16 +317,21 @@ struct FewShape {
     static constexpr int kBytes = TB * kPitch;                        // of a wave
 };
 
-template <int MATH, int W, int FS, int R, int PF, int TB, int NW>
-__global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
+//
+// few_products: a.T <= TB tokens, token t the row rows(t) of a.x, by the R row tiles of `st`. Leaves the waves' sums in
+// LDS as float [wave][tile][token][16 rows + 1], every wave past the barrier.
+struct EveryRow {  // token t is row t
+    __device__ __forceinline__ int64_t operator()(int64_t t) const { return t; }
+};
+
+template <int MATH, int W, int FS, int R, int PF, int TB, int NW, typename Rows>
+__device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, PF> st, const Rows& rows, char* lds) {
     using M = Mt<MATH>;
     using St = Stream<W, FS, R, PF>;
     using Sh = FewShape<MATH, PF, TB>;
     constexpr int kB = M::kBytes;
-    extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     char* xs = lds + w * Sh::kBytes;
-    const int64_t tile0 = (int64_t)blockIdx.x * R;
     const int T = (int)a.T, end = (int)a.n * kB;  // bytes of a row
     const int mine = a.nc > w ? (int)((a.nc - w + NW - 1) / NW) : 0;  // this wave's chunks
     u32x4 x[Sh::kUnits];
@@ -335,9 +350,8 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
     const auto load = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < Sh::kUnits; ++i)
-            __builtin_memcpy(&x[i], xb + min(token_of(i), T - 1) * ldb + min(byte_of(i, i0), most), 16);
+            __builtin_memcpy(&x[i], xb + rows(min(token_of(i), T - 1)) * ldb + min(byte_of(i, i0), most), 16);
     };
-    St st(a, tile0, lane);
     load(0);
 #pragma unroll
     for (int p = 0; p < PF; ++p) st.fetch(p, w + p * NW);
@@ -373,7 +387,7 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
             const int at = end & ~15, c = at / (kChunk * kB), p = c / NW - i0;
             wave_fence();  // behind the zeros that another lane wrote there
             if (c % NW == w && p >= 0 && p < PF && lane < T)
-                put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + lane * a.ldx * kB, at, end));
+                put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + rows(lane) * a.ldx * kB, at, end));
         }
         // this wave alone reads what it staged
         wave_fence();
@@ -414,6 +428,15 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) red[((w * R + r) * 16 + 4 * (lane >> 4) + v) * 17 + (lane & 15)] = sum[r][v];
     __syncthreads();
+}
+
+template <int MATH, int W, int FS, int R, int PF, int TB, int NW>
+__global__ __launch_bounds__(64 * NW) void k_matvec_few(MvArgs a) {
+    extern __shared__ __align__(16) char lds[];
+    const int64_t tile0 = (int64_t)blockIdx.x * R;
+    const int T = (int)a.T;
+    few_products<MATH, W, FS, R, PF, TB, NW>(a, Stream<W, FS, R, PF>(a, tile0, threadIdx.x & 63), EveryRow(), lds);
+    const float* red = reinterpret_cast<const float*>(lds);
     for (int i = threadIdx.x; i < T * R * 16; i += (64 * NW)) {
         const int t = i / (R * 16), r = i / 16 % R;
         const int64_t row = (tile0 + r) * 16 + (i & 15);

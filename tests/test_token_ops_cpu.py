@@ -93,3 +93,48 @@ def test_lora_binding_refuses_host_tensors():
     z = torch.zeros
     with pytest.raises(ValueError):
         bk.lora(z(2, 8), z(1, 4, 8), z(1, 6, 4), z(2, dtype=torch.int32))
+
+
+def test_experts_refuses():
+    f, nb = bk.LIB.bakron_experts, bk.LIB.bakron_packed_bytes
+    ws = bk.LIB.bakron_experts_workspace_bytes
+    gb, db, wb = 4 * nb(32, 64, 4, 32), 4 * nb(64, 32, 2, 0), ws(5, 2, 4, 64, 32)
+    assert wb > 0
+    ok = dict(gate=A, up=B, gb=gb, bits=4, group=32, down=C, db=db, dbits=2, dgroup=0, E=4, n=64, I=32, X=D, xtype=BF16, T=5, ldx=64,
+              xs=None, ids=E, w=F, k=2, act=0, Y=G, ytype=F32, ldy=64, ws=at(8 << 36), wb=wb, stream=None)
+
+    def call(**kw):
+        return f(*{**ok, **kw}.values())
+
+    for kw in (dict(gate=None), dict(up=None), dict(down=None), dict(X=None), dict(ids=None), dict(w=None), dict(Y=None), dict(T=-1),
+               dict(T=(1 << 40) + 1), dict(n=0), dict(I=0), dict(n=(1 << 18) + 1, ldx=1 << 19, ldy=1 << 19), dict(I=(1 << 18) + 1),
+               dict(E=0), dict(E=1025), dict(k=0), dict(k=65), dict(bits=5), dict(dbits=0), dict(group=16), dict(dgroup=33),
+               dict(xtype=5), dict(ytype=I8), dict(act=2), dict(act=-1), dict(ldx=63), dict(ldy=63), dict(gate=at((1 << 36) + 8)),
+               dict(down=at((3 << 36) + 4)), dict(ws=at((8 << 36) + 8)), dict(Y=A), dict(Y=B), dict(Y=C), dict(Y=D), dict(Y=E), dict(Y=F),
+               dict(ws=A), dict(ws=D), dict(ws=E), dict(ws=G), dict(xs=G), dict(xs=at(8 << 36))):
+        assert call(**kw) == INVALID, kw
+    for kw in (dict(gb=gb - 1), dict(db=db - 1), dict(wb=wb - 1), dict(ws=None)):
+        assert call(**kw) == WORKSPACE, kw
+    assert call(T=0) == OK
+    assert call(T=0, gate=None, up=None, down=None, X=None, ids=None, w=None, Y=None, ws=None) == OK
+    for bad in ((0, 2, 4, 64, 32), (-1, 2, 4, 64, 32), (5, 0, 4, 64, 32), (5, 65, 4, 64, 32), (5, 2, 0, 64, 32), (5, 2, 1025, 64, 32),
+                (5, 2, 4, 0, 32), (5, 2, 4, 64, (1 << 18) + 1)):
+        assert ws(*bad) == 0, bad
+
+
+def test_experts_workspace_does_not_grow_past_a_round():
+    """Prompts go through in rounds: the workspace of a million tokens is that of a round."""
+    ws = bk.LIB.bakron_experts_workspace_bytes
+    assert ws(1 << 20, 8, 64, 2048, 1408) == ws(1 << 14, 8, 64, 2048, 1408) < 1 << 30
+    assert ws(1, 2, 8, 4096, 14336) < 1 << 20
+
+
+def test_packed_experts_refuse_other_bytes():
+    nb = bk.LIB.bakron_packed_bytes(64, 256, 4, 128)
+    data = torch.zeros(3 * nb, dtype=torch.uint8)
+    assert bk.PackedExperts(data, 3, 64, 256, 4, 128).nbytes == 3 * nb
+    for d, e in ((data[:-1], 3), (data, 2), (data, 0), (data.int(), 3), (data[:1].expand(3 * nb), 3)):
+        with pytest.raises(ValueError):
+            bk.PackedExperts(d, e, 64, 256, 4, 128)
+    with pytest.raises(ValueError):
+        bk.pack_experts(torch.zeros(2, 4, 64, dtype=torch.uint8), torch.ones(2, 4), 4)
