@@ -203,7 +203,9 @@ def prepare(case, seed):
 def _lora(st):
     case = st["case"]
     x = st["x"].float()
-    y = torch.zeros(case["T"], case["m"], device=x.device) if st.get("base") is None else st["base"].float()
+    y = torch.zeros(case["T"], case["m"], device=x.device)
+    if st.get("base") is not None:
+        y += st["base"].float()
     ids = st["ids"]
     for a in range(case["R"]):
         rows = (ids == a).nonzero()[:, 0]
