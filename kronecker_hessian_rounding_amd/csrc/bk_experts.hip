@@ -10,6 +10,8 @@ extern template void launch_experts_first<kBF16>(const ExpertArgs&, int, int, hi
 extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, hipStream_t);
 extern template void launch_experts_second<kF32>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_second_few<2>(const ExpertArgs&, int, int, void*, int, int64_t, hipStream_t);
+extern template void launch_experts_second_few<3>(const ExpertArgs&, int, int, void*, int, int64_t, hipStream_t);
 
 namespace {
 
@@ -110,12 +112,15 @@ int64_t round_tokens(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
 }
 
 struct Layout {
-    size_t used, list, tokens, pair, weight, h, part, bytes;
-    int64_t ldh, most;
+    size_t used, list, tokens, pair, weight, h, part;  // more tokens
+    size_t named, planes;                              // few
+    size_t bytes;
+    int64_t ldh, plane, most;
 };
 Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     const int64_t t = round_tokens(T, k, E, n, I), p = t * k;
-    Layout l;
+    Layout l = {};
+    l.plane = (I + kChunk - 1) / kChunk * kChunk * 2;
     l.most = std::min(E, p) + p / kExpertTokens;
     l.ldh = (I + 3) / 4 * 4;
     size_t at = 0;
@@ -124,6 +129,12 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
+    if (few_tokens(T, k)) {
+        l.named = take(4 * (1 + 17 * std::min(E, T * k)));
+        l.planes = take(3 * l.plane * T * k);
+        l.bytes = at;
+        return l;
+    }
     l.used = take(4);
     l.list = take(sizeof(ExpertTile) * l.most);
     l.tokens = take(4 * p);
@@ -152,6 +163,16 @@ MvArgs product(const void* packed, const PackShape& p, int64_t m, int64_t n, int
         while (((int64_t)*fs * kStep << a.gshift) < group) ++a.gshift;
     }
     return a;
+}
+
+void launch_first(const ExpertArgs& e, int xtype, int W, int fs, hipStream_t stream) {
+    switch (xtype) {
+        case BAKRON_F32: launch_experts_first<kF32>(e, W, fs, stream); break;
+        case BAKRON_F16: launch_experts_first<kF16>(e, W, fs, stream); break;
+        case BAKRON_BF16: launch_experts_first<kBF16>(e, W, fs, stream); break;
+        case BAKRON_I8: launch_experts_first<kI8>(e, W, fs, stream); break;
+        default: launch_experts_first<kF8>(e, W, fs, stream); break;
+    }
 }
 
 }  // namespace
@@ -188,6 +209,23 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     e.second.x = (const char*)e.h;
     e.second.ldx = l.ldh;
     const int64_t xb = xtype == BAKRON_F32 ? 4 : xtype == BAKRON_I8 || xtype == BAKRON_E4M3 ? 1 : 2;
+    if (few_tokens(T, k)) {
+        e.ids = ids;
+        e.pair_weights = weights;
+        e.T = (int)T;
+        e.k = (int)k;
+        e.E = (int)E;
+        e.slots = (int)std::min(E, T * k);
+        e.named = (int32_t*)(w + l.named);
+        e.planes = w + l.planes;
+        e.plane = l.plane;
+        e.first.x = (const char*)x;
+        e.first.xs = xs;
+        launch_first(e, xtype, p1.W, fs1, stream);
+        if (xtype == BAKRON_F32) launch_experts_second_few<3>(e, p2.W, fs2, y, ytype, ldy, stream);
+        else launch_experts_second_few<2>(e, p2.W, fs2, y, ytype, ldy, stream);
+        return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
+    }
     const int64_t round = round_tokens(T, k, E, n, I);
     for (int64_t t0 = 0; t0 < T; t0 += round) {
         const int64_t tokens = std::min(round, T - t0), pairs = tokens * k;
@@ -197,13 +235,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         PlanArgs p = {ids + t0 * k, weights + t0 * k, pairs, (int)k, (int)E, kExpertTokens, (int32_t*)(w + l.used),
                       (ExpertTile*)(w + l.list), (int32_t*)(w + l.tokens), (int32_t*)(w + l.pair), (float*)(w + l.weight)};
         hipLaunchKernelGGL(k_experts_plan, dim3(1), dim3(1024), 0, stream, p);
-        switch (xtype) {
-            case BAKRON_F32: launch_experts_first<kF32>(e, p1.W, fs1, stream); break;
-            case BAKRON_F16: launch_experts_first<kF16>(e, p1.W, fs1, stream); break;
-            case BAKRON_BF16: launch_experts_first<kBF16>(e, p1.W, fs1, stream); break;
-            case BAKRON_I8: launch_experts_first<kI8>(e, p1.W, fs1, stream); break;
-            default: launch_experts_first<kF8>(e, p1.W, fs1, stream); break;
-        }
+        launch_first(e, xtype, p1.W, fs1, stream);
         launch_experts_second<kF32>(e, p2.W, fs2, stream);
         SumArgs s = {ids + t0 * k, e.part, (char*)y + t0 * ldy * (ytype == BAKRON_F32 ? 4 : 2), tokens, n, ldy, (int)k, (int)E, ytype};
         hipLaunchKernelGGL(k_experts_sum, dim3((unsigned)(tokens * ((n + 1023) / 1024))), dim3(256), 0, stream, s);

@@ -4,10 +4,15 @@
 // G_e, U_e (I x n) and D_e (n x I) packed as bk_matvec.hpp says, the experts of a matrix one behind the other.
 //
 // A pair is (token, slot); a leader is a pair whose expert no earlier slot of its token names, and it carries the
-// weights of those that repeat it. The plan lists the leaders by expert, cut into tiles of tokens of one expert.
-// The first product takes a tile of G and the same one of U by a tile of tokens and leaves h = w act(g) u in fp32,
-// a row for each leader; the second leaves w D h in fp32 by leaders, and the sum over a token's leaders, in the
-// order of its slots, is y. No result depends on the order within a list.
+// weights of those that repeat it. The first product takes a row tile of G and the same one of U by tokens of one expert
+// and leaves h = w act(g) u, a row for each leader.
+//
+// Few tokens (T <= 16, and at most 512 pairs): two launches. A workgroup of the first finds its expert's tokens in the ids by itself, and
+// one more lists the experts that are named, with their tokens, for the second, in which a workgroup takes row tiles of
+// all named experts' D: their columns follow each other as if they were one long layer's, so that its sums are y.
+// More: a plan lists the leaders by expert, cut into tiles of tokens of one expert; the second product leaves w D h by
+// leaders, and the sum over a token's leaders, in the order of its slots, is y.
+// No result depends on the order within a list.
 #pragma once
 
 #include "bk_matvec.hpp"
@@ -31,6 +36,13 @@ struct ExpertArgs {
     const float* weights;
     float* h;                     // [pair][ldh]
     int64_t ldh;
+    // few tokens
+    const int32_t* ids;
+    const float* pair_weights;
+    int T, k, E, slots;           // slots: experts, or pairs where they are fewer; 0 on the other path
+    int32_t* named;               // the experts that are named: how many, which, and [slot][16] pairs of their tokens or -1
+    char* planes;                 // h as bf16 pieces, largest first: [pair][piece][plane] bytes
+    int64_t plane;
     float* part;                  // [pair][n]
     int64_t n, I;
     int act;
@@ -108,8 +120,338 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
 
 constexpr int kExpertTokens = 16;  // tokens of a list's tile
 
+// ---------------------------------------------------------------- few tokens
+constexpr int kFewTokens = 16, kFewPairs = 512;  // of the few tokens' path: what LDS holds of the map
+inline bool few_tokens(int64_t T, int64_t k) { return T <= kFewTokens && T * k <= kFewPairs; }
+
+// The named experts, by one workgroup: an expert's slot is its place among the pairs that are the first to name one.
+// Row `slot` of the map: the leader of each token that names the expert, or -1.
+__device__ __forceinline__ void list_named(const ExpertArgs& e, char* lds) {
+    const int pairs = e.T * e.k, threads = blockDim.x, waves = threads / 64;
+    int* id = reinterpret_cast<int*>(lds);    // [pairs]
+    int* first = id + kFewPairs;                   // [pairs]: the first pair with this pair's id
+    int* slot = first + kFewPairs;                // [pairs]: of first ones
+    int* base = slot + kFewPairs;                 // [waves]
+    for (int p = threadIdx.x; p < pairs; p += threads) {
+        const int x = e.ids[p];
+        id[p] = x >= 0 && x < e.E ? x : -1;
+    }
+    __syncthreads();
+    int total = 0;
+    for (int p0 = 0; p0 < pairs; p0 += threads) {
+        const int p = p0 + threadIdx.x;
+        bool leader = false;
+        if (p < pairs && id[p] >= 0) {
+            int f = 0;
+            while (id[f] != id[p]) ++f;
+            first[p] = f;
+            leader = f == p;
+        }
+        const uint64_t b = __ballot(leader);
+        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+        if (lane == 0) base[w] = __popcll(b);
+        __syncthreads();
+        int before = total;
+        for (int i = 0; i < waves; ++i) {
+            before += i < w ? base[i] : 0;
+            total += base[i];
+        }
+        if (leader) {
+            const int s = before + __popcll(b & (((uint64_t)1 << lane) - 1));
+            slot[p] = s;
+            e.named[1 + s] = id[p];
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) e.named[0] = total;
+    int32_t* map = e.named + 1 + e.slots;
+    for (int i = threadIdx.x; i < total * 16; i += threads) map[i] = -1;
+    __syncthreads();  // (the map's own lines: written and then overwritten by this workgroup)
+    for (int p = threadIdx.x; p < pairs; p += threads)
+        if (id[p] >= 0) {
+            bool leader = true;
+            for (int i = p / e.k * e.k; i < p; ++i) leader = leader && id[i] != id[p];
+            if (leader) map[slot[first[p]] * 16 + p / e.k] = p;
+        }
+}
+
+// h as NP bf16 pieces whose sum is h to within 2^-17 (two) or 2^-25 (three) of it: all but the last are cut off, the last
+// is rounded. An infinity or NaN stays in the first.
+template <int NP>
+__device__ __forceinline__ void store_pieces(char* row, int64_t plane, int64_t i, float h) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        __bf16 b;
+        if (p == NP - 1) b = (__bf16)h;
+        else b = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(__builtin_canonicalizef(h)) >> 16));
+        *reinterpret_cast<__bf16*>(row + p * plane + 2 * i) = b;
+        const float r = h - (float)b;
+        h = r == r ? r : 0.0f;
+    }
+}
+
+template <int MATH, int W, int FS, int PF, int TB, int NW>
+__global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int NP = MATH == kF32 ? 3 : 2;
+    if (blockIdx.x == gridDim.x - 1) return list_named(e, lds);
+    const int tiles = (int)(e.plane / 32), lane = threadIdx.x & 63;  // with those that pad h
+    const int slot = blockIdx.x / tiles;
+    const int64_t tile = blockIdx.x % tiles;
+    // the expert: the slot itself, or the id of a pair that is the first to name it
+    int expert = slot;
+    const int pairs = e.T * e.k;
+    if (e.slots < e.E) {
+        expert = e.ids[slot];
+        if (expert < 0 || expert >= e.E) return;
+        bool seen = false;
+        for (int p = lane; p < slot; p += 64) seen = seen || e.ids[p] == expert;
+        if (__ballot(seen)) return;
+    }
+    // lane t < T: token t's leader and weight for this expert
+    int pair = -1;
+    float weight = 0.0f;
+    if (lane < e.T)
+        for (int p = lane * e.k; p < (lane + 1) * e.k; ++p)
+            if (e.ids[p] == expert) {
+                if (pair < 0) pair = p;
+                weight += e.pair_weights[p];
+            }
+    const uint32_t members = (uint32_t)__ballot(pair >= 0);
+    const int count = __popc(members);
+    if (count == 0) return;
+    // lane c: the c-th of them
+    int token = 0;
+    {
+        uint32_t m = members;
+        for (int c = 0; c < count; ++c, m &= m - 1)
+            if (lane == c) token = __builtin_ctz(m);
+    }
+    pair = __shfl(pair, token);
+    weight = __shfl(weight, token);
+    float xs = e.first.xs && lane < count ? e.first.xs[token] : 1.0f;
+    const bool real = tile < e.first.tiles;
+    if (real) {
+        MvArgs a = e.first, b = e.first;
+        a.codes += expert * e.first_stride;
+        a.scales = (const float*)((const char*)a.scales + expert * e.first_stride);
+        b.codes = e.up_codes + expert * e.first_stride;
+        b.scales = (const float*)((const char*)e.up_scales + expert * e.first_stride);
+        a.T = count;
+        const auto rows = [&](int64_t t) { return (int64_t)__shfl(token, (int)t); };
+        few_products<MATH, W, FS, 2, PF, TB, NW>(a, Stream<W, FS, 2, PF>(a, b, tile, lane), rows, lds);
+    }
+    const float* red = reinterpret_cast<const float*>(lds);
+    for (int i0 = 0; i0 < count * 16; i0 += 64 * NW) {
+        const int i = i0 + threadIdx.x, t = i >> 4, r = i & 15;
+        const int64_t row = tile * 16 + r;
+        const int64_t to = __shfl(pair, t & 63);
+        const float w = __shfl(weight, t & 63), s = unit<MATH, W>() * __shfl(xs, t & 63);
+        if (i >= count * 16) continue;
+        float h = 0.0f;
+        if (row < e.I) {
+            float g = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                g += red[((k * 2) * 16 + t) * 17 + r];
+                u += red[((k * 2 + 1) * 16 + t) * 17 + r];
+            }
+            h = w * (activation(g * s, e.act) * (u * s));
+        }
+        store_pieces<NP>(e.planes + to * NP * e.plane, e.plane, row, h);
+    }
+}
+
+// The second product of few tokens. A workgroup takes row tile blockIdx.x of every named expert's D; its waves share the
+// chunks of all of them, wave w taking w, w + NW, .. of slot * nc + chunk, and each stages h's pieces for its next PF
+// chunks in LDS of its own, as few_products does x: a token that does not name the expert has zeros there.
+template <int NP, int PF, int TB>
+struct SecondShape {
+    static constexpr int kUnits = (TB * PF * NP * 16 + 63) / 64;  // 16-byte units of a lane in a set
+    static constexpr int kPiece = PF * 256;                       // from piece to piece of a token
+    static constexpr int kPitch = NP * kPiece + 16;               // from token to token: 4 banks
+    static constexpr int kBytes = TB * kPitch;                    // of a wave
+};
+
+template <int NP, int W, int FS, int PF, int TB, int NW>
+__global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, void* y, int ytype, int64_t ldy) {
+    using M = Mt<kBF16>;
+    using Sh = SecondShape<NP, PF, TB>;
+    using Wd = typename Share<W>::T;
+    constexpr int kScales = kSteps / FS;
+    extern __shared__ __align__(16) char lds[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const MvArgs& a = e.second;
+    const int64_t tile = blockIdx.x;
+    const int live = __builtin_amdgcn_readfirstlane(e.named[0]);
+    int16_t* map = reinterpret_cast<int16_t*>(lds + NW * Sh::kBytes);  // [live][TB]
+    const int32_t* from = e.named + 1 + e.slots;
+    for (int i = threadIdx.x; i < live * TB; i += 64 * NW) map[i] = (int16_t)from[i / TB * 16 + i % TB];
+    __syncthreads();
+    const int nc = (int)a.nc, total = live * nc;
+    const int mine = total > w ? (total - w + NW - 1) / NW : 0;
+    struct At {
+        int slot, chunk;
+    };
+    const auto ahead = [&](At p) __attribute__((always_inline)) {  // the wave's next chunk; past the last, the last
+        p.chunk += NW;
+        while (p.chunk >= nc) {
+            p.chunk -= nc;
+            ++p.slot;
+        }
+        return p;
+    };
+    float sum[4] = {};
+    if (mine > 0) {
+        char* xs = lds + w * Sh::kBytes;
+        u32x4 x[Sh::kUnits];
+        uint32_t some = 0;  // units whose token names the expert
+        At next[PF];
+        next[0] = At{w / nc, w % nc};
+#pragma unroll
+        for (int p = 1; p < PF; ++p) next[p] = ahead(next[p - 1]);
+        const auto clamp = [&](At p) __attribute__((always_inline)) { return p.slot < live ? p : At{live - 1, nc - 1}; };
+        // unit of this lane: 16 bytes `u` of a piece of a token's row in chunk p of the set
+        const auto load = [&]() __attribute__((always_inline)) {
+            some = 0;
+#pragma unroll
+            for (int i = 0; i < Sh::kUnits; ++i) {
+                const int v = lane + 64 * i, u = v % 16, piece = v / 16 % NP, p = v / (16 * NP) % PF;
+                const int token = min(v / (16 * NP * PF), TB - 1);
+                At c = clamp(next[0]);
+#pragma unroll
+                for (int k = 1; k < PF; ++k) {
+                    const At n = clamp(next[k]);
+                    c.slot = p == k ? n.slot : c.slot;
+                    c.chunk = p == k ? n.chunk : c.chunk;
+                }
+                const int pair = map[c.slot * TB + token];
+                some |= (uint32_t)(pair >= 0) << i;
+                x[i] = *reinterpret_cast<const u32x4*>(e.planes + ((int64_t)max(pair, 0) * NP + piece) * e.plane +
+                                                       c.chunk * 256 + u * 16);
+            }
+        };
+        Wd d[PF];
+        float s[PF][kScales];
+        const auto fetch = [&](int p) __attribute__((always_inline)) {
+            const At c = clamp(next[p]);
+            const int expert = __builtin_amdgcn_readfirstlane(e.named[1 + c.slot]);
+            const char* codes = a.codes + expert * e.second_stride;
+            const float* sp = (const float*)((const char*)a.scales + expert * e.second_stride) + tile * a.ngp * 16;
+            d[p] = (reinterpret_cast<const Wd*>(codes) + (tile * a.nc + c.chunk) * 64)[lane];
+#pragma unroll
+            for (int f = 0; f < kScales; ++f)
+                s[p][f] = (sp + (((int64_t)c.chunk * kScales + f) >> a.gshift) * 16)[lane & 15];
+        };
+        load();
+#pragma unroll
+        for (int p = 0; p < PF; ++p) fetch(p);
+        const char* xl = xs + min(lane & 15, TB - 1) * Sh::kPitch + (lane >> 4) * 16;
+        int after = 0;  // as in few_products: keeps a set's writes behind the reads of the set before
+        for (int i0 = 0; i0 < mine; i0 += PF) {
+#pragma unroll
+            for (int i = 0; i < Sh::kUnits; ++i) {
+                const int v = lane + 64 * i, u = v % 16, piece = v / 16 % NP, p = v / (16 * NP) % PF, token = v / (16 * NP * PF);
+                if (token < TB)
+                    *reinterpret_cast<u32x4*>(xs + token * Sh::kPitch + piece * Sh::kPiece + p * 256 + u * 16 + after) =
+                        some >> i & 1 ? x[i] : u32x4{0, 0, 0, 0};
+            }
+            wave_fence();
+            {
+                At p = next[PF - 1];
+#pragma unroll
+                for (int k = 0; k < PF; ++k) next[k] = p = ahead(p);
+            }
+            load();
+#pragma unroll
+            for (int p = 0; p < PF; ++p) {
+                if (i0 + p < mine)
+#pragma unroll
+                    for (int f = 0; f < kScales; ++f) {
+                        f32x4 acc = {};
+#pragma unroll
+                        for (int j = 0; j < FS; ++j) {
+                            bf16x8 v[NP];
+#pragma unroll
+                            for (int q = 0; q < NP; ++q) {  // the smallest piece first into the sum
+                                v[q] = *reinterpret_cast<const bf16x8*>(xl + (NP - 1 - q) * Sh::kPiece + p * 256 + (f * FS + j) * 64);
+                                asm("" : "+v"(after) : "v"(v[q]));
+                            }
+                            const bf16x8 b = weights<kBF16, W>(d[p], f * FS + j);
+#pragma unroll
+                            for (int q = 0; q < NP; ++q) acc = M::mma(v[q], b, acc);
+                        }
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) sum[v] = fmaf(s[p][f], acc[v], sum[v]);
+                    }
+                fetch(p);
+            }
+            if constexpr (PF == 1) asm volatile("" ::: "memory");  // or all loads move over the loop's edge, to their use
+        }
+    }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(lds);  // [wave][token][16 rows + 1]
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[(w * 16 + 4 * (lane >> 4) + v) * 17 + (lane & 15)] = sum[v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < e.T * 16; i += 64 * NW) {
+        const int t = i >> 4;
+        const int64_t row = tile * 16 + (i & 15);
+        if (row >= e.n) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) v += red[(k * 16 + t) * 17 + (i & 15)];
+        store_elem(y, ytype, t * ldy + row, v);
+    }
+}
+
+template <int MATH, int W, int FS, int TB>
+void launch_first_tokens(const ExpertArgs& e, hipStream_t stream) {
+    constexpr int NW = 8, PF = TB <= 4 ? 8 / W : MATH == kF32 ? 1 : 2;
+    constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17, list = sizeof(int) * (3 * kFewPairs + NW);
+    constexpr size_t lds = std::max<size_t>({(size_t)NW * FewShape<MATH, PF, TB>::kBytes, red, list});
+    const unsigned grid = (unsigned)(e.slots * (e.plane / 32) + 1);
+    hipLaunchKernelGGL((k_experts_first_few<MATH, W, FS, PF, TB, NW>), dim3(grid), dim3(64 * NW), lds, stream, e);
+}
+template <int MATH, int W, int FS>
+void launch_first_few(const ExpertArgs& e, hipStream_t stream) {
+    if (e.T == 1) launch_first_tokens<MATH, W, FS, 1>(e, stream);
+    else if (e.T <= 4) launch_first_tokens<MATH, W, FS, 4>(e, stream);
+    else if (e.T <= 8) launch_first_tokens<MATH, W, FS, 8>(e, stream);
+    else launch_first_tokens<MATH, W, FS, 16>(e, stream);
+}
+
+template <int NP, int W, int FS, int TB>
+void launch_second_tokens(const ExpertArgs& e, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : NP == 3 ? 1 : 2;
+    const size_t red = sizeof(float) * NW * 16 * 17;
+    const size_t lds = std::max(red, (size_t)NW * SecondShape<NP, PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
+    hipLaunchKernelGGL((k_experts_second_few<NP, W, FS, PF, TB, NW>), dim3(e.second.tiles), dim3(64 * NW), lds, stream, e, y,
+                       ytype, ldy);
+}
+template <int NP, int W, int FS>
+void launch_second_few(const ExpertArgs& e, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    if (e.T == 1) launch_second_tokens<NP, W, FS, 1>(e, y, ytype, ldy, stream);
+    else if (e.T <= 4) launch_second_tokens<NP, W, FS, 4>(e, y, ytype, ldy, stream);
+    else if (e.T <= 8) launch_second_tokens<NP, W, FS, 8>(e, y, ytype, ldy, stream);
+    else launch_second_tokens<NP, W, FS, 16>(e, y, ytype, ldy, stream);
+}
+template <int NP>
+void launch_experts_second_few(const ExpertArgs& e, int W, int fs, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    if (W == 4) {
+        if (fs == 1) launch_second_few<NP, 4, 1>(e, y, ytype, ldy, stream);
+        else launch_second_few<NP, 4, 4>(e, y, ytype, ldy, stream);
+    } else {
+        if (fs == 1) launch_second_few<NP, 2, 1>(e, y, ytype, ldy, stream);
+        else launch_second_few<NP, 2, 4>(e, y, ytype, ldy, stream);
+    }
+}
+
+// ---------------------------------------------------------------- more tokens
+
 template <int MATH, int W, int FS>
 void launch_first_shape(const ExpertArgs& e, hipStream_t stream) {
+    if (e.slots) return launch_first_few<MATH, W, FS>(e, stream);
     constexpr int NW = 8, TB = kExpertTokens, PF = MATH == kF32 ? 1 : 2;
     constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17;
     constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, TB>::kBytes, red);

@@ -347,10 +347,12 @@ __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, P
     const char* xb = end >= 16 ? a.x : a.codes;
     const int64_t ldb = end >= 16 ? a.ldx * kB : 0;
     const int most = max(end - 16, 0);
+    const char* row_of[Sh::kUnits];
+#pragma unroll
+    for (int i = 0; i < Sh::kUnits; ++i) row_of[i] = xb + rows(min(token_of(i), T - 1)) * ldb;
     const auto load = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < Sh::kUnits; ++i)
-            __builtin_memcpy(&x[i], xb + rows(min(token_of(i), T - 1)) * ldb + min(byte_of(i, i0), most), 16);
+        for (int i = 0; i < Sh::kUnits; ++i) __builtin_memcpy(&x[i], row_of[i] + min(byte_of(i, i0), most), 16);
     };
     load(0);
 #pragma unroll
@@ -386,8 +388,9 @@ __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, P
         if (end % 16 != 0) {  // the unit that the row ends in, if it is in this set
             const int at = end & ~15, c = at / (kChunk * kB), p = c / NW - i0;
             wave_fence();  // behind the zeros that another lane wrote there
+            const int64_t row = rows(min(lane, T - 1));
             if (c % NW == w && p >= 0 && p < PF && lane < T)
-                put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + rows(lane) * a.ldx * kB, at, end));
+                put(lane, ((p - c) * kChunk * kB + at) / 16, cut_unit<kB>(a.x + row * a.ldx * kB, at, end));
         }
         // this wave alone reads what it staged
         wave_fence();

@@ -109,7 +109,7 @@ def test_against_64_bits(T, E, k, n, I, bits, group, dbits, dgroup, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, I8])
-@pytest.mark.parametrize("T,E,k", [(1, 1000, 64), (2, 70, 60), (16, 1024, 32), (40, 2, 2), (300, 4, 2), (17, 128, 8), (64, 16, 1), (9000, 2, 2)])
+@pytest.mark.parametrize("T,E,k", [(1, 1000, 64), (2, 70, 60), (16, 1024, 32), (9, 1024, 64), (8, 90, 64), (16, 4, 3), (40, 2, 2), (300, 4, 2), (17, 128, 8), (64, 16, 1), (9000, 2, 2)])
 def test_launch_shapes(T, E, k, dtype):
     """Many experts and slots, all tokens at few experts, and more pairs than one round of launches takes."""
     check(T, E, k, 40, 33, 4, 32, 4, 32, dtype, F32, none=0.1, seed=T)
