@@ -10,8 +10,8 @@ extern template void launch_experts_first<kBF16>(const ExpertArgs&, int, int, hi
 extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, hipStream_t);
 extern template void launch_experts_second<kF32>(const ExpertArgs&, int, int, hipStream_t);
-extern template void launch_experts_second_few<2>(const ExpertArgs&, int, int, void*, int, int64_t, hipStream_t);
-extern template void launch_experts_second_few<3>(const ExpertArgs&, int, int, void*, int, int64_t, hipStream_t);
+extern template void launch_experts_second_few<2>(const ExpertArgs&, int, int, int, void*, int, int64_t, hipStream_t);
+extern template void launch_experts_second_few<3>(const ExpertArgs&, int, int, int, void*, int, int64_t, hipStream_t);
 
 namespace {
 
@@ -103,6 +103,30 @@ __global__ __launch_bounds__(256) void k_experts_sum(SumArgs a) {
     store4(a.y, a.ytype, t * a.ldy + i, y, count);
 }
 
+// y of few tokens whose second product was split.
+__global__ __launch_bounds__(256) void k_experts_splits(const float* part, int splits, int64_t T, int64_t n, void* y, int ytype,
+                                                        int64_t ldy) {
+    const int64_t per = (n + 1023) / 1024, t = blockIdx.x / per, i = (blockIdx.x % per) * 1024 + threadIdx.x * 4;
+    if (i >= n) return;
+    const int count = (int)min<int64_t>(4, n - i);
+    f4 v = {};
+    for (int s = 0; s < splits; ++s) {
+        const float* p = part + (s * T + t) * n + i;
+        f4 u = {};
+        if (count == 4) __builtin_memcpy(&u, p, 16);
+        else
+            for (int e = 0; e < 4; ++e) u[e] = e < count ? p[e] : 0.0f;
+        v += u;
+    }
+    store4(y, ytype, t * ldy + i, v, count);
+}
+
+// Splits of the few tokens' second product: see launch_second_tokens.
+int second_splits(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
+    const int64_t tiles = (n + kRowTile - 1) / kRowTile, chunks = (I + kChunk - 1) / kChunk * std::min(E, T * k);
+    return T > 4 && tiles * chunks >= 1 << 15 ? 4 : 1;
+}
+
 // Tokens of one round of launches: the workspace holds 2^14 pairs at most, and a grid fewer than 2^32 threads.
 int64_t round_tokens(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     int64_t t = std::max<int64_t>(1, std::min(T, ((int64_t)1 << 14) / k));
@@ -132,6 +156,8 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     if (few_tokens(T, k)) {
         l.named = take(4 * (1 + 17 * std::min(E, T * k)));
         l.planes = take(3 * l.plane * T * k);
+        const int splits = second_splits(T, k, E, n, I);
+        if (splits > 1) l.part = take(4 * splits * T * n);
         l.bytes = at;
         return l;
     }
@@ -222,8 +248,12 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         e.first.x = (const char*)x;
         e.first.xs = xs;
         launch_first(e, xtype, p1.W, fs1, stream);
-        if (xtype == BAKRON_F32) launch_experts_second_few<3>(e, p2.W, fs2, y, ytype, ldy, stream);
-        else launch_experts_second_few<2>(e, p2.W, fs2, y, ytype, ldy, stream);
+        const int splits = second_splits(T, k, E, n, I);
+        if (xtype == BAKRON_F32) launch_experts_second_few<3>(e, p2.W, fs2, splits, y, ytype, ldy, stream);
+        else launch_experts_second_few<2>(e, p2.W, fs2, splits, y, ytype, ldy, stream);
+        if (splits > 1)
+            hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, e.part, splits,
+                               T, n, y, ytype, ldy);
         return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
     }
     const int64_t round = round_tokens(T, k, E, n, I);

@@ -122,6 +122,7 @@ constexpr int kExpertTokens = 16;  // tokens of a list's tile
 
 // ---------------------------------------------------------------- few tokens
 constexpr int kFewTokens = 16, kFewPairs = 512;  // of the few tokens' path: what LDS holds of the map
+// splits of the second product: enough work in its layers that four row tiles share a token's h
 inline bool few_tokens(int64_t T, int64_t k) { return T <= kFewTokens && T * k <= kFewPairs; }
 
 // The named experts, by one workgroup: an expert's slot is its place among the pairs that are the first to name one.
@@ -193,30 +194,69 @@ __device__ __forceinline__ void store_pieces(char* row, int64_t plane, int64_t i
 template <int MATH, int W, int FS, int PF, int TB, int NW>
 __global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
     extern __shared__ __align__(16) char lds[];
-    constexpr int NP = MATH == kF32 ? 3 : 2;
+    constexpr int NP = MATH == kF32 ? 3 : 2, kWords = kFewPairs / 64;
     if (blockIdx.x == gridDim.x - 1) return list_named(e, lds);
     const int tiles = (int)(e.plane / 32), lane = threadIdx.x & 63;  // with those that pad h
     const int slot = blockIdx.x / tiles;
     const int64_t tile = blockIdx.x % tiles;
+    // lane p of word v holds pair 64 v + p: its id (-1: no expert) and weight
+    const int pairs = e.T * e.k, words = (pairs + 63) / 64;
+    int id[kWords];
+    float wt[kWords];
+#pragma unroll
+    for (int v = 0; v < kWords; ++v) {
+        id[v] = -1;
+        wt[v] = 0.0f;
+        if (v < words) {
+            const int p = min(64 * v + lane, pairs - 1);
+            id[v] = e.ids[p];
+            wt[v] = e.pair_weights[p];
+            if (64 * v + lane >= pairs || id[v] >= e.E) id[v] = -1;
+        }
+    }
     // the expert: the slot itself, or the id of a pair that is the first to name it
     int expert = slot;
-    const int pairs = e.T * e.k;
     if (e.slots < e.E) {
-        expert = e.ids[slot];
-        if (expert < 0 || expert >= e.E) return;
-        bool seen = false;
-        for (int p = lane; p < slot; p += 64) seen = seen || e.ids[p] == expert;
-        if (__ballot(seen)) return;
+#pragma unroll
+        for (int v = 0; v < kWords; ++v)
+            if (v == slot >> 6) expert = __builtin_amdgcn_readlane(id[v], slot & 63);
+        if (expert < 0) return;
     }
-    // lane t < T: token t's leader and weight for this expert
+    uint64_t named[kWords + 1];
+#pragma unroll
+    for (int v = 0; v < kWords; ++v) {
+        named[v] = v < words ? __ballot(id[v] == expert) : 0;
+        if (e.slots < e.E && ((v < slot >> 6 && named[v]) ||
+                              (v == slot >> 6 && (named[v] & (((uint64_t)1 << (slot & 63)) - 1)))))
+            return;
+    }
+    named[kWords] = 0;
+    // lane t < T: token t's leader and weight for this expert, from the k bits of its pairs
     int pair = -1;
     float weight = 0.0f;
-    if (lane < e.T)
-        for (int p = lane * e.k; p < (lane + 1) * e.k; ++p)
-            if (e.ids[p] == expert) {
-                if (pair < 0) pair = p;
-                weight += e.pair_weights[p];
+    {
+        const int at = lane * e.k;
+        uint64_t lo = 0, hi = 0;
+#pragma unroll
+        for (int v = 0; v < kWords; ++v)
+            if (v < words) {
+                lo = at >> 6 == v ? named[v] : lo;
+                hi = at >> 6 == v ? named[v + 1] : hi;
             }
+        uint64_t bits = (at & 63 ? lo >> (at & 63) | hi << (64 - (at & 63)) : lo) & (~(uint64_t)0 >> (64 - e.k));
+        if (lane >= e.T) bits = 0;
+        if (bits) pair = at + __builtin_ctzll(bits);
+        while (__ballot(bits != 0)) {  // once, but for an expert that comes twice in a row
+            const int p = bits ? at + __builtin_ctzll(bits) : 0;
+#pragma unroll
+            for (int v = 0; v < kWords; ++v)
+                if (v < words) {
+                    const float x = __shfl(wt[v], p & 63);
+                    weight += bits && p >> 6 == v ? x : 0.0f;
+                }
+            bits &= bits - 1;
+        }
+    }
     const uint32_t members = (uint32_t)__ballot(pair >= 0);
     const int count = __popc(members);
     if (count == 0) return;
@@ -262,8 +302,8 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
     }
 }
 
-// The second product of few tokens. A workgroup takes row tile blockIdx.x of every named expert's D; its waves share the
-// chunks of all of them, wave w taking w, w + NW, .. of slot * nc + chunk, and each stages h's pieces for its next PF
+// The second product of few tokens. A workgroup takes R row tiles of every named expert's D; its waves (and with `splits`
+// those of as many workgroups) share the chunks of all of them, wave w of W taking w, w + W, .. of slot * nc + chunk, and each stages h's pieces for its next PF
 // chunks in LDS of its own, as few_products does x: a token that does not name the expert has zeros there.
 template <int NP, int PF, int TB>
 struct SecondShape {
@@ -273,8 +313,8 @@ struct SecondShape {
     static constexpr int kBytes = TB * kPitch;                    // of a wave
 };
 
-template <int NP, int W, int FS, int PF, int TB, int NW>
-__global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, void* y, int ytype, int64_t ldy) {
+template <int NP, int W, int FS, int R, int PF, int TB, int NW>
+__global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, int splits, void* y, int ytype, int64_t ldy) {
     using M = Mt<kBF16>;
     using Sh = SecondShape<NP, PF, TB>;
     using Wd = typename Share<W>::T;
@@ -282,32 +322,33 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, vo
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const MvArgs& a = e.second;
-    const int64_t tile = blockIdx.x;
+    const int split = blockIdx.x % splits, wave = split * NW + w, all = splits * NW;
+    const int64_t tile0 = (int64_t)(blockIdx.x / splits) * R;
     const int live = __builtin_amdgcn_readfirstlane(e.named[0]);
     int16_t* map = reinterpret_cast<int16_t*>(lds + NW * Sh::kBytes);  // [live][TB]
     const int32_t* from = e.named + 1 + e.slots;
     for (int i = threadIdx.x; i < live * TB; i += 64 * NW) map[i] = (int16_t)from[i / TB * 16 + i % TB];
     __syncthreads();
     const int nc = (int)a.nc, total = live * nc;
-    const int mine = total > w ? (total - w + NW - 1) / NW : 0;
+    const int mine = total > wave ? (total - wave + all - 1) / all : 0;
     struct At {
         int slot, chunk;
     };
     const auto ahead = [&](At p) __attribute__((always_inline)) {  // the wave's next chunk; past the last, the last
-        p.chunk += NW;
+        p.chunk += all;
         while (p.chunk >= nc) {
             p.chunk -= nc;
             ++p.slot;
         }
         return p;
     };
-    float sum[4] = {};
+    float sum[R][4] = {};
     if (mine > 0) {
         char* xs = lds + w * Sh::kBytes;
         u32x4 x[Sh::kUnits];
         uint32_t some = 0;  // units whose token names the expert
         At next[PF];
-        next[0] = At{w / nc, w % nc};
+        next[0] = At{wave / nc, wave % nc};
 #pragma unroll
         for (int p = 1; p < PF; ++p) next[p] = ahead(next[p - 1]);
         const auto clamp = [&](At p) __attribute__((always_inline)) { return p.slot < live ? p : At{live - 1, nc - 1}; };
@@ -331,17 +372,21 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, vo
                                                        c.chunk * 256 + u * 16);
             }
         };
-        Wd d[PF];
-        float s[PF][kScales];
+        Wd d[PF][R];
+        float s[PF][R][kScales];
         const auto fetch = [&](int p) __attribute__((always_inline)) {
             const At c = clamp(next[p]);
             const int expert = __builtin_amdgcn_readfirstlane(e.named[1 + c.slot]);
             const char* codes = a.codes + expert * e.second_stride;
-            const float* sp = (const float*)((const char*)a.scales + expert * e.second_stride) + tile * a.ngp * 16;
-            d[p] = (reinterpret_cast<const Wd*>(codes) + (tile * a.nc + c.chunk) * 64)[lane];
+            const float* scales = (const float*)((const char*)a.scales + expert * e.second_stride);
 #pragma unroll
-            for (int f = 0; f < kScales; ++f)
-                s[p][f] = (sp + (((int64_t)c.chunk * kScales + f) >> a.gshift) * 16)[lane & 15];
+            for (int r = 0; r < R; ++r) {
+                const int64_t tile = min(tile0 + r, (int64_t)a.tiles - 1);
+                d[p][r] = (reinterpret_cast<const Wd*>(codes) + (tile * a.nc + c.chunk) * 64)[lane];
+#pragma unroll
+                for (int f = 0; f < kScales; ++f)
+                    s[p][r][f] = (scales + (tile * a.ngp + (((int64_t)c.chunk * kScales + f) >> a.gshift)) * 16)[lane & 15];
+            }
         };
         load();
 #pragma unroll
@@ -368,7 +413,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, vo
                 if (i0 + p < mine)
 #pragma unroll
                     for (int f = 0; f < kScales; ++f) {
-                        f32x4 acc = {};
+                        f32x4 acc[R] = {};
 #pragma unroll
                         for (int j = 0; j < FS; ++j) {
                             bf16x8 v[NP];
@@ -377,12 +422,17 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, vo
                                 v[q] = *reinterpret_cast<const bf16x8*>(xl + (NP - 1 - q) * Sh::kPiece + p * 256 + (f * FS + j) * 64);
                                 asm("" : "+v"(after) : "v"(v[q]));
                             }
-                            const bf16x8 b = weights<kBF16, W>(d[p], f * FS + j);
 #pragma unroll
-                            for (int q = 0; q < NP; ++q) acc = M::mma(v[q], b, acc);
+                            for (int r = 0; r < R; ++r) {
+                                const bf16x8 b = weights<kBF16, W>(d[p][r], f * FS + j);
+#pragma unroll
+                                for (int q = 0; q < NP; ++q) acc[r] = M::mma(v[q], b, acc[r]);
+                            }
                         }
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) sum[v] = fmaf(s[p][f], acc[v], sum[v]);
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) sum[r][v] = fmaf(s[p][r][f], acc[r][v], sum[r][v]);
                     }
                 fetch(p);
             }
@@ -390,18 +440,21 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, vo
         }
     }
     __syncthreads();
-    float* red = reinterpret_cast<float*>(lds);  // [wave][token][16 rows + 1]
+    float* red = reinterpret_cast<float*>(lds);  // [wave][tile][token][16 rows + 1]
 #pragma unroll
-    for (int v = 0; v < 4; ++v) red[(w * 16 + 4 * (lane >> 4) + v) * 17 + (lane & 15)] = sum[v];
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[((w * R + r) * 16 + 4 * (lane >> 4) + v) * 17 + (lane & 15)] = sum[r][v];
     __syncthreads();
-    for (int i = threadIdx.x; i < e.T * 16; i += 64 * NW) {
-        const int t = i >> 4;
-        const int64_t row = tile * 16 + (i & 15);
+    for (int i = threadIdx.x; i < e.T * R * 16; i += 64 * NW) {
+        const int t = i / (R * 16), r = i / 16 % R;
+        const int64_t row = (tile0 + r) * 16 + (i & 15);
         if (row >= e.n) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) v += red[(k * 16 + t) * 17 + (i & 15)];
-        store_elem(y, ytype, t * ldy + row, v);
+        for (int k = 0; k < NW; ++k) v += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
+        if (splits > 1) e.part[((int64_t)split * e.T + t) * e.n + row] = v;
+        else store_elem(y, ytype, t * ldy + row, v);
     }
 }
 
@@ -422,28 +475,35 @@ void launch_first_few(const ExpertArgs& e, hipStream_t stream) {
 }
 
 template <int NP, int W, int FS, int TB>
-void launch_second_tokens(const ExpertArgs& e, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_second_tokens(const ExpertArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : NP == 3 ? 1 : 2;
-    const size_t red = sizeof(float) * NW * 16 * 17;
-    const size_t lds = std::max(red, (size_t)NW * SecondShape<NP, PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
-    hipLaunchKernelGGL((k_experts_second_few<NP, W, FS, PF, TB, NW>), dim3(e.second.tiles), dim3(64 * NW), lds, stream, e, y,
-                       ytype, ldy);
+    const auto launch = [&](auto tiles) {
+        constexpr int R = decltype(tiles)::value;
+        const size_t red = sizeof(float) * NW * R * 16 * 17;
+        const size_t lds = std::max(red, (size_t)NW * SecondShape<NP, PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
+        hipLaunchKernelGGL((k_experts_second_few<NP, W, FS, R, PF, TB, NW>), dim3((e.second.tiles + R - 1) / R * splits),
+                           dim3(64 * NW), lds, stream, e, splits, y, ytype, ldy);
+    };
+    if constexpr (TB > 4) {
+        if (splits > 1) return launch(std::integral_constant<int, 4>());
+    }
+    launch(std::integral_constant<int, 1>());
 }
 template <int NP, int W, int FS>
-void launch_second_few(const ExpertArgs& e, void* y, int ytype, int64_t ldy, hipStream_t stream) {
-    if (e.T == 1) launch_second_tokens<NP, W, FS, 1>(e, y, ytype, ldy, stream);
-    else if (e.T <= 4) launch_second_tokens<NP, W, FS, 4>(e, y, ytype, ldy, stream);
-    else if (e.T <= 8) launch_second_tokens<NP, W, FS, 8>(e, y, ytype, ldy, stream);
-    else launch_second_tokens<NP, W, FS, 16>(e, y, ytype, ldy, stream);
+void launch_second_few(const ExpertArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    if (e.T == 1) launch_second_tokens<NP, W, FS, 1>(e, splits, y, ytype, ldy, stream);
+    else if (e.T <= 4) launch_second_tokens<NP, W, FS, 4>(e, splits, y, ytype, ldy, stream);
+    else if (e.T <= 8) launch_second_tokens<NP, W, FS, 8>(e, splits, y, ytype, ldy, stream);
+    else launch_second_tokens<NP, W, FS, 16>(e, splits, y, ytype, ldy, stream);
 }
 template <int NP>
-void launch_experts_second_few(const ExpertArgs& e, int W, int fs, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_experts_second_few(const ExpertArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     if (W == 4) {
-        if (fs == 1) launch_second_few<NP, 4, 1>(e, y, ytype, ldy, stream);
-        else launch_second_few<NP, 4, 4>(e, y, ytype, ldy, stream);
+        if (fs == 1) launch_second_few<NP, 4, 1>(e, splits, y, ytype, ldy, stream);
+        else launch_second_few<NP, 4, 4>(e, splits, y, ytype, ldy, stream);
     } else {
-        if (fs == 1) launch_second_few<NP, 2, 1>(e, y, ytype, ldy, stream);
-        else launch_second_few<NP, 2, 4>(e, y, ytype, ldy, stream);
+        if (fs == 1) launch_second_few<NP, 2, 1>(e, splits, y, ytype, ldy, stream);
+        else launch_second_few<NP, 2, 4>(e, splits, y, ytype, ldy, stream);
     }
 }
 

@@ -115,6 +115,12 @@ def test_launch_shapes(T, E, k, dtype):
     check(T, E, k, 40, 33, 4, 32, 4, 32, dtype, F32, none=0.1, seed=T)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, I8])
+@pytest.mark.parametrize("T,E,k,n,I,dbits,dgroup", [(6, 8, 4, 4099, 2050, 4, 128), (16, 4, 3, 8200, 2048, 2, 64), (9, 4, 4, 4112, 4000, 4, 32)])
+def test_second_product_in_splits(T, E, k, n, I, dbits, dgroup, dtype):
+    check(T, E, k, n, I, 4, 128, dbits, dgroup, dtype, F32, none=0.2, seed=T)
+
+
 @pytest.mark.parametrize("T,k", [(4, 3), (40, 4)])
 def test_padding_repeats_and_empty_rows(T, k):
     """No expert at all, ids on either side of the range, one expert twice in a row."""
