@@ -5,13 +5,18 @@ namespace bk {
 
 // compiled in bk_experts_*.hip, one file for each type of x
 extern template void launch_experts_first<kF32>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first_few<kF32>(const FewArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kF16>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first_few<kF16>(const FewArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kBF16>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first_few<kBF16>(const FewArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first_few<kI8>(const FewArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first_few<kF8>(const FewArgs&, int, int, hipStream_t);
 extern template void launch_experts_second<kF32>(const ExpertArgs&, int, int, hipStream_t);
-extern template void launch_experts_second_few<2>(const ExpertArgs&, int, int, int, void*, int, int64_t, hipStream_t);
-extern template void launch_experts_second_few<3>(const ExpertArgs&, int, int, int, void*, int, int64_t, hipStream_t);
+extern template void launch_experts_second_few<2>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
+extern template void launch_experts_second_few<3>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
 
 namespace {
 
@@ -172,7 +177,7 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     return l;
 }
 
-MvArgs product(const void* packed, const PackShape& p, int64_t m, int64_t n, int64_t group, int* fs) {
+MvArgs layer_args(const void* packed, const PackShape& p, int64_t m, int64_t n, int64_t group, int* fs) {
     MvArgs a = {};
     a.codes = (const char*)packed;
     a.scales = (const float*)((const char*)packed + p.scale_offset);
@@ -212,10 +217,57 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     const PackShape p1 = pack_shape(I, n, bits, group), p2 = pack_shape(n, I, dbits, dgroup);
     const Layout l = layout(T, k, E, n, I);
     char* w = (char*)ws;
+    if (few_tokens(T, k)) {
+        int fs;
+        FewArgs f = {};
+        f.ids = ids;
+        f.weights = weights;
+        f.xs = xs;
+        f.named = (int32_t*)(w + l.named);
+        f.planes = w + l.planes;
+        f.plane = (int32_t)l.plane;
+        f.part = (float*)(w + l.part);
+        f.T = (int32_t)T;
+        f.k = (int32_t)k;
+        f.E = (int32_t)E;
+        f.slots = (int32_t)std::min(E, T * k);
+        f.act = act;
+        const auto product = [&](const void* packed, const PackShape& p, int64_t m, int64_t cols, int64_t g) {
+            const MvArgs a = layer_args(packed, p, m, cols, g, &fs);
+            f.gate = a.codes;
+            f.stride = (int64_t)p.bytes;
+            f.scale_offset = (int64_t)p.scale_offset;
+            f.m = (int32_t)m;
+            f.n = (int32_t)cols;
+            f.tiles = (int32_t)a.tiles;
+            f.nc = (int32_t)a.nc;
+            f.ngp = (int32_t)a.ngp;
+            f.gshift = a.gshift;
+        };
+        product(gate, p1, I, n, group);
+        f.up = (const char*)up;
+        f.x = (const char*)x;
+        f.ldx = ldx;
+        switch (xtype) {
+            case BAKRON_F32: launch_experts_first_few<kF32>(f, p1.W, fs, stream); break;
+            case BAKRON_F16: launch_experts_first_few<kF16>(f, p1.W, fs, stream); break;
+            case BAKRON_BF16: launch_experts_first_few<kBF16>(f, p1.W, fs, stream); break;
+            case BAKRON_I8: launch_experts_first_few<kI8>(f, p1.W, fs, stream); break;
+            default: launch_experts_first_few<kF8>(f, p1.W, fs, stream); break;
+        }
+        product(down, p2, n, I, dgroup);
+        const int splits = second_splits(T, k, E, n, I);
+        if (xtype == BAKRON_F32) launch_experts_second_few<3>(f, p2.W, fs, splits, y, ytype, ldy, stream);
+        else launch_experts_second_few<2>(f, p2.W, fs, splits, y, ytype, ldy, stream);
+        if (splits > 1)
+            hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, f.part, splits,
+                               T, n, y, ytype, ldy);
+        return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
+    }
     ExpertArgs e = {};
     int fs1, fs2;
-    e.first = product(gate, p1, I, n, group, &fs1);
-    e.second = product(down, p2, n, I, dgroup, &fs2);
+    e.first = layer_args(gate, p1, I, n, group, &fs1);
+    e.second = layer_args(down, p2, n, I, dgroup, &fs2);
     e.up_codes = (const char*)up;
     e.up_scales = (const float*)((const char*)up + p1.scale_offset);
     e.first_stride = (int64_t)p1.bytes;
@@ -235,27 +287,6 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     e.second.x = (const char*)e.h;
     e.second.ldx = l.ldh;
     const int64_t xb = xtype == BAKRON_F32 ? 4 : xtype == BAKRON_I8 || xtype == BAKRON_E4M3 ? 1 : 2;
-    if (few_tokens(T, k)) {
-        e.ids = ids;
-        e.pair_weights = weights;
-        e.T = (int)T;
-        e.k = (int)k;
-        e.E = (int)E;
-        e.slots = (int)std::min(E, T * k);
-        e.named = (int32_t*)(w + l.named);
-        e.planes = w + l.planes;
-        e.plane = l.plane;
-        e.first.x = (const char*)x;
-        e.first.xs = xs;
-        launch_first(e, xtype, p1.W, fs1, stream);
-        const int splits = second_splits(T, k, E, n, I);
-        if (xtype == BAKRON_F32) launch_experts_second_few<3>(e, p2.W, fs2, splits, y, ytype, ldy, stream);
-        else launch_experts_second_few<2>(e, p2.W, fs2, splits, y, ytype, ldy, stream);
-        if (splits > 1)
-            hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, e.part, splits,
-                               T, n, y, ytype, ldy);
-        return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
-    }
     const int64_t round = round_tokens(T, k, E, n, I);
     for (int64_t t0 = 0; t0 < T; t0 += round) {
         const int64_t tokens = std::min(round, T - t0), pairs = tokens * k;

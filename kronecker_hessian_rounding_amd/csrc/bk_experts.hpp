@@ -36,18 +36,49 @@ struct ExpertArgs {
     const float* weights;
     float* h;                     // [pair][ldh]
     int64_t ldh;
-    // few tokens
-    const int32_t* ids;
-    const float* pair_weights;
-    int T, k, E, slots;           // slots: experts, or pairs where they are fewer; 0 on the other path
-    int32_t* named;               // the experts that are named: how many, which, and [slot][16] pairs of their tokens or -1
-    char* planes;                 // h as bf16 pieces, largest first: [pair][piece][plane] bytes
-    int64_t plane;
     float* part;                  // [pair][n]
     int64_t n, I;
     int act;
     int most_tiles;               // the list's bound
 };
+
+// Of few tokens: what a workgroup reads first of all, in as few lines as it takes (each is a miss).
+struct FewArgs {
+    const int32_t* ids;
+    const float* weights;
+    const char* gate;             // packed, of expert 0; of the second product its only layer
+    const char* up;
+    const char* x;
+    const float* xs;
+    int32_t* named;               // the experts that are named: how many, which, and [slot][16] pairs of their tokens or -1
+    char* planes;                 // h as bf16 pieces, largest first: [pair][piece][plane] bytes
+    int64_t stride, scale_offset; // bytes from expert to expert, and from a layer's codes to its scales
+    int64_t ldx;
+    int32_t T, k, E, slots;       // slots: experts, or pairs where they are fewer
+    int32_t m, n, tiles, nc, ngp, gshift;
+    int32_t plane, act;
+    float* part;                  // [split][token][m] of the second product
+};
+
+__device__ __forceinline__ MvArgs layer_of(const FewArgs& e, const char* packed, int expert) {
+    MvArgs a;
+    a.codes = packed + expert * e.stride;
+    a.scales = (const float*)(a.codes + e.scale_offset);
+    a.x = e.x;
+    a.xs = nullptr;
+    a.y = nullptr;
+    a.m = e.m;
+    a.n = e.n;
+    a.T = 0;
+    a.ldx = e.ldx;
+    a.ldy = 0;
+    a.nc = e.nc;
+    a.ngp = e.ngp;
+    a.tiles = (uint32_t)e.tiles;
+    a.gshift = e.gshift;
+    a.ytype = 0;
+    return a;
+}
 
 struct Listed {  // token t is row list[t]
     const int32_t* list;
@@ -127,7 +158,7 @@ inline bool few_tokens(int64_t T, int64_t k) { return T <= kFewTokens && T * k <
 
 // The named experts, by one workgroup: an expert's slot is its place among the pairs that are the first to name one.
 // Row `slot` of the map: the leader of each token that names the expert, or -1.
-__device__ __forceinline__ void list_named(const ExpertArgs& e, char* lds) {
+__device__ __forceinline__ void list_named(const FewArgs& e, char* lds) {
     const int pairs = e.T * e.k, threads = blockDim.x, waves = threads / 64;
     int* id = reinterpret_cast<int*>(lds);    // [pairs]
     int* first = id + kFewPairs;                   // [pairs]: the first pair with this pair's id
@@ -191,12 +222,13 @@ __device__ __forceinline__ void store_pieces(char* row, int64_t plane, int64_t i
     }
 }
 
-template <int MATH, int W, int FS, int PF, int TB, int NW>
-__global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
+template <int MATH, int W, int FS, int PF, int TB, int NW, int kWords>  // kWords: words of 64 pairs at most
+__global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
     extern __shared__ __align__(16) char lds[];
-    constexpr int NP = MATH == kF32 ? 3 : 2, kWords = kFewPairs / 64;
+    constexpr int NP = MATH == kF32 ? 3 : 2;
     if (blockIdx.x == gridDim.x - 1) return list_named(e, lds);
-    const int tiles = (int)(e.plane / 32), lane = threadIdx.x & 63;  // with those that pad h
+    const int tiles = e.plane / 32, lane = threadIdx.x & 63;  // with those that pad h
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slot = blockIdx.x / tiles;
     const int64_t tile = blockIdx.x % tiles;
     // lane p of word v holds pair 64 v + p: its id (-1: no expert) and weight
@@ -210,7 +242,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
         if (v < words) {
             const int p = min(64 * v + lane, pairs - 1);
             id[v] = e.ids[p];
-            wt[v] = e.pair_weights[p];
+            wt[v] = e.weights[p];
             if (64 * v + lane >= pairs || id[v] >= e.E) id[v] = -1;
         }
     }
@@ -222,6 +254,11 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
             if (v == slot >> 6) expert = __builtin_amdgcn_readlane(id[v], slot & 63);
         if (expert < 0) return;
     }
+    // the weights' first chunks are on their way before the tokens are known
+    MvArgs a = layer_of(e, e.gate, expert), b = layer_of(e, e.up, expert);
+    Stream<W, FS, 2, PF> st(a, b, tile, lane);
+#pragma unroll
+    for (int p = 0; p < PF; ++p) st.fetch(p, wave + p * NW);
     uint64_t named[kWords + 1];
 #pragma unroll
     for (int v = 0; v < kWords; ++v) {
@@ -269,17 +306,12 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
     }
     pair = __shfl(pair, token);
     weight = __shfl(weight, token);
-    float xs = e.first.xs && lane < count ? e.first.xs[token] : 1.0f;
-    const bool real = tile < e.first.tiles;
+    float xs = e.xs && lane < count ? e.xs[token] : 1.0f;
+    const bool real = tile < e.tiles;
     if (real) {
-        MvArgs a = e.first, b = e.first;
-        a.codes += expert * e.first_stride;
-        a.scales = (const float*)((const char*)a.scales + expert * e.first_stride);
-        b.codes = e.up_codes + expert * e.first_stride;
-        b.scales = (const float*)((const char*)e.up_scales + expert * e.first_stride);
         a.T = count;
         const auto rows = [&](int64_t t) { return (int64_t)__shfl(token, (int)t); };
-        few_products<MATH, W, FS, 2, PF, TB, NW>(a, Stream<W, FS, 2, PF>(a, b, tile, lane), rows, lds);
+        few_products<MATH, W, FS, 2, PF, TB, NW, true>(a, st, rows, lds);
     }
     const float* red = reinterpret_cast<const float*>(lds);
     for (int i0 = 0; i0 < count * 16; i0 += 64 * NW) {
@@ -289,7 +321,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(ExpertArgs e) {
         const float w = __shfl(weight, t & 63), s = unit<MATH, W>() * __shfl(xs, t & 63);
         if (i >= count * 16) continue;
         float h = 0.0f;
-        if (row < e.I) {
+        if (row < e.m) {
             float g = 0.0f, u = 0.0f;
 #pragma unroll
             for (int k = 0; k < NW; ++k) {
@@ -314,27 +346,20 @@ struct SecondShape {
 };
 
 template <int NP, int W, int FS, int R, int PF, int TB, int NW>
-__global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, int splits, void* y, int ytype, int64_t ldy) {
+__global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int splits, void* y, int ytype, int64_t ldy) {
     using M = Mt<kBF16>;
     using Sh = SecondShape<NP, PF, TB>;
     using Wd = typename Share<W>::T;
     constexpr int kScales = kSteps / FS;
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const MvArgs& a = e.second;
     const int split = blockIdx.x % splits, wave = split * NW + w, all = splits * NW;
     const int64_t tile0 = (int64_t)(blockIdx.x / splits) * R;
-    const int live = __builtin_amdgcn_readfirstlane(e.named[0]);
-    int16_t* map = reinterpret_cast<int16_t*>(lds + NW * Sh::kBytes);  // [live][TB]
-    const int32_t* from = e.named + 1 + e.slots;
-    for (int i = threadIdx.x; i < live * TB; i += 64 * NW) map[i] = (int16_t)from[i / TB * 16 + i % TB];
-    __syncthreads();
-    const int nc = (int)a.nc, total = live * nc;
-    const int mine = total > wave ? (total - wave + all - 1) / all : 0;
+    const int nc = e.nc;
     struct At {
         int slot, chunk;
     };
-    const auto ahead = [&](At p) __attribute__((always_inline)) {  // the wave's next chunk; past the last, the last
+    const auto ahead = [&](At p) __attribute__((always_inline)) {  // the wave's next chunk
         p.chunk += all;
         while (p.chunk >= nc) {
             p.chunk -= nc;
@@ -342,16 +367,42 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, in
         }
         return p;
     };
+    At next[PF];
+    next[0] = At{wave / nc, wave % nc};
+#pragma unroll
+    for (int p = 1; p < PF; ++p) next[p] = ahead(next[p - 1]);
+    Wd d[PF][R];
+    float s[PF][R][kScales];
+    // (behind the named experts' last chunk: some expert's, and never used)
+    const auto fetch = [&](int p) __attribute__((always_inline)) {
+        const int id = __builtin_amdgcn_readfirstlane(e.named[1 + min(next[p].slot, e.slots - 1)]);
+        const char* codes = e.gate + min(max(id, 0), e.E - 1) * e.stride;
+        const float* scales = (const float*)(codes + e.scale_offset);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t tile = min(tile0 + r, (int64_t)e.tiles - 1);
+            d[p][r] = (reinterpret_cast<const Wd*>(codes) + (tile * nc + next[p].chunk) * 64)[lane];
+#pragma unroll
+            for (int f = 0; f < kScales; ++f)
+                s[p][r][f] = (scales + (tile * e.ngp + (((int64_t)next[p].chunk * kScales + f) >> e.gshift)) * 16)[lane & 15];
+        }
+    };
+    const int32_t* from = e.named + 1 + e.slots;
+    int16_t* map = reinterpret_cast<int16_t*>(lds + NW * Sh::kBytes);  // [slots][TB], -1 behind the named ones
+    const int live = __builtin_amdgcn_readfirstlane(e.named[0]);
+#pragma unroll
+    for (int p = 0; p < PF; ++p) fetch(p);
+    for (int i = threadIdx.x; i < e.slots * TB; i += 64 * NW) {
+        const int pair = from[i / TB * 16 + i % TB];
+        map[i] = (int16_t)(i / TB < live ? pair : -1);
+    }
+    __syncthreads();
+    const int total = live * nc, mine = total > wave ? (total - wave + all - 1) / all : 0;
     float sum[R][4] = {};
     if (mine > 0) {
         char* xs = lds + w * Sh::kBytes;
         u32x4 x[Sh::kUnits];
         uint32_t some = 0;  // units whose token names the expert
-        At next[PF];
-        next[0] = At{wave / nc, wave % nc};
-#pragma unroll
-        for (int p = 1; p < PF; ++p) next[p] = ahead(next[p - 1]);
-        const auto clamp = [&](At p) __attribute__((always_inline)) { return p.slot < live ? p : At{live - 1, nc - 1}; };
         // unit of this lane: 16 bytes `u` of a piece of a token's row in chunk p of the set
         const auto load = [&]() __attribute__((always_inline)) {
             some = 0;
@@ -359,38 +410,19 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, in
             for (int i = 0; i < Sh::kUnits; ++i) {
                 const int v = lane + 64 * i, u = v % 16, piece = v / 16 % NP, p = v / (16 * NP) % PF;
                 const int token = min(v / (16 * NP * PF), TB - 1);
-                At c = clamp(next[0]);
+                At c = next[0];
 #pragma unroll
                 for (int k = 1; k < PF; ++k) {
-                    const At n = clamp(next[k]);
-                    c.slot = p == k ? n.slot : c.slot;
-                    c.chunk = p == k ? n.chunk : c.chunk;
+                    c.slot = p == k ? next[k].slot : c.slot;
+                    c.chunk = p == k ? next[k].chunk : c.chunk;
                 }
-                const int pair = map[c.slot * TB + token];
+                const int pair = map[min(c.slot, e.slots - 1) * TB + token];
                 some |= (uint32_t)(pair >= 0) << i;
                 x[i] = *reinterpret_cast<const u32x4*>(e.planes + ((int64_t)max(pair, 0) * NP + piece) * e.plane +
                                                        c.chunk * 256 + u * 16);
             }
         };
-        Wd d[PF][R];
-        float s[PF][R][kScales];
-        const auto fetch = [&](int p) __attribute__((always_inline)) {
-            const At c = clamp(next[p]);
-            const int expert = __builtin_amdgcn_readfirstlane(e.named[1 + c.slot]);
-            const char* codes = a.codes + expert * e.second_stride;
-            const float* scales = (const float*)((const char*)a.scales + expert * e.second_stride);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int64_t tile = min(tile0 + r, (int64_t)a.tiles - 1);
-                d[p][r] = (reinterpret_cast<const Wd*>(codes) + (tile * a.nc + c.chunk) * 64)[lane];
-#pragma unroll
-                for (int f = 0; f < kScales; ++f)
-                    s[p][r][f] = (scales + (tile * a.ngp + (((int64_t)c.chunk * kScales + f) >> a.gshift)) * 16)[lane & 15];
-            }
-        };
         load();
-#pragma unroll
-        for (int p = 0; p < PF; ++p) fetch(p);
         const char* xl = xs + min(lane & 15, TB - 1) * Sh::kPitch + (lane >> 4) * 16;
         int after = 0;  // as in few_products: keeps a set's writes behind the reads of the set before
         for (int i0 = 0; i0 < mine; i0 += PF) {
@@ -449,39 +481,56 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(ExpertArgs e, in
     for (int i = threadIdx.x; i < e.T * R * 16; i += 64 * NW) {
         const int t = i / (R * 16), r = i / 16 % R;
         const int64_t row = (tile0 + r) * 16 + (i & 15);
-        if (row >= e.n) continue;
+        if (row >= e.m) continue;
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) v += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
-        if (splits > 1) e.part[((int64_t)split * e.T + t) * e.n + row] = v;
+        if (splits > 1) e.part[((int64_t)split * e.T + t) * e.m + row] = v;
         else store_elem(y, ytype, t * ldy + row, v);
     }
 }
 
 template <int MATH, int W, int FS, int TB>
-void launch_first_tokens(const ExpertArgs& e, hipStream_t stream) {
-    constexpr int NW = 8, PF = TB <= 4 ? 8 / W : MATH == kF32 ? 1 : 2;
+void launch_first_tokens(const FewArgs& e, hipStream_t stream) {
+    constexpr int NW = 4, PF = TB <= 4 ? 16 / W : 1;
     constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17, list = sizeof(int) * (3 * kFewPairs + NW);
     constexpr size_t lds = std::max<size_t>({(size_t)NW * FewShape<MATH, PF, TB>::kBytes, red, list});
     const unsigned grid = (unsigned)(e.slots * (e.plane / 32) + 1);
-    hipLaunchKernelGGL((k_experts_first_few<MATH, W, FS, PF, TB, NW>), dim3(grid), dim3(64 * NW), lds, stream, e);
+    if constexpr (TB > 1) {
+        if (e.T * e.k > 64) {
+            hipLaunchKernelGGL((k_experts_first_few<MATH, W, FS, PF, TB, NW, kFewPairs / 64>), dim3(grid), dim3(64 * NW), lds,
+                               stream, e);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_experts_first_few<MATH, W, FS, PF, TB, NW, 1>), dim3(grid), dim3(64 * NW), lds, stream, e);
 }
 template <int MATH, int W, int FS>
-void launch_first_few(const ExpertArgs& e, hipStream_t stream) {
+void launch_first_few(const FewArgs& e, hipStream_t stream) {
     if (e.T == 1) launch_first_tokens<MATH, W, FS, 1>(e, stream);
     else if (e.T <= 4) launch_first_tokens<MATH, W, FS, 4>(e, stream);
     else if (e.T <= 8) launch_first_tokens<MATH, W, FS, 8>(e, stream);
     else launch_first_tokens<MATH, W, FS, 16>(e, stream);
 }
+template <int MATH>
+void launch_experts_first_few(const FewArgs& e, int W, int fs, hipStream_t stream) {
+    if (W == 4) {
+        if (fs == 1) launch_first_few<MATH, 4, 1>(e, stream);
+        else launch_first_few<MATH, 4, 4>(e, stream);
+    } else {
+        if (fs == 1) launch_first_few<MATH, 2, 1>(e, stream);
+        else launch_first_few<MATH, 2, 4>(e, stream);
+    }
+}
 
 template <int NP, int W, int FS, int TB>
-void launch_second_tokens(const ExpertArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_second_tokens(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : NP == 3 ? 1 : 2;
     const auto launch = [&](auto tiles) {
         constexpr int R = decltype(tiles)::value;
         const size_t red = sizeof(float) * NW * R * 16 * 17;
         const size_t lds = std::max(red, (size_t)NW * SecondShape<NP, PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
-        hipLaunchKernelGGL((k_experts_second_few<NP, W, FS, R, PF, TB, NW>), dim3((e.second.tiles + R - 1) / R * splits),
+        hipLaunchKernelGGL((k_experts_second_few<NP, W, FS, R, PF, TB, NW>), dim3((unsigned)((e.tiles + R - 1) / R * splits)),
                            dim3(64 * NW), lds, stream, e, splits, y, ytype, ldy);
     };
     if constexpr (TB > 4) {
@@ -490,14 +539,14 @@ void launch_second_tokens(const ExpertArgs& e, int splits, void* y, int ytype, i
     launch(std::integral_constant<int, 1>());
 }
 template <int NP, int W, int FS>
-void launch_second_few(const ExpertArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_second_few(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     if (e.T == 1) launch_second_tokens<NP, W, FS, 1>(e, splits, y, ytype, ldy, stream);
     else if (e.T <= 4) launch_second_tokens<NP, W, FS, 4>(e, splits, y, ytype, ldy, stream);
     else if (e.T <= 8) launch_second_tokens<NP, W, FS, 8>(e, splits, y, ytype, ldy, stream);
     else launch_second_tokens<NP, W, FS, 16>(e, splits, y, ytype, ldy, stream);
 }
 template <int NP>
-void launch_experts_second_few(const ExpertArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     if (W == 4) {
         if (fs == 1) launch_second_few<NP, 4, 1>(e, splits, y, ytype, ldy, stream);
         else launch_second_few<NP, 4, 4>(e, splits, y, ytype, ldy, stream);
@@ -511,7 +560,6 @@ void launch_experts_second_few(const ExpertArgs& e, int W, int fs, int splits, v
 
 template <int MATH, int W, int FS>
 void launch_first_shape(const ExpertArgs& e, hipStream_t stream) {
-    if (e.slots) return launch_first_few<MATH, W, FS>(e, stream);
     constexpr int NW = 8, TB = kExpertTokens, PF = MATH == kF32 ? 1 : 2;
     constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17;
     constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, TB>::kBytes, red);

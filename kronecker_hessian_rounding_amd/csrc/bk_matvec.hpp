@@ -324,7 +324,8 @@ struct EveryRow {  // token t is row t
     __device__ __forceinline__ int64_t operator()(int64_t t) const { return t; }
 };
 
-template <int MATH, int W, int FS, int R, int PF, int TB, int NW, typename Rows>
+// kFetched: the wave's first PF chunks of `st` are fetched already.
+template <int MATH, int W, int FS, int R, int PF, int TB, int NW, bool kFetched = false, typename Rows>
 __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, PF> st, const Rows& rows, char* lds) {
     using M = Mt<MATH>;
     using St = Stream<W, FS, R, PF>;
@@ -355,8 +356,9 @@ __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, P
         for (int i = 0; i < Sh::kUnits; ++i) __builtin_memcpy(&x[i], row_of[i] + min(byte_of(i, i0), most), 16);
     };
     load(0);
+    if constexpr (!kFetched)
 #pragma unroll
-    for (int p = 0; p < PF; ++p) st.fetch(p, w + p * NW);
+        for (int p = 0; p < PF; ++p) st.fetch(p, w + p * NW);
     float sum[R][4] = {};
     const char* xl = xs + min((lane & 15), T - 1) * Sh::kPitch + (lane >> 4) * 8 * Sh::kL;
     // 0, but known to the compiler only as made from every operand read so far: a set's writes, whose addresses it is
