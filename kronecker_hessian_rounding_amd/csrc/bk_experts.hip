@@ -4,17 +4,18 @@
 namespace bk {
 
 // compiled in bk_experts_*.hip, one file for each type of x
-extern template void launch_experts_first<kF32>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kF32>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_first_few<kF32>(const FewArgs&, int, int, hipStream_t);
-extern template void launch_experts_first<kF16>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kF16>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_first_few<kF16>(const FewArgs&, int, int, hipStream_t);
-extern template void launch_experts_first<kBF16>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kBF16>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_first_few<kBF16>(const FewArgs&, int, int, hipStream_t);
-extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_first_few<kI8>(const FewArgs&, int, int, hipStream_t);
-extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_first_few<kF8>(const FewArgs&, int, int, hipStream_t);
-extern template void launch_experts_second<kF32>(const ExpertArgs&, int, int, hipStream_t);
+extern template void launch_experts_second<kH2>(const ExpertArgs&, int, int, int, hipStream_t);
+extern template void launch_experts_second<kH3>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_second_few<2>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
 extern template void launch_experts_second_few<3>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
 
@@ -136,22 +137,22 @@ int second_splits(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
 int64_t round_tokens(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     int64_t t = std::max<int64_t>(1, std::min(T, ((int64_t)1 << 14) / k));
     const int64_t tiles = (std::max(n, I) + kRowTile - 1) / kRowTile;
-    while (t > 1 && tiles * (std::min(E, t * k) + t * k / kExpertTokens) * kMvThreads >= (int64_t)1 << 32) t /= 2;
+    while (t > 1 && (tiles + 8) * (std::min(E, t * k) + t * k / kListFew) * 256 >= (int64_t)1 << 32) t /= 2;
     return t;
 }
 
 struct Layout {
-    size_t used, list, tokens, pair, weight, h, part;  // more tokens
-    size_t named, planes;                              // few
+    size_t planes, part;
+    size_t used, list, tokens, pair, weight;  // more tokens
+    size_t named;                             // few
     size_t bytes;
-    int64_t ldh, plane, most;
+    int64_t plane, most;
 };
 Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     const int64_t t = round_tokens(T, k, E, n, I), p = t * k;
     Layout l = {};
     l.plane = (I + kChunk - 1) / kChunk * kChunk * 2;
-    l.most = std::min(E, p) + p / kExpertTokens;
-    l.ldh = (I + 3) / 4 * 4;
+    l.most = std::min(E, p) + p / kListFew;
     size_t at = 0;
     const auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -171,7 +172,7 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     l.tokens = take(4 * p);
     l.pair = take(4 * p);
     l.weight = take(4 * p);
-    l.h = take(4 * p * l.ldh);
+    l.planes = take(3 * l.plane * p);
     l.part = take(4 * p * n);
     l.bytes = at;
     return l;
@@ -196,13 +197,13 @@ MvArgs layer_args(const void* packed, const PackShape& p, int64_t m, int64_t n, 
     return a;
 }
 
-void launch_first(const ExpertArgs& e, int xtype, int W, int fs, hipStream_t stream) {
+void launch_first(const ExpertArgs& e, int tile, int xtype, int W, int fs, hipStream_t stream) {
     switch (xtype) {
-        case BAKRON_F32: launch_experts_first<kF32>(e, W, fs, stream); break;
-        case BAKRON_F16: launch_experts_first<kF16>(e, W, fs, stream); break;
-        case BAKRON_BF16: launch_experts_first<kBF16>(e, W, fs, stream); break;
-        case BAKRON_I8: launch_experts_first<kI8>(e, W, fs, stream); break;
-        default: launch_experts_first<kF8>(e, W, fs, stream); break;
+        case BAKRON_F32: launch_experts_first<kF32>(e, tile, W, fs, stream); break;
+        case BAKRON_F16: launch_experts_first<kF16>(e, tile, W, fs, stream); break;
+        case BAKRON_BF16: launch_experts_first<kBF16>(e, tile, W, fs, stream); break;
+        case BAKRON_I8: launch_experts_first<kI8>(e, tile, W, fs, stream); break;
+        default: launch_experts_first<kF8>(e, tile, W, fs, stream); break;
     }
 }
 
@@ -217,6 +218,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     const PackShape p1 = pack_shape(I, n, bits, group), p2 = pack_shape(n, I, dbits, dgroup);
     const Layout l = layout(T, k, E, n, I);
     char* w = (char*)ws;
+    const int pieces = ytype == BAKRON_F32 ? 3 : 2;
     if (few_tokens(T, k)) {
         int fs;
         FewArgs f = {};
@@ -232,6 +234,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         f.E = (int32_t)E;
         f.slots = (int32_t)std::min(E, T * k);
         f.act = act;
+        f.pieces = pieces;
         const auto product = [&](const void* packed, const PackShape& p, int64_t m, int64_t cols, int64_t g) {
             const MvArgs a = layer_args(packed, p, m, cols, g, &fs);
             f.gate = a.codes;
@@ -257,7 +260,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         }
         product(down, p2, n, I, dgroup);
         const int splits = second_splits(T, k, E, n, I);
-        if (xtype == BAKRON_F32) launch_experts_second_few<3>(f, p2.W, fs, splits, y, ytype, ldy, stream);
+        if (pieces == 3) launch_experts_second_few<3>(f, p2.W, fs, splits, y, ytype, ldy, stream);
         else launch_experts_second_few<2>(f, p2.W, fs, splits, y, ytype, ldy, stream);
         if (splits > 1)
             hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, f.part, splits,
@@ -277,27 +280,32 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     e.tokens = (const int32_t*)(w + l.tokens);
     e.pairs = (const int32_t*)(w + l.pair);
     e.weights = (const float*)(w + l.weight);
-    e.h = (float*)(w + l.h);
-    e.ldh = l.ldh;
+    e.planes = w + l.planes;
+    e.plane = l.plane;
+    e.pieces = pieces;
     e.part = (float*)(w + l.part);
     e.n = n;
     e.I = I;
     e.act = act;
     e.first.ldx = ldx;
-    e.second.x = (const char*)e.h;
-    e.second.ldx = l.ldh;
+    e.second.x = e.planes;
+    e.second.n = l.plane / 2;  // zeros behind I
+    e.second.ldx = pieces * l.plane / 2;
     const int64_t xb = xtype == BAKRON_F32 ? 4 : xtype == BAKRON_I8 || xtype == BAKRON_E4M3 ? 1 : 2;
     const int64_t round = round_tokens(T, k, E, n, I);
     for (int64_t t0 = 0; t0 < T; t0 += round) {
         const int64_t tokens = std::min(round, T - t0), pairs = tokens * k;
         e.first.x = (const char*)x + t0 * ldx * xb;
         e.first.xs = xs ? xs + t0 : nullptr;
-        e.most_tiles = (int)(std::min(E, pairs) + pairs / kExpertTokens);
-        PlanArgs p = {ids + t0 * k, weights + t0 * k, pairs, (int)k, (int)E, kExpertTokens, (int32_t*)(w + l.used),
+        // tiles of 64 tokens where an expert has more than 16 on average
+        const int tile = pairs > kListFew * std::min(E, pairs) ? kListMany : kListFew;
+        e.most_tiles = (int)(std::min(E, pairs) + pairs / tile);
+        PlanArgs p = {ids + t0 * k, weights + t0 * k, pairs, (int)k, (int)E, tile, (int32_t*)(w + l.used),
                       (ExpertTile*)(w + l.list), (int32_t*)(w + l.tokens), (int32_t*)(w + l.pair), (float*)(w + l.weight)};
         hipLaunchKernelGGL(k_experts_plan, dim3(1), dim3(1024), 0, stream, p);
-        launch_first(e, xtype, p1.W, fs1, stream);
-        launch_experts_second<kF32>(e, p2.W, fs2, stream);
+        launch_first(e, tile, xtype, p1.W, fs1, stream);
+        if (pieces == 3) launch_experts_second<kH3>(e, tile, p2.W, fs2, stream);
+        else launch_experts_second<kH2>(e, tile, p2.W, fs2, stream);
         SumArgs s = {ids + t0 * k, e.part, (char*)y + t0 * ldy * (ytype == BAKRON_F32 ? 4 : 2), tokens, n, ldy, (int)k, (int)E, ytype};
         hipLaunchKernelGGL(k_experts_sum, dim3((unsigned)(tokens * ((n + 1023) / 1024))), dim3(256), 0, stream, s);
     }

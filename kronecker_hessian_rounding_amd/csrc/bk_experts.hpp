@@ -34,11 +34,11 @@ struct ExpertArgs {
     const int32_t* tokens;        // of each leader, in the order of the list
     const int32_t* pairs;
     const float* weights;
-    float* h;                     // [pair][ldh]
-    int64_t ldh;
+    char* planes;                 // h as bf16 pieces, largest first: [pair][piece][plane] bytes
+    int64_t plane;
     float* part;                  // [pair][n]
     int64_t n, I;
-    int act;
+    int act, pieces;
     int most_tiles;               // the list's bound
 };
 
@@ -51,12 +51,12 @@ struct FewArgs {
     const char* x;
     const float* xs;
     int32_t* named;               // the experts that are named: how many, which, and [slot][16] pairs of their tokens or -1
-    char* planes;                 // h as bf16 pieces, largest first: [pair][piece][plane] bytes
+    char* planes;                 // h as bf16 pieces: [pair][piece][plane] bytes
     int64_t stride, scale_offset; // bytes from expert to expert, and from a layer's codes to its scales
     int64_t ldx;
     int32_t T, k, E, slots;       // slots: experts, or pairs where they are fewer
     int32_t m, n, tiles, nc, ngp, gshift;
-    int32_t plane, act;
+    int32_t plane, act, pieces;
     float* part;                  // [split][token][m] of the second product
 };
 
@@ -91,65 +91,28 @@ __device__ __forceinline__ float activation(float v, int act) {
     return v / (1.0f + expf(-z));
 }
 
-template <int MATH, int W, int FS, int PF, int TB, int NW>
-__global__ __launch_bounds__(64 * NW) void k_experts_first(ExpertArgs e) {
-    extern __shared__ __align__(16) char lds[];
-    const uint32_t li = blockIdx.x / e.first.tiles, tile = blockIdx.x % e.first.tiles;
-    if ((int)li >= *e.tiles_used) return;
-    const ExpertTile l = e.list[li];
-    MvArgs a = e.first, b = e.first;
-    a.codes += l.expert * e.first_stride;
-    a.scales = (const float*)((const char*)a.scales + l.expert * e.first_stride);
-    b.codes = e.up_codes + l.expert * e.first_stride;
-    b.scales = (const float*)((const char*)e.up_scales + l.expert * e.first_stride);
-    a.T = l.count;
-    few_products<MATH, W, FS, 2, PF, TB, NW>(a, Stream<W, FS, 2, PF>(a, b, tile, threadIdx.x & 63),
-                                             Listed{e.tokens + l.begin}, lds);
-    const float* red = reinterpret_cast<const float*>(lds);
-    for (int i = threadIdx.x; i < l.count * 16; i += 64 * NW) {
-        const int t = i >> 4, r = i & 15;
-        const int64_t row = (int64_t)tile * 16 + r;
-        if (row >= e.I) continue;
-        float g = 0.0f, u = 0.0f;
+// h between the products: bf16 pieces, the largest first, of which all but the last are cut off and the last is rounded.
+// Three hold 25 bits of h, for a y in fp32; two hold 17, for a y of 16 bits, whose own rounding is 2^5 to 2^8 times
+// theirs. (A third piece is a third more MFMAs and reads of h.) An infinity or NaN stays in the first.
+template <int N>
+__device__ __forceinline__ void store_pieces(char* row, int64_t plane, int pieces, int64_t i, const float (&h)[N]) {
+    float r[N];
 #pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            g += red[((k * 2) * 16 + t) * 17 + r];
-            u += red[((k * 2 + 1) * 16 + t) * 17 + r];
+    for (int e = 0; e < N; ++e) r[e] = h[e];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        if (p >= pieces) break;
+        uint16_t b[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            if (p == pieces - 1) b[e] = __builtin_bit_cast(uint16_t, (__bf16)r[e]);
+            else b[e] = (uint16_t)(__float_as_uint(__builtin_canonicalizef(r[e])) >> 16);
+            const float left = r[e] - __uint_as_float((uint32_t)b[e] << 16);
+            r[e] = left == left ? left : 0.0f;
         }
-        const float s = unit<MATH, W>() * (a.xs ? a.xs[e.tokens[l.begin + t]] : 1.0f);
-        g *= s;
-        u *= s;
-        e.h[(int64_t)e.pairs[l.begin + t] * e.ldh + row] = e.weights[l.begin + t] * (activation(g, e.act) * u);
+        __builtin_memcpy(__builtin_assume_aligned(row + p * plane + 2 * i, 2 * N), b, 2 * N);
     }
 }
-
-template <int MATH, int W, int FS, int R, int PF, int TB, int NW>
-__global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
-    extern __shared__ __align__(16) char lds[];
-    const uint32_t blocks = (e.second.tiles + R - 1) / R;
-    const uint32_t li = blockIdx.x / blocks;
-    const int64_t tile0 = (int64_t)(blockIdx.x % blocks) * R;
-    if ((int)li >= *e.tiles_used) return;
-    const ExpertTile l = e.list[li];
-    MvArgs a = e.second;
-    a.codes += l.expert * e.second_stride;
-    a.scales = (const float*)((const char*)a.scales + l.expert * e.second_stride);
-    a.T = l.count;
-    few_products<MATH, W, FS, R, PF, TB, NW>(a, Stream<W, FS, R, PF>(a, tile0, threadIdx.x & 63),
-                                             Listed{e.pairs + l.begin}, lds);
-    const float* red = reinterpret_cast<const float*>(lds);
-    for (int i = threadIdx.x; i < l.count * R * 16; i += 64 * NW) {
-        const int t = i / (R * 16), r = i / 16 % R;
-        const int64_t row = (tile0 + r) * 16 + (i & 15);
-        if (row >= e.n) continue;
-        float y = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) y += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
-        e.part[(int64_t)e.pairs[l.begin + t] * e.n + row] = y * unit<MATH, W>();
-    }
-}
-
-constexpr int kExpertTokens = 16;  // tokens of a list's tile
 
 // ---------------------------------------------------------------- few tokens
 constexpr int kFewTokens = 16, kFewPairs = 512;  // of the few tokens' path: what LDS holds of the map
@@ -207,25 +170,9 @@ __device__ __forceinline__ void list_named(const FewArgs& e, char* lds) {
         }
 }
 
-// h as NP bf16 pieces whose sum is h to within 2^-17 (two) or 2^-25 (three) of it: all but the last are cut off, the last
-// is rounded. An infinity or NaN stays in the first.
-template <int NP>
-__device__ __forceinline__ void store_pieces(char* row, int64_t plane, int64_t i, float h) {
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        __bf16 b;
-        if (p == NP - 1) b = (__bf16)h;
-        else b = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(__builtin_canonicalizef(h)) >> 16));
-        *reinterpret_cast<__bf16*>(row + p * plane + 2 * i) = b;
-        const float r = h - (float)b;
-        h = r == r ? r : 0.0f;
-    }
-}
-
 template <int MATH, int W, int FS, int PF, int TB, int NW, int kWords>  // kWords: words of 64 pairs at most
 __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
     extern __shared__ __align__(16) char lds[];
-    constexpr int NP = MATH == kF32 ? 3 : 2;
     if (blockIdx.x == gridDim.x - 1) return list_named(e, lds);
     const int tiles = e.plane / 32, lane = threadIdx.x & 63;  // with those that pad h
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -330,7 +277,8 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
             }
             h = w * (activation(g * s, e.act) * (u * s));
         }
-        store_pieces<NP>(e.planes + to * NP * e.plane, e.plane, row, h);
+        const float hh[1] = {h};
+        store_pieces<1>(e.planes + to * e.pieces * e.plane, e.plane, e.pieces, row, hh);
     }
 }
 
@@ -557,44 +505,192 @@ void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void
 }
 
 // ---------------------------------------------------------------- more tokens
-
-template <int MATH, int W, int FS>
-void launch_first_shape(const ExpertArgs& e, hipStream_t stream) {
-    constexpr int NW = 8, TB = kExpertTokens, PF = MATH == kF32 ? 1 : 2;
-    constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17;
-    constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, TB>::kBytes, red);
-    hipLaunchKernelGGL((k_experts_first<MATH, W, FS, PF, TB, NW>), dim3(e.first.tiles * (unsigned)e.most_tiles), dim3(64 * NW),
-                       lds, stream, e);
+// The list's tiles hold at most 16 tokens where an expert has about as few (few_products), else as many as a workgroup of
+// mm_products takes.
+struct FirstTile {
+    MvArgs a, b;
+    ExpertTile l;
+};
+__device__ __forceinline__ FirstTile first_tile(const ExpertArgs& e, uint32_t li) {
+    FirstTile f;
+    f.l = e.list[li];
+    f.a = f.b = e.first;
+    f.a.codes += f.l.expert * e.first_stride;
+    f.a.scales = (const float*)((const char*)f.a.scales + f.l.expert * e.first_stride);
+    f.b.codes = e.up_codes + f.l.expert * e.first_stride;
+    f.b.scales = (const float*)((const char*)e.up_scales + f.l.expert * e.first_stride);
+    f.a.T = f.l.count;
+    return f;
+}
+__device__ __forceinline__ MvArgs second_tile(const ExpertArgs& e, const ExpertTile& l) {
+    MvArgs a = e.second;
+    a.codes += l.expert * e.second_stride;
+    a.scales = (const float*)((const char*)a.scales + l.expert * e.second_stride);
+    a.T = l.count;
+    return a;
 }
 
-template <int MATH>
-void launch_experts_first(const ExpertArgs& e, int W, int fs, hipStream_t stream) {
-    if (W == 4) {
-        if (fs == 1) launch_first_shape<MATH, 4, 1>(e, stream);
-        else launch_first_shape<MATH, 4, 4>(e, stream);
+template <int MATH, int W, int FS, int PF, int NW>
+__global__ __launch_bounds__(64 * NW) void k_experts_first(ExpertArgs e) {
+    extern __shared__ __align__(16) char lds[];
+    const uint32_t tiles = (uint32_t)(e.plane / 32);  // with those that pad h
+    const uint32_t li = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    if ((int)li >= *e.tiles_used) return;
+    const FirstTile f = first_tile(e, li);
+    if (tile < e.first.tiles)
+        few_products<MATH, W, FS, 2, PF, 16, NW>(f.a, Stream<W, FS, 2, PF>(f.a, f.b, tile, threadIdx.x & 63),
+                                                 Listed{e.tokens + f.l.begin}, lds);
+    const float* red = reinterpret_cast<const float*>(lds);
+    for (int i = threadIdx.x; i < f.l.count * 16; i += 64 * NW) {
+        const int t = i >> 4, r = i & 15, at = f.l.begin + t;
+        const int64_t row = (int64_t)tile * 16 + r;
+        float h[1] = {0.0f};
+        if (row < e.I) {
+            float g = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                g += red[((k * 2) * 16 + t) * 17 + r];
+                u += red[((k * 2 + 1) * 16 + t) * 17 + r];
+            }
+            const float s = unit<MATH, W>() * (f.a.xs ? f.a.xs[e.tokens[at]] : 1.0f);
+            h[0] = e.weights[at] * (activation(g * s, e.act) * (u * s));
+        }
+        store_pieces<1>(e.planes + (int64_t)e.pairs[at] * e.pieces * e.plane, e.plane, e.pieces, row, h);
+    }
+}
+
+template <int MATH, int W, int FS, int R, int PF, int NW>
+__global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
+    extern __shared__ __align__(16) char lds[];
+    const uint32_t blocks = (e.second.tiles + R - 1) / R;
+    const uint32_t li = blockIdx.x / blocks;
+    const int64_t tile0 = (int64_t)(blockIdx.x % blocks) * R;
+    if ((int)li >= *e.tiles_used) return;
+    const ExpertTile l = e.list[li];
+    const MvArgs a = second_tile(e, l);
+    few_products<MATH, W, FS, R, PF, 16, NW>(a, Stream<W, FS, R, PF>(a, tile0, threadIdx.x & 63), Listed{e.pairs + l.begin}, lds);
+    const float* red = reinterpret_cast<const float*>(lds);
+    for (int i = threadIdx.x; i < l.count * R * 16; i += 64 * NW) {
+        const int t = i / (R * 16), r = i / 16 % R;
+        const int64_t row = (tile0 + r) * 16 + (i & 15);
+        if (row >= e.n) continue;
+        float y = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) y += red[((k * R + r) * 16 + t) * 17 + (i & 15)];
+        e.part[(int64_t)e.pairs[l.begin + t] * e.n + row] = y;
+    }
+}
+
+// 16 RW rows of G and of U (and so of h) by 16 NT tokens.
+template <int MATH, int W, int FS, int NT, int RW, int CH>
+__global__ __launch_bounds__(64 * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_first_mm(ExpertArgs e) {
+    constexpr int kThreads = 64 * RW, kRows = 16 * RW, kPitch = 2 * kRows + 4;
+    extern __shared__ __align__(16) char lds[];
+    const uint32_t blocks = (uint32_t)((e.plane / 2 + kRows - 1) / kRows);
+    const uint32_t li = blockIdx.x / blocks;
+    const int64_t tile_b = (int64_t)(blockIdx.x % blocks) * RW;
+    if ((int)li >= *e.tiles_used) return;
+    const FirstTile f = first_tile(e, li);
+    const auto stream = [&](int rg, int lane) __attribute__((always_inline)) {
+        return Stream<W, FS, 2, 2>(f.a, f.b, tile_b + rg, lane);
+    };
+    const auto sink = [&](int n0, int toks, const float* red, int) __attribute__((always_inline)) {
+        for (int i = threadIdx.x; i < toks * (kRows / 4); i += kThreads) {
+            const int tok = i / (kRows / 4), r = i % (kRows / 4) * 4;
+            const int t = 16 * n0 + tok, at = f.l.begin + t;
+            const int64_t row = tile_b * 16 + r;
+            if (t >= f.l.count || 2 * row >= e.plane) continue;
+            const float* p = red + tok * kPitch + r / 16 * 32 + r % 16;
+            const f32x4 g = *reinterpret_cast<const f32x4*>(p), u = *reinterpret_cast<const f32x4*>(p + 16);
+            const float s = unit<MATH, W>() * (f.a.xs ? f.a.xs[e.tokens[at]] : 1.0f), w = e.weights[at];
+            float h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = row + k < e.I ? w * (activation(g[k] * s, e.act) * (u[k] * s)) : 0.0f;
+            store_pieces<4>(e.planes + (int64_t)e.pairs[at] * e.pieces * e.plane, e.plane, e.pieces, row, h);
+        }
+    };
+    mm_products<MATH, W, FS, NT, 2, 1, RW, CH>(f.a, 0, Listed{e.tokens + f.l.begin}, stream, lds, sink);
+}
+
+template <int MATH, int W, int FS, int NT, int R, int RW, int CH>
+__global__ __launch_bounds__(64 * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
+    constexpr int kThreads = 64 * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
+    extern __shared__ __align__(16) char lds[];
+    const uint32_t blocks = (e.second.tiles + R * RW - 1) / (R * RW);
+    const uint32_t li = blockIdx.x / blocks;
+    const int64_t tile_b = (int64_t)(blockIdx.x % blocks) * R * RW;
+    if ((int)li >= *e.tiles_used) return;
+    const ExpertTile l = e.list[li];
+    const MvArgs a = second_tile(e, l);
+    const auto stream = [&](int rg, int lane) __attribute__((always_inline)) {
+        return Stream<W, FS, R, 2>(a, tile_b + rg * R, lane);
+    };
+    const auto sink = [&](int n0, int toks, const float* red, int) __attribute__((always_inline)) {
+        for (int i = threadIdx.x; i < toks * (kRows / 4); i += kThreads) {
+            const int tok = i / (kRows / 4), r = i % (kRows / 4) * 4, t = 16 * n0 + tok;
+            const int64_t row = tile_b * 16 + r;
+            if (t >= l.count || row >= e.n) continue;
+            const f32x4 y = *reinterpret_cast<const f32x4*>(red + tok * kPitch + r);
+            store4(e.part, BAKRON_F32, (int64_t)e.pairs[l.begin + t] * e.n + row, y, (int)min<int64_t>(4, e.n - row));
+        }
+    };
+    mm_products<MATH, W, FS, NT, R, 1, RW, CH>(a, 0, Listed{e.pairs + l.begin}, stream, lds, sink);
+}
+
+constexpr int kListFew = 16, kListMany = 64;  // tokens of a list's tile
+
+template <int MATH, int W, int FS>
+void launch_first_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
+    if (tile == kListFew) {
+        constexpr int NW = 4, PF = 1;
+        constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17;
+        constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, 16>::kBytes, red);
+        hipLaunchKernelGGL((k_experts_first<MATH, W, FS, PF, NW>), dim3((unsigned)(e.plane / 32 * e.most_tiles)), dim3(64 * NW),
+                           lds, stream, e);
     } else {
-        if (fs == 1) launch_first_shape<MATH, 2, 1>(e, stream);
-        else launch_first_shape<MATH, 2, 4>(e, stream);
+        constexpr int NT = kListMany / 16, RW = 4, CH = 1;
+        constexpr size_t red = sizeof(float) * 16 * (32 * RW + 4);
+        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, CH>::kBytes, red);
+        const int64_t blocks = (e.plane / 2 + 16 * RW - 1) / (16 * RW);
+        hipLaunchKernelGGL((k_experts_first_mm<MATH, W, FS, NT, RW, CH>), dim3((unsigned)(blocks * e.most_tiles)), dim3(64 * RW), lds,
+                           stream, e);
+    }
+}
+template <int MATH>
+void launch_experts_first(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream) {
+    if (W == 4) {
+        if (fs == 1) launch_first_shape<MATH, 4, 1>(e, tile, stream);
+        else launch_first_shape<MATH, 4, 4>(e, tile, stream);
+    } else {
+        if (fs == 1) launch_first_shape<MATH, 2, 1>(e, tile, stream);
+        else launch_first_shape<MATH, 2, 4>(e, tile, stream);
     }
 }
 
 template <int MATH, int W, int FS>
-void launch_second_shape(const ExpertArgs& e, hipStream_t stream) {
-    constexpr int NW = 8, TB = kExpertTokens, PF = MATH == kF32 ? 1 : 2, R = 2;
-    constexpr size_t red = sizeof(float) * NW * R * 16 * 17;
-    constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, TB>::kBytes, red);
-    hipLaunchKernelGGL((k_experts_second<MATH, W, FS, R, PF, TB, NW>),
-                       dim3((e.second.tiles + R - 1) / R * (unsigned)e.most_tiles), dim3(64 * NW), lds, stream, e);
-}
-
-template <int MATH>
-void launch_experts_second(const ExpertArgs& e, int W, int fs, hipStream_t stream) {
-    if (W == 4) {
-        if (fs == 1) launch_second_shape<MATH, 4, 1>(e, stream);
-        else launch_second_shape<MATH, 4, 4>(e, stream);
+void launch_second_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
+    if (tile == kListFew) {
+        constexpr int NW = 4, PF = 1, R = 2;
+        constexpr size_t red = sizeof(float) * NW * R * 16 * 17;
+        constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, 16>::kBytes, red);
+        hipLaunchKernelGGL((k_experts_second<MATH, W, FS, R, PF, NW>), dim3((e.second.tiles + R - 1) / R * (unsigned)e.most_tiles),
+                           dim3(64 * NW), lds, stream, e);
     } else {
-        if (fs == 1) launch_second_shape<MATH, 2, 1>(e, stream);
-        else launch_second_shape<MATH, 2, 4>(e, stream);
+        constexpr int NT = kListMany / 16, R = 2, RW = 4, CH = 1;
+        constexpr size_t red = sizeof(float) * 16 * (16 * R * RW + 4);
+        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, CH>::kBytes, red);
+        hipLaunchKernelGGL((k_experts_second_mm<MATH, W, FS, NT, R, RW, CH>),
+                           dim3((e.second.tiles + R * RW - 1) / (R * RW) * (unsigned)e.most_tiles), dim3(64 * RW), lds, stream, e);
+    }
+}
+template <int MATH>
+void launch_experts_second(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream) {
+    if (W == 4) {
+        if (fs == 1) launch_second_shape<MATH, 4, 1>(e, tile, stream);
+        else launch_second_shape<MATH, 4, 4>(e, tile, stream);
+    } else {
+        if (fs == 1) launch_second_shape<MATH, 2, 1>(e, tile, stream);
+        else launch_second_shape<MATH, 2, 4>(e, tile, stream);
     }
 }
 

@@ -2,6 +2,6 @@
 #include "bk_experts.hpp"
 
 namespace bk {
-template void launch_experts_first<kF32>(const ExpertArgs&, int, int, hipStream_t);
+template void launch_experts_first<kF32>(const ExpertArgs&, int, int, int, hipStream_t);
 template void launch_experts_first_few<kF32>(const FewArgs&, int, int, hipStream_t);
 }  // namespace bk

@@ -64,14 +64,15 @@ struct MvArgs {
 };
 
 // ---------------------------------------------------------------- operands
-enum Math { kBF16, kF16, kF8, kI8, kF32 };
+enum Math { kBF16, kF16, kF8, kI8, kF32, kH2, kH3 };
 
-// kBytes: of an element of x in memory; kLds: of one (fp32: of a piece of one) in LDS.
+// kBytes: of an element of x in memory; kLds: of one (fp32: of a piece of one) in LDS. kH2 and kH3 are rows that lie
+// in memory as two or three planes of bf16 pieces, the largest first, a.n elements each.
 template <int MATH> struct Mt;
 template <> struct Mt<kBF16> {
     using Op = bf16x8;
     using Acc = f32x4;
-    static constexpr int kBytes = 2, kLds = 2, kPieces = 1;
+    static constexpr int kBytes = 2, kLds = 2, kPieces = 1, kPlanes = 1;
     static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -79,10 +80,16 @@ template <> struct Mt<kBF16> {
 template <> struct Mt<kF32> : Mt<kBF16> {
     static constexpr int kBytes = 4, kPieces = 3;
 };
+template <> struct Mt<kH2> : Mt<kBF16> {
+    static constexpr int kPieces = 2, kPlanes = 2;
+};
+template <> struct Mt<kH3> : Mt<kBF16> {
+    static constexpr int kPieces = 3, kPlanes = 3;
+};
 template <> struct Mt<kF16> {
     using Op = f16x8;
     using Acc = f32x4;
-    static constexpr int kBytes = 2, kLds = 2, kPieces = 1;
+    static constexpr int kBytes = 2, kLds = 2, kPieces = 1, kPlanes = 1;
     static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
@@ -93,7 +100,7 @@ template <> struct Mt<kF8> : Mt<kF16> {
 template <> struct Mt<kI8> {
     using Op = u32x2;
     using Acc = i32x4;
-    static constexpr int kBytes = 1, kLds = 1, kPieces = 1;
+    static constexpr int kBytes = 1, kLds = 1, kPieces = 1, kPlanes = 1;
     static __device__ __forceinline__ Acc mma(Op a, Op b, Acc c) {
         return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0,
                                                      0);
@@ -308,7 +315,8 @@ struct Stream {
 template <int MATH, int PF, int TB>
 struct FewShape {
     static constexpr int kB = Mt<MATH>::kBytes;
-    static constexpr int kRowUnits = PF * kChunk * kB / 16;           // 16-byte units of a token row in a set
+    static constexpr int kPlane = PF * kChunk * kB / 16;              // 16-byte units of a plane of a token row in a set
+    static constexpr int kRowUnits = kPlane * Mt<MATH>::kPlanes;      // of a token row
     static constexpr int kUnits = (TB * kRowUnits + 63) / 64;         // units of a lane
     static constexpr int kPieces = Mt<MATH>::kPieces;
     static constexpr int kL = Mt<MATH>::kLds;
@@ -341,7 +349,7 @@ __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, P
     const auto place_of = [&](int i) { return (lane + i * 64) % Sh::kRowUnits; };
     const auto byte_of = [&](int i, int i0) {
         constexpr int kPer = kChunk * kB / 16;
-        const int u = place_of(i);
+        const int u = place_of(i) % Sh::kPlane;
         return ((i0 + u / kPer) * NW + w) * kChunk * kB + u % kPer * 16;
     };
     // a row below 16 bytes has no whole unit: the loads, whose values are then not used, go elsewhere
@@ -350,7 +358,7 @@ __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, P
     const int most = max(end - 16, 0);
     const char* row_of[Sh::kUnits];
 #pragma unroll
-    for (int i = 0; i < Sh::kUnits; ++i) row_of[i] = xb + rows(min(token_of(i), T - 1)) * ldb;
+    for (int i = 0; i < Sh::kUnits; ++i) row_of[i] = xb + rows(min(token_of(i), T - 1)) * ldb + place_of(i) / Sh::kPlane * (int64_t)end;
     const auto load = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < Sh::kUnits; ++i) __builtin_memcpy(&x[i], row_of[i] + min(byte_of(i, i0), most), 16);
@@ -376,7 +384,7 @@ __device__ __forceinline__ void few_products(const MvArgs& a, Stream<W, FS, R, P
             *reinterpret_cast<u32x4*>(dst + place * 32) = f16_of_e4m3(v[0], v[1]);
             *reinterpret_cast<u32x4*>(dst + place * 32 + 16) = f16_of_e4m3(v[2], v[3]);
         } else {
-            *reinterpret_cast<u32x4*>(dst + place * 16) = v;
+            *reinterpret_cast<u32x4*>(dst + place / Sh::kPlane * Sh::kPiece + place % Sh::kPlane * 16) = v;
         }
     };
     for (int i0 = 0; i0 < mine; i0 += PF) {
@@ -532,26 +540,23 @@ constexpr int mm_pass(int tiles, int each, int room) {
     return n;
 }
 
-template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH>
-__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)))
-void k_matmul(MvArgs a, int token_blocks) {
+// mm_products: tokens t0 .. of a.T, token t the row rows(t) of a.x, by the row tiles that `stream(rg)` of each row group
+// streams. The sums pass through LDS a few token tiles at a time: sink(n0, tokens, red, pass) is called by all threads
+// with token tiles n0 .. there as float [KS][pass][16 R RW + 4], red's columns the rows of row group 0, tile 0 and so on.
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH, typename Rows, typename Streams, typename Sink>
+__device__ __forceinline__ void mm_products(const MvArgs& a, int64_t t0, const Rows& row, const Streams& stream, char* lds,
+                                            const Sink& sink) {
     using M = Mt<MATH>;
     using St = Stream<W, FS, R, 2>;
     constexpr int KC = KS * CH;  // chunks of an iteration
     using Tile = MmTile<MATH, NT, KC>;
     constexpr int kB = M::kBytes, kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
     constexpr int kUnitCols = 16 / (kB == 4 ? 2 : kB);        // columns of a staged unit: 16 bytes of x, fp32 32
-    constexpr int kRowUnits = KC * kChunk / kUnitCols;        // units of a token row in an iteration
-    constexpr int kUnits = 16 * NT * kRowUnits / kThreads;    // units a thread stages
+    constexpr int kRowUnits = KC * kChunk / kUnitCols;        // units of a token row (of each plane) in an iteration
+    constexpr int kPl = M::kPlanes;
+    constexpr int kUnits = 16 * NT * kRowUnits / kThreads * kPl;  // units a thread stages: i % kPl is the plane
     static_assert(16 * NT * kRowUnits % kThreads == 0, "units divide over the threads");
-    extern __shared__ __align__(16) char lds[];
     float* red = reinterpret_cast<float*>(lds);               // [KS][16][kPitch], after the loop
-
-    // workgroups 8 apart share an XCD: give each XCD a run of row blocks, token blocks innermost, so that those
-    // that read the same weights run side by side
-    const uint32_t total = gridDim.x, per = total / 8, extra = total % 8;
-    const uint32_t xcd = blockIdx.x % 8, id = xcd * per + min(xcd, extra) + blockIdx.x / 8;
-    const int64_t tile_b = (int64_t)(id / token_blocks) * R * RW, t0 = (int64_t)(id % token_blocks) * 16 * NT;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kg = wave / RW, rg = wave % RW;
     const int q = lane >> 4, t = lane & 15;
@@ -560,13 +565,12 @@ void k_matmul(MvArgs a, int token_blocks) {
     constexpr int kAhead = KS > 1 && kUnits * kParts <= 6 ? 2 : 1;  // iterations that x is fetched ahead: few
                                                                    // workgroups hide less, and registers allow
     u32x4 raw[kAhead][kUnits][kParts];
-    // this thread stages unit `un` of the token rows row0 + i kRowStep
+    // this thread stages unit `un` of the token rows row0 + i kRowStep, of every plane
     constexpr int kRowStep = kThreads / kRowUnits;
     static_assert(kThreads % kRowUnits == 0, "a thread keeps its unit");
     const int row0 = threadIdx.x / kRowUnits, un = threadIdx.x % kRowUnits;
-    const int end = (int)a.n * kB;  // bytes of a row
+    const int end = (int)a.n * kB;  // bytes of a row (of a plane)
     const int64_t ldb = a.ldx * kB;
-    const char* x0 = a.x + t0 * ldb;
     const int last_row = (int)min<int64_t>(16 * NT, a.T - t0) - 1;
     // rows past the last token repeat it, units past the row's end its last one; a row shorter than a unit has no
     // whole one: the loads, whose values are then not used, go elsewhere
@@ -574,7 +578,7 @@ void k_matmul(MvArgs a, int token_blocks) {
     const char* rows[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-        rows[i] = some ? x0 + min(row0 + i * kRowStep, last_row) * ldb : a.codes;
+        rows[i] = some ? a.x + row(t0 + min(row0 + i / kPl * kRowStep, last_row)) * ldb + i % kPl * (int64_t)end : a.codes;
     const auto load = [&](int it, u32x4 (&to)[kUnits][kParts]) __attribute__((always_inline)) {
         const int at = min((it * KC * kChunk + un * kUnitCols) * kB, some ? end - 16 * kParts : 0);
 #pragma unroll
@@ -583,7 +587,7 @@ void k_matmul(MvArgs a, int token_blocks) {
             for (int h = 0; h < kParts; ++h) __builtin_memcpy(&to[i][h], rows[i] + at + 16 * h, 16);
     };
     // unit `ru` of a token row's iteration, into its operands' slots
-    const auto put = [&](char* buf, int row, int ru, const u32x4 (&v)[kParts]) __attribute__((always_inline)) {
+    const auto put = [&](char* buf, int row, int ru, int plane, const u32x4 (&v)[kParts]) __attribute__((always_inline)) {
         const int u = ru % (kChunk / kUnitCols), ck = ru / (kChunk / kUnitCols);
         char* dst = buf + (ck * NT + (row >> 4)) * Tile::kSlabs * 1024;
         if constexpr (MATH == kI8) {  // columns 16 u ..: step u / 2, lanes of q = 2 (u % 2) and the next
@@ -613,33 +617,33 @@ void k_matmul(MvArgs a, int token_blocks) {
                 for (int c = 0; c < 3; ++c)  // the smallest piece first into the sum
                     *reinterpret_cast<u32x4*>(dst + (2 - c) * 4096 + at) = u32x4{lo[c][0], lo[c][1], hi[c][0], hi[c][1]};
             } else {
-                *reinterpret_cast<u32x4*>(dst + at) = v[0];
+                *reinterpret_cast<u32x4*>(dst + (kPl - 1 - plane) * 4096 + at) = v[0];
             }
         }
     };
     const auto store = [&](int it, char* buf, const u32x4 (&from)[kUnits][kParts]) __attribute__((always_inline)) {
         // the unit that a row's end cuts, if there is one in this iteration (else -1)
         const int first = it * KC * kChunk * kB, last = end / (16 * kParts) * 16 * kParts;
-        const int cut = end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
+        const int cut = M::kPlanes == 1 && end != last && last >= first && last < first + KC * kChunk * kB ? (last - first) / (16 * kParts) : -1;
         if (first + (un + 1) * 16 * kParts <= end) {
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i * kRowStep, un, from[i]);
+            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i / kPl * kRowStep, un, i % kPl, from[i]);
         } else if (un != cut) {  // past the end
             const u32x4 zero[kParts] = {};
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i * kRowStep, un, zero);
+            for (int i = 0; i < kUnits; ++i) put(buf, row0 + i / kPl * kRowStep, un, i % kPl, zero);
         }
         if (cut >= 0)
-            for (int row = threadIdx.x; row < 16 * NT; row += kThreads) {
-                const char* src = a.x + min(t0 + row, a.T - 1) * a.ldx * kB;
+            for (int r = threadIdx.x; r < 16 * NT; r += kThreads) {
+                const char* src = a.x + row(min(t0 + r, a.T - 1)) * a.ldx * kB;
                 u32x4 v[kParts];
 #pragma unroll
                 for (int h = 0; h < kParts; ++h) v[h] = cut_unit<kB>(src, last + 16 * h, end);
-                put(buf, row, cut, v);
+                put(buf, r, cut, 0, v);
             }
     };
 
-    St st(a, tile_b + rg * R, lane);
+    St st = stream(rg, lane);
     const int iters = (int)((a.nc + KC - 1) / KC);
     load(0, raw[0]);
     st.fetch(0, kg);
@@ -731,20 +735,38 @@ void k_matmul(MvArgs a, int token_blocks) {
                 for (int v = 0; v < 4; ++v)
                     red[(kg * 16 * NP + (n - n0) * 16 + 4 * q + v) * kPitch + (rg * R + r) * 16 + t] = sum[r][n][v];
         __syncthreads();
-        const int toks = 16 * (NP < NT - n0 ? NP : NT - n0);
+        sink(n0, 16 * (NP < NT - n0 ? NP : NT - n0), red, 16 * NP);
+    }
+}
+
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH>
+__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)))
+void k_matmul(MvArgs a, int token_blocks) {
+    constexpr int kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
+    extern __shared__ __align__(16) char lds[];
+    // workgroups 8 apart share an XCD: give each XCD a run of row blocks, token blocks innermost, so that those
+    // that read the same weights run side by side
+    const uint32_t total = gridDim.x, per = total / 8, extra = total % 8;
+    const uint32_t xcd = blockIdx.x % 8, id = xcd * per + min(xcd, extra) + blockIdx.x / 8;
+    const int64_t tile_b = (int64_t)(id / token_blocks) * R * RW, t0 = (int64_t)(id % token_blocks) * 16 * NT;
+    const auto stream = [&](int rg, int lane) __attribute__((always_inline)) {
+        return Stream<W, FS, R, 2>(a, tile_b + rg * R, lane);
+    };
+    const auto sink = [&](int n0, int toks, const float* red, int pass) __attribute__((always_inline)) {
         for (int i = threadIdx.x; i < toks * (kRows / 4); i += kThreads) {
             const int tok = i / (kRows / 4), row = i % (kRows / 4) * 4;
             const int64_t tt = t0 + 16 * n0 + tok, o = tile_b * 16 + row;
             if (tt < a.T && o < a.m) {
                 f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) y += *reinterpret_cast<const f32x4*>(red + (k * 16 * NP + tok) * kPitch + row);
+                for (int k = 0; k < KS; ++k) y += *reinterpret_cast<const f32x4*>(red + (k * pass + tok) * kPitch + row);
                 y *= unit<MATH, W>();
                 if (a.xs) y *= a.xs[tt];
                 store4(a.y, a.ytype, tt * a.ldy + o, y, (int)min<int64_t>(4, a.m - o));
             }
         }
-    }
+    };
+    mm_products<MATH, W, FS, NT, R, KS, RW, CH>(a, t0, EveryRow(), stream, lds, sink);
 }
 
 template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH = 1>
