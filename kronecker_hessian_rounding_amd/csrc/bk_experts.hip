@@ -44,39 +44,57 @@ struct PlanArgs {
 
 // One workgroup: leaders counted by expert, the counts' running sums, then each leader to its place (the order
 // within an expert's list is that in which they come, and nothing depends on it).
+constexpr int64_t kRoundPairs = 1 << 14;
 __global__ __launch_bounds__(1024) void k_experts_plan(PlanArgs a) {
-    __shared__ int count[1024], begin[1024], tiles[1024], next[1024];
-    const int e = threadIdx.x;
+    __shared__ int16_t id[kRoundPairs];
+    __shared__ int count[1024], next[1024], sums[2][16];
+    const int e = threadIdx.x, lane = e & 63, wave = e >> 6, pairs = (int)a.pairs;
     count[e] = 0;
-    __syncthreads();
-    for (int64_t p = threadIdx.x; p < a.pairs; p += 1024)
-        if (leads(a.ids, p, a.k, a.E)) atomicAdd(&count[a.ids[p]], 1);
-    __syncthreads();
-    const int mine = count[e], mine_tiles = (mine + a.tile - 1) / a.tile;
-    begin[e] = mine;
-    tiles[e] = mine_tiles;
-    for (int d = 1; d < 1024; d *= 2) {
-        __syncthreads();
-        const int b = e >= d ? begin[e - d] : 0, t = e >= d ? tiles[e - d] : 0;
-        __syncthreads();
-        begin[e] += b;
-        tiles[e] += t;
+    for (int p = e; p < pairs; p += 1024) {
+        const int x = a.ids[p];
+        id[p] = (int16_t)(x >= 0 && x < a.E ? x : -1);
     }
     __syncthreads();
-    const int first = begin[e] - mine, first_tile = tiles[e] - mine_tiles;
+    const auto leader = [&](int p) {
+        if (id[p] < 0) return false;
+        for (int i = p / a.k * a.k; i < p; ++i)
+            if (id[i] == id[p]) return false;
+        return true;
+    };
+    for (int p = e; p < pairs; p += 1024)
+        if (leader(p)) atomicAdd(&count[id[p]], 1);
+    __syncthreads();
+    const int mine = count[e], mine_tiles = (mine + a.tile - 1) / a.tile;
+    int upto = mine, upto_tiles = mine_tiles;  // sums up to this expert
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int b = __shfl_up(upto, d), t = __shfl_up(upto_tiles, d);
+        upto += lane >= d ? b : 0;
+        upto_tiles += lane >= d ? t : 0;
+    }
+    if (lane == 63) {
+        sums[0][wave] = upto;
+        sums[1][wave] = upto_tiles;
+    }
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) {
+        upto += sums[0][i];
+        upto_tiles += sums[1][i];
+    }
+    const int first = upto - mine, first_tile = upto_tiles - mine_tiles;
     next[e] = first;
     for (int i = 0; i < mine_tiles; ++i)
         a.list[first_tile + i] = ExpertTile{e, first + i * a.tile, min(a.tile, mine - i * a.tile), 0};
-    if (e == 1023) *a.tiles_used = tiles[e];
+    if (e == 1023) *a.tiles_used = upto_tiles;
     __syncthreads();
-    for (int64_t p = threadIdx.x; p < a.pairs; p += 1024)
-        if (leads(a.ids, p, a.k, a.E)) {
-            const int x = a.ids[p], at = atomicAdd(&next[x], 1);
+    for (int p = e; p < pairs; p += 1024)
+        if (leader(p)) {
+            const int at = atomicAdd(&next[id[p]], 1);
             float w = a.weights[p];
-            for (int64_t i = p + 1; i < (p / a.k + 1) * a.k; ++i)
-                if (a.ids[i] == x) w += a.weights[i];
-            a.tokens[at] = (int32_t)(p / a.k);
-            a.pair[at] = (int32_t)p;
+            for (int i = p + 1; i < (p / a.k + 1) * a.k; ++i)
+                if (id[i] == id[p]) w += a.weights[i];
+            a.tokens[at] = p / a.k;
+            a.pair[at] = p;
             a.weight[at] = w;
         }
 }
@@ -133,9 +151,9 @@ int second_splits(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     return T > 4 && tiles * chunks >= 1 << 15 ? 4 : 1;
 }
 
-// Tokens of one round of launches: the workspace holds 2^14 pairs at most, and a grid fewer than 2^32 threads.
+// Tokens of one round of launches: the plan and the workspace hold 2^14 pairs at most, and a grid fewer than 2^32 threads.
 int64_t round_tokens(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
-    int64_t t = std::max<int64_t>(1, std::min(T, ((int64_t)1 << 14) / k));
+    int64_t t = std::max<int64_t>(1, std::min(T, kRoundPairs / k));
     const int64_t tiles = (std::max(n, I) + kRowTile - 1) / kRowTile;
     while (t > 1 && (tiles + 8) * (std::min(E, t * k) + t * k / kListFew) * 256 >= (int64_t)1 << 32) t /= 2;
     return t;

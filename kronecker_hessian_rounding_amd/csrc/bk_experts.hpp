@@ -88,7 +88,8 @@ struct Listed {  // token t is row list[t]
 __device__ __forceinline__ float activation(float v, int act) {
     // v sigmoid(v), or gelu's tanh form v sigmoid(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3)
     const float z = act == BAKRON_ACT_SILU ? v : 1.5957691216057308f * fmaf(0.044715f * v * v, v, v);
-    return v / (1.0f + expf(-z));
+    // (the hardware's exponential and reciprocal are within 1 ulp; the argument's rounding weighs most where v is smallest)
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
 // h between the products: bf16 pieces, the largest first, of which all but the last are cut off and the last is rounded.
@@ -507,6 +508,8 @@ void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void
 // ---------------------------------------------------------------- more tokens
 // The list's tiles hold at most 16 tokens where an expert has about as few (few_products), else as many as a workgroup of
 // mm_products takes.
+constexpr int kListFew = 16, kListMany = 64;  // tokens of a list's tile
+
 struct FirstTile {
     MvArgs a, b;
     ExpertTile l;
@@ -582,9 +585,9 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
 }
 
 // 16 RW rows of G and of U (and so of h) by 16 NT tokens.
-template <int MATH, int W, int FS, int NT, int RW, int CH>
-__global__ __launch_bounds__(64 * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_first_mm(ExpertArgs e) {
-    constexpr int kThreads = 64 * RW, kRows = 16 * RW, kPitch = 2 * kRows + 4;
+template <int MATH, int W, int FS, int NT, int KS, int RW, int CH>
+__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_first_mm(ExpertArgs e) {
+    constexpr int kThreads = 64 * KS * RW, kRows = 16 * RW, kPitch = 2 * kRows + 4;
     extern __shared__ __align__(16) char lds[];
     const uint32_t blocks = (uint32_t)((e.plane / 2 + kRows - 1) / kRows);
     const uint32_t li = blockIdx.x / blocks;
@@ -594,14 +597,19 @@ __global__ __launch_bounds__(64 * RW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const auto stream = [&](int rg, int lane) __attribute__((always_inline)) {
         return Stream<W, FS, 2, 2>(f.a, f.b, tile_b + rg, lane);
     };
-    const auto sink = [&](int n0, int toks, const float* red, int) __attribute__((always_inline)) {
+    const auto sink = [&](int n0, int toks, const float* red, int pass) __attribute__((always_inline)) {
         for (int i = threadIdx.x; i < toks * (kRows / 4); i += kThreads) {
             const int tok = i / (kRows / 4), r = i % (kRows / 4) * 4;
             const int t = 16 * n0 + tok, at = f.l.begin + t;
             const int64_t row = tile_b * 16 + r;
             if (t >= f.l.count || 2 * row >= e.plane) continue;
-            const float* p = red + tok * kPitch + r / 16 * 32 + r % 16;
-            const f32x4 g = *reinterpret_cast<const f32x4*>(p), u = *reinterpret_cast<const f32x4*>(p + 16);
+            f32x4 g = {}, u = {};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const float* p = red + (k * pass + tok) * kPitch + r / 16 * 32 + r % 16;
+                g += *reinterpret_cast<const f32x4*>(p);
+                u += *reinterpret_cast<const f32x4*>(p + 16);
+            }
             const float s = unit<MATH, W>() * (f.a.xs ? f.a.xs[e.tokens[at]] : 1.0f), w = e.weights[at];
             float h[4];
 #pragma unroll
@@ -609,35 +617,38 @@ __global__ __launch_bounds__(64 * RW) __attribute__((amdgpu_waves_per_eu(2))) vo
             store_pieces<4>(e.planes + (int64_t)e.pairs[at] * e.pieces * e.plane, e.plane, e.pieces, row, h);
         }
     };
-    mm_products<MATH, W, FS, NT, 2, 1, RW, CH>(f.a, 0, Listed{e.tokens + f.l.begin}, stream, lds, sink);
+    mm_products<MATH, W, FS, NT, 2, KS, RW, CH>(f.a, 0, Listed{e.tokens + f.l.begin}, stream, lds, sink);
 }
 
-template <int MATH, int W, int FS, int NT, int R, int RW, int CH>
-__global__ __launch_bounds__(64 * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
-    constexpr int kThreads = 64 * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
+template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH>
+__global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
+    constexpr int kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
     extern __shared__ __align__(16) char lds[];
     const uint32_t blocks = (e.second.tiles + R * RW - 1) / (R * RW);
-    const uint32_t li = blockIdx.x / blocks;
+    constexpr uint32_t kParts = kListMany / (16 * NT);  // of a list's tile
+    const uint32_t li = blockIdx.x / blocks / kParts;
     const int64_t tile_b = (int64_t)(blockIdx.x % blocks) * R * RW;
+    const int t0 = (int)(blockIdx.x / blocks % kParts) * 16 * NT;
     if ((int)li >= *e.tiles_used) return;
     const ExpertTile l = e.list[li];
+    if (t0 >= l.count) return;
     const MvArgs a = second_tile(e, l);
     const auto stream = [&](int rg, int lane) __attribute__((always_inline)) {
         return Stream<W, FS, R, 2>(a, tile_b + rg * R, lane);
     };
-    const auto sink = [&](int n0, int toks, const float* red, int) __attribute__((always_inline)) {
+    const auto sink = [&](int n0, int toks, const float* red, int pass) __attribute__((always_inline)) {
         for (int i = threadIdx.x; i < toks * (kRows / 4); i += kThreads) {
-            const int tok = i / (kRows / 4), r = i % (kRows / 4) * 4, t = 16 * n0 + tok;
+            const int tok = i / (kRows / 4), r = i % (kRows / 4) * 4, t = t0 + 16 * n0 + tok;
             const int64_t row = tile_b * 16 + r;
             if (t >= l.count || row >= e.n) continue;
-            const f32x4 y = *reinterpret_cast<const f32x4*>(red + tok * kPitch + r);
+            f32x4 y = {};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) y += *reinterpret_cast<const f32x4*>(red + (k * pass + tok) * kPitch + r);
             store4(e.part, BAKRON_F32, (int64_t)e.pairs[l.begin + t] * e.n + row, y, (int)min<int64_t>(4, e.n - row));
         }
     };
-    mm_products<MATH, W, FS, NT, R, 1, RW, CH>(a, 0, Listed{e.pairs + l.begin}, stream, lds, sink);
+    mm_products<MATH, W, FS, NT, R, KS, RW, CH>(a, t0, Listed{e.pairs + l.begin}, stream, lds, sink);
 }
-
-constexpr int kListFew = 16, kListMany = 64;  // tokens of a list's tile
 
 template <int MATH, int W, int FS>
 void launch_first_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
@@ -648,11 +659,11 @@ void launch_first_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
         hipLaunchKernelGGL((k_experts_first<MATH, W, FS, PF, NW>), dim3((unsigned)(e.plane / 32 * e.most_tiles)), dim3(64 * NW),
                            lds, stream, e);
     } else {
-        constexpr int NT = kListMany / 16, RW = 4, CH = 1;
-        constexpr size_t red = sizeof(float) * 16 * (32 * RW + 4);
-        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, CH>::kBytes, red);
+        constexpr int NT = kListMany / 16, KS = 1, RW = 4, CH = MATH == kI8 ? 2 : 1;
+        constexpr size_t red = sizeof(float) * KS * 16 * (32 * RW + 4);
+        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, KS * CH>::kBytes, red);
         const int64_t blocks = (e.plane / 2 + 16 * RW - 1) / (16 * RW);
-        hipLaunchKernelGGL((k_experts_first_mm<MATH, W, FS, NT, RW, CH>), dim3((unsigned)(blocks * e.most_tiles)), dim3(64 * RW), lds,
+        hipLaunchKernelGGL((k_experts_first_mm<MATH, W, FS, NT, KS, RW, CH>), dim3((unsigned)(blocks * e.most_tiles)), dim3(64 * KS * RW), lds,
                            stream, e);
     }
 }
@@ -676,11 +687,12 @@ void launch_second_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
         hipLaunchKernelGGL((k_experts_second<MATH, W, FS, R, PF, NW>), dim3((e.second.tiles + R - 1) / R * (unsigned)e.most_tiles),
                            dim3(64 * NW), lds, stream, e);
     } else {
-        constexpr int NT = kListMany / 16, R = 2, RW = 4, CH = 1;
-        constexpr size_t red = sizeof(float) * 16 * (16 * R * RW + 4);
-        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, CH>::kBytes, red);
-        hipLaunchKernelGGL((k_experts_second_mm<MATH, W, FS, NT, R, RW, CH>),
-                           dim3((e.second.tiles + R * RW - 1) / (R * RW) * (unsigned)e.most_tiles), dim3(64 * RW), lds, stream, e);
+        constexpr int NT = 2, R = 2, KS = 1, RW = 8, CH = 1;
+        constexpr size_t red = sizeof(float) * KS * 16 * (16 * R * RW + 4);
+        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, KS * CH>::kBytes, red);
+        hipLaunchKernelGGL((k_experts_second_mm<MATH, W, FS, NT, R, KS, RW, CH>),
+                           dim3((e.second.tiles + R * RW - 1) / (R * RW) * (unsigned)e.most_tiles * (kListMany / (16 * NT))),
+                           dim3(64 * KS * RW), lds, stream, e);
     }
 }
 template <int MATH>
