@@ -422,15 +422,20 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
  *     smaller rank are padded with zeros.
  *   scales: [R] fp32, or NULL for 1. ids: [T] int32; an id outside 0 .. R - 1 means no adapter: Y[t] = base[t].
  *   base: T x m of btype (F32, F16 or BF16), ldb >= m, or NULL for 0. Y: T x m of ytype, ldy >= m.
- *   Products are exact (8 and 16 bits) or fp32, u and all sums are fp32, and Y is rounded once. Token t's result depends on
- *   its own row and adapter only. For given sizes, types and ids it is deterministic. No workspace.
+ *   Products are exact (8 and 16 bits) or fp32, all sums are fp32, u is fp32 (past 64 tokens of 16-bit adapters it enters its
+ *   second product with 22 bits or more where Y is fp32, else 17 or more), and Y is rounded once. Token t's result depends on
+ *   its own row and adapter only. For given sizes, types and ids it is deterministic.
+ *   ws: at least bakron_lora_workspace_bytes(T, r) bytes, 16-byte aligned (0 up to 64 tokens: NULL will do). Calls that
+ *     overlap need one each.
  *   Y may be base itself (same pointer, type and ld); no other overlap of Y with a buffer of the call is allowed.
  * Errors: INVALID_ARG for NULL X, A, B, ids or Y (T > 0), T < 0 or > 2^40, n, m < 1 or >= 2^28, r < 1 or > 512, R < 1 or
- *   > 2^31 - 1, bad types or ld, or overlap.
+ *   > 2^31 - 1, bad types, ld or alignment, or overlap; WORKSPACE if ws is too small.
  */
+size_t bakron_lora_workspace_bytes(int64_t T, int64_t r);
 int bakron_lora(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx, const float* xscale, const void* A,
                 const void* B, int32_t wtype, int64_t R, int64_t r, int64_t m, const float* scales, const int32_t* ids,
-                const void* base, int32_t btype, int64_t ldb, void* Y, int32_t ytype, int64_t ldy, void* stream);
+                const void* base, int32_t btype, int64_t ldb, void* Y, int32_t ytype, int64_t ldy, void* ws, size_t ws_bytes,
+                void* stream);
 
 /*
  * Root-mean-square norm of each query and key head, with the position rotation, in one pass over the rows that a

@@ -96,7 +96,9 @@ def _load() -> ctypes.CDLL:
     ci = ctypes.c_int
     lib.bakron_lora.restype = ci
     lib.bakron_lora.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i32, i64, i64, i64, vp, vp, vp, i32, i64, vp, i32, i64,
-                                vp]
+                                vp, sz, vp]
+    lib.bakron_lora_workspace_bytes.restype = sz
+    lib.bakron_lora_workspace_bytes.argtypes = [i64, i64]
     lib.bakron_head_norm.restype = ci
     lib.bakron_head_norm.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, i32, i64, i64, vp, vp, i32, f32, ci, vp, ci,
                                      vp, i64, ci, vp, i64, i64, vp, i64, i64, vp]
@@ -122,7 +124,7 @@ EXPORTS = ("bakron_abi_version", "bakron_status_str", "bakron_hessian_accum_work
            "bakron_ldl_pair_async",
            "bakron_solve_workspace_bytes", "bakron_solve", "bakron_solve_noalloc", "bakron_rht",
            "bakron_layer_report", "bakron_packed_bytes", "bakron_pack", "bakron_matvec", "bakron_rmsnorm",
-           "bakron_lora", "bakron_head_norm", "bakron_route",
+           "bakron_lora_workspace_bytes", "bakron_lora", "bakron_head_norm", "bakron_route",
            "bakron_experts_workspace_bytes", "bakron_experts")
 
 
@@ -816,11 +818,14 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, b
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out must be a tensor of %s" % out_dtype)
         out_dtype = out.dtype
+    # of this call alone: calls on two streams, or two captured graphs, share nothing
+    nb = LIB.bakron_lora_workspace_bytes(T, r)
+    ws = x.new_empty((nb,), dtype=torch.uint8) if nb else None
     st = LIB.bakron_lora(x.data_ptr(), ROW_TYPES[xtype], T, n, ldx,
                          None if x_scale is None else _token_scales(x_scale, "x_scale", T, dev), a.data_ptr(), b.data_ptr(),
                          ROW_TYPES[a.dtype], R, r, m, None if scales is None else _token_scales(scales, "scales", R, dev),
                          ids.data_ptr(), pb or None, btype, ldb, out.data_ptr(), ROW_TYPES[out_dtype], ldy,
-                         torch._C._cuda_getCurrentRawStream(dev))
+                         ws.data_ptr() if nb else None, nb, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check("bakron_lora", st)
     return out

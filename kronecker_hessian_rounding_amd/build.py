@@ -26,7 +26,7 @@ LIB = os.path.join(OUT_DIR, "libbakron.so")
 SOURCES = ["bk_api.hip", "bk_accum.hip", "bk_ldl.hip", "bk_solve.hip", "bk_rotate.hip", "bk_report.hip", "bk_sketch.hip",
            "bk_matvec.hip", "bk_matvec_f32.hip", "bk_matvec_f16.hip", "bk_matvec_bf16.hip", "bk_matvec_i8.hip",
            "bk_matvec_e4m3.hip", "bk_norm.hip", "bk_lora.hip",
-           "bk_heads.hip", "bk_route.hip",
+           "bk_lora_f32.hip", "bk_lora_f16.hip", "bk_lora_bf16.hip", "bk_heads.hip", "bk_route.hip",
            "bk_experts.hip", "bk_experts_f32.hip", "bk_experts_f16.hip", "bk_experts_bf16.hip", "bk_experts_i8.hip",
            "bk_experts_e4m3.hip", "bk_experts_second.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -38,7 +38,7 @@ CFLAGS = [
     "-I", os.path.join(os.path.dirname(HERE), "include"),
 ]
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-FILE_FLAGS = {src: VGPR_FORM for src in SOURCES if src == "bk_ldl.hip" or src.startswith(("bk_matvec_", "bk_experts_"))}
+FILE_FLAGS = {src: VGPR_FORM for src in SOURCES if src == "bk_ldl.hip" or src.startswith(("bk_matvec_", "bk_experts_", "bk_lora"))}
 
 
 def _scratch_users(remarks: str):

@@ -368,9 +368,14 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
                               yscale, (hipStream_t)stream);
 }
 
+size_t bakron_lora_workspace_bytes(int64_t T, int64_t r) {
+    return T < 1 || T > (int64_t)1 << 40 || r < 1 || r > bk::kMaxRank ? 0 : bk::lora_workspace_bytes(T, r);
+}
+
 int bakron_lora(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx, const float* xscale, const void* A,
                 const void* B, int32_t wtype, int64_t R, int64_t r, int64_t m, const float* scales, const int32_t* ids,
-                const void* base, int32_t btype, int64_t ldb, void* Y, int32_t ytype, int64_t ldy, void* stream) {
+                const void* base, int32_t btype, int64_t ldb, void* Y, int32_t ytype, int64_t ldy, void* ws, size_t ws_bytes,
+                void* stream) {
     constexpr int64_t kMax = (int64_t)1 << 28;
     if (T < 0 || T > (int64_t)1 << 40 || n < 1 || m < 1 || n >= kMax || m >= kMax || r < 1 || r > bk::kMaxRank || R < 1 ||
         R > 0x7fffffff)
@@ -387,8 +392,16 @@ int bakron_lora(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx,
     for (const Rows& i : in)
         if (overlap(i, y)) return BAKRON_E_INVALID_ARG;
     if (overlap(b, y) && !(same_rows(b, y) && btype == ytype)) return BAKRON_E_INVALID_ARG;
+    const size_t need = bk::lora_workspace_bytes(T, r);
+    if (need) {
+        const Rows w = {ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes};
+        if (((uintptr_t)ws & 15) != 0 || overlap(w, y) || overlap(w, b)) return BAKRON_E_INVALID_ARG;
+        for (const Rows& i : in)
+            if (overlap(i, w)) return BAKRON_E_INVALID_ARG;
+        if (!ws || ws_bytes < need) return BAKRON_E_WORKSPACE;
+    }
     return bk::launch_lora(X, xtype, T, n, ldx, xscale, A, B, wtype, R, r, m, scales, ids, base, btype, ldb, Y, ytype, ldy,
-                           (hipStream_t)stream);
+                           ws, (hipStream_t)stream);
 }
 
 int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const void* K, int64_t hk, int64_t kt, int64_t kh,

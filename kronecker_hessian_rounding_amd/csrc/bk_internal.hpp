@@ -90,7 +90,8 @@ int launch_rmsnorm(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, 
 constexpr int64_t kMaxRank = 512;
 int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, const float* xs, const void* A, const void* B,
                 int wtype, int64_t R, int64_t r, int64_t m, const float* scales, const int32_t* ids, const void* base,
-                int btype, int64_t ldb, void* y, int ytype, int64_t ldy, hipStream_t stream);
+                int btype, int64_t ldb, void* y, int ytype, int64_t ldy, void* ws, hipStream_t stream);
+size_t lora_workspace_bytes(int64_t T, int64_t r);
 
 // --- norm and position rotation of heads (bk_heads.hip) ---
 constexpr int64_t kMaxHeadDim = 512;

@@ -1,0 +1,710 @@
+// bk_lora.hpp -- low-rank adapters of many requests beside a shared projection (included once for each type of
+// adapters, so that the kernels compile side by side).
+//
+// Token t names an adapter a (or none); with A_a (r x n), B_a (m x r):
+//   u_tk = xs_t sum_j x_tj A_a[k][j],   y_ti = base_ti + s_a sum_k u_tk B_a[i][k].
+//
+// Few tokens: one launch (k_lora). A workgroup takes up to 16 tokens of one adapter and a range of rows of B. It forms u
+// for them first (each workgroup of a range anew: r n elements of A, which the caches hold), then its outputs, so
+// that nothing passes through memory in between. Its first rows of B and of the base are on their way meanwhile.
+// More: u through memory in fp32 (k_lora_down: 32 tokens and a part of the columns a workgroup), then the outputs
+// (k_lora_up: 64 tokens and a range of rows), which stream the base and y.
+//
+// The first product runs on the matrix cores in the adapter's type (x in 8 bits is converted to it without loss) with fp32
+// sums. u stays fp32 on its way; the second product runs on the fp32 matrix cores in k_lora, and in k_lora_up on those of the
+// adapter's type with u in pieces (see there).
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "bk_common.hpp"
+#include "bk_internal.hpp"
+#include "bk_rows.hpp"
+
+namespace bk {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+struct LoraArgs {
+    const char* x;
+    const float* xs;
+    const char* a;
+    const char* b;
+    const float* scales;
+    const int32_t* ids;
+    const void* base;
+    void* y;
+    int64_t T, n, m, r, R;
+    int64_t ldx, ldb, ldy;
+    int btype, ytype;
+    int slots, row_blocks;     // workgroups of a token tile: adapters, ranges of rows
+    int64_t rows_each;         // rows of a range, a multiple of 64
+    // more tokens
+    float* u;                  // [split][T][rp]
+    int splits, rp;
+};
+
+// The operands of the first product. A block is the columns of one operand read: a row's share is its 4 lanes'
+// kElems contiguous elements each, so columns are multiplied in another order than they lie in, the same for both.
+template <typename X, typename W> struct First {
+    static constexpr int kElems = 16, kBlock = 64;  // of a lane, of a block
+    typedef W op __attribute__((ext_vector_type(8)));
+    struct Part { op p[2]; };
+    static __device__ __forceinline__ f32x4 mma(const Part& a, const Part& b, f32x4 c) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (std::is_same_v<W, __bf16>)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[i], c, 0, 0, 0);
+            else
+                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.p[i], b.p[i], c, 0, 0, 0);
+        }
+        return c;
+    }
+};
+template <> struct First<float, float> {
+    static constexpr int kElems = 8, kBlock = 32;
+    struct Part { f32x8 p; };
+    static __device__ __forceinline__ f32x4 mma(const Part& a, const Part& b, f32x4 c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.p[i], b.p[i], c, 0, 0, 0);
+        return c;
+    }
+};
+
+struct i8 { int8_t v; };
+struct e4m3 { uint8_t v; };
+
+// kElems elements of type S from p on, as an operand's part; no alignment beyond the element's is needed.
+template <typename F, typename S, typename W>
+__device__ __forceinline__ typename F::Part convert(const uint32_t (&w)[F::kElems * sizeof(S) / 4]) {
+    typename F::Part out;
+    if constexpr (std::is_same_v<S, W>) {
+        __builtin_memcpy(&out, w, sizeof out);
+    } else {
+        W v[16];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if constexpr (std::is_same_v<S, i8>) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * d + e] = (W)(float)(int8_t)(w[d] >> (8 * e));
+            } else if constexpr (std::is_same_v<W, __bf16>) {
+                const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[d], 1.0f, false);
+                const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[d], 1.0f, true);
+                v[4 * d] = lo[0], v[4 * d + 1] = lo[1], v[4 * d + 2] = hi[0], v[4 * d + 3] = hi[1];
+            } else {
+                const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[d], 1.0f, false);
+                const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[d], 1.0f, true);
+                v[4 * d] = lo[0], v[4 * d + 1] = lo[1], v[4 * d + 2] = hi[0], v[4 * d + 3] = hi[1];
+            }
+        }
+        __builtin_memcpy(&out, v, sizeof out);
+    }
+    return out;
+}
+// A lane's elements as they lie in memory, converted where they are used, so that the loads stay in flight until then.
+template <typename F, typename S> struct Words {
+    uint32_t w[F::kElems * sizeof(S) / 4];
+};
+template <typename F, typename S>
+__device__ __forceinline__ Words<F, S> whole_words(const S* p) {
+    Words<F, S> r;
+    __builtin_memcpy(r.w, p, sizeof r.w);
+    return r;
+}
+// the first `count` elements (zeros behind them)
+template <typename F, typename S, typename W>
+__device__ __forceinline__ typename F::Part cut_part(const S* p, int count) {
+    S v[F::kElems];
+#pragma unroll
+    for (int e = 0; e < F::kElems; ++e) {
+        S z = {};
+        if (e < count) z = p[e];
+        v[e] = z;
+    }
+    uint32_t w[F::kElems * sizeof(S) / 4];
+    __builtin_memcpy(w, v, sizeof w);
+    return convert<F, S, W>(w);
+}
+
+// 16 elements of a row in flight, of 2 or 4 bytes each, and as values (4 j ..).
+__device__ __forceinline__ u32x4 load_unit(const char* p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+template <bool kWide> struct Raw16;
+template <> struct Raw16<false> {
+    u32x4 a, b;
+    __device__ __forceinline__ void fetch(const void* row, int64_t i) {
+        const char* p = (const char*)row + 2 * i;
+        a = load_unit(p);
+        b = load_unit(p + 16);
+    }
+    template <int J>
+    __device__ __forceinline__ f32x4 value(int type) const {
+        const u32x4 w = J < 2 ? a : b;
+        f32x4 f;
+        if (type == BAKRON_F16) {
+            const f16x8 h = __builtin_bit_cast(f16x8, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = (float)h[J % 2 * 4 + e];
+        } else {
+            const bf16x8 h = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = (float)h[J % 2 * 4 + e];
+        }
+        return f;
+    }
+};
+template <> struct Raw16<true> {
+    u32x4 a, b, c, d;
+    __device__ __forceinline__ void fetch(const void* row, int64_t i) {
+        const char* p = (const char*)row + 4 * i;
+        a = load_unit(p);
+        b = load_unit(p + 16);
+        c = load_unit(p + 32);
+        d = load_unit(p + 48);
+    }
+    template <int J>
+    __device__ __forceinline__ f32x4 value(int) const {
+        return __builtin_bit_cast(f32x4, J == 0 ? a : J == 1 ? b : J == 2 ? c : d);
+    }
+};
+// y = base + g * sum for 16 whole rows of a token; raw holds the base. kWideY: y is fp32.
+template <bool kWideY, bool kWide>
+__device__ __forceinline__ void finish16(bool based, int btype, const Raw16<kWide>& raw, float g, const f32x4 (&sum)[4], void* y,
+                                         int ytype, int64_t yi) {
+    const auto part = [&](auto jc) __attribute__((always_inline)) {
+        constexpr int J = decltype(jc)::value;
+        f32x4 b = {};
+        if (based) b = raw.template value<J>(btype);
+        f4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(g, sum[J][e], b[e]);
+        if constexpr (kWideY) store4(y, BAKRON_F32, yi + 4 * J, v, 4);
+        else if (ytype == BAKRON_F16) store4(y, BAKRON_F16, yi + 4 * J, v, 4);
+        else store4(y, BAKRON_BF16, yi + 4 * J, v, 4);
+    };
+    part(std::integral_constant<int, 0>());
+    part(std::integral_constant<int, 1>());
+    part(std::integral_constant<int, 2>());
+    part(std::integral_constant<int, 3>());
+}
+// The same for 16 tokens by the 64 rows from i0 on of which the range's end cuts some: through kBox floats of LDS of
+// the wave's own, so that one short loop serves every type. `live` lanes' columns are stored; t is lane c's token.
+constexpr int kBox = 16 * 68;
+__device__ __forceinline__ void finish_cut(const LoraArgs& a, float* box, int64_t i0, int64_t row1, bool live, int64_t t, float g,
+                                           const f32x4 (&sum)[4], int lane) {
+    const uint32_t columns = (uint32_t)__ballot(live && lane < 16);
+    wave_fence();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(box + (lane & 15) * 68 + 16 * (lane >> 4) + 4 * j) = g * sum[j];
+    wave_fence();
+#pragma unroll 1
+    for (int col = 0; col < 16; ++col) {
+        const int64_t row = i0 + lane, tt = __shfl(t, col);
+        if ((columns >> col & 1) && row < row1) {
+            float v = box[col * 68 + lane];
+            if (a.base) v += load_elem(a.base, a.btype, tt * a.ldb + row);
+            store_elem(a.y, a.ytype, tt * a.ldy + row, v);
+        }
+    }
+}
+
+// The first product of RT rank tiles from rank k0 on by the NT column tiles of tokens xr over blocks first, first + step, ..
+// of a row and, for the last of them, the block that its end cuts. The lane's sums: ranks 16 j + 4 q .. of column c.
+template <typename X, typename W, int RT, int NT, int PF>
+__device__ __forceinline__ void first_product(const X* const (&xr)[NT], const W* ar, int64_t r, int64_t n, int k0, int first,
+                                              int step, int q, int c, f32x4 (&acc)[RT][NT]) {
+    using F = First<X, W>;
+    using Part = typename F::Part;
+    const int blocks = (int)(n / F::kBlock);  // whole ones
+    const W* row[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) row[j] = ar + min<int64_t>(k0 + 16 * j + c, r - 1) * n;
+    if (first < blocks) {
+        // PF blocks in flight (past the last one, the last again)
+        Words<F, X> xp[PF][NT];
+        Words<F, W> ap[PF][RT];
+        const auto fetch = [&](int s, int b) __attribute__((always_inline)) {
+            const int64_t at = (int64_t)min(b, blocks - 1) * F::kBlock + q * F::kElems;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) xp[s][t] = whole_words<F, X>(xr[t] + at);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) ap[s][j] = whole_words<F, W>(row[j] + at);
+        };
+#pragma unroll
+        for (int s = 0; s < PF; ++s) fetch(s, first + s * step);
+        for (int b = first; b < blocks; b += PF * step) {
+#pragma unroll
+            for (int s = 0; s < PF; ++s) {
+                if (b + s * step < blocks)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const Part x = convert<F, X, W>(xp[s][t].w);
+#pragma unroll
+                        for (int j = 0; j < RT; ++j) acc[j][t] = F::mma(convert<F, W, W>(ap[s][j].w), x, acc[j][t]);
+                    }
+                fetch(s, b + (s + PF) * step);
+            }
+        }
+    }
+    if (n % F::kBlock != 0 && first == blocks % step) {  // the block that the row's end cuts
+        const int64_t at = (int64_t)blocks * F::kBlock + q * F::kElems;
+        const int cut = (int)max<int64_t>(0, min<int64_t>(F::kElems, n - at));
+        Part xc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xc[t] = cut_part<F, X, W>(xr[t] + min(at, n), cut);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const Part ac = cut_part<F, W, W>(row[j] + min(at, n), cut);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[j][t] = F::mma(ac, xc[t], acc[j][t]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- few tokens
+// RT: tiles of 16 ranks of a pass; kPasses: r may be more than one takes; kEven: a lane's ranks of a pass are all there, or
+// none is; kWide, kWideY: the base, and y, is fp32. (Branches around loads, and loops around the whole, make the compiler wait for all
+// that is in flight.)
+constexpr int kLoraWaves = 8;
+
+template <typename X, typename W, int RT, bool kPasses, bool kEven, bool kWide, bool kWideY>
+__global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
+    constexpr int NW = kLoraWaves, PF = 8 / RT;
+    constexpr int RP = 16 * RT, KE = 4 * RT;  // ranks of a pass, and of a lane in it
+    extern __shared__ __align__(16) char lds[];
+    const int rp = !kPasses ? RP : (int)((a.r + RP - 1) / RP * RP), pitch = rp + 4;
+    float* u = (float*)lds;                  // [16 tokens][pitch]
+    float* red = u + 16 * pitch;             // [wave][RP ranks][17]
+    float* box = red + NW * RP * 17;         // of waves with a cut row block: at most one of a range
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, c = lane & 15;
+    // workgroups 8 apart share an XCD: the ranges of one group of tokens run there, for the A that they share
+    const int span = blockIdx.x / (8 * a.row_blocks), off = blockIdx.x % (8 * a.row_blocks);
+    const int group = span * 8 + off % 8, rb = off / 8, slot = group % a.slots;
+    const int64_t t0 = (int64_t)(group / a.slots) * 16;
+    if (t0 >= a.T) return;
+    const int64_t row0 = rb * a.rows_each, row1 = min(a.m, row0 + a.rows_each);
+    const int tokens = (int)min<int64_t>(16, a.T - t0);
+    // the adapter of token c (-1: none); this workgroup's is the slot-th of those that the tile names
+    int mine = c < tokens ? a.ids[t0 + c] : 0;
+    if (mine < 0 || mine >= a.R) mine = -1;
+    uint32_t left = ((uint32_t)1 << tokens) - 1, members = 0;
+    int ad = -1;
+    for (int i = 0; i <= slot; ++i) {
+        if (left == 0) return;
+        ad = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+        members = (uint32_t)__ballot(lane < tokens && mine == ad);
+        left &= ~members;
+    }
+    // column c of the products is the c-th token of the adapter (the first again past the last)
+    const int count = __popc(members);
+    int tok = __builtin_ctz(members);
+    {
+        uint32_t s = members;
+        for (int k = 1; k < count; ++k) {
+            s &= s - 1;
+            if (c == k) tok = __builtin_ctz(s);
+        }
+    }
+    const int64_t t = t0 + tok;
+    const bool live = c < count;
+    const W* br = (const W*)a.b + (int64_t)max(ad, 0) * a.m * a.r;
+    // Rows of B for tile j of row block i0: 16 (c / 4) + 4 j + c % 4 as operand, so that a lane's sums are 16
+    // consecutive rows, 16 q .., of token c. Of the ranks k0 .. of a pass lane group q has its own quarter.
+    const auto load_b = [&](W (&v)[4][KE], int64_t i0, int k0) __attribute__((always_inline)) {
+        const int at = k0 + q * KE;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const W* p = br + min(i0 + 16 * (c >> 2) + 4 * j + (c & 3), a.m - 1) * a.r;
+            if constexpr (kEven) __builtin_memcpy(v[j], p + (at < a.r ? at : 0), sizeof v[j]);
+            else
+#pragma unroll
+                for (int e = 0; e < KE; ++e) v[j][e] = at + e < a.r ? p[at + e] : (W)0.0f;
+        }
+    };
+    W b[4][KE];
+    Raw16<kWide> raw = {};
+    const int64_t whole = row1 - (row1 - row0) % 64;  // row blocks up to here are whole
+    const auto load_rows = [&](int64_t i0) __attribute__((always_inline)) {
+        load_b(b, min(i0, a.m - 1), 0);
+        if (a.base && i0 < whole) raw.fetch(a.base, t * a.ldb + i0 + 16 * q);
+    };
+    if constexpr (kEven) load_rows(row0 + 64 * w);
+    float f = 0.0f;
+    if (ad >= 0) {
+        f = (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t] : 1.0f);
+        const X* const xr[1] = {(const X*)a.x + t * a.ldx};
+        int k0 = 0;
+        do {
+            f32x4 acc[RT][1] = {};
+            first_product<X, W, RT, 1, PF>(xr, (const W*)a.a + (int64_t)ad * a.r * a.n, a.r, a.n, k0, w, NW, q, c, acc);
+            // sums of the waves, in their order
+            if (kPasses) __syncthreads();
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) red[(w * RP + 16 * j + 4 * q + v) * 17 + c] = acc[j][0][v];
+            __syncthreads();
+            for (int e = threadIdx.x; e < 16 * RP; e += 64 * NW) {
+                const int k = e >> 4, tk = e & 15;
+                float s = 0.0f;
+#pragma unroll
+                for (int i2 = 0; i2 < NW; ++i2) s += red[(i2 * RP + k) * 17 + tk];
+                u[tk * pitch + k0 + k] = k0 + k < a.r ? s : 0.0f;
+            }
+            k0 += RP;
+        } while (kPasses && k0 < rp);
+        __syncthreads();
+    }
+    if constexpr (!kEven) load_rows(row0 + 64 * w);
+    const float* ur = u + c * pitch + q * KE;
+    const auto product = [&](int64_t i0, f32x4 (&acc)[4]) __attribute__((always_inline)) {
+        if (ad < 0) return;
+        int k0 = 0;
+        do {
+            if (kPasses && k0) load_b(b, i0, k0);
+            const bool some = k0 + q * KE < a.r;
+#pragma unroll
+            for (int k = 0; k < KE; k += 4) {
+                const f32x4 uk = *reinterpret_cast<const f32x4*>(ur + k0 + k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(some ? (float)b[j][k + e] : 0.0f, uk[e], acc[j], 0, 0, 0);
+            }
+            k0 += RP;
+        } while (kPasses && k0 < rp);
+    };
+    int64_t i0 = row0 + 64 * w;
+    for (; i0 < whole; i0 += 64 * NW) {
+        f32x4 acc[4] = {};
+        product(i0, acc);
+        if (live) finish16<kWideY>(a.base != nullptr, a.btype, raw, f, acc, a.y, a.ytype, t * a.ldy + i0 + 16 * q);
+        if (i0 + 64 * NW < row1) load_rows(i0 + 64 * NW);
+    }
+    if (i0 < row1) {
+        f32x4 acc[4] = {};
+        product(i0, acc);
+        finish_cut(a, box, i0, row1, live, t, f, acc, lane);
+    }
+}
+
+// ---------------------------------------------------------------- more tokens
+constexpr int kDownWaves = 8, kDownTokens = 32, kUpTokens = 64, kUpWaves = 4;
+
+// u of 32 tokens over a part of the columns: [split][token][rp], 0 behind r. A token without an adapter has none.
+template <typename X, typename W, int RT>
+__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
+    constexpr int NW = kDownWaves, RP = 16 * RT;
+    extern __shared__ __align__(16) char lds[];
+    float* red = (float*)lds;  // [wave][RP ranks][33]
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, c = lane & 15, tk = lane & 31;
+    const int split = blockIdx.x % a.splits, slot = blockIdx.x / a.splits % a.slots;
+    const int64_t t0 = (int64_t)(blockIdx.x / a.splits / a.slots) * kDownTokens;
+    const int tokens = (int)min<int64_t>(kDownTokens, a.T - t0);
+    int mine = tk < tokens ? a.ids[t0 + tk] : 0;
+    if (mine < 0 || mine >= a.R) mine = -1;
+    uint32_t left = (uint32_t)__ballot(lane < tokens && mine >= 0);
+    for (int i = 0; left; ++i) {
+        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+        const uint32_t members = (uint32_t)__ballot(lane < tokens && mine == ad);
+        left &= ~members;
+        if (i % a.slots != slot) continue;
+        const int count = __popc(members);
+        int tok = __builtin_ctz(members);  // lane k < 32: the k-th member (the first again past the last)
+        {
+            uint32_t s = members;
+            for (int k = 1; k < count; ++k) {
+                s &= s - 1;
+                if (tk == k) tok = __builtin_ctz(s);
+            }
+        }
+        const W* ar = (const W*)a.a + (int64_t)ad * a.r * a.n;
+        const X* const x0 = (const X*)a.x + (t0 + __shfl(tok, c)) * a.ldx;
+        const X* const x1 = (const X*)a.x + (t0 + __shfl(tok, c + 16)) * a.ldx;
+        for (int k0 = 0; k0 < a.rp; k0 += RP) {
+            f32x4 acc[RT][2] = {};
+            if (count > 16) {
+                const X* const xr[2] = {x0, x1};
+                first_product<X, W, RT, 2, RT == 4 ? 1 : 2>(xr, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, acc);
+            } else {
+                const X* const xr[1] = {x0};
+                f32x4 one[RT][1] = {};
+                first_product<X, W, RT, 1, RT == 4 ? 1 : 2>(xr, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, one);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[j][0] = one[j][0];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) red[(w * RP + 16 * j + 4 * q + v) * 33 + 16 * t + c] = acc[j][t][v];
+            __syncthreads();
+            for (int e = threadIdx.x; e < RP * kDownTokens; e += 64 * NW) {
+                const int k = e % RP, col = e / RP;
+                if (col >= count || k0 + k >= a.rp) continue;
+                float s = 0.0f;
+#pragma unroll
+                for (int i2 = 0; i2 < NW; ++i2) s += red[(i2 * RP + k) * 33 + col];
+                uint32_t m = members;  // the col-th member
+                for (int k2 = 0; k2 < col; ++k2) m &= m - 1;
+                a.u[((int64_t)split * a.T + t0 + __builtin_ctz(m)) * a.rp + k0 + k] = k0 + k < a.r ? s : 0.0f;
+            }
+        }
+    }
+}
+
+// The second product: y of 64 tokens by a range of rows. u, with the token's and the adapter's factors, lies in LDS as
+// operand: in NP pieces of the adapter's type, of which all but the last are cut off and the last is rounded. bf16: 3
+// pieces hold 25 bits, for a y in fp32; 2 hold 17, for a y of 16 bits, whose own rounding is 2^5 to 2^8 times
+// theirs. fp16: 2 pieces hold 22 bits, of u times the power of two that takes the token's largest value to 2^14 (undone in
+// fp32); 3 hold all. fp32: one, on the fp32 matrix cores. S: steps of 32 ranks.
+// Bound by HBM (base and y are read and written once), so that a wave's loads of the base are all in flight in front of the
+// products.
+template <typename W, int NP, int S> struct Second {
+    typedef W op __attribute__((ext_vector_type(8)));
+    static constexpr int kBytes = 8 * sizeof(W);                                  // of an operand of a lane
+    static constexpr int kOps = NP * S * (kUpTokens / 16) * 64 * kBytes, kLds = kOps + (kUpTokens + kUpWaves * kBox) * 4;
+    static __device__ __forceinline__ f32x4 mma(op a, op b, f32x4 c) {
+        if constexpr (std::is_same_v<W, __bf16>) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+        else if constexpr (std::is_same_v<W, _Float16>) return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+        else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+            return c;
+        }
+    }
+};
+
+template <typename W, int NP, int S, bool kEven, bool kWide, bool kWideY>
+__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_up(LoraArgs a) {
+    using Sd = Second<W, NP, S>;
+    using Op = typename Sd::op;
+    constexpr int NT = kUpTokens / 16;
+    constexpr bool kScaled = std::is_same_v<W, _Float16>;
+    extern __shared__ __align__(16) char lds[];
+    W* ops = (W*)lds;                                          // [piece][step][tile][lane][8]
+    float* undo = (float*)(lds + Sd::kOps);                    // [token]
+    float* box = undo + kUpTokens;                             // [wave][kBox]
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, c = lane & 15;
+    const int64_t t0 = (int64_t)(blockIdx.x / a.row_blocks) * kUpTokens;
+    // whole row blocks first; the last range is that of the rows behind them
+    const int64_t whole = a.m / 64 * 64, row0 = min((blockIdx.x % a.row_blocks) * a.rows_each, whole);
+    const int64_t row1 = row0 < whole ? min(whole, row0 + a.rows_each) : a.m;
+    const int tokens = (int)min<int64_t>(kUpTokens, a.T - t0);
+    int mine = lane < tokens ? a.ids[t0 + lane] : -1;
+    if (mine < 0 || mine >= a.R) mine = -1;
+    {
+        // four threads a token, ranks 4 part .., 16 apart
+        const int t = threadIdx.x >> 2, part = threadIdx.x & 3;
+        const int ad = __shfl(mine, t & 63);
+        const float f = ad < 0 ? 0.0f : (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t0 + t] : 1.0f);
+        f32x4 v[2 * S];
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * S; ++i) {
+            const int k = 16 * i + 4 * part;
+            v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (ad >= 0 && k < a.rp) {
+                for (int s = 0; s < a.splits; ++s)
+                    v[i] += *reinterpret_cast<const f32x4*>(a.u + ((int64_t)s * a.T + t0 + t) * a.rp + k);
+                v[i] *= f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]));
+        }
+        if constexpr (kScaled) {
+            top = fmaxf(top, __shfl_xor(top, 1));
+            top = fmaxf(top, __shfl_xor(top, 2));
+            // the exponent of the largest value, in both factors' range
+            const int ex = top > 0.0f && top < INFINITY ? min(max(14 - (int)((__float_as_uint(top) >> 23) - 127), -126), 126) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+            for (int i = 0; i < 2 * S; ++i) v[i] *= up;
+            if (part == 0) undo[t] = __uint_as_float((uint32_t)(127 - ex) << 23);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * S; ++i) {
+            const int k = 16 * i + 4 * part;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                W h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = v[i][e];
+                    if constexpr (std::is_same_v<W, float>) h[e] = x;
+                    else {
+                        if (p < NP - 1) {  // cut off
+                            x = __builtin_canonicalizef(x);
+                            if constexpr (std::is_same_v<W, __bf16>) h[e] = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(x) >> 16));
+                            else h[e] = (_Float16)__uint_as_float(x == x ? __float_as_uint(x) & 0xFFFFE000u : __float_as_uint(x));
+                        } else h[e] = (W)x;
+                        const float rest = x - (float)h[e];
+                        v[i][e] = rest == rest ? rest : 0.0f;
+                    }
+                }
+                __builtin_memcpy(ops + ((((p * S + k / 32) * NT + (t >> 4)) * 64 + k % 32 / 8 * 16 + (t & 15)) * 8 + k % 8), h, sizeof h);
+            }
+        }
+    }
+    __syncthreads();
+    const auto token = [&](int n) __attribute__((always_inline)) { return t0 + min(16 * n + c, tokens - 1); };
+    // acc of the tokens of adapter ad for the 64 rows from i0 on
+    const auto product = [&](int64_t i0, int ad, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
+        const W* br = (const W*)a.b + (int64_t)ad * a.m * a.r;
+        constexpr int SB = kEven && sizeof(W) == 2 && S < 4 ? S : 1;  // steps whose rows of B are in registers at once
+#pragma unroll 1
+        for (int s0 = 0; s0 < S && 32 * s0 < a.r; s0 += SB) {
+            Op b[4][SB];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const W* p = br + min(i0 + 16 * (c >> 2) + 4 * j + (c & 3), a.m - 1) * a.r;
+#pragma unroll
+                for (int s = 0; s < SB; ++s) {
+                    const int at = 32 * (s0 + s) + 8 * q;
+                    if constexpr (kEven) {
+                        __builtin_memcpy(&b[j][s], p + (at < a.r ? at : 0), sizeof(Op));
+                        if (at >= a.r) b[j][s] = Op{};
+                    } else
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) b[j][s][e] = at + e < a.r ? p[at + e] : (W)0.0f;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (members >> (16 * n) & 0xFFFF)
+#pragma unroll
+                    for (int p = NP - 1; p >= 0; --p)  // the smallest piece first into the sum
+#pragma unroll
+                        for (int s = 0; s < SB; ++s) {
+                            const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s0 + s) * NT + n) * 64 + lane) * 8);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[n][j] = Sd::mma(b[j][s], uo, acc[n][j]);
+                        }
+        }
+    };
+    if (row0 == whole) {  // a wave for 16 tokens
+        uint64_t left = w * 16 < tokens ? __ballot(lane < tokens && lane >> 4 == w) : 0;
+        while (left) {
+            const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            const uint64_t members = __ballot(lane < tokens && lane >> 4 == w && mine == ad);
+            left &= ~members;
+            f32x4 acc[NT][4] = {}, own[4] = {};
+            if (ad >= 0) product(row0, ad, members, acc);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (n == w)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) own[j] = acc[n][j];
+            finish_cut(a, box + w * kBox, row0, row1, members >> (16 * w) >> c & 1, token(w), kScaled ? undo[16 * w + c] : 1.0f, own,
+                       lane);
+        }
+        return;
+    }
+    for (int64_t i0 = row0 + 64 * w; i0 < row1; i0 += 64 * kUpWaves) {
+        constexpr bool kAhead = !std::is_same_v<W, float>;  // fp32 rows of B leave no registers for the base
+        Raw16<kWide> raw[NT] = {};
+        if (kAhead && a.base)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
+        uint64_t left = __ballot(lane < tokens);
+        while (left) {
+            const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            const uint64_t members = __ballot(lane < tokens && mine == ad);
+            left &= ~members;
+            f32x4 acc[NT][4] = {};
+            if (ad >= 0) product(i0, ad, members, acc);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (members >> (16 * n) >> c & 1) {
+                    if (!kAhead && a.base) raw[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
+                    finish16<kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
+                                    token(n) * a.ldy + i0 + 16 * q);
+                }
+        }
+    }
+}
+
+template <typename X, typename W, int RT, bool kPasses, bool kEven>
+void launch_few(const LoraArgs& a, hipStream_t stream) {
+    constexpr int NW = kLoraWaves;
+    const size_t rp = ((size_t)a.r + 16 * RT - 1) / (16 * RT) * (16 * RT);
+    const size_t lds = sizeof(float) * (16 * (rp + 4) + NW * 16 * RT * 17 + kBox);
+    const int64_t groups = (a.T + 15) / 16 * a.slots;
+    const dim3 grid((unsigned)((groups + 7) / 8 * 8 * a.row_blocks)), threads(64 * NW);
+    const bool wide = a.base && a.btype == BAKRON_F32;
+    if (a.ytype == BAKRON_F32) {
+        if (wide) hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, true, true>), grid, threads, lds, stream, a);
+        else hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, false, true>), grid, threads, lds, stream, a);
+    } else {
+        if (wide) hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, true, false>), grid, threads, lds, stream, a);
+        else hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, false, false>), grid, threads, lds, stream, a);
+    }
+}
+
+template <typename X, typename W, int RT>
+void launch_down(const LoraArgs& a, hipStream_t stream) {
+    const int64_t tiles = (a.T + kDownTokens - 1) / kDownTokens;
+    hipLaunchKernelGGL((k_lora_down<X, W, RT>), dim3((unsigned)(tiles * a.slots * a.splits)), dim3(64 * kDownWaves),
+                       sizeof(float) * kDownWaves * 16 * RT * 33, stream, a);
+}
+
+template <typename W, int NP, int S, bool kEven, bool kWideY>
+void launch_up(const LoraArgs& a, hipStream_t stream) {
+    const int64_t tiles = (a.T + kUpTokens - 1) / kUpTokens;
+    constexpr size_t lds = Second<W, NP, S>::kLds;
+    const dim3 grid((unsigned)(tiles * a.row_blocks)), threads(64 * kUpWaves);
+    if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
+    else hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
+}
+template <typename W, int NP, bool kWideY>
+void launch_up_ranks(const LoraArgs& a, hipStream_t stream) {
+    if (a.r % 8 != 0) launch_up<W, NP, 4, false, kWideY>(a, stream);
+    else if (a.r <= 32) launch_up<W, NP, 1, true, kWideY>(a, stream);
+    else if (a.r <= 64) launch_up<W, NP, 2, true, kWideY>(a, stream);
+    else launch_up<W, NP, 4, true, kWideY>(a, stream);
+}
+
+inline bool lora_few(int64_t T, int64_t r) { return T <= 64 || r > 128; }
+
+template <typename X, typename W>
+void launch_lora_types(const LoraArgs& a, hipStream_t stream) {
+    if (lora_few(a.T, a.r)) {
+        if (a.r % 4 != 0) launch_few<X, W, 1, true, false>(a, stream);
+        else if (a.r <= 16 || a.r % 8 != 0 || (a.r > 32 && a.r % 16 != 0)) launch_few<X, W, 1, true, true>(a, stream);
+        else if (a.r <= 32) launch_few<X, W, 2, false, true>(a, stream);
+        else launch_few<X, W, 4, true, true>(a, stream);
+        return;
+    }
+    if (a.r <= 16) launch_down<X, W, 1>(a, stream);
+    else if (a.r <= 32) launch_down<X, W, 2>(a, stream);
+    else launch_down<X, W, 4>(a, stream);
+    constexpr bool kF32 = std::is_same_v<W, float>;
+    if (a.ytype == BAKRON_F32) launch_up_ranks<W, kF32 ? 1 : 3, true>(a, stream);
+    else launch_up_ranks<W, kF32 ? 1 : 2, false>(a, stream);
+}
+
+// by the type of x; W that of the adapters
+template <typename W>
+void launch_lora_adapters(const LoraArgs& a, int xtype, hipStream_t stream) {
+    if constexpr (std::is_same_v<W, float>) launch_lora_types<float, float>(a, stream);
+    else if (xtype == BAKRON_I8) launch_lora_types<i8, W>(a, stream);
+    else if (xtype == BAKRON_E4M3) launch_lora_types<e4m3, W>(a, stream);
+    else launch_lora_types<W, W>(a, stream);
+}
+
+}  // namespace bk

@@ -75,18 +75,20 @@ def test_against_64_bits(T, n, m, r, R, xt, wt):
 
 
 @pytest.mark.parametrize("xt,wt", [(BF16, BF16), (F32, F32)])
-@pytest.mark.parametrize("T,run,m", [(16, 16, 300), (300, 37, 200), (5000, 500, 96), (4200, 1, 64), (70, 1, 9000)])
-def test_launch_shapes(T, run, m, xt, wt):
-    """Runs of one adapter and every token with another; few and many tiles of tokens; many rows."""
-    x, a, b, ids, scales, _ = inputs(T, 72, m, 12, 9, xt, wt, seed=T, run=run)
+@pytest.mark.parametrize("T,run,m,r", [(16, 16, 300, 12), (64, 1, 2000, 16), (65, 1, 2000, 16), (300, 37, 200, 24), (5000, 500, 96, 12), (4200, 1, 64, 8),
+                                       (70, 1, 9000, 64), (500, 60, 333, 128), (130, 3, 4500, 100), (200, 7, 129, 130), (2100, 33, 64, 5)])
+def test_launch_shapes(T, run, m, r, xt, wt):
+    """Runs of one adapter and every token with another; few and many tiles of tokens; many rows; every rank's tiles."""
+    x, a, b, ids, scales, _ = inputs(T, 72, m, r, 9, xt, wt, seed=T, run=run)
     base = torch.randn(T, m, generator=gen(2)).to(wt)
     check(call(x, a, b, ids, base, scales), x, a, b, ids, base, scales, None)
 
 
+@pytest.mark.parametrize("T", [21, 150])
 @pytest.mark.parametrize("xt,wt", COMBOS)
-def test_exact_on_integers(xt, wt):
+def test_exact_on_integers(xt, wt, T):
     """Small integers: every partial sum is an integer below 2^24, so the result is exact, whatever the order."""
-    T, n, m, r, R = 21, 150, 140, 20, 4
+    n, m, r, R = 150, 140, 20, 4
     g = gen(4)
     x = torch.randint(-4, 5, (T, n), generator=g).to(torch.int8 if xt == I8 else F32).to(xt)
     a, b = (torch.randint(-2, 3, s, generator=g).float().to(wt) for s in ((R, r, n), (R, m, r)))
@@ -96,10 +98,11 @@ def test_exact_on_integers(xt, wt):
     assert torch.equal(y.cpu().double(), form64(x, a, b, ids, base, torch.full((R,), 2.0), None)[0])
 
 
+@pytest.mark.parametrize("T", [37, 101])
 @pytest.mark.parametrize("xt,wt", [(BF16, BF16), (F32, F32), (I8, F16), (E4M3, BF16)])
-def test_strided_rows_and_place(xt, wt):
+def test_strided_rows_and_place(xt, wt, T):
     """Column ranges of wider buffers at odd offsets, in place on the base; nothing else is written."""
-    T, n, m, r, R = 37, 131, 270, 16, 3
+    n, m, r, R = 131, 270, 16, 3
     x, a, b, ids, scales, xs = inputs(T, n, m, r, R, xt, wt, seed=6, run=4)
     base = torch.randn(T, m, generator=gen(7)).to(wt)
     ref = call(x, a, b, ids, base, scales, xs)
@@ -114,31 +117,34 @@ def test_strided_rows_and_place(xt, wt):
     assert bool((yb == 7.0).all())
 
 
-def test_tokens_without_an_adapter():
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T", [20, 140])
+def test_tokens_without_an_adapter(T, dtype):
     """Ids on either side of the range leave the base as it is; a NaN or infinity of one request stays its own."""
-    x, a, b, ids, scales, _ = inputs(20, 96, 80, 16, 3, BF16, BF16, none=0.0)
-    base = torch.randn(20, 80, generator=gen(8)).to(BF16)
+    x, a, b, ids, scales, _ = inputs(T, 96, 80, 16, 3, dtype, dtype, none=0.0)
+    base = torch.randn(T, 80, generator=gen(8)).to(dtype)
     ids[3], ids[4], ids[5], ids[6] = -1, 3, -2 ** 31, 2 ** 31 - 1
     y = call(x, a, b, ids, base, scales)
     assert torch.equal(y[3:7].cpu(), base[3:7])
     check(y, x, a, b, ids, base, scales, None)
     assert bool((call(x, a, b, torch.full_like(ids, -1), out_dtype=BF16) == 0).all())
-    ids[:] = torch.arange(20, dtype=torch.int32) % 3
+    ids[:] = torch.arange(T, dtype=torch.int32) % 3
     ref = call(x, a, b, ids, base, scales)
     x[1, 5] = float("nan")
     a[2, 3, 7] = float("inf")
     b[2, 9, 1] = float("nan")
     y = call(x, a, b, ids, base, scales)
-    clean = [t for t in range(20) if t != 1 and t % 3 != 2]
+    clean = [t for t in range(T) if t != 1 and t % 3 != 2]
     assert torch.equal(y[clean], ref[clean]) and bool(torch.isnan(y[1]).all())
 
 
-def test_other_rows_do_not_matter():
+@pytest.mark.parametrize("T", [50, 90])
+def test_other_rows_do_not_matter(T):
     """A token's result stays bit for bit when the other rows, and their adapters, change."""
-    x, a, b, ids, scales, _ = inputs(50, 700, 333, 24, 5, BF16, BF16, seed=9)
-    base = torch.randn(50, 333, generator=gen(9)).to(BF16)
+    x, a, b, ids, scales, _ = inputs(T, 700, 333, 24, 5, BF16, BF16, seed=9)
+    base = torch.randn(T, 333, generator=gen(9)).to(BF16)
     y = call(x, a, b, ids, base, scales)
-    x2, _, _, ids2, _, _ = inputs(50, 700, 333, 24, 5, BF16, BF16, seed=10)
+    x2, _, _, ids2, _, _ = inputs(T, 700, 333, 24, 5, BF16, BF16, seed=10)
     for t in (0, 17, 49):
         x3, ids3 = x2.clone(), ids2.clone()
         x3[t], ids3[t] = x[t], ids[t]
@@ -190,7 +196,20 @@ def test_refusals():
             f()
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [5, 80])
+def test_values_over_the_types_range(T, dtype):
+    """u far above and below what 16 bits hold in fp16, and zeros: the second product keeps them."""
+    n, m, r, R = 64, 96, 16, 4
+    x, a, b, _, _, _ = inputs(T, n, m, r, R, dtype, dtype, none=0.0)
+    ids = torch.arange(T, dtype=torch.int32) % R
+    a = a.float() * torch.tensor([1.0, 2.0 ** 12, 2.0 ** -12, 0.0])[:, None, None]
+    xs = torch.where(torch.arange(T) % 3 == 0, 2.0 ** 20, 2.0 ** -20)
+    a = a.to(dtype)
+    check(call(x, a, b, ids, None, None, xs, out_dtype=F32), x, a, b, ids, None, None, xs)
+
+
+@pytest.mark.parametrize("T", [1, 40, 100])
 def test_stream_and_graph(T):
     x, a, b, ids, scales, _ = (t.cuda() for t in inputs(T, 512, 384, 16, 5, BF16, BF16))
     base = torch.randn(T, 384, device="cuda").to(BF16)

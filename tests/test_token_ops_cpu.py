@@ -73,7 +73,7 @@ def test_binding_refuses_host_tensors():
 def test_lora_refuses():
     f = bk.LIB.bakron_lora
     ok = dict(X=A, xtype=BF16, T=3, n=64, ldx=64, xs=None, A=B, B=C, wtype=BF16, R=4, r=8, m=32, scales=D, ids=E, base=F,
-              btype=F32, ldb=32, Y=G, ytype=F16, ldy=32, stream=None)
+              btype=F32, ldb=32, Y=G, ytype=F16, ldy=32, ws=None, wb=0, stream=None)
 
     def call(**kw):
         return f(*{**ok, **kw}.values())
@@ -87,6 +87,15 @@ def test_lora_refuses():
         assert call(**kw) == INVALID, kw
     assert call(T=0) == OK
     assert call(T=0, X=None, A=None, B=None, ids=None, base=None, Y=None) == OK
+    wb = bk.LIB.bakron_lora_workspace_bytes(100, 8)
+    assert bk.LIB.bakron_lora_workspace_bytes(64, 8) == 0 < wb
+    W = at(8 << 36)
+    for kw in (dict(), dict(ws=W, wb=wb - 1), dict(ws=None, wb=wb)):
+        assert call(T=100, **kw) == WORKSPACE, kw
+    for kw in (dict(ws=G), dict(ws=A), dict(ws=F), dict(ws=E), dict(ws=at((8 << 36) + 8)), dict(ws=at((7 << 36) - 16))):
+        assert call(T=100, **{"ws": W, "wb": wb, **kw}) == INVALID, kw
+    for bad in ((-1, 8), ((1 << 40) + 1, 8), (100, 0), (100, 513)):
+        assert bk.LIB.bakron_lora_workspace_bytes(*bad) == 0
 
 
 def test_lora_binding_refuses_host_tensors():
