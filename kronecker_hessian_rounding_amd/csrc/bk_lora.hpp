@@ -220,7 +220,7 @@ __device__ __forceinline__ void finish_cut(const LoraArgs& a, float* box, int64_
 // The first product of RT rank tiles from rank k0 on by the NT column tiles of tokens xr over blocks first, first + step, ..
 // of a row and, for the last of them, the block that its end cuts. The lane's sums: ranks 16 j + 4 q .. of column c.
 template <typename X, typename W, int RT, int NT, int PF>
-__device__ __forceinline__ void first_product(const X* const (&xr)[NT], const W* ar, int64_t r, int64_t n, int k0, int first,
+__device__ __forceinline__ void first_product(const X* const (&xr)[NT], const bool (&live)[NT], const W* ar, int64_t r, int64_t n, int k0, int first,
                                               int step, int q, int c, f32x4 (&acc)[RT][NT]) {
     using F = First<X, W>;
     using Part = typename F::Part;
@@ -229,31 +229,39 @@ __device__ __forceinline__ void first_product(const X* const (&xr)[NT], const W*
 #pragma unroll
     for (int j = 0; j < RT; ++j) row[j] = ar + min<int64_t>(k0 + 16 * j + c, r - 1) * n;
     if (first < blocks) {
-        // PF blocks in flight (past the last one, the last again)
+        // PF blocks in flight (past the last one, the last again); columns past the last token are not read
         Words<F, X> xp[PF][NT];
         Words<F, W> ap[PF][RT];
         const auto fetch = [&](int s, int b) __attribute__((always_inline)) {
             const int64_t at = (int64_t)min(b, blocks - 1) * F::kBlock + q * F::kElems;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) xp[s][t] = whole_words<F, X>(xr[t] + at);
+            for (int t = 0; t < NT; ++t) {
+                xp[s][t] = Words<F, X>{};
+                if (live[t]) xp[s][t] = whole_words<F, X>(xr[t] + at);
+            }
 #pragma unroll
             for (int j = 0; j < RT; ++j) ap[s][j] = whole_words<F, W>(row[j] + at);
         };
+        const auto product = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < PF; ++s) fetch(s, first + s * step);
-        for (int b = first; b < blocks; b += PF * step) {
+            for (int t = 0; t < NT; ++t) {
+                const Part x = convert<F, X, W>(xp[s][t].w);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[j][t] = F::mma(convert<F, W, W>(ap[s][j].w), x, acc[j][t]);
+            }
+        };
+        int b = first;
+#pragma unroll
+        for (int s = 0; s < PF; ++s) fetch(s, b + s * step);
+        for (; b + PF * step < blocks; b += PF * step)
 #pragma unroll
             for (int s = 0; s < PF; ++s) {
-                if (b + s * step < blocks)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const Part x = convert<F, X, W>(xp[s][t].w);
-#pragma unroll
-                        for (int j = 0; j < RT; ++j) acc[j][t] = F::mma(convert<F, W, W>(ap[s][j].w), x, acc[j][t]);
-                    }
+                product(s);
                 fetch(s, b + (s + PF) * step);
             }
-        }
+#pragma unroll
+        for (int s = 0; s < PF; ++s)
+            if (b + s * step < blocks) product(s);
     }
     if (n % F::kBlock != 0 && first == blocks % step) {  // the block that the row's end cuts
         const int64_t at = (int64_t)blocks * F::kBlock + q * F::kElems;
@@ -331,22 +339,26 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
                 for (int e = 0; e < KE; ++e) v[j][e] = at + e < a.r ? p[at + e] : (W)0.0f;
         }
     };
-    W b[4][KE];
-    Raw16<kWide> raw = {};
     const int64_t whole = row1 - (row1 - row0) % 64;  // row blocks up to here are whole
-    const auto load_rows = [&](int64_t i0) __attribute__((always_inline)) {
-        load_b(b, min(i0, a.m - 1), 0);
-        if (a.base && i0 < whole) raw.fetch(a.base, t * a.ldb + i0 + 16 * q);
+    struct Rows {
+        W b[4][KE];
+        Raw16<kWide> raw;
     };
-    if constexpr (kEven) load_rows(row0 + 64 * w);
+    const auto load_rows = [&](Rows& r, int64_t i0) __attribute__((always_inline)) {
+        load_b(r.b, min(i0, a.m - 1), 0);
+        if (a.base && whole > row0) r.raw.fetch(a.base, t * a.ldb + min(i0, whole - 64) + 16 * q);
+    };
+    Rows next = {};
+    if constexpr (kEven) load_rows(next, row0 + 64 * w);
     float f = 0.0f;
     if (ad >= 0) {
         f = (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t] : 1.0f);
         const X* const xr[1] = {(const X*)a.x + t * a.ldx};
+        const bool lv[1] = {live};
         int k0 = 0;
         do {
             f32x4 acc[RT][1] = {};
-            first_product<X, W, RT, 1, PF>(xr, (const W*)a.a + (int64_t)ad * a.r * a.n, a.r, a.n, k0, w, NW, q, c, acc);
+            first_product<X, W, RT, 1, PF>(xr, lv, (const W*)a.a + (int64_t)ad * a.r * a.n, a.r, a.n, k0, w, NW, q, c, acc);
             // sums of the waves, in their order
             if (kPasses) __syncthreads();
 #pragma unroll
@@ -365,9 +377,9 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
         } while (kPasses && k0 < rp);
         __syncthreads();
     }
-    if constexpr (!kEven) load_rows(row0 + 64 * w);
+    if constexpr (!kEven) load_rows(next, row0 + 64 * w);
     const float* ur = u + c * pitch + q * KE;
-    const auto product = [&](int64_t i0, f32x4 (&acc)[4]) __attribute__((always_inline)) {
+    const auto product = [&](int64_t i0, W (&b)[4][KE], f32x4 (&acc)[4]) __attribute__((always_inline)) {
         if (ad < 0) return;
         int k0 = 0;
         do {
@@ -387,14 +399,16 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     };
     int64_t i0 = row0 + 64 * w;
     for (; i0 < whole; i0 += 64 * NW) {
+        Rows cur = next;
+        if constexpr (kEven) load_rows(next, i0 + 64 * NW);
         f32x4 acc[4] = {};
-        product(i0, acc);
-        if (live) finish16<kWideY>(a.base != nullptr, a.btype, raw, f, acc, a.y, a.ytype, t * a.ldy + i0 + 16 * q);
-        if (i0 + 64 * NW < row1) load_rows(i0 + 64 * NW);
+        product(i0, cur.b, acc);
+        if (live) finish16<kWideY>(a.base != nullptr, a.btype, cur.raw, f, acc, a.y, a.ytype, t * a.ldy + i0 + 16 * q);
+        if constexpr (!kEven) load_rows(next, i0 + 64 * NW);
     }
     if (i0 < row1) {
         f32x4 acc[4] = {};
-        product(i0, acc);
+        product(i0, next.b, acc);
         finish_cut(a, box, i0, row1, live, t, f, acc, lane);
     }
 }
@@ -437,11 +451,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
             f32x4 acc[RT][2] = {};
             if (count > 16) {
                 const X* const xr[2] = {x0, x1};
-                first_product<X, W, RT, 2, RT == 4 ? 1 : 2>(xr, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, acc);
+                const bool lv[2] = {true, c + 16 < count};
+                first_product<X, W, RT, 2, RT == 4 ? 1 : 2>(xr, lv, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, acc);
             } else {
                 const X* const xr[1] = {x0};
+                const bool lv[1] = {c < count};
                 f32x4 one[RT][1] = {};
-                first_product<X, W, RT, 1, RT == 4 ? 1 : 2>(xr, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, one);
+                first_product<X, W, RT, 1, RT == 4 ? 1 : 2>(xr, lv, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, one);
 #pragma unroll
                 for (int j = 0; j < RT; ++j) acc[j][0] = one[j][0];
             }
