@@ -54,7 +54,7 @@ int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, con
         if (lora_few(a.T, r)) {
             const int64_t tiles = (a.T + 15) / 16;
             a.slots = (int)std::min<int64_t>({16, a.T, R + 1});
-            ranges = std::max<int64_t>(1, std::min((m + 511) / 512, 2 * cus / (tiles * a.slots)));
+            ranges = std::max<int64_t>(1, std::min((m + 511) / 512, cus / (tiles * a.slots)));
             a.rows_each = ((m + ranges - 1) / ranges + 63) / 64 * 64;
             a.row_blocks = (int)((m + a.rows_each - 1) / a.rows_each);
         } else {

@@ -76,6 +76,8 @@ template <> struct First<float, float> {
     }
 };
 
+template <typename W> struct Vec8 { typedef W type __attribute__((ext_vector_type(8))); };
+
 struct i8 { int8_t v; };
 struct e4m3 { uint8_t v; };
 
@@ -278,21 +280,64 @@ __device__ __forceinline__ void first_product(const X* const (&xr)[NT], const bo
     }
 }
 
+// The second product. u, with the token's and the adapter's factors, lies in LDS as operand: in NP pieces of the adapter's
+// type, of which all but the last are cut off and the last is rounded. bf16: 3 pieces hold 25 bits, for a y in
+// fp32; 2 hold 17, for a y of 16 bits, whose own rounding is 2^5 to 2^8 times theirs. fp16: 2 pieces hold 22 bits, of u
+// times the power of two that takes the token's largest value to 2^14 (undone in fp32); 3 hold all. fp32: one, on the fp32
+// matrix cores. (fp32 products for all types cost a 64-token batch 3.8 us of 18.)
+template <typename W, bool kWideY>
+constexpr int pieces() {
+    return std::is_same_v<W, float> ? 1 : kWideY ? 3 : 2;
+}
+template <typename W>
+__device__ __forceinline__ f32x4 second_mma(typename Vec8<W>::type a, typename Vec8<W>::type b, f32x4 c) {
+    if constexpr (std::is_same_v<W, __bf16>) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    else if constexpr (std::is_same_v<W, _Float16>) return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+}
+// The power of two for fp16 pieces of values up to `top`, as the exponent; both it and its inverse are normal.
+__device__ __forceinline__ int piece_exponent(float top) {
+    return top > 0.0f && top < INFINITY ? min(max(14 - (int)((__float_as_uint(top) >> 23) - 127), -126), 126) : 0;
+}
+__device__ __forceinline__ float power(int ex) { return __uint_as_float((uint32_t)(127 + ex) << 23); }
+// Cuts the next piece off x (the last one: rounds it).
+template <typename W, bool kLast>
+__device__ __forceinline__ W cut_piece(float& x) {
+    W h;
+    if constexpr (std::is_same_v<W, float> || kLast) h = (W)x;
+    else {
+        x = __builtin_canonicalizef(x);
+        if constexpr (std::is_same_v<W, __bf16>) h = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(x) >> 16));
+        else h = (_Float16)__uint_as_float(x == x ? __float_as_uint(x) & 0xFFFFE000u : __float_as_uint(x));
+    }
+    const float rest = x - (float)h;
+    x = rest == rest ? rest : 0.0f;
+    return h;
+}
+
 // ---------------------------------------------------------------- few tokens
-// RT: tiles of 16 ranks of a pass; kPasses: r may be more than one takes; kEven: a lane's ranks of a pass are all there, or
-// none is; kWide, kWideY: the base, and y, is fp32. (Branches around loads, and loops around the whole, make the compiler wait for all
-// that is in flight.)
+// RT: tiles of 16 ranks of a pass of the first product, S: steps of 32 ranks of the second; kPasses: r may be more than they
+// take; kEven: a lane's 8 ranks of a step are all there, or none is; kWide, kWideY: the base, and y, is fp32.
+// (Branches around loads, and loops around the whole, make the compiler wait for all that is in flight.)
 constexpr int kLoraWaves = 8;
 
-template <typename X, typename W, int RT, bool kPasses, bool kEven, bool kWide, bool kWideY>
+template <typename X, typename W, int RT, int S, bool kPasses, bool kEven, bool kWide, bool kWideY>
 __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
-    constexpr int NW = kLoraWaves, PF = 8 / RT;
-    constexpr int RP = 16 * RT, KE = 4 * RT;  // ranks of a pass, and of a lane in it
+    using Op = typename Vec8<W>::type;
+    constexpr int NW = kLoraWaves, PF = 8 / RT, RP = 16 * RT, NP = pieces<W, kWideY>();
+    constexpr bool kScaled = std::is_same_v<W, _Float16>;
     extern __shared__ __align__(16) char lds[];
-    const int rp = !kPasses ? RP : (int)((a.r + RP - 1) / RP * RP), pitch = rp + 4;
-    float* u = (float*)lds;                  // [16 tokens][pitch]
-    float* red = u + 16 * pitch;             // [wave][RP ranks][17]
-    float* box = red + NW * RP * 17;         // of waves with a cut row block: at most one of a range
+    const int steps = kPasses ? (int)((a.r + 31) / 32) : S, pitch = 32 * steps + 4;
+    W* ops = (W*)lds;                                // [piece][step][lane][8]
+    float* u = (float*)(ops + NP * steps * 512);     // [16 tokens][pitch]
+    float* factor = u + 16 * pitch;                  // [16 tokens]
+    float* undo = factor + 16;                       // [16 tokens]
+    float* red = undo + 16;                          // [wave][RP ranks][17]
+    float* box = red + NW * RP * 17;                 // of the wave with a cut row block: at most one of a range
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
     // workgroups 8 apart share an XCD: the ranges of one group of tokens run there, for the A that they share
@@ -327,32 +372,32 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     const bool live = c < count;
     const W* br = (const W*)a.b + (int64_t)max(ad, 0) * a.m * a.r;
     // Rows of B for tile j of row block i0: 16 (c / 4) + 4 j + c % 4 as operand, so that a lane's sums are 16
-    // consecutive rows, 16 q .., of token c. Of the ranks k0 .. of a pass lane group q has its own quarter.
-    const auto load_b = [&](W (&v)[4][KE], int64_t i0, int k0) __attribute__((always_inline)) {
-        const int at = k0 + q * KE;
+    // consecutive rows, 16 q .., of token c; of a step's ranks lane group q has 8 q ..
+    const auto load_b = [&](Op (&v)[4], int64_t i0, int step) __attribute__((always_inline)) {
+        const int at = 32 * step + 8 * q;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const W* p = br + min(i0 + 16 * (c >> 2) + 4 * j + (c & 3), a.m - 1) * a.r;
-            if constexpr (kEven) __builtin_memcpy(v[j], p + (at < a.r ? at : 0), sizeof v[j]);
+            if constexpr (kEven) __builtin_memcpy(&v[j], p + (at < a.r ? at : 0), sizeof v[j]);
             else
 #pragma unroll
-                for (int e = 0; e < KE; ++e) v[j][e] = at + e < a.r ? p[at + e] : (W)0.0f;
+                for (int e = 0; e < 8; ++e) v[j][e] = at + e < a.r ? p[at + e] : (W)0.0f;
         }
     };
     const int64_t whole = row1 - (row1 - row0) % 64;  // row blocks up to here are whole
     struct Rows {
-        W b[4][KE];
+        Op b[S][4];
         Raw16<kWide> raw;
     };
     const auto load_rows = [&](Rows& r, int64_t i0) __attribute__((always_inline)) {
-        load_b(r.b, min(i0, a.m - 1), 0);
+#pragma unroll
+        for (int s = 0; s < S; ++s) load_b(r.b[s], min(i0, a.m - 1), s);
         if (a.base && whole > row0) r.raw.fetch(a.base, t * a.ldb + min(i0, whole - 64) + 16 * q);
     };
     Rows next = {};
     if constexpr (kEven) load_rows(next, row0 + 64 * w);
-    float f = 0.0f;
     if (ad >= 0) {
-        f = (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t] : 1.0f);
+        if (w == 0 && lane < 16) factor[c] = (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t] : 1.0f);
         const X* const xr[1] = {(const X*)a.x + t * a.ldx};
         const bool lv[1] = {live};
         int k0 = 0;
@@ -371,45 +416,69 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
                 float s = 0.0f;
 #pragma unroll
                 for (int i2 = 0; i2 < NW; ++i2) s += red[(i2 * RP + k) * 17 + tk];
-                u[tk * pitch + k0 + k] = k0 + k < a.r ? s : 0.0f;
+                if (k0 + k < 32 * steps) u[tk * pitch + k0 + k] = k0 + k < a.r ? s * factor[tk] : 0.0f;
             }
             k0 += RP;
-        } while (kPasses && k0 < rp);
+        } while (kPasses && k0 < 32 * steps);
+        if (RP < 32 && !kPasses)
+            for (int e = threadIdx.x; e < 16 * 16; e += 64 * NW) u[(e & 15) * pitch + 16 + (e >> 4)] = 0.0f;
+        __syncthreads();
+        // operands: 32 threads a token
+        const int tk = threadIdx.x >> 5, part = threadIdx.x & 31;
+        float up = 1.0f;
+        if constexpr (kScaled) {
+            float top = 0.0f;
+            for (int s = 0; s < steps; ++s) top = fmaxf(top, fabsf(u[tk * pitch + 32 * s + part]));
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            const int ex = piece_exponent(top);
+            up = power(ex);
+            if (part == 0) undo[tk] = power(-ex);
+        }
+        for (int s = 0; s < steps; ++s) {
+            float x = u[tk * pitch + 32 * s + part] * up;
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                ops[((p * steps + s) * 64 + part / 8 * 16 + tk) * 8 + part % 8] = p == NP - 1 ? cut_piece<W, true>(x) : cut_piece<W, false>(x);
+        }
         __syncthreads();
     }
     if constexpr (!kEven) load_rows(next, row0 + 64 * w);
-    const float* ur = u + c * pitch + q * KE;
-    const auto product = [&](int64_t i0, W (&b)[4][KE], f32x4 (&acc)[4]) __attribute__((always_inline)) {
+    const float g = kScaled && ad >= 0 ? undo[c] : 1.0f;
+    const auto step_product = [&](int s, Op (&b)[4], f32x4 (&acc)[4]) __attribute__((always_inline)) {
+        if (kEven && 32 * s + 8 * q >= a.r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = Op{};
+#pragma unroll
+        for (int p = NP - 1; p >= 0; --p) {  // the smallest piece first into the sum
+            const Op uo = *reinterpret_cast<const Op*>(ops + ((p * steps + s) * 64 + lane) * 8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = second_mma<W>(b[j], uo, acc[j]);
+        }
+    };
+    const auto product = [&](int64_t i0, Rows& r, f32x4 (&acc)[4]) __attribute__((always_inline)) {
         if (ad < 0) return;
-        int k0 = 0;
-        do {
-            if (kPasses && k0) load_b(b, i0, k0);
-            const bool some = k0 + q * KE < a.r;
 #pragma unroll
-            for (int k = 0; k < KE; k += 4) {
-                const f32x4 uk = *reinterpret_cast<const f32x4*>(ur + k0 + k);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(some ? (float)b[j][k + e] : 0.0f, uk[e], acc[j], 0, 0, 0);
+        for (int s = 0; s < S; ++s) step_product(s, r.b[s], acc);
+        if constexpr (kPasses)
+            for (int s = S; s < steps; ++s) {
+                load_b(r.b[0], i0, s);
+                step_product(s, r.b[0], acc);
             }
-            k0 += RP;
-        } while (kPasses && k0 < rp);
     };
     int64_t i0 = row0 + 64 * w;
     for (; i0 < whole; i0 += 64 * NW) {
         Rows cur = next;
         if constexpr (kEven) load_rows(next, i0 + 64 * NW);
         f32x4 acc[4] = {};
-        product(i0, cur.b, acc);
-        if (live) finish16<kWideY>(a.base != nullptr, a.btype, cur.raw, f, acc, a.y, a.ytype, t * a.ldy + i0 + 16 * q);
+        product(i0, cur, acc);
+        if (live) finish16<kWideY>(a.base != nullptr, a.btype, cur.raw, g, acc, a.y, a.ytype, t * a.ldy + i0 + 16 * q);
         if constexpr (!kEven) load_rows(next, i0 + 64 * NW);
     }
     if (i0 < row1) {
         f32x4 acc[4] = {};
-        product(i0, next.b, acc);
-        finish_cut(a, box, i0, row1, live, t, f, acc, lane);
+        product(i0, next, acc);
+        finish_cut(a, box, i0, row1, live, t, g, acc, lane);
     }
 }
 
@@ -483,37 +552,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
     }
 }
 
-// The second product: y of 64 tokens by a range of rows. u, with the token's and the adapter's factors, lies in LDS as
-// operand: in NP pieces of the adapter's type, of which all but the last are cut off and the last is rounded. bf16: 3
-// pieces hold 25 bits, for a y in fp32; 2 hold 17, for a y of 16 bits, whose own rounding is 2^5 to 2^8 times
-// theirs. fp16: 2 pieces hold 22 bits, of u times the power of two that takes the token's largest value to 2^14 (undone in
-// fp32); 3 hold all. fp32: one, on the fp32 matrix cores. S: steps of 32 ranks.
-// Bound by HBM (base and y are read and written once), so that a wave's loads of the base are all in flight in front of the
-// products.
-template <typename W, int NP, int S> struct Second {
-    typedef W op __attribute__((ext_vector_type(8)));
-    static constexpr int kBytes = 8 * sizeof(W);                                  // of an operand of a lane
-    static constexpr int kOps = NP * S * (kUpTokens / 16) * 64 * kBytes, kLds = kOps + (kUpTokens + kUpWaves * kBox) * 4;
-    static __device__ __forceinline__ f32x4 mma(op a, op b, f32x4 c) {
-        if constexpr (std::is_same_v<W, __bf16>) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-        else if constexpr (std::is_same_v<W, _Float16>) return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-        else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-            return c;
-        }
-    }
-};
-
+// y of 64 tokens by a range of rows. Bound by HBM (base and y are read and written once), so that a wave's loads of the
+// base are all in flight in front of the products. S: steps of 32 ranks.
 template <typename W, int NP, int S, bool kEven, bool kWide, bool kWideY>
 __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_up(LoraArgs a) {
-    using Sd = Second<W, NP, S>;
-    using Op = typename Sd::op;
+    using Op = typename Vec8<W>::type;
     constexpr int NT = kUpTokens / 16;
     constexpr bool kScaled = std::is_same_v<W, _Float16>;
     extern __shared__ __align__(16) char lds[];
     W* ops = (W*)lds;                                          // [piece][step][tile][lane][8]
-    float* undo = (float*)(lds + Sd::kOps);                    // [token]
+    float* undo = (float*)(ops + NP * S * NT * 512);                    // [token]
     float* box = undo + kUpTokens;                             // [wave][kBox]
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
@@ -546,12 +594,11 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
         if constexpr (kScaled) {
             top = fmaxf(top, __shfl_xor(top, 1));
             top = fmaxf(top, __shfl_xor(top, 2));
-            // the exponent of the largest value, in both factors' range
-            const int ex = top > 0.0f && top < INFINITY ? min(max(14 - (int)((__float_as_uint(top) >> 23) - 127), -126), 126) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+            const int ex = piece_exponent(top);
+            const float up = power(ex);
 #pragma unroll
             for (int i = 0; i < 2 * S; ++i) v[i] *= up;
-            if (part == 0) undo[t] = __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (part == 0) undo[t] = power(-ex);
         }
 #pragma unroll
         for (int i = 0; i < 2 * S; ++i) {
@@ -562,16 +609,8 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float x = v[i][e];
-                    if constexpr (std::is_same_v<W, float>) h[e] = x;
-                    else {
-                        if (p < NP - 1) {  // cut off
-                            x = __builtin_canonicalizef(x);
-                            if constexpr (std::is_same_v<W, __bf16>) h[e] = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(x) >> 16));
-                            else h[e] = (_Float16)__uint_as_float(x == x ? __float_as_uint(x) & 0xFFFFE000u : __float_as_uint(x));
-                        } else h[e] = (W)x;
-                        const float rest = x - (float)h[e];
-                        v[i][e] = rest == rest ? rest : 0.0f;
-                    }
+                    h[e] = p == NP - 1 ? cut_piece<W, true>(x) : cut_piece<W, false>(x);
+                    v[i][e] = x;
                 }
                 __builtin_memcpy(ops + ((((p * S + k / 32) * NT + (t >> 4)) * 64 + k % 32 / 8 * 16 + (t & 15)) * 8 + k % 8), h, sizeof h);
             }
@@ -609,7 +648,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
                         for (int s = 0; s < SB; ++s) {
                             const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s0 + s) * NT + n) * 64 + lane) * 8);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[n][j] = Sd::mma(b[j][s], uo, acc[n][j]);
+                            for (int j = 0; j < 4; ++j) acc[n][j] = second_mma<W>(b[j][s], uo, acc[n][j]);
                         }
         }
     };
@@ -655,20 +694,20 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     }
 }
 
-template <typename X, typename W, int RT, bool kPasses, bool kEven>
+template <typename X, typename W, int RT, int S, bool kPasses, bool kEven>
 void launch_few(const LoraArgs& a, hipStream_t stream) {
     constexpr int NW = kLoraWaves;
-    const size_t rp = ((size_t)a.r + 16 * RT - 1) / (16 * RT) * (16 * RT);
-    const size_t lds = sizeof(float) * (16 * (rp + 4) + NW * 16 * RT * 17 + kBox);
+    const bool wide = a.base && a.btype == BAKRON_F32, wide_y = a.ytype == BAKRON_F32;
+    const size_t steps = kPasses ? (size_t)(a.r + 31) / 32 : S, np = wide_y ? pieces<W, true>() : pieces<W, false>();
+    const size_t lds = np * steps * 512 * sizeof(W) + sizeof(float) * (16 * (32 * steps + 4) + 32 + NW * 16 * RT * 17 + kBox);
     const int64_t groups = (a.T + 15) / 16 * a.slots;
     const dim3 grid((unsigned)((groups + 7) / 8 * 8 * a.row_blocks)), threads(64 * NW);
-    const bool wide = a.base && a.btype == BAKRON_F32;
-    if (a.ytype == BAKRON_F32) {
-        if (wide) hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, true, true>), grid, threads, lds, stream, a);
-        else hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, false, true>), grid, threads, lds, stream, a);
+    if (wide_y) {
+        if (wide) hipLaunchKernelGGL((k_lora<X, W, RT, S, kPasses, kEven, true, true>), grid, threads, lds, stream, a);
+        else hipLaunchKernelGGL((k_lora<X, W, RT, S, kPasses, kEven, false, true>), grid, threads, lds, stream, a);
     } else {
-        if (wide) hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, true, false>), grid, threads, lds, stream, a);
-        else hipLaunchKernelGGL((k_lora<X, W, RT, kPasses, kEven, false, false>), grid, threads, lds, stream, a);
+        if (wide) hipLaunchKernelGGL((k_lora<X, W, RT, S, kPasses, kEven, true, false>), grid, threads, lds, stream, a);
+        else hipLaunchKernelGGL((k_lora<X, W, RT, S, kPasses, kEven, false, false>), grid, threads, lds, stream, a);
     }
 }
 
@@ -682,7 +721,7 @@ void launch_down(const LoraArgs& a, hipStream_t stream) {
 template <typename W, int NP, int S, bool kEven, bool kWideY>
 void launch_up(const LoraArgs& a, hipStream_t stream) {
     const int64_t tiles = (a.T + kUpTokens - 1) / kUpTokens;
-    constexpr size_t lds = Second<W, NP, S>::kLds;
+    constexpr size_t lds = NP * S * (kUpTokens / 16) * 512 * sizeof(W) + (kUpTokens + kUpWaves * kBox) * 4;
     const dim3 grid((unsigned)(tiles * a.row_blocks)), threads(64 * kUpWaves);
     if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
     else hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
@@ -700,10 +739,10 @@ inline bool lora_few(int64_t T, int64_t r) { return T <= 64 || r > 128; }
 template <typename X, typename W>
 void launch_lora_types(const LoraArgs& a, hipStream_t stream) {
     if (lora_few(a.T, a.r)) {
-        if (a.r % 4 != 0) launch_few<X, W, 1, true, false>(a, stream);
-        else if (a.r <= 16 || a.r % 8 != 0 || (a.r > 32 && a.r % 16 != 0)) launch_few<X, W, 1, true, true>(a, stream);
-        else if (a.r <= 32) launch_few<X, W, 2, false, true>(a, stream);
-        else launch_few<X, W, 4, true, true>(a, stream);
+        if (a.r % 8 != 0) launch_few<X, W, 4, 1, true, false>(a, stream);
+        else if (a.r <= 16) launch_few<X, W, 1, 1, false, true>(a, stream);
+        else if (a.r <= 32) launch_few<X, W, 2, 1, false, true>(a, stream);
+        else launch_few<X, W, 4, sizeof(W) == 4 ? 1 : 2, true, true>(a, stream);
         return;
     }
     if (a.r <= 16) launch_down<X, W, 1>(a, stream);
