@@ -61,8 +61,9 @@ int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, con
             a.splits = column_splits(a.T);
             a.slots = (int)std::max<int64_t>(1, std::min<int64_t>({16, R, 4 * cus / ((a.T + kDownTokens - 1) / kDownTokens * a.splits)}));
             const int64_t whole = m / 64 * 64;
-            ranges = std::max<int64_t>(1, std::min((whole + 255) / 256, 8 * cus / ((a.T + kUpTokens - 1) / kUpTokens)));
-            a.rows_each = std::max<int64_t>(64, ((whole + ranges - 1) / ranges + 63) / 64 * 64);
+            constexpr int64_t kRows = 64 * kUpWaves;  // of a workgroup's turn
+            ranges = std::max<int64_t>(1, 2 * cus / ((a.T + kUpTokens - 1) / kUpTokens));
+            a.rows_each = std::max<int64_t>(1, ((whole + kRows - 1) / kRows + ranges - 1) / ranges) * kRows;
             a.row_blocks = (int)((whole + a.rows_each - 1) / a.rows_each) + (m > whole);
         }
         if (wtype == BAKRON_F32) launch_lora_adapters<float>(a, xtype, stream);

@@ -220,10 +220,12 @@ __device__ __forceinline__ void finish_cut(const LoraArgs& a, float* box, int64_
 }
 
 // The first product of RT rank tiles from rank k0 on by the NT column tiles of tokens xr over blocks first, first + step, ..
-// of a row and, for the last of them, the block that its end cuts. The lane's sums: ranks 16 j + 4 q .. of column c.
+// of a row and, for the last of them, the block that its end cuts. The lane's sums: ranks 16 j + 4 q .. of column c. Whole
+// blocks are counted from `turn` on, and around: rows a power of two apart fall on one memory channel, column by column,
+// and workgroups that start in different columns use different ones.
 template <typename X, typename W, int RT, int NT, int PF>
 __device__ __forceinline__ void first_product(const X* const (&xr)[NT], const bool (&live)[NT], const W* ar, int64_t r, int64_t n, int k0, int first,
-                                              int step, int q, int c, f32x4 (&acc)[RT][NT]) {
+                                              int step, int turn, int q, int c, f32x4 (&acc)[RT][NT]) {
     using F = First<X, W>;
     using Part = typename F::Part;
     const int blocks = (int)(n / F::kBlock);  // whole ones
@@ -235,7 +237,9 @@ __device__ __forceinline__ void first_product(const X* const (&xr)[NT], const bo
         Words<F, X> xp[PF][NT];
         Words<F, W> ap[PF][RT];
         const auto fetch = [&](int s, int b) __attribute__((always_inline)) {
-            const int64_t at = (int64_t)min(b, blocks - 1) * F::kBlock + q * F::kElems;
+            int k = min(b, blocks - 1) + turn;
+            k -= k >= blocks ? blocks : 0;
+            const int64_t at = (int64_t)k * F::kBlock + q * F::kElems;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 xp[s][t] = Words<F, X>{};
@@ -403,7 +407,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
         int k0 = 0;
         do {
             f32x4 acc[RT][1] = {};
-            first_product<X, W, RT, 1, PF>(xr, lv, (const W*)a.a + (int64_t)ad * a.r * a.n, a.r, a.n, k0, w, NW, q, c, acc);
+            first_product<X, W, RT, 1, PF>(xr, lv, (const W*)a.a + (int64_t)ad * a.r * a.n, a.r, a.n, k0, w, NW, 0, q, c, acc);
             // sums of the waves, in their order
             if (kPasses) __syncthreads();
 #pragma unroll
@@ -514,6 +518,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
             }
         }
         const W* ar = (const W*)a.a + (int64_t)ad * a.r * a.n;
+        const int blocks = (int)(a.n / First<X, W>::kBlock), turn = blocks ? blockIdx.x / 8 * 2 % blocks : 0;
         const X* const x0 = (const X*)a.x + (t0 + __shfl(tok, c)) * a.ldx;
         const X* const x1 = (const X*)a.x + (t0 + __shfl(tok, c + 16)) * a.ldx;
         for (int k0 = 0; k0 < a.rp; k0 += RP) {
@@ -521,12 +526,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
             if (count > 16) {
                 const X* const xr[2] = {x0, x1};
                 const bool lv[2] = {true, c + 16 < count};
-                first_product<X, W, RT, 2, RT == 4 ? 1 : 2>(xr, lv, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, acc);
+                first_product<X, W, RT, 2, RT == 4 ? 1 : 2>(xr, lv, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, turn, q, c, acc);
             } else {
                 const X* const xr[1] = {x0};
                 const bool lv[1] = {c < count};
                 f32x4 one[RT][1] = {};
-                first_product<X, W, RT, 1, RT == 4 ? 1 : 2>(xr, lv, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, q, c, one);
+                first_product<X, W, RT, 1, RT == 4 ? 1 : 2>(xr, lv, ar, a.r, a.n, k0, split * NW + w, a.splits * NW, turn, q, c, one);
 #pragma unroll
                 for (int j = 0; j < RT; ++j) acc[j][0] = one[j][0];
             }
@@ -670,10 +675,21 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
         }
         return;
     }
-    for (int64_t i0 = row0 + 64 * w; i0 < row1; i0 += 64 * kUpWaves) {
-        constexpr bool kAhead = !std::is_same_v<W, float>;  // fp32 rows of B leave no registers for the base
-        Raw16<kWide> raw[NT] = {};
+    // a base of 16 bits is one row block ahead; more leaves no registers
+    constexpr bool kAhead = !kWide && sizeof(W) == 2 && kEven;
+    Raw16<kWide> next[NT] = {};
+    const auto load_base = [&](int64_t i0) __attribute__((always_inline)) {
         if (kAhead && a.base)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) next[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
+    };
+    if (row0 + 64 * w < row1) load_base(row0 + 64 * w);
+    for (int64_t i0 = row0 + 64 * w; i0 < row1; i0 += 64 * kUpWaves) {
+        Raw16<kWide> raw[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) raw[n] = next[n];
+        if (i0 + 64 * kUpWaves < row1) load_base(i0 + 64 * kUpWaves);
+        if (!kAhead && a.base)
 #pragma unroll
             for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
         uint64_t left = __ballot(lane < tokens);
@@ -686,7 +702,6 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 if (members >> (16 * n) >> c & 1) {
-                    if (!kAhead && a.base) raw[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
                     finish16<kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
                                     token(n) * a.ldy + i0 + 16 * q);
                 }
