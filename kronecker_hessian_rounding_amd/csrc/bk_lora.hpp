@@ -27,6 +27,7 @@ namespace bk {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
@@ -133,80 +134,96 @@ __device__ __forceinline__ typename F::Part cut_part(const S* p, int count) {
     return convert<F, S, W>(w);
 }
 
-// 16 elements of a row in flight, of 2 or 4 bytes each, and as values (4 j ..).
-__device__ __forceinline__ u32x4 load_unit(const char* p) {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
+// The second product takes 64 rows of B as four operand tiles; which row of a tile is which is free. Lane group q's sums
+// of tile j are the four rows from tile_row(j, q) on: 16 bytes of y (fp32: of a tile; 16 bits: of two) lie together, and
+// next to them those of the next group, so that an access of 16 bytes a lane covers 64 bytes of a token's row.
+template <bool kWideY>
+__device__ __forceinline__ int tile_row(int j, int q) {
+    return kWideY ? 16 * j + 4 * q : 32 * (j >> 1) + 8 * q + 4 * (j & 1);
 }
-template <bool kWide> struct Raw16;
-template <> struct Raw16<false> {
-    u32x4 a, b;
-    __device__ __forceinline__ void fetch(const void* row, int64_t i) {
-        const char* p = (const char*)row + 2 * i;
-        a = load_unit(p);
-        b = load_unit(p + 16);
+__device__ __forceinline__ f32x4 value4(u32x2 w, int type) {
+    f32x4 f;
+    if (type == BAKRON_F16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        const h4 h = __builtin_bit_cast(h4, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = (float)h[e];
+    } else {
+        f[0] = __uint_as_float(w[0] << 16);
+        f[1] = __uint_as_float(w[0] & 0xFFFF0000u);
+        f[2] = __uint_as_float(w[1] << 16);
+        f[3] = __uint_as_float(w[1] & 0xFFFF0000u);
     }
-    template <int J>
-    __device__ __forceinline__ f32x4 value(int type) const {
-        const u32x4 w = J < 2 ? a : b;
-        f32x4 f;
-        if (type == BAKRON_F16) {
-            const f16x8 h = __builtin_bit_cast(f16x8, w);
+    return f;
+}
+// A lane's 16 values of the base in flight (fp32: kWide), `row` the 64 rows' first element.
+template <bool kWide, bool kWideY> struct Raw16;
+template <bool kWideY> struct Raw16<true, kWideY> {
+    u32x4 v[4];
+    __device__ __forceinline__ void fetch(const void* base, int64_t row, int q) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = (float)h[J % 2 * 4 + e];
-        } else {
-            const bf16x8 h = __builtin_bit_cast(bf16x8, w);
+        for (int j = 0; j < 4; ++j) __builtin_memcpy(&v[j], (const float*)base + row + tile_row<kWideY>(j, q), 16);
+    }
+    __device__ __forceinline__ f32x4 value(int j, int) const { return __builtin_bit_cast(f32x4, v[j]); }
+};
+template <> struct Raw16<false, false> {
+    u32x4 v[2];
+    __device__ __forceinline__ void fetch(const void* base, int64_t row, int q) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = (float)h[J % 2 * 4 + e];
-        }
-        return f;
+        for (int j = 0; j < 2; ++j) __builtin_memcpy(&v[j], (const uint16_t*)base + row + tile_row<false>(2 * j, q), 16);
+    }
+    __device__ __forceinline__ f32x4 value(int j, int type) const {
+        const u32x4 w = v[j / 2];
+        return value4(j % 2 ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]}, type);
     }
 };
-template <> struct Raw16<true> {
-    u32x4 a, b, c, d;
-    __device__ __forceinline__ void fetch(const void* row, int64_t i) {
-        const char* p = (const char*)row + 4 * i;
-        a = load_unit(p);
-        b = load_unit(p + 16);
-        c = load_unit(p + 32);
-        d = load_unit(p + 48);
+template <> struct Raw16<false, true> {
+    u32x2 v[4];
+    __device__ __forceinline__ void fetch(const void* base, int64_t row, int q) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) __builtin_memcpy(&v[j], (const uint16_t*)base + row + tile_row<true>(j, q), 8);
     }
-    template <int J>
-    __device__ __forceinline__ f32x4 value(int) const {
-        return __builtin_bit_cast(f32x4, J == 0 ? a : J == 1 ? b : J == 2 ? c : d);
-    }
+    __device__ __forceinline__ f32x4 value(int j, int type) const { return value4(v[j], type); }
 };
-// y = base + g * sum for 16 whole rows of a token; raw holds the base. kWideY: y is fp32.
-template <bool kWideY, bool kWide>
-__device__ __forceinline__ void finish16(bool based, int btype, const Raw16<kWide>& raw, float g, const f32x4 (&sum)[4], void* y,
-                                         int ytype, int64_t yi) {
-    const auto part = [&](auto jc) __attribute__((always_inline)) {
-        constexpr int J = decltype(jc)::value;
+// y = base + g * sum for a lane's 16 rows of 64 whole ones of a token; raw holds the base.
+template <bool kWide, bool kWideY>
+__device__ __forceinline__ void finish16(bool based, int btype, const Raw16<kWide, kWideY>& raw, float g, const f32x4 (&sum)[4],
+                                         void* y, int ytype, int64_t row, int q) {
+    f32x4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
         f32x4 b = {};
-        if (based) b = raw.template value<J>(btype);
-        f4 v;
+        if (based) b = raw.value(j, btype);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(g, sum[J][e], b[e]);
-        if constexpr (kWideY) store4(y, BAKRON_F32, yi + 4 * J, v, 4);
-        else if (ytype == BAKRON_F16) store4(y, BAKRON_F16, yi + 4 * J, v, 4);
-        else store4(y, BAKRON_BF16, yi + 4 * J, v, 4);
-    };
-    part(std::integral_constant<int, 0>());
-    part(std::integral_constant<int, 1>());
-    part(std::integral_constant<int, 2>());
-    part(std::integral_constant<int, 3>());
+        for (int e = 0; e < 4; ++e) v[j][e] = fmaf(g, sum[j][e], b[e]);
+    }
+    if constexpr (kWideY) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) __builtin_memcpy((float*)y + row + tile_row<true>(j, q), &v[j], 16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            uint16_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = v[j + e / 4][e % 4];
+                h[e] = ytype == BAKRON_F16 ? __builtin_bit_cast(uint16_t, (_Float16)x) : __builtin_bit_cast(uint16_t, (__bf16)x);
+            }
+            __builtin_memcpy((uint16_t*)y + row + tile_row<false>(j, q), h, 16);
+        }
+    }
 }
 // The same for 16 tokens by the 64 rows from i0 on of which the range's end cuts some: through kBox floats of LDS of
 // the wave's own, so that one short loop serves every type. `live` lanes' columns are stored; t is lane c's token.
 constexpr int kBox = 16 * 68;
+template <bool kWideY>
 __device__ __forceinline__ void finish_cut(const LoraArgs& a, float* box, int64_t i0, int64_t row1, bool live, int64_t t, float g,
                                            const f32x4 (&sum)[4], int lane) {
     const uint32_t columns = (uint32_t)__ballot(live && lane < 16);
     wave_fence();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(box + (lane & 15) * 68 + 16 * (lane >> 4) + 4 * j) = g * sum[j];
+        *reinterpret_cast<f32x4*>(box + (lane & 15) * 68 + tile_row<kWideY>(j, lane >> 4)) = g * sum[j];
     wave_fence();
 #pragma unroll 1
     for (int col = 0; col < 16; ++col) {
@@ -375,13 +392,12 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     const int64_t t = t0 + tok;
     const bool live = c < count;
     const W* br = (const W*)a.b + (int64_t)max(ad, 0) * a.m * a.r;
-    // Rows of B for tile j of row block i0: 16 (c / 4) + 4 j + c % 4 as operand, so that a lane's sums are 16
-    // consecutive rows, 16 q .., of token c; of a step's ranks lane group q has 8 q ..
+    // Rows of B for tile j of row block i0 (tile_row); of a step's ranks lane group q has 8 q ..
     const auto load_b = [&](Op (&v)[4], int64_t i0, int step) __attribute__((always_inline)) {
         const int at = 32 * step + 8 * q;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const W* p = br + min(i0 + 16 * (c >> 2) + 4 * j + (c & 3), a.m - 1) * a.r;
+            const W* p = br + min(i0 + tile_row<kWideY>(j, c >> 2) + (c & 3), a.m - 1) * a.r;
             if constexpr (kEven) __builtin_memcpy(&v[j], p + (at < a.r ? at : 0), sizeof v[j]);
             else
 #pragma unroll
@@ -391,12 +407,12 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     const int64_t whole = row1 - (row1 - row0) % 64;  // row blocks up to here are whole
     struct Rows {
         Op b[S][4];
-        Raw16<kWide> raw;
+        Raw16<kWide, kWideY> raw;
     };
     const auto load_rows = [&](Rows& r, int64_t i0) __attribute__((always_inline)) {
 #pragma unroll
         for (int s = 0; s < S; ++s) load_b(r.b[s], min(i0, a.m - 1), s);
-        if (a.base && whole > row0) r.raw.fetch(a.base, t * a.ldb + min(i0, whole - 64) + 16 * q);
+        if (a.base && whole > row0) r.raw.fetch(a.base, t * a.ldb + min(i0, whole - 64), q);
     };
     Rows next = {};
     if constexpr (kEven) load_rows(next, row0 + 64 * w);
@@ -476,13 +492,13 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
         if constexpr (kEven) load_rows(next, i0 + 64 * NW);
         f32x4 acc[4] = {};
         product(i0, cur, acc);
-        if (live) finish16<kWideY>(a.base != nullptr, a.btype, cur.raw, g, acc, a.y, a.ytype, t * a.ldy + i0 + 16 * q);
+        if (live) finish16<kWide, kWideY>(a.base != nullptr, a.btype, cur.raw, g, acc, a.y, a.ytype, t * a.ldy + i0, q);
         if constexpr (!kEven) load_rows(next, i0 + 64 * NW);
     }
     if (i0 < row1) {
         f32x4 acc[4] = {};
         product(i0, next, acc);
-        finish_cut(a, box, i0, row1, live, t, g, acc, lane);
+        finish_cut<kWideY>(a, box, i0, row1, live, t, g, acc, lane);
     }
 }
 
@@ -626,13 +642,13 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     // acc of the tokens of adapter ad for the 64 rows from i0 on
     const auto product = [&](int64_t i0, int ad, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
         const W* br = (const W*)a.b + (int64_t)ad * a.m * a.r;
-        constexpr int SB = kEven && sizeof(W) == 2 && S < 4 ? S : 1;  // steps whose rows of B are in registers at once
+        constexpr int SB = 1;  // steps whose rows of B are in registers at once
 #pragma unroll 1
         for (int s0 = 0; s0 < S && 32 * s0 < a.r; s0 += SB) {
             Op b[4][SB];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const W* p = br + min(i0 + 16 * (c >> 2) + 4 * j + (c & 3), a.m - 1) * a.r;
+                const W* p = br + min(i0 + tile_row<kWideY>(j, c >> 2) + (c & 3), a.m - 1) * a.r;
 #pragma unroll
                 for (int s = 0; s < SB; ++s) {
                     const int at = 32 * (s0 + s) + 8 * q;
@@ -670,28 +686,28 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
                 if (n == w)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) own[j] = acc[n][j];
-            finish_cut(a, box + w * kBox, row0, row1, members >> (16 * w) >> c & 1, token(w), kScaled ? undo[16 * w + c] : 1.0f, own,
+            finish_cut<kWideY>(a, box + w * kBox, row0, row1, members >> (16 * w) >> c & 1, token(w), kScaled ? undo[16 * w + c] : 1.0f, own,
                        lane);
         }
         return;
     }
     // a base of 16 bits is one row block ahead; more leaves no registers
     constexpr bool kAhead = !kWide && sizeof(W) == 2 && kEven;
-    Raw16<kWide> next[NT] = {};
+    Raw16<kWide, kWideY> next[NT] = {};
     const auto load_base = [&](int64_t i0) __attribute__((always_inline)) {
         if (kAhead && a.base)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) next[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
+            for (int n = 0; n < NT; ++n) next[n].fetch(a.base, token(n) * a.ldb + i0, q);
     };
     if (row0 + 64 * w < row1) load_base(row0 + 64 * w);
     for (int64_t i0 = row0 + 64 * w; i0 < row1; i0 += 64 * kUpWaves) {
-        Raw16<kWide> raw[NT];
+        Raw16<kWide, kWideY> raw[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) raw[n] = next[n];
         if (i0 + 64 * kUpWaves < row1) load_base(i0 + 64 * kUpWaves);
         if (!kAhead && a.base)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, token(n) * a.ldb + i0 + 16 * q);
+            for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, token(n) * a.ldb + i0, q);
         uint64_t left = __ballot(lane < tokens);
         while (left) {
             const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
@@ -702,8 +718,8 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 if (members >> (16 * n) >> c & 1) {
-                    finish16<kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
-                                    token(n) * a.ldy + i0 + 16 * q);
+                    finish16<kWide, kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
+                                    token(n) * a.ldy + i0, q);
                 }
         }
     }
