@@ -363,9 +363,10 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     const int q = lane >> 4, c = lane & 15;
     // workgroups 8 apart share an XCD: the ranges of one group of tokens run there, for the A that they share
     const int span = blockIdx.x / (8 * a.row_blocks), off = blockIdx.x % (8 * a.row_blocks);
-    const int group = span * 8 + off % 8, rb = off / 8, slot = group % a.slots;
-    const int64_t t0 = (int64_t)(group / a.slots) * 16;
-    if (t0 >= a.T) return;
+    // (slots outermost: often only the first have work)
+    const int group = span * 8 + off % 8, rb = off / 8, tiles = (int)((a.T + 15) / 16), slot = group / tiles;
+    const int64_t t0 = (int64_t)(group % tiles) * 16;
+    if (slot >= a.slots) return;
     const int64_t row0 = rb * a.rows_each, row1 = min(a.m, row0 + a.rows_each);
     const int tokens = (int)min<int64_t>(16, a.T - t0);
     // the adapter of token c (-1: none); this workgroup's is the slot-th of those that the tile names
@@ -513,8 +514,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
     float* red = (float*)lds;  // [wave][RP ranks][33]
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15, tk = lane & 31;
-    const int split = blockIdx.x % a.splits, slot = blockIdx.x / a.splits % a.slots;
-    const int64_t t0 = (int64_t)(blockIdx.x / a.splits / a.slots) * kDownTokens;
+    // slots outermost: often only the first has work, and its workgroups are to spread over all XCDs
+    const uint32_t tiles = (uint32_t)((a.T + kDownTokens - 1) / kDownTokens);
+    const int split = blockIdx.x % a.splits, slot = blockIdx.x / a.splits / tiles;
+    const int64_t t0 = (int64_t)(blockIdx.x / a.splits % tiles) * kDownTokens;
     const int tokens = (int)min<int64_t>(kDownTokens, a.T - t0);
     int mine = tk < tokens ? a.ids[t0 + tk] : 0;
     if (mine < 0 || mine >= a.R) mine = -1;
