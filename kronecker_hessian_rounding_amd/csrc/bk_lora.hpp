@@ -340,6 +340,39 @@ __device__ __forceinline__ W cut_piece(float& x) {
     return h;
 }
 
+// A lane's 8 ranks from `at` on of the rows of B that tile_row gives it (rows past the last: the last again), 0 from rank
+// r on. kEven: r is a multiple of 8, so that all are there or none. Else a read of 8 goes past the row's end, into the
+// next row, and what it finds there is dropped; where B itself ends, elements are read one by one.
+template <typename W, bool kEven, bool kWideY>
+__device__ __forceinline__ void load_rows_of_b(typename Vec8<W>::type (&v)[4], const LoraArgs& a, int64_t adapter, int64_t i0, int at,
+                                               int c) {
+    const W* b = (const W*)a.b;
+    int64_t pos[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        pos[j] = (adapter * a.m + min(i0 + tile_row<kWideY>(j, c >> 2) + (c & 3), a.m - 1)) * a.r + (kEven && at >= a.r ? 0 : at);
+    if constexpr (kEven) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) __builtin_memcpy(&v[j], b + pos[j], sizeof v[j]);
+    } else {
+        const int64_t last = a.R * a.m * a.r - 8;
+        const bool cut = max(max(pos[0], pos[1]), max(pos[2], pos[3])) > last;
+        if (__ballot(cut)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[j][e] = at + e < a.r ? b[pos[j] + e] : (W)0.0f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) __builtin_memcpy(&v[j], b + pos[j], sizeof v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = at + e < a.r ? v[j][e] : (W)0.0f;
+    }
+}
+
 // ---------------------------------------------------------------- few tokens
 // RT: tiles of 16 ranks of a pass of the first product, S: steps of 32 ranks of the second; kPasses: r may be more than they
 // take; kEven: a lane's 8 ranks of a step are all there, or none is; kWide, kWideY: the base, and y, is fp32.
@@ -392,19 +425,6 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     }
     const int64_t t = t0 + tok;
     const bool live = c < count;
-    const W* br = (const W*)a.b + (int64_t)max(ad, 0) * a.m * a.r;
-    // Rows of B for tile j of row block i0 (tile_row); of a step's ranks lane group q has 8 q ..
-    const auto load_b = [&](Op (&v)[4], int64_t i0, int step) __attribute__((always_inline)) {
-        const int at = 32 * step + 8 * q;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const W* p = br + min(i0 + tile_row<kWideY>(j, c >> 2) + (c & 3), a.m - 1) * a.r;
-            if constexpr (kEven) __builtin_memcpy(&v[j], p + (at < a.r ? at : 0), sizeof v[j]);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[j][e] = at + e < a.r ? p[at + e] : (W)0.0f;
-        }
-    };
     const int64_t whole = row1 - (row1 - row0) % 64;  // row blocks up to here are whole
     struct Rows {
         Op b[S][4];
@@ -412,7 +432,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     };
     const auto load_rows = [&](Rows& r, int64_t i0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) load_b(r.b[s], min(i0, a.m - 1), s);
+        for (int s = 0; s < S; ++s) load_rows_of_b<W, kEven, kWideY>(r.b[s], a, max(ad, 0), min(i0, a.m - 1), 32 * s + 8 * q, c);
         if (a.base && whole > row0) r.raw.fetch(a.base, t * a.ldb + min(i0, whole - 64), q);
     };
     Rows next = {};
@@ -483,7 +503,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
         for (int s = 0; s < S; ++s) step_product(s, r.b[s], acc);
         if constexpr (kPasses)
             for (int s = S; s < steps; ++s) {
-                load_b(r.b[0], i0, s);
+                load_rows_of_b<W, kEven, kWideY>(r.b[0], a, ad, i0, 32 * s + 8 * q, c);
                 step_product(s, r.b[0], acc);
             }
     };
@@ -596,10 +616,10 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     const int tokens = (int)min<int64_t>(kUpTokens, a.T - t0);
     int mine = lane < tokens ? a.ids[t0 + lane] : -1;
     if (mine < 0 || mine >= a.R) mine = -1;
-    {
-        // four threads a token, ranks 4 part .., 16 apart
-        const int t = threadIdx.x >> 2, part = threadIdx.x & 3;
-        const int ad = __shfl(mine, t & 63);
+    // four threads a token, ranks 4 part .., 16 apart
+    const int ut = threadIdx.x >> 2, part = threadIdx.x & 3, uad = __shfl(mine, ut & 63);
+    if (ut < kUpTokens) {
+        const int t = ut, ad = uad;
         const float f = ad < 0 ? 0.0f : (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t0 + t] : 1.0f);
         f32x4 v[2 * S];
         float top = 0.0f;
@@ -644,36 +664,22 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     const auto token = [&](int n) __attribute__((always_inline)) { return t0 + min(16 * n + c, tokens - 1); };
     // acc of the tokens of adapter ad for the 64 rows from i0 on
     const auto product = [&](int64_t i0, int ad, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
-        const W* br = (const W*)a.b + (int64_t)ad * a.m * a.r;
-        constexpr int SB = 1;  // steps whose rows of B are in registers at once
 #pragma unroll 1
-        for (int s0 = 0; s0 < S && 32 * s0 < a.r; s0 += SB) {
-            Op b[4][SB];
+        for (int s = 0; s < S && 32 * s < a.r; ++s) {
+            Op b[4];
+            load_rows_of_b<W, kEven, kWideY>(b, a, ad, i0, 32 * s + 8 * q, c);
+            if (kEven && 32 * s + 8 * q >= a.r)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const W* p = br + min(i0 + tile_row<kWideY>(j, c >> 2) + (c & 3), a.m - 1) * a.r;
-#pragma unroll
-                for (int s = 0; s < SB; ++s) {
-                    const int at = 32 * (s0 + s) + 8 * q;
-                    if constexpr (kEven) {
-                        __builtin_memcpy(&b[j][s], p + (at < a.r ? at : 0), sizeof(Op));
-                        if (at >= a.r) b[j][s] = Op{};
-                    } else
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) b[j][s][e] = at + e < a.r ? p[at + e] : (W)0.0f;
-                }
-            }
+                for (int j = 0; j < 4; ++j) b[j] = Op{};
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 if (members >> (16 * n) & 0xFFFF)
 #pragma unroll
-                    for (int p = NP - 1; p >= 0; --p)  // the smallest piece first into the sum
+                    for (int p = NP - 1; p >= 0; --p) {  // the smallest piece first into the sum
+                        const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s) * NT + n) * 64 + lane) * 8);
 #pragma unroll
-                        for (int s = 0; s < SB; ++s) {
-                            const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s0 + s) * NT + n) * 64 + lane) * 8);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[n][j] = second_mma<W>(b[j][s], uo, acc[n][j]);
-                        }
+                        for (int j = 0; j < 4; ++j) acc[n][j] = second_mma<W>(b[j], uo, acc[n][j]);
+                    }
         }
     };
     if (row0 == whole) {  // a wave for 16 tokens
@@ -773,7 +779,8 @@ inline bool lora_few(int64_t T, int64_t r) { return T <= 64 || r > 128; }
 template <typename X, typename W>
 void launch_lora_types(const LoraArgs& a, hipStream_t stream) {
     if (lora_few(a.T, a.r)) {
-        if (a.r % 8 != 0) launch_few<X, W, 4, 1, true, false>(a, stream);
+        if (a.r % 8 != 0 && a.r <= 16) launch_few<X, W, 1, 1, false, false>(a, stream);
+        else if (a.r % 8 != 0) launch_few<X, W, 4, 1, true, false>(a, stream);
         else if (a.r <= 16) launch_few<X, W, 1, 1, false, true>(a, stream);
         else if (a.r <= 32) launch_few<X, W, 2, 1, false, true>(a, stream);
         else launch_few<X, W, 4, sizeof(W) == 4 ? 1 : 2, true, true>(a, stream);
