@@ -422,10 +422,10 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
  *     smaller rank are padded with zeros.
  *   scales: [R] fp32, or NULL for 1. ids: [T] int32; an id outside 0 .. R - 1 means no adapter: Y[t] = base[t].
  *   base: T x m of btype (F32, F16 or BF16), ldb >= m, or NULL for 0. Y: T x m of ytype, ldy >= m.
- *   Products are exact (8 and 16 bits) or fp32, all sums are fp32, u is fp32 (past 64 tokens of 16-bit adapters it enters its
- *   second product with 22 bits or more where Y is fp32, else 17 or more), and Y is rounded once. Token t's result depends on
+ *   Products are exact (8 and 16 bits) or fp32, all sums are fp32, u is fp32 (with 16-bit adapters it enters its second
+ *   product with 22 bits or more where Y is fp32, else 17 or more), and Y is rounded once. Token t's result depends on
  *   its own row and adapter only. For given sizes, types and ids it is deterministic.
- *   ws: at least bakron_lora_workspace_bytes(T, r) bytes, 16-byte aligned (0 up to 64 tokens: NULL will do). Calls that
+ *   ws: at least bakron_lora_workspace_bytes(T, r) bytes, 16-byte aligned (0 for up to 128 tokens with r <= 32: NULL will do). Calls that
  *     overlap need one each.
  *   Y may be base itself (same pointer, type and ld); no other overlap of Y with a buffer of the call is allowed.
  * Errors: INVALID_ARG for NULL X, A, B, ids or Y (T > 0), T < 0 or > 2^40, n, m < 1 or >= 2^28, r < 1 or > 512, R < 1 or

@@ -12,13 +12,13 @@ namespace {
 
 // Tokens of one round of launches (a grid has fewer than 2^32 threads), and the parts of the columns that u is formed in.
 constexpr int64_t kRound = (int64_t)1 << 16;
-int column_splits(int64_t T) { return T <= 2048 ? 4 : T <= 4096 ? 2 : 1; }
+int most_splits(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(16, 256 / ((T + kDownTokens - 1) / kDownTokens))); }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t T, int64_t r) {
     const int64_t t = std::min(T, kRound);
-    return lora_few(t, r) ? 0 : sizeof(float) * column_splits(t) * t * ((r + 15) / 16 * 16);
+    return lora_few(t, r) ? 0 : sizeof(float) * most_splits(t) * t * ((r + 15) / 16 * 16);
 }
 
 int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, const float* xs, const void* A, const void* B,
@@ -58,13 +58,17 @@ int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, con
             a.rows_each = ((m + ranges - 1) / ranges + 63) / 64 * 64;
             a.row_blocks = (int)((m + a.rows_each - 1) / a.rows_each);
         } else {
-            a.splits = column_splits(a.T);
+            // a wave of a split has a block of columns at least
+            const int64_t blocks = n / (wtype == BAKRON_F32 ? 32 : 64);
+            a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most_splits(a.T), blocks / kDownWaves));
             a.slots = (int)std::max<int64_t>(1, std::min<int64_t>({16, R, 4 * cus / ((a.T + kDownTokens - 1) / kDownTokens * a.splits)}));
             const int64_t whole = m / 64 * 64;
             constexpr int64_t kRows = 64 * kUpWaves;  // of a workgroup's turn
             ranges = std::max<int64_t>(1, 2 * cus / ((a.T + kUpTokens - 1) / kUpTokens));
             a.rows_each = std::max<int64_t>(1, ((whole + kRows - 1) / kRows + ranges - 1) / ranges) * kRows;
             a.row_blocks = (int)((whole + a.rows_each - 1) / a.rows_each) + (m > whole);
+            const int64_t each = (a.T + kUpTokens - 1) / kUpTokens * a.row_blocks;
+            a.up_slots = (int)std::max<int64_t>(1, std::min<int64_t>({16, R + 1, a.T, 2 * cus / each}));
         }
         if (wtype == BAKRON_F32) launch_lora_adapters<float>(a, xtype, stream);
         else if (wtype == BAKRON_F16) launch_lora_adapters<_Float16>(a, xtype, stream);

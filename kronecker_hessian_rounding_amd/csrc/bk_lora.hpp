@@ -47,7 +47,7 @@ struct LoraArgs {
     int64_t rows_each;         // rows of a range, a multiple of 64
     // more tokens
     float* u;                  // [split][T][rp]
-    int splits, rp;
+    int splits, rp, up_slots;
 };
 
 // The operands of the first product. A block is the columns of one operand read: a row's share is its 4 lanes'
@@ -609,13 +609,27 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     float* box = undo + kUpTokens;                             // [wave][kBox]
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
-    const int64_t t0 = (int64_t)(blockIdx.x / a.row_blocks) * kUpTokens;
+    const uint32_t tiles = (uint32_t)((a.T + kUpTokens - 1) / kUpTokens);
+    const int slot = blockIdx.x / a.row_blocks / tiles;  // outermost: often only the first has work
+    const int64_t t0 = (int64_t)(blockIdx.x / a.row_blocks % tiles) * kUpTokens;
     // whole row blocks first; the last range is that of the rows behind them
     const int64_t whole = a.m / 64 * 64, row0 = min((blockIdx.x % a.row_blocks) * a.rows_each, whole);
     const int64_t row1 = row0 < whole ? min(whole, row0 + a.rows_each) : a.m;
     const int tokens = (int)min<int64_t>(kUpTokens, a.T - t0);
     int mine = lane < tokens ? a.ids[t0 + lane] : -1;
     if (mine < 0 || mine >= a.R) mine = -1;
+    // the tokens of this slot's adapters (no adapter counts as one): every slots-th of those that the tile names
+    uint64_t ours = 0;
+    {
+        uint64_t left = __ballot(lane < tokens);
+        for (int i = 0; left; ++i) {
+            const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            const uint64_t members = __ballot(lane < tokens && mine == ad);
+            left &= ~members;
+            if (i % a.up_slots == slot) ours |= members;
+        }
+    }
+    if (ours == 0) return;
     // four threads a token, ranks 4 part .., 16 apart
     const int ut = threadIdx.x >> 2, part = threadIdx.x & 3, uad = __shfl(mine, ut & 63);
     if (ut < kUpTokens) {
@@ -627,7 +641,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
         for (int i = 0; i < 2 * S; ++i) {
             const int k = 16 * i + 4 * part;
             v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (ad >= 0 && k < a.rp) {
+            if (ad >= 0 && k < a.rp && (ours >> t & 1)) {
                 for (int s = 0; s < a.splits; ++s)
                     v[i] += *reinterpret_cast<const f32x4*>(a.u + ((int64_t)s * a.T + t0 + t) * a.rp + k);
                 v[i] *= f;
@@ -662,28 +676,35 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     }
     __syncthreads();
     const auto token = [&](int n) __attribute__((always_inline)) { return t0 + min(16 * n + c, tokens - 1); };
-    // acc of the tokens of adapter ad for the 64 rows from i0 on
+    // (of other slots' tokens the base is not read: the first of ours again)
+    const auto base_token = [&](int n) __attribute__((always_inline)) {
+        return t0 + (ours >> (16 * n + c) & 1 ? 16 * n + c : (int)__builtin_ctzll(ours));
+    };
+    // acc of the tokens of adapter ad for the 64 rows from i0 on, a step of ranks at a time
+    const auto multiply = [&](Op (&b)[4], int s, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
+        if (kEven && 32 * s + 8 * q >= a.r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = Op{};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (members >> (16 * n) & 0xFFFF)
+#pragma unroll
+                for (int p = NP - 1; p >= 0; --p) {  // the smallest piece first into the sum
+                    const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s) * NT + n) * 64 + lane) * 8);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[n][j] = second_mma<W>(b[j], uo, acc[n][j]);
+                }
+    };
     const auto product = [&](int64_t i0, int ad, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int s = 0; s < S && 32 * s < a.r; ++s) {
             Op b[4];
             load_rows_of_b<W, kEven, kWideY>(b, a, ad, i0, 32 * s + 8 * q, c);
-            if (kEven && 32 * s + 8 * q >= a.r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = Op{};
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (members >> (16 * n) & 0xFFFF)
-#pragma unroll
-                    for (int p = NP - 1; p >= 0; --p) {  // the smallest piece first into the sum
-                        const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s) * NT + n) * 64 + lane) * 8);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[n][j] = second_mma<W>(b[j], uo, acc[n][j]);
-                    }
+            multiply(b, s, members, acc);
         }
     };
     if (row0 == whole) {  // a wave for 16 tokens
-        uint64_t left = w * 16 < tokens ? __ballot(lane < tokens && lane >> 4 == w) : 0;
+        uint64_t left = ours & ((uint64_t)0xFFFF << (16 * w));
         while (left) {
             const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
             const uint64_t members = __ballot(lane < tokens && lane >> 4 == w && mine == ad);
@@ -706,31 +727,63 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     const auto load_base = [&](int64_t i0) __attribute__((always_inline)) {
         if (kAhead && a.base)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) next[n].fetch(a.base, token(n) * a.ldb + i0, q);
+            for (int n = 0; n < NT; ++n) next[n].fetch(a.base, base_token(n) * a.ldb + i0, q);
     };
-    if (row0 + 64 * w < row1) load_base(row0 + 64 * w);
-    for (int64_t i0 = row0 + 64 * w; i0 < row1; i0 += 64 * kUpWaves) {
-        Raw16<kWide, kWideY> raw[NT];
+    // turns: the adapters of a row block, then those of the next; the rows of B are a turn ahead (r <= 32)
+    constexpr bool kTurnAhead = S == 1 && kEven && sizeof(W) == 2;
+    struct Turn {
+        int64_t i0;
+        uint64_t left, members;
+        int ad;
+    };
+    const auto pick = [&](Turn& t) __attribute__((always_inline)) {
+        t.ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(t.left));
+        t.members = __ballot(lane < tokens && mine == t.ad);
+        t.left &= ~t.members;
+    };
+    Turn cur = {row0 + 64 * w, ours, 0, 0};
+    if (cur.i0 >= row1) return;
+    pick(cur);
+    load_base(cur.i0);
+    Raw16<kWide, kWideY> raw[NT];
+    Op b[4] = {};
+    if constexpr (kTurnAhead) load_rows_of_b<W, kEven, kWideY>(b, a, max(cur.ad, 0), cur.i0, 8 * q, c);
+    bool fresh = true;  // the first turn of its row block
+    while (true) {
+        if (fresh) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) raw[n] = next[n];
-        if (i0 + 64 * kUpWaves < row1) load_base(i0 + 64 * kUpWaves);
-        if (!kAhead && a.base)
+            for (int n = 0; n < NT; ++n) raw[n] = next[n];
+            if (cur.i0 + 64 * kUpWaves < row1) load_base(cur.i0 + 64 * kUpWaves);
+            if (!kAhead && a.base)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, token(n) * a.ldb + i0, q);
-        uint64_t left = __ballot(lane < tokens);
-        while (left) {
-            const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-            const uint64_t members = __ballot(lane < tokens && mine == ad);
-            left &= ~members;
-            f32x4 acc[NT][4] = {};
-            if (ad >= 0) product(i0, ad, members, acc);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (members >> (16 * n) >> c & 1) {
-                    finish16<kWide, kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
-                                    token(n) * a.ldy + i0, q);
-                }
+                for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, base_token(n) * a.ldb + cur.i0, q);
         }
+        Turn then = cur;
+        fresh = cur.left == 0;
+        if (fresh) {
+            then.i0 += 64 * kUpWaves;
+            then.left = ours;
+        }
+        const bool more = then.i0 < row1;
+        pick(then);
+        Op ahead[4];
+        if constexpr (kTurnAhead)
+            load_rows_of_b<W, kEven, kWideY>(ahead, a, max(then.ad, 0), more ? then.i0 : cur.i0, 8 * q, c);
+        f32x4 acc[NT][4] = {};
+        if (cur.ad >= 0) {
+            if constexpr (kTurnAhead) multiply(b, 0, cur.members, acc);
+            else product(cur.i0, cur.ad, cur.members, acc);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (cur.members >> (16 * n) >> c & 1)
+                finish16<kWide, kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
+                                        token(n) * a.ldy + cur.i0, q);
+        if (!more) break;
+        if constexpr (kTurnAhead)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = ahead[j];
+        cur = then;
     }
 }
 
@@ -762,7 +815,7 @@ template <typename W, int NP, int S, bool kEven, bool kWideY>
 void launch_up(const LoraArgs& a, hipStream_t stream) {
     const int64_t tiles = (a.T + kUpTokens - 1) / kUpTokens;
     constexpr size_t lds = NP * S * (kUpTokens / 16) * 512 * sizeof(W) + (kUpTokens + kUpWaves * kBox) * 4;
-    const dim3 grid((unsigned)(tiles * a.row_blocks)), threads(64 * kUpWaves);
+    const dim3 grid((unsigned)(tiles * a.row_blocks * a.up_slots)), threads(64 * kUpWaves);
     if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
     else hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
 }
@@ -774,7 +827,7 @@ void launch_up_ranks(const LoraArgs& a, hipStream_t stream) {
     else launch_up<W, NP, 4, true, kWideY>(a, stream);
 }
 
-inline bool lora_few(int64_t T, int64_t r) { return T <= 64 || r > 128; }
+inline bool lora_few(int64_t T, int64_t r) { return (T <= 128 && r <= 32) || r > 128; }
 
 template <typename X, typename W>
 void launch_lora_types(const LoraArgs& a, hipStream_t stream) {

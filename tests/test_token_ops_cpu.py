@@ -87,13 +87,13 @@ def test_lora_refuses():
         assert call(**kw) == INVALID, kw
     assert call(T=0) == OK
     assert call(T=0, X=None, A=None, B=None, ids=None, base=None, Y=None) == OK
-    wb = bk.LIB.bakron_lora_workspace_bytes(100, 8)
-    assert bk.LIB.bakron_lora_workspace_bytes(64, 8) == 0 < wb
+    wb = bk.LIB.bakron_lora_workspace_bytes(200, 8)
+    assert bk.LIB.bakron_lora_workspace_bytes(128, 32) == 0 < wb
     W = at(8 << 36)
     for kw in (dict(), dict(ws=W, wb=wb - 1), dict(ws=None, wb=wb)):
-        assert call(T=100, **kw) == WORKSPACE, kw
+        assert call(T=200, **kw) == WORKSPACE, kw
     for kw in (dict(ws=G), dict(ws=A), dict(ws=F), dict(ws=E), dict(ws=at((8 << 36) + 8)), dict(ws=at((7 << 36) - 16))):
-        assert call(T=100, **{"ws": W, "wb": wb, **kw}) == INVALID, kw
+        assert call(T=200, **{"ws": W, "wb": wb, **kw}) == INVALID, kw
     for bad in ((-1, 8), ((1 << 40) + 1, 8), (100, 0), (100, 513)):
         assert bk.LIB.bakron_lora_workspace_bytes(*bad) == 0
 
