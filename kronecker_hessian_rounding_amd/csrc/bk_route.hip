@@ -6,8 +6,9 @@
 // decides on the logits themselves and sigmoid's on 64-bit scores: sigmoids crowd below 1, where 32 bits
 // would make many of them equal.
 //
-// One wave a row, expert 64 i + lane in register i of a lane. A round is a maximum over the wave of (value,
-// index); the lane that owned it looks for its next one.
+// One wave a row, expert 64 i + lane in register i of a lane. Keys are integers whose order is that of the values (0 for
+// what is never chosen). A round is a maximum over the wave, by DPP within rows of 16 lanes and by scalars over the four;
+// the lane that owns it (the lowest index, where several do) looks for its next one.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -37,9 +38,33 @@ __device__ __forceinline__ T wave_add(T v) {
     return v;
 }
 
+template <int kCtrl>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max_dpp<0xB1>(v);   // neighbours, pairs, half rows, rows
+    v = max_dpp<0x4E>(v);
+    v = max_dpp<0x141>(v);
+    v = max_dpp<0x140>(v);
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+// Integers in the order of the values, both zeros alike; above 0 for every value but -infinity and NaN, which get 0.
+__device__ __forceinline__ uint32_t order(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return v > -INFINITY ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0;
+}
+__device__ __forceinline__ uint64_t order(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+    return v > -INFINITY ? b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000u) : 0;
+}
+
 template <int NV, bool kSigmoid>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
-    using Key = std::conditional_t<kSigmoid, double, float>;
+    using Key = std::conditional_t<kSigmoid, uint64_t, uint32_t>;
     const int lane = threadIdx.x & 63;
     const int64_t waves = (int64_t)gridDim.x * 4;
     for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += waves) {
@@ -54,55 +79,65 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
         for (int i = 0; i < NV; ++i) {
             const int e = 64 * i + lane;
             if constexpr (kSigmoid) {
-                key[i] = 1.0 / (1.0 + exp(-(double)l[i])) + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
+                const double v = 1.0 / (1.0 + exp(-(double)l[i])) + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
+                key[i] = l[i] > -INFINITY ? order(v) : 0;
             } else {
-                key[i] = l[i];
+                key[i] = order(l[i]);
             }
-            if (!(l[i] > -INFINITY) || !(key[i] > -INFINITY)) key[i] = -INFINITY;  // masked, or NaN: never chosen
         }
         // the lane's own best, the lowest index among equals
         Key best;
         int at;
         const auto look = [&]() __attribute__((always_inline)) {
             best = key[0];
-            at = lane;
+            at = 0;
 #pragma unroll
             for (int i = 1; i < NV; ++i)
                 if (key[i] > best) {
                     best = key[i];
-                    at = 64 * i + lane;
+                    at = i;
                 }
         };
         look();
         float mx = -INFINITY, chosen_l = 0.0f;
         int chosen = -1;
         for (int j = 0; j < a.k; ++j) {
-            Key b = best;
-            int e = at;
-#pragma unroll
-            for (int w = 1; w < 64; w *= 2) {
-                const Key ob = __shfl_xor(b, w);
-                const int oe = __shfl_xor(e, w);
-                if (ob > b || (ob == b && oe < e)) {
-                    b = ob;
-                    e = oe;
+            uint64_t owners;
+            if constexpr (kSigmoid) {
+                const uint32_t hi = wave_max((uint32_t)(best >> 32));
+                if (hi == 0) break;  // nothing left to choose
+                const bool top = (uint32_t)(best >> 32) == hi;
+                owners = __ballot(top);
+                if (owners & (owners - 1)) {
+                    const uint32_t lo = wave_max(top ? (uint32_t)best : 0);
+                    owners = __ballot(top && (uint32_t)best == lo);
                 }
+            } else {
+                const uint32_t b = wave_max(best);
+                if (b == 0) break;
+                owners = __ballot(best == b);
             }
-            if (!(b > -INFINITY)) break;  // nothing left to choose
+            // the lowest register, then the lowest lane
+            int owner = __builtin_ctzll(owners), reg = __builtin_amdgcn_readlane(at, owner);
+            for (owners &= owners - 1; owners; owners &= owners - 1) {
+                const int o = __builtin_ctzll(owners), r = __builtin_amdgcn_readlane(at, o);
+                owner = r < reg ? o : owner;
+                reg = min(r, reg);
+            }
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (64 * i + lane == e) {
+                if (i == reg) {
                     v = l[i];
-                    key[i] = -INFINITY;
+                    if (lane == owner) key[i] = 0;
                 }
-            v = __shfl(v, e & 63);
+            v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), owner));
             if (j == 0) mx = v;
             if (lane == j) {
-                chosen = e;
+                chosen = 64 * reg + owner;
                 chosen_l = v;
             }
-            if (at == e) look();
+            if (lane == owner) look();
         }
         float w = 0.0f;
         if constexpr (kSigmoid) {
