@@ -239,7 +239,7 @@ __device__ __forceinline__ void finish_cut(const LoraArgs& a, float* box, int64_
 // The first product of RT rank tiles from rank k0 on by the NT column tiles of tokens xr over blocks first, first + step, ..
 // of a row and, for the last of them, the block that its end cuts. The lane's sums: ranks 16 j + 4 q .. of column c. Whole
 // blocks are counted from `turn` on, and around: rows a power of two apart fall on one memory channel, column by column,
-// and workgroups that start in different columns use different ones.
+// and tiles of tokens that start in different columns use different ones. (The splits of a tile share its turn.)
 template <typename X, typename W, int RT, int NT, int PF>
 __device__ __forceinline__ void first_product(const X* const (&xr)[NT], const bool (&live)[NT], const W* ar, int64_t r, int64_t n, int k0, int first,
                                               int step, int turn, int q, int c, f32x4 (&acc)[RT][NT]) {
@@ -557,7 +557,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
             }
         }
         const W* ar = (const W*)a.a + (int64_t)ad * a.r * a.n;
-        const int blocks = (int)(a.n / First<X, W>::kBlock), turn = blocks ? blockIdx.x / 8 * 2 % blocks : 0;
+        const int blocks = (int)(a.n / First<X, W>::kBlock), turn = blocks ? (int)(t0 / kDownTokens) * 2 % blocks : 0;
         const X* const x0 = (const X*)a.x + (t0 + __shfl(tok, c)) * a.ldx;
         const X* const x1 = (const X*)a.x + (t0 + __shfl(tok, c + 16)) * a.ldx;
         for (int k0 = 0; k0 < a.rp; k0 += RP) {

@@ -2,8 +2,9 @@
 
 Tolerance: u = 2^-24. Products of 8- and 16-bit values are exact in fp32, those of fp32 have one rounding. A sum of n terms
 over 8 waves, at most n / 8 + 8 fp32 roundings of at most 2 u each in a row (the matrix core's being no better than
-truncation), gives u_k; the second product has r more, then the factors 3 and the base's addition 1. All relative to the
-sum of magnitudes; then half a step of the output's type.
+truncation), gives u_k; the second product has r more, then the factors 3 and the base's addition 1. A 16-bit
+output takes u with 17 bits (2^-17), an fp32 one with 22 (2^-22). All relative to the sum of magnitudes; then half a step of
+the output's type.
 """
 import pytest
 import torch
@@ -49,7 +50,8 @@ def check(y, x, a, b, ids, base, scales, xs):
     ref, mag = form64(x, a, b, ids, base, scales, xs)
     fi = torch.finfo(y.dtype)
     n, r = x.shape[1], a.shape[1]
-    tol = mag * 2 * U * (n / 8 + 8 + r + 4) + ref.abs() * fi.eps / 2 + fi.tiny * fi.eps
+    piece = 2.0 ** -22 if y.dtype == F32 else 2.0 ** -17
+    tol = mag * (2 * U * (n / 8 + 8 + r + 4) + piece) + ref.abs() * fi.eps / 2 + fi.tiny * fi.eps
     err = (y.cpu().double() - ref).abs()
     assert y.shape == ref.shape and bool((err <= tol).all()), float((err / tol).max())
 
@@ -82,6 +84,15 @@ def test_launch_shapes(T, run, m, r, xt, wt):
     x, a, b, ids, scales, _ = inputs(T, 72, m, r, 9, xt, wt, seed=T, run=run)
     base = torch.randn(T, m, generator=gen(2)).to(wt)
     check(call(x, a, b, ids, base, scales), x, a, b, ids, base, scales, None)
+
+
+@pytest.mark.parametrize("xt,wt", [(BF16, BF16), (F32, F32), (I8, F16)])
+@pytest.mark.parametrize("T,n,m,r", [(1, 4096, 130, 64), (41, 13056, 100, 64), (140, 6661, 90, 16), (594, 6661, 70, 40), (822, 7424, 66, 13), (16, 6016, 128, 100)])
+def test_columns_in_splits(T, n, m, r, xt, wt):
+    """Long rows, whose columns several workgroups share: every split's columns once."""
+    x, a, b, ids, scales, xs = inputs(T, n, m, r, 3, xt, wt, seed=n, run=9)
+    base = torch.randn(T, m, generator=gen(2))
+    check(call(x, a, b, ids, base, scales, xs, out_dtype=F32), x, a, b, ids, base, scales, xs)
 
 
 @pytest.mark.parametrize("T", [21, 250])
