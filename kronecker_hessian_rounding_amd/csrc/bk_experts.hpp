@@ -383,14 +383,22 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
                         some >> i & 1 ? x[i] : u32x4{0, 0, 0, 0};
             }
             wave_fence();
+            At now[PF];
             {
                 At p = next[PF - 1];
 #pragma unroll
-                for (int k = 0; k < PF; ++k) next[k] = p = ahead(p);
+                for (int k = 0; k < PF; ++k) {
+                    now[k] = next[k];
+                    next[k] = p = ahead(p);
+                }
             }
             load();
 #pragma unroll
             for (int p = 0; p < PF; ++p) {
+                // which of the lane's tokens name the expert: the others' sums stay, whatever its scales hold
+                int16_t own[4] = {0, 0, 0, 0};
+                if constexpr (TB >= 4)
+                    __builtin_memcpy(own, __builtin_assume_aligned(map + min(now[p].slot, e.slots - 1) * TB + min(4 * (lane >> 4), TB - 4), 8), 8);
                 if (i0 + p < mine)
 #pragma unroll
                     for (int f = 0; f < kScales; ++f) {
@@ -413,7 +421,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
 #pragma unroll
                         for (int r = 0; r < R; ++r)
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) sum[r][v] = fmaf(s[p][r][f], acc[r][v], sum[r][v]);
+                            for (int v = 0; v < 4; ++v) sum[r][v] = own[v] >= 0 ? fmaf(s[p][r][f], acc[r][v], sum[r][v]) : sum[r][v];
                     }
                 fetch(p);
             }

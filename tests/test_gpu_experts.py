@@ -155,6 +155,21 @@ def test_other_rows_do_not_matter(T):
     assert torch.equal(z[0], y[0]) and bool(torch.isnan(z[1]).all())
 
 
+@pytest.mark.parametrize("T", [1, 3, 7, 16, 60])
+def test_other_experts_do_not_matter(T):
+    """Scales that are not finite stay with the tokens that name their expert."""
+    E, k, n, I = 6, 2, 200, 150
+    raw = [layers(E, I, n, 4, 128, 1), layers(E, I, n, 4, 128, 2), layers(E, n, I, 4, 128, 3)]
+    x, (ids, wt) = tokens(T, n, BF16, 4).cuda(), chosen(T, E, k, 5)
+    mk = lambda: [bk.pack_experts(c.cuda(), s.cuda(), 4, 128) for c, s in raw]
+    y = bk.experts(x, *mk(), ids.cuda(), wt.cuda())
+    for i, v in enumerate((float("inf"), float("nan"), float("inf"))):
+        raw[i][1][4, 3] = v
+    z = bk.experts(x, *mk(), ids.cuda(), wt.cuda())
+    clean = ~(ids == 4).any(1)
+    assert torch.equal(z[clean.cuda()], y[clean.cuda()]) and bool((~torch.isfinite(z[(~clean).cuda()])).any(1).all())
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, I8])
 @pytest.mark.parametrize("T", [6, 90])
 def test_strided_rows(T, dtype):
