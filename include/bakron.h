@@ -425,8 +425,8 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
  *   Products are exact (8 and 16 bits) or fp32, all sums are fp32, u is fp32 (with 16-bit adapters it enters its second
  *   product with 22 bits or more where Y is fp32, else 17 or more), and Y is rounded once. Token t's result depends on
  *   its own row and adapter only. For given sizes, types and ids it is deterministic.
- *   ws: at least bakron_lora_workspace_bytes(T, r) bytes, 16-byte aligned (0 for up to 128 tokens with r <= 32: NULL will do). Calls that
- *     overlap need one each.
+ *   ws: at least bakron_lora_workspace_bytes(T, r) bytes, 16-byte aligned (0 for up to 128 tokens with r <= 32, and for
+ *     r > 128: NULL will do). Calls that overlap need one each.
  *   Y may be base itself (same pointer, type and ld); no other overlap of Y with a buffer of the call is allowed.
  * Errors: INVALID_ARG for NULL X, A, B, ids or Y (T > 0), T < 0 or > 2^40, n, m < 1 or >= 2^28, r < 1 or > 512, R < 1 or
  *   > 2^31 - 1, bad types, ld or alignment, or overlap; WORKSPACE if ws is too small.
@@ -492,8 +492,9 @@ int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t
  *     twice in a row counts with both weights. weights: T x k fp32, contiguous.
  *   act: BAKRON_ACT_SILU, v / (1 + exp(-v)), or BAKRON_ACT_GELU, gelu's tanh form.
  *   Y: T x n, BAKRON_F32, F16 or BF16, ldy >= n.
- *   The products are exact with fp32 accumulation as bakron_matvec's; the values between the two products and all
- *   sums are fp32, and Y is rounded once. Token t's result depends on its own row only. Deterministic.
+ *   The products are exact with fp32 accumulation as bakron_matvec's, all sums are fp32, act and the values between the two
+ *   products are formed in fp32 (they enter the second with 25 bits where Y is fp32, else with 17), and Y is rounded once.
+ *   Token t's result depends on its own row only. Deterministic.
  *   ws: at least bakron_experts_workspace_bytes(T, k, E, n, I) bytes (0 for sizes that bakron_experts refuses, and T = 0),
  *     16-byte aligned. Calls that overlap need one each.
  * Errors: INVALID_ARG for NULL pointers (T > 0), T < 0 or > 2^40, n or I < 1 or > 2^18, E < 1 or > 1024, k < 1 or > 64,

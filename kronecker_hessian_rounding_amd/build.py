@@ -4,7 +4,8 @@ The library is written for gfx950 only. Packed fp32 instructions are disabled
 (-packed-fp32-ops) for every device compile. In the LDL the fp64 MFMA
 instructions take their accumulators in ordinary VGPRs (-amdgpu-mfma-vgpr-form):
 with accumulation registers the compiler copied every tile's accumulators
-between the two register files on each pass of the k-loop. The Hessian kernels
+between the two register files on each pass of the k-loop. So do the products with packed
+layers and adapters, whose sums ordinary instructions read. The Hessian kernels
 measured a few per cent slower with the option, so it is set per file.
 
 The build fails if any kernel spills registers to scratch memory: several kernels

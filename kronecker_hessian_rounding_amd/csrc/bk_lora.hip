@@ -10,7 +10,8 @@ extern template void launch_lora_adapters<__bf16>(const LoraArgs&, int, hipStrea
 
 namespace {
 
-// Tokens of one round of launches (a grid has fewer than 2^32 threads), and the parts of the columns that u is formed in.
+// Tokens of one round of launches (a grid has fewer than 2^32 threads), and the parts of the columns that u is formed in:
+// as many workgroups as compute units, and at most 16 parts, whose sums the second launch adds in their order.
 constexpr int64_t kRound = (int64_t)1 << 16;
 int most_splits(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(16, 256 / ((T + kDownTokens - 1) / kDownTokens))); }
 
@@ -52,6 +53,8 @@ int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, con
         a.y = (char*)y + t0 * ldy * wide(ytype);
         int64_t ranges;
         if (lora_few(a.T, r)) {
+            // Ranges of 512 rows at least (a turn of the 8 waves), and a workgroup a unit, since each range forms u again (64
+            // tokens, rank 16, 4096 -> 14336: these 18 us, twice as many 25).
             const int64_t tiles = (a.T + 15) / 16;
             a.slots = (int)std::min<int64_t>({16, a.T, R + 1});
             ranges = std::max<int64_t>(1, std::min((m + 511) / 512, cus / (tiles * a.slots)));
@@ -63,6 +66,8 @@ int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, con
             a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most_splits(a.T), blocks / kDownWaves));
             a.slots = (int)std::max<int64_t>(1, std::min<int64_t>({16, R, 4 * cus / ((a.T + kDownTokens - 1) / kDownTokens * a.splits)}));
             const int64_t whole = m / 64 * 64;
+            // Two workgroups a unit (4096 tokens, 14336 rows: 77 us, with one 96, with four 77). Slots share a tile's
+            // adapters over workgroups where ranges alone leave units idle.
             constexpr int64_t kRows = 64 * kUpWaves;  // of a workgroup's turn
             ranges = std::max<int64_t>(1, 2 * cus / ((a.T + kUpTokens - 1) / kUpTokens));
             a.rows_each = std::max<int64_t>(1, ((whole + kRows - 1) / kRows + ranges - 1) / ranges) * kRows;

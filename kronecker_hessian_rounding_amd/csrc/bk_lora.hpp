@@ -10,9 +10,8 @@
 // More: u through memory in fp32 (k_lora_down: 32 tokens and a part of the columns a workgroup), then the outputs
 // (k_lora_up: 64 tokens and a range of rows), which stream the base and y.
 //
-// The first product runs on the matrix cores in the adapter's type (x in 8 bits is converted to it without loss) with fp32
-// sums. u stays fp32 on its way; the second product runs on the fp32 matrix cores in k_lora, and in k_lora_up on those of the
-// adapter's type with u in pieces (see there).
+// Both products run on the matrix cores in the adapter's type with fp32 sums (x in 8 bits is converted to it without loss); u
+// stays fp32 on its way and enters the second in pieces (see pieces()).
 #pragma once
 
 #include <algorithm>
@@ -43,11 +42,11 @@ struct LoraArgs {
     int64_t T, n, m, r, R;
     int64_t ldx, ldb, ldy;
     int btype, ytype;
-    int slots, row_blocks;     // workgroups of a token tile: adapters, ranges of rows
+    int slots, row_blocks;     // workgroups of a token tile: adapters (each takes every slots-th), ranges of rows
     int64_t rows_each;         // rows of a range, a multiple of 64
     // more tokens
     float* u;                  // [split][T][rp]
-    int splits, rp, up_slots;
+    int splits, rp, up_slots;  // parts of the columns; r rounded up to 16; slots of k_lora_up
 };
 
 // The operands of the first product. A block is the columns of one operand read: a row's share is its 4 lanes'
@@ -374,8 +373,11 @@ __device__ __forceinline__ void load_rows_of_b(typename Vec8<W>::type (&v)[4], c
 }
 
 // ---------------------------------------------------------------- few tokens
-// RT: tiles of 16 ranks of a pass of the first product, S: steps of 32 ranks of the second; kPasses: r may be more than they
-// take; kEven: a lane's 8 ranks of a step are all there, or none is; kWide, kWideY: the base, and y, is fp32.
+// Bound by latency: ids, x and A, their sums through LDS, the operands, then y (one token, rank 16, 4096 x 4096: 8.0 us of
+// GPU time; 64 tokens of 43 adapters, rank 16, 4096 -> 14336: 16.1). B's first rows and the base, which need nothing of the
+// first product, are fetched in front of it, and columns past an adapter's last token are not read (33 -> 25 us for that
+// batch). RT: tiles of 16 ranks of a pass of the first product, S: steps of 32 ranks of the second; kPasses: r may be more
+// than they take; kEven: a lane's 8 ranks of a step are all there, or none is; kWide, kWideY: the base, and y, is fp32.
 // (Branches around loads, and loops around the whole, make the compiler wait for all that is in flight.)
 constexpr int kLoraWaves = 8;
 
@@ -524,9 +526,13 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
 }
 
 // ---------------------------------------------------------------- more tokens
+// In one launch, each range of rows would form u anew: 4096 tokens, rank 64, 4096 -> 14336 took 334 us, 103 in two.
 constexpr int kDownWaves = 8, kDownTokens = 32, kUpTokens = 64, kUpWaves = 4;
 
 // u of 32 tokens over a part of the columns: [split][token][rp], 0 behind r. A token without an adapter has none.
+// Bound by the loads of x and A, which every wave takes straight from memory as operands: 25 us at 4096 tokens, rank 64, 4096
+// columns (2.2 GFLOP; x's 34 MB would be 7). One block of loads ahead for 4 rank tiles, two for fewer: with 4 tiles two are
+// 33 to 36 us, since a unit then holds fewer waves.
 template <typename X, typename W, int RT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
     constexpr int NW = kDownWaves, RP = 16 * RT;
@@ -596,8 +602,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
     }
 }
 
-// y of 64 tokens by a range of rows. Bound by HBM (base and y are read and written once), so that a wave's loads of the
-// base are all in flight in front of the products. S: steps of 32 ranks.
+// y of 64 tokens by a range of rows. Base and y are read and written once (4096 tokens of 14336 rows in bf16: 235 MB, 49 us
+// of HBM; it takes 76, 3.1 TB/s), so that a wave's loads of the base are all in flight in front of the products; what holds
+// it is the loads' latency with 2 waves a SIMD (58 % of its time, vector instructions 26 %). 64 tokens share a row of B:
+// with 32 it took 102. S: steps of 32 ranks.
 template <typename W, int NP, int S, bool kEven, bool kWide, bool kWideY>
 __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_up(LoraArgs a) {
     using Op = typename Vec8<W>::type;
@@ -827,6 +835,11 @@ void launch_up_ranks(const LoraArgs& a, hipStream_t stream) {
     else launch_up<W, NP, 4, true, kWideY>(a, stream);
 }
 
+// One launch or two. r = 16, 4096 x 4096, 128 tokens of mixed adapters (of one): one launch 13.1 us (14.8), two 20 (14);
+// 4096 -> 14336, 128 tokens: 24 (25.8) and 47 (15); 192 tokens: 38 (40) and 52 (14.5). Up to 128 tokens
+// one launch is ahead by more where adapters are mixed than it is behind where there is one (ids lie on the device, so the
+// choice cannot look at them). Rank 64, one token, 4096 x 4096: one launch 21.7, two 15.2, since the columns of A are
+// split over workgroups there. Above 128, u's pieces pass k_lora_up's LDS and registers.
 inline bool lora_few(int64_t T, int64_t r) { return (T <= 128 && r <= 32) || r > 128; }
 
 template <typename X, typename W>

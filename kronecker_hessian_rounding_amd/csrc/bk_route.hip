@@ -9,6 +9,10 @@
 // One wave a row, expert 64 i + lane in register i of a lane. Keys are integers whose order is that of the values (0 for
 // what is never chosen). A round is a maximum over the wave, by DPP within rows of 16 lanes and by scalars over the four;
 // the lane that owns it (the lowest index, where several do) looks for its next one.
+// Bytes are few (8192 x 256 bf16 logits are 1 us of HBM); what a call takes is the chain of k rounds of
+// dependent instructions, and with sigmoid the 64-bit exponentials, 4 a lane for 256 experts. 1 x 128, k = 8: 3.5 us of GPU
+// time, 1.1 above an empty kernel; 8192 x 256 bf16, k = 8, sigmoid: 14.8 us. With shuffles through LDS and comparisons of
+// (value, index) pairs in place of DPP and integers the same took 6.6 and 21.8.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
