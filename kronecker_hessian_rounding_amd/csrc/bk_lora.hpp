@@ -133,7 +133,7 @@ __device__ __forceinline__ typename F::Part cut_part(const S* p, int count) {
     return convert<F, S, W>(w);
 }
 
-// The second product takes 64 rows of B as four operand tiles; which row of a tile is which is free. Lane group q's sums
+// k_lora (and k_lora_up behind whole row blocks) takes 64 rows of B as four operand tiles; which row is which is free. Lane group q's sums
 // of tile j are the four rows from tile_row(j, q) on: 16 bytes of y (fp32: of a tile; 16 bits: of two) lie together, and
 // next to them those of the next group, so that an access of 16 bytes a lane covers 64 bytes of a token's row.
 template <bool kWideY>
@@ -344,7 +344,7 @@ __device__ __forceinline__ W cut_piece(float& x) {
 // next row, and what it finds there is dropped; where B itself ends, elements are read one by one.
 template <typename W, bool kEven, bool kWideY>
 __device__ __forceinline__ void load_rows_of_b(typename Vec8<W>::type (&v)[4], const LoraArgs& a, int64_t adapter, int64_t i0, int at,
-                                               int c) {
+                                                int c) {
     const W* b = (const W*)a.b;
     int64_t pos[4];
 #pragma unroll
@@ -526,8 +526,8 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
 }
 
 // ---------------------------------------------------------------- more tokens
-// In one launch, each range of rows would form u anew: 4096 tokens, rank 64, 4096 -> 14336 took 334 us, 103 in two.
-constexpr int kDownWaves = 8, kDownTokens = 32, kUpTokens = 64, kUpWaves = 4;
+// In one launch, each range of rows would form u anew: 4096 tokens, rank 64, 4096 -> 14336 took 334 us, 85 in two.
+constexpr int kDownWaves = 8, kDownTokens = 32, kUpTokens = 64, kUpWaves = 4, kUpRows = 128;
 
 // u of 32 tokens over a part of the columns: [split][token][rp], 0 behind r. A token without an adapter has none.
 // Bound by the loads of x and A, which every wave takes straight from memory as operands: 25 us at 4096 tokens, rank 64, 4096
@@ -602,26 +602,83 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
     }
 }
 
-// y of 64 tokens by a range of rows. Base and y are read and written once (4096 tokens of 14336 rows in bf16: 235 MB, 49 us
-// of HBM; it takes 76, 3.1 TB/s), so that a wave's loads of the base are all in flight in front of the products; what holds
-// it is the loads' latency with 2 waves a SIMD (58 % of its time, vector instructions 26 %). 64 tokens share a row of B:
-// with 32 it took 102. S: steps of 32 ranks.
+// k_lora_up takes tokens as the rows of its products and 128 rows of B as the columns, eight tiles: lane c of a tile has 8
+// rows of y that lie together (fp32: twice 4), so that 16 lanes cover 256 bytes of a token's row. With B's rows as the
+// products' rows, 4 lanes cover 64 bytes, and to read and write no more than base and y in such pieces takes 76 us where a
+// copy takes 45 (4096 tokens of 14336 rows in bf16).
+template <bool kWideY>
+__device__ __forceinline__ int up_row(int j, int c) {
+    return kWideY ? 64 * (j >> 2) + 4 * c + (j & 3) : 8 * c + j;
+}
+// A lane's 8 values of the base in flight, `row` the 128 rows' first element.
+template <bool kWide, bool kWideY> struct Raw8 {
+    typedef std::conditional_t<kWide, u32x4, u32x2> Four;
+    Four v[2];
+    __device__ __forceinline__ void fetch(const void* base, int64_t row, int c) {
+        typedef std::conditional_t<kWide, float, uint16_t> E;
+        if constexpr (!kWideY && !kWide) {
+            __builtin_memcpy(v, (const E*)base + row + up_row<kWideY>(0, c), 16);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) __builtin_memcpy(&v[h], (const E*)base + row + up_row<kWideY>(4 * h, c), sizeof(Four));
+        }
+    }
+    __device__ __forceinline__ f32x4 value(int h, int type) const {
+        if constexpr (kWide) return __builtin_bit_cast(f32x4, v[h]);
+        else return value4(v[h], type);
+    }
+};
+// y = base + g * sum for a lane's 8 rows of 128 whole ones of a token.
+template <bool kWide, bool kWideY>
+__device__ __forceinline__ void finish8(bool based, int btype, const Raw8<kWide, kWideY>& raw, float g, const float (&sum)[8], void* y,
+                                        int ytype, int64_t row, int c) {
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        f32x4 b = {};
+        if (based) b = raw.value(h, btype);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * h + e] = fmaf(g, sum[4 * h + e], b[e]);
+    }
+    if constexpr (kWideY) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) __builtin_memcpy((float*)y + row + up_row<true>(4 * h, c), v + 4 * h, 16);
+    } else {
+        uint16_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o[e] = ytype == BAKRON_F16 ? __builtin_bit_cast(uint16_t, (_Float16)v[e]) : __builtin_bit_cast(uint16_t, (__bf16)v[e]);
+        __builtin_memcpy((uint16_t*)y + row + up_row<false>(0, c), o, 16);
+    }
+}
+
+// y of 64 tokens by a range of rows. Base and y are read and written once (4096 tokens of 14336 rows in bf16: 235 MB, 45 us
+// as a copy, and in this kernel without its products; with them 66, 3.6 TB/s). The rest is the row block's B on its way
+// through LDS and a barrier a turn. With each wave reading B as operands for itself it took 111 (16 lanes at 16 lines),
+// with 64 rows of B as the products' rows, each wave all 64 tokens, 76. S: steps of 32 ranks.
+template <typename W, int S> struct UpShape {
+    static constexpr int kBlock = kUpRows * 32 * S;                                 // elements of B in LDS at a time
+    static constexpr int kBuffers = kBlock * sizeof(W) <= 16384 ? 2 : 1;            // (two leave room for two workgroups a unit)
+    static constexpr size_t kBytes = std::max(kBuffers * kBlock * sizeof(W), kUpWaves * kBox * sizeof(float));
+};
+
 template <typename W, int NP, int S, bool kEven, bool kWide, bool kWideY>
 __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_up(LoraArgs a) {
     using Op = typename Vec8<W>::type;
     constexpr int NT = kUpTokens / 16;
     constexpr bool kScaled = std::is_same_v<W, _Float16>;
     extern __shared__ __align__(16) char lds[];
-    W* ops = (W*)lds;                                          // [piece][step][tile][lane][8]
-    float* undo = (float*)(ops + NP * S * NT * 512);                    // [token]
-    float* box = undo + kUpTokens;                             // [wave][kBox]
+    W* blocks = (W*)lds;                                       // [buffer][kBlock]
+    float* box = (float*)lds;                                  // [wave][kBox], where no blocks are
+    W* ops = (W*)(lds + UpShape<W, S>::kBytes);                // [piece][step][tile][lane][8]
+    float* undo = (float*)(ops + NP * S * NT * 512);           // [token]
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
     const uint32_t tiles = (uint32_t)((a.T + kUpTokens - 1) / kUpTokens);
     const int slot = blockIdx.x / a.row_blocks / tiles;  // outermost: often only the first has work
     const int64_t t0 = (int64_t)(blockIdx.x / a.row_blocks % tiles) * kUpTokens;
     // whole row blocks first; the last range is that of the rows behind them
-    const int64_t whole = a.m / 64 * 64, row0 = min((blockIdx.x % a.row_blocks) * a.rows_each, whole);
+    const int64_t whole = a.m / kUpRows * kUpRows, row0 = min((blockIdx.x % a.row_blocks) * a.rows_each, whole);
     const int64_t row1 = row0 < whole ? min(whole, row0 + a.rows_each) : a.m;
     const int tokens = (int)min<int64_t>(kUpTokens, a.T - t0);
     int mine = lane < tokens ? a.ids[t0 + lane] : -1;
@@ -683,62 +740,88 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
         }
     }
     __syncthreads();
-    const auto token = [&](int n) __attribute__((always_inline)) { return t0 + min(16 * n + c, tokens - 1); };
-    // (of other slots' tokens the base is not read: the first of ours again)
-    const auto base_token = [&](int n) __attribute__((always_inline)) {
-        return t0 + (ours >> (16 * n + c) & 1 ? 16 * n + c : (int)__builtin_ctzll(ours));
-    };
-    // acc of the tokens of adapter ad for the 64 rows from i0 on, a step of ranks at a time
-    const auto multiply = [&](Op (&b)[4], int s, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
-        if (kEven && 32 * s + 8 * q >= a.r)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = Op{};
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (members >> (16 * n) & 0xFFFF)
-#pragma unroll
-                for (int p = NP - 1; p >= 0; --p) {  // the smallest piece first into the sum
-                    const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s) * NT + n) * 64 + lane) * 8);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[n][j] = second_mma<W>(b[j], uo, acc[n][j]);
-                }
-    };
-    const auto product = [&](int64_t i0, int ad, uint64_t members, f32x4 (&acc)[NT][4]) __attribute__((always_inline)) {
-#pragma unroll 1
-        for (int s = 0; s < S && 32 * s < a.r; ++s) {
-            Op b[4];
-            load_rows_of_b<W, kEven, kWideY>(b, a, ad, i0, 32 * s + 8 * q, c);
-            multiply(b, s, members, acc);
-        }
-    };
     if (row0 == whole) {  // a wave for 16 tokens
         uint64_t left = ours & ((uint64_t)0xFFFF << (16 * w));
         while (left) {
             const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
             const uint64_t members = __ballot(lane < tokens && lane >> 4 == w && mine == ad);
             left &= ~members;
-            f32x4 acc[NT][4] = {}, own[4] = {};
-            if (ad >= 0) product(row0, ad, members, acc);
+#pragma unroll 1
+            for (int64_t i0 = row0; i0 < row1; i0 += 64) {
+                f32x4 sum[4] = {};
+#pragma unroll 1
+                for (int s = 0; s < S && 32 * s < a.r && ad >= 0; ++s) {
+                    Op b[4];
+                    load_rows_of_b<W, kEven, kWideY>(b, a, ad, i0, 32 * s + 8 * q, c);
+                    if (kEven && 32 * s + 8 * q >= a.r)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (n == w)
+                        for (int j = 0; j < 4; ++j) b[j] = Op{};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) own[j] = acc[n][j];
-            finish_cut<kWideY>(a, box + w * kBox, row0, row1, members >> (16 * w) >> c & 1, token(w), kScaled ? undo[16 * w + c] : 1.0f, own,
-                       lane);
+                    for (int p = NP - 1; p >= 0; --p) {
+                        const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s) * NT + w) * 64 + lane) * 8);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sum[j] = second_mma<W>(b[j], uo, sum[j]);
+                    }
+                }
+                finish_cut<kWideY>(a, box + w * kBox, i0, row1, members >> (16 * w) >> c & 1, t0 + min(16 * w + c, tokens - 1),
+                                   kScaled ? undo[16 * w + c] : 1.0f, sum, lane);
+            }
         }
         return;
     }
-    // a base of 16 bits is one row block ahead; more leaves no registers
-    constexpr bool kAhead = !kWide && sizeof(W) == 2 && kEven;
-    Raw16<kWide, kWideY> next[NT] = {};
-    const auto load_base = [&](int64_t i0) __attribute__((always_inline)) {
-        if (kAhead && a.base)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) next[n].fetch(a.base, base_token(n) * a.ldb + i0, q);
+    // a wave: 16 of the tokens by 128 rows at a time, whose B the waves bring to LDS together, in the order of the operands:
+    // [step][tile][lane][8], 2 S pieces of 8 ranks a thread
+    const uint64_t own = ours & ((uint64_t)0xFFFF << (16 * w)), some = own ? own : ours;
+    const auto token = [&](int v) __attribute__((always_inline)) { return 16 * w + 4 * q + v; };
+    const auto piece = [&](int i, int* row) __attribute__((always_inline)) {
+        const int u = threadIdx.x + 64 * kUpWaves * i;
+        *row = u / (4 * S);
+        return u % (4 * S);
     };
-    // turns: the adapters of a row block, then those of the next; the rows of B are a turn ahead (r <= 32)
-    constexpr bool kTurnAhead = S == 1 && kEven && sizeof(W) == 2;
+    const auto load_b = [&](Op (&b)[2 * S], int ad, int64_t i0) __attribute__((always_inline)) {
+        int64_t pos[2 * S], top = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * S; ++i) {
+            int row;
+            const int at = 8 * piece(i, &row);
+            pos[i] = (ad * a.m + i0 + row) * a.r + (kEven && at >= a.r ? 0 : at);
+            top = max(top, pos[i]);
+        }
+        if (kEven || __ballot(top > a.R * a.m * a.r - 8) == 0) {  // (as load_rows_of_b)
+#pragma unroll
+            for (int i = 0; i < 2 * S; ++i) __builtin_memcpy(&b[i], (const W*)a.b + pos[i], sizeof b[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * S; ++i) {
+                int row;
+                const int at = 8 * piece(i, &row);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[i][e] = at + e < a.r ? ((const W*)a.b)[pos[i] + e] : (W)0.0f;
+            }
+        }
+    };
+    const auto put_b = [&](const Op (&b)[2 * S], W* to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2 * S; ++i) {
+            int row;
+            const int k = piece(i, &row), tile = kWideY ? row / 64 * 4 + row % 4 : row % 8, col = kWideY ? row % 64 / 4 : row / 8;
+            Op o = b[i];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 8 * k + (kEven ? 0 : e) < a.r ? o[e] : (W)0.0f;
+            *reinterpret_cast<Op*>(to + (((k / 4) * 8 + tile) * 64 + k % 4 * 16 + col) * 8) = o;
+        }
+    };
+    // a base of 16 bits is one row block ahead
+    constexpr bool kAhead = !kWide;
+    typedef Raw8<kWide, kWideY> Raw;
+    // (of tokens of other slots, or past the last, the base is not read: the first of ours again)
+    const auto load_base = [&](Raw (&raw)[4], int64_t i0) __attribute__((always_inline)) {
+        if (a.base)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                raw[v].fetch(a.base, (t0 + (own >> token(v) & 1 ? token(v) : (int)__builtin_ctzll(some))) * a.ldb + i0, c);
+    };
+    // turns: the adapters of a row block, then those of the next, for all waves alike
     struct Turn {
         int64_t i0;
         uint64_t left, members;
@@ -749,48 +832,61 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
         t.members = __ballot(lane < tokens && mine == t.ad);
         t.left &= ~t.members;
     };
-    Turn cur = {row0 + 64 * w, ours, 0, 0};
-    if (cur.i0 >= row1) return;
+    Turn cur = {row0, ours, 0, 0};
     pick(cur);
-    load_base(cur.i0);
-    Raw16<kWide, kWideY> raw[NT];
-    Op b[4] = {};
-    if constexpr (kTurnAhead) load_rows_of_b<W, kEven, kWideY>(b, a, max(cur.ad, 0), cur.i0, 8 * q, c);
+    Op stage[2 * S];
+    load_b(stage, max(cur.ad, 0), cur.i0);
+    Raw raw[4], next[4] = {};
+    if (kAhead) load_base(next, cur.i0);
     bool fresh = true;  // the first turn of its row block
-    while (true) {
-        if (fresh) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) raw[n] = next[n];
-            if (cur.i0 + 64 * kUpWaves < row1) load_base(cur.i0 + 64 * kUpWaves);
-            if (!kAhead && a.base)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) raw[n].fetch(a.base, base_token(n) * a.ldb + cur.i0, q);
-        }
+    for (int buffer = 0;; buffer = (buffer + 1) % UpShape<W, S>::kBuffers) {
+        W* const block = blocks + buffer * UpShape<W, S>::kBlock;
+        put_b(stage, block);
+        const bool began = fresh;
         Turn then = cur;
         fresh = cur.left == 0;
         if (fresh) {
-            then.i0 += 64 * kUpWaves;
+            then.i0 += kUpRows;
             then.left = ours;
         }
         const bool more = then.i0 < row1;
         pick(then);
-        Op ahead[4];
-        if constexpr (kTurnAhead)
-            load_rows_of_b<W, kEven, kWideY>(ahead, a, max(then.ad, 0), more ? then.i0 : cur.i0, 8 * q, c);
-        f32x4 acc[NT][4] = {};
-        if (cur.ad >= 0) {
-            if constexpr (kTurnAhead) multiply(b, 0, cur.members, acc);
-            else product(cur.i0, cur.ad, cur.members, acc);
+        if (more) load_b(stage, max(then.ad, 0), then.i0);
+        if (began) {
+            if (!kAhead) {
+                load_base(raw, cur.i0);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) raw[v] = next[v];
+                if (cur.i0 + kUpRows < row1) load_base(next, cur.i0 + kUpRows);
+            }
         }
+        __syncthreads();
+        const uint64_t members = cur.members & own;
+        if (members) {
+            f32x4 acc[8] = {};
+            if (cur.ad >= 0)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (cur.members >> (16 * n) >> c & 1)
-                finish16<kWide, kWideY>(a.base != nullptr, a.btype, raw[n], kScaled ? undo[16 * n + c] : 1.0f, acc[n], a.y, a.ytype,
-                                        token(n) * a.ldy + cur.i0, q);
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int p = NP - 1; p >= 0; --p) {  // the smallest piece first into the sum
+                        const Op uo = *reinterpret_cast<const Op*>(ops + (((p * S + s) * NT + w) * 64 + lane) * 8);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            acc[j] = second_mma<W>(uo, *reinterpret_cast<const Op*>(block + ((s * 8 + j) * 64 + lane) * 8), acc[j]);
+                    }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (members >> token(v) & 1) {
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = acc[j][v];
+                    finish8<kWide, kWideY>(a.base != nullptr, a.btype, raw[v], kScaled ? undo[token(v)] : 1.0f, f, a.y, a.ytype,
+                                           (t0 + token(v)) * a.ldy + cur.i0, c);
+                }
+        }
         if (!more) break;
-        if constexpr (kTurnAhead)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = ahead[j];
+        if (UpShape<W, S>::kBuffers == 1) __syncthreads();
         cur = then;
     }
 }
@@ -822,14 +918,15 @@ void launch_down(const LoraArgs& a, hipStream_t stream) {
 template <typename W, int NP, int S, bool kEven, bool kWideY>
 void launch_up(const LoraArgs& a, hipStream_t stream) {
     const int64_t tiles = (a.T + kUpTokens - 1) / kUpTokens;
-    constexpr size_t lds = NP * S * (kUpTokens / 16) * 512 * sizeof(W) + (kUpTokens + kUpWaves * kBox) * 4;
+    constexpr size_t lds = UpShape<W, S>::kBytes + NP * S * (kUpTokens / 16) * 512 * sizeof(W) + kUpTokens * 4;
     const dim3 grid((unsigned)(tiles * a.row_blocks * a.up_slots)), threads(64 * kUpWaves);
     if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
     else hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
 }
 template <typename W, int NP, bool kWideY>
 void launch_up_ranks(const LoraArgs& a, hipStream_t stream) {
-    if (a.r % 8 != 0) launch_up<W, NP, 4, false, kWideY>(a, stream);
+    if (a.r % 8 != 0 && a.r <= 32) launch_up<W, NP, 1, false, kWideY>(a, stream);
+    else if (a.r % 8 != 0) launch_up<W, NP, 4, false, kWideY>(a, stream);
     else if (a.r <= 32) launch_up<W, NP, 1, true, kWideY>(a, stream);
     else if (a.r <= 64) launch_up<W, NP, 2, true, kWideY>(a, stream);
     else launch_up<W, NP, 4, true, kWideY>(a, stream);

@@ -86,6 +86,17 @@ def test_launch_shapes(T, run, m, r, xt, wt):
     check(call(x, a, b, ids, base, scales), x, a, b, ids, base, scales, None)
 
 
+@pytest.mark.parametrize("xt,wt,bt,yt", [(BF16, BF16, BF16, BF16), (BF16, BF16, F32, BF16), (F16, F16, F16, F32), (F32, F32, BF16, F32),
+                                         (F32, F32, F32, F16)])
+@pytest.mark.parametrize("m", [127, 128, 129, 191, 256, 383, 1100])
+@pytest.mark.parametrize("r", [16, 13, 40, 88])
+def test_row_blocks(m, r, xt, wt, bt, yt):
+    """More tokens, rows in whole blocks and behind them, base and result of other types than the adapters'."""
+    x, a, b, ids, scales, _ = inputs(203, 100, m, r, 5, xt, wt, seed=m + r, run=70)
+    base = torch.randn(203, m, generator=gen(2)).to(bt)
+    check(call(x, a, b, ids, base, scales, out_dtype=yt), x, a, b, ids, base, scales, None)
+
+
 @pytest.mark.parametrize("xt,wt", [(BF16, BF16), (F32, F32), (I8, F16)])
 @pytest.mark.parametrize("T,n,m,r", [(1, 4096, 130, 64), (41, 13056, 100, 64), (140, 6661, 90, 16), (594, 6661, 70, 40), (822, 7424, 66, 13), (16, 6016, 128, 100)])
 def test_columns_in_splits(T, n, m, r, xt, wt):
