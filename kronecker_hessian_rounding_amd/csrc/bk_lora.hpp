@@ -133,9 +133,10 @@ __device__ __forceinline__ typename F::Part cut_part(const S* p, int count) {
     return convert<F, S, W>(w);
 }
 
-// k_lora (and k_lora_up behind whole row blocks) takes 64 rows of B as four operand tiles; which row is which is free. Lane group q's sums
-// of tile j are the four rows from tile_row(j, q) on: 16 bytes of y (fp32: of a tile; 16 bits: of two) lie together, and
-// next to them those of the next group, so that an access of 16 bytes a lane covers 64 bytes of a token's row.
+// k_lora (and k_lora_up behind whole row blocks) takes 64 rows of B as four operand tiles; which row is which is free. Lane
+// group q's sums of tile j are the four rows from tile_row(j, q) on: 16 bytes of y (fp32: of a tile; 16 bits: of two) lie
+// together, and next to them those of the next group, so that an access of 16 bytes a lane covers 64 bytes of a token's
+// row.
 template <bool kWideY>
 __device__ __forceinline__ int tile_row(int j, int q) {
     return kWideY ? 16 * j + 4 * q : 32 * (j >> 1) + 8 * q + 4 * (j & 1);
