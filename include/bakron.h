@@ -422,8 +422,8 @@ int bakron_rmsnorm(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t l
  *     smaller rank are padded with zeros.
  *   scales: [R] fp32, or NULL for 1. ids: [T] int32; an id outside 0 .. R - 1 means no adapter: Y[t] = base[t].
  *   base: T x m of btype (F32, F16 or BF16), ldb >= m, or NULL for 0. Y: T x m of ytype, ldy >= m.
- *   Products are exact (8 and 16 bits) or fp32, all sums are fp32, u is fp32 (with 16-bit adapters it enters its second
- *   product with 22 bits or more where Y is fp32, else 17 or more), and Y is rounded once. Token t's result depends on
+ *   Products are exact (8 and 16 bits) or fp32, all sums are fp32, u is fp32 and enters its second product
+ *   whole (16-bit adapters: its 24 bits in three pieces; fp16: to 2^-38 of the token's largest u), and Y is rounded once. Token t's result depends on
  *   its own row and adapter only. For given sizes, types and ids it is deterministic.
  *   ws: at least bakron_lora_workspace_bytes(T, r) bytes, 16-byte aligned (0 for up to 128 tokens with r <= 32, and for
  *     r > 128: NULL will do). Calls that overlap need one each.

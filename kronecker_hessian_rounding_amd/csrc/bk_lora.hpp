@@ -301,14 +301,13 @@ __device__ __forceinline__ void first_product(const X* const (&xr)[NT], const bo
     }
 }
 
-// The second product. u, with the token's and the adapter's factors, lies in LDS as operand: in NP pieces of the adapter's
-// type, of which all but the last are cut off and the last is rounded. bf16: 3 pieces hold 25 bits, for a y in
-// fp32; 2 hold 17, for a y of 16 bits, whose own rounding is 2^5 to 2^8 times theirs. fp16: 2 pieces hold 22 bits, of u
-// times the power of two that takes the token's largest value to 2^14 (undone in fp32); 3 hold all. fp32: one, on the fp32
-// matrix cores. (fp32 products for all types cost a 64-token batch 3.8 us of 18.)
-template <typename W, bool kWideY>
+// The second product. u, with the token's and the adapter's factors, lies in LDS as operand: in three pieces of the
+// adapter's type, of which all but the last are cut off and the last is rounded, so that they hold all 24 bits of u: bf16 has 8 in
+// each; fp16 11, of u times the power of two that takes the token's largest value to 2^14 (undone in fp32). fp32: one,
+// on the fp32 matrix cores. (fp32 products for all types cost a 64-token batch 3.8 us of 18.)
+template <typename W>
 constexpr int pieces() {
-    return std::is_same_v<W, float> ? 1 : kWideY ? 3 : 2;
+    return std::is_same_v<W, float> ? 1 : 3;
 }
 template <typename W>
 __device__ __forceinline__ f32x4 second_mma(typename Vec8<W>::type a, typename Vec8<W>::type b, f32x4 c) {
@@ -374,8 +373,8 @@ __device__ __forceinline__ void load_rows_of_b(typename Vec8<W>::type (&v)[4], c
 }
 
 // ---------------------------------------------------------------- few tokens
-// Bound by latency: ids, x and A, their sums through LDS, the operands, then y (one token, rank 16, 4096 x 4096: 8.0 us of
-// GPU time; 64 tokens of 43 adapters, rank 16, 4096 -> 14336: 16.1). B's first rows and the base, which need nothing of the
+// Bound by latency: ids, x and A, their sums through LDS, the operands, then y (one token, rank 16, 4096 x 4096: 8.1 us of
+// GPU time; 64 tokens of 43 adapters, rank 16, 4096 -> 14336: 16.3). B's first rows and the base, which need nothing of the
 // first product, are fetched in front of it, and columns past an adapter's last token are not read (33 -> 25 us for that
 // batch). RT: tiles of 16 ranks of a pass of the first product, S: steps of 32 ranks of the second; kPasses: r may be more
 // than they take; kEven: a lane's 8 ranks of a step are all there, or none is; kWide, kWideY: the base, and y, is fp32.
@@ -385,7 +384,7 @@ constexpr int kLoraWaves = 8;
 template <typename X, typename W, int RT, int S, bool kPasses, bool kEven, bool kWide, bool kWideY>
 __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
     using Op = typename Vec8<W>::type;
-    constexpr int NW = kLoraWaves, PF = 8 / RT, RP = 16 * RT, NP = pieces<W, kWideY>();
+    constexpr int NW = kLoraWaves, PF = 8 / RT, RP = 16 * RT, NP = pieces<W>();
     constexpr bool kScaled = std::is_same_v<W, _Float16>;
     extern __shared__ __align__(16) char lds[];
     const int steps = kPasses ? (int)((a.r + 31) / 32) : S, pitch = 32 * steps + 4;
@@ -527,7 +526,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
 }
 
 // ---------------------------------------------------------------- more tokens
-// In one launch, each range of rows would form u anew: 4096 tokens, rank 64, 4096 -> 14336 took 334 us, 85 in two.
+// In one launch, each range of rows would form u anew: 4096 tokens, rank 64, 4096 -> 14336 took 334 us, 88 in two.
 constexpr int kDownWaves = 8, kDownTokens = 32, kUpTokens = 64, kUpWaves = 4, kUpRows = 128;
 
 // u of 32 tokens over a part of the columns: [split][token][rp], 0 behind r. A token without an adapter has none.
@@ -663,10 +662,10 @@ template <typename W, int S> struct UpShape {
     static constexpr size_t kBytes = std::max(kBuffers * kBlock * sizeof(W), kUpWaves * kBox * sizeof(float));
 };
 
-template <typename W, int NP, int S, bool kEven, bool kWide, bool kWideY>
+template <typename W, int S, bool kEven, bool kWide, bool kWideY>
 __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_up(LoraArgs a) {
     using Op = typename Vec8<W>::type;
-    constexpr int NT = kUpTokens / 16;
+    constexpr int NT = kUpTokens / 16, NP = pieces<W>();
     constexpr bool kScaled = std::is_same_v<W, _Float16>;
     extern __shared__ __align__(16) char lds[];
     W* blocks = (W*)lds;                                       // [buffer][kBlock]
@@ -896,7 +895,7 @@ template <typename X, typename W, int RT, int S, bool kPasses, bool kEven>
 void launch_few(const LoraArgs& a, hipStream_t stream) {
     constexpr int NW = kLoraWaves;
     const bool wide = a.base && a.btype == BAKRON_F32, wide_y = a.ytype == BAKRON_F32;
-    const size_t steps = kPasses ? (size_t)(a.r + 31) / 32 : S, np = wide_y ? pieces<W, true>() : pieces<W, false>();
+    const size_t steps = kPasses ? (size_t)(a.r + 31) / 32 : S, np = pieces<W>();
     const size_t lds = np * steps * 512 * sizeof(W) + sizeof(float) * (16 * (32 * steps + 4) + 32 + NW * 16 * RT * 17 + kBox);
     const int64_t groups = (a.T + 15) / 16 * a.slots;
     const dim3 grid((unsigned)((groups + 7) / 8 * 8 * a.row_blocks)), threads(64 * NW);
@@ -916,21 +915,21 @@ void launch_down(const LoraArgs& a, hipStream_t stream) {
                        sizeof(float) * kDownWaves * 16 * RT * 33, stream, a);
 }
 
-template <typename W, int NP, int S, bool kEven, bool kWideY>
+template <typename W, int S, bool kEven, bool kWideY>
 void launch_up(const LoraArgs& a, hipStream_t stream) {
     const int64_t tiles = (a.T + kUpTokens - 1) / kUpTokens;
-    constexpr size_t lds = UpShape<W, S>::kBytes + NP * S * (kUpTokens / 16) * 512 * sizeof(W) + kUpTokens * 4;
+    constexpr size_t lds = UpShape<W, S>::kBytes + pieces<W>() * S * (kUpTokens / 16) * 512 * sizeof(W) + kUpTokens * 4;
     const dim3 grid((unsigned)(tiles * a.row_blocks * a.up_slots)), threads(64 * kUpWaves);
-    if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
-    else hipLaunchKernelGGL((k_lora_up<W, NP, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
+    if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
+    else hipLaunchKernelGGL((k_lora_up<W, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
 }
-template <typename W, int NP, bool kWideY>
+template <typename W, bool kWideY>
 void launch_up_ranks(const LoraArgs& a, hipStream_t stream) {
-    if (a.r % 8 != 0 && a.r <= 32) launch_up<W, NP, 1, false, kWideY>(a, stream);
-    else if (a.r % 8 != 0) launch_up<W, NP, 4, false, kWideY>(a, stream);
-    else if (a.r <= 32) launch_up<W, NP, 1, true, kWideY>(a, stream);
-    else if (a.r <= 64) launch_up<W, NP, 2, true, kWideY>(a, stream);
-    else launch_up<W, NP, 4, true, kWideY>(a, stream);
+    if (a.r % 8 != 0 && a.r <= 32) launch_up<W, 1, false, kWideY>(a, stream);
+    else if (a.r % 8 != 0) launch_up<W, 4, false, kWideY>(a, stream);
+    else if (a.r <= 32) launch_up<W, 1, true, kWideY>(a, stream);
+    else if (a.r <= 64) launch_up<W, 2, true, kWideY>(a, stream);
+    else launch_up<W, 4, true, kWideY>(a, stream);
 }
 
 // One launch or two. r = 16, 4096 x 4096, 128 tokens of mixed adapters (of one): one launch 13.1 us (14.8), two 20 (14);
@@ -953,9 +952,8 @@ void launch_lora_types(const LoraArgs& a, hipStream_t stream) {
     if (a.r <= 16) launch_down<X, W, 1>(a, stream);
     else if (a.r <= 32) launch_down<X, W, 2>(a, stream);
     else launch_down<X, W, 4>(a, stream);
-    constexpr bool kF32 = std::is_same_v<W, float>;
-    if (a.ytype == BAKRON_F32) launch_up_ranks<W, kF32 ? 1 : 3, true>(a, stream);
-    else launch_up_ranks<W, kF32 ? 1 : 2, false>(a, stream);
+    if (a.ytype == BAKRON_F32) launch_up_ranks<W, true>(a, stream);
+    else launch_up_ranks<W, false>(a, stream);
 }
 
 // by the type of x; W that of the adapters

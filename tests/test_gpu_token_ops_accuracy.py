@@ -1,0 +1,64 @@
+"""What passes between the two products of lora and experts, and the last roundings, on the GPU.
+
+Inputs whose second product adds no error show every bit of what enters it: a value of 24 bits that reaches an output
+by itself has to come out whole in fp32, and rounded once, to nearest even, in 16 bits.
+"""
+import pytest
+import torch
+
+import kronecker_hessian_rounding_amd as bk
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24  # half a step of fp32
+F32, F16, BF16, I8, E4M3 = torch.float32, torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn
+KEPT = {F32: 24, F16: 11, BF16: 8}  # bits of a value of the type
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def whole_numbers(shape, out, seed):
+    """24-bit numbers, 2^23 .. 2^24 - 1. For a 16-bit output each lies one beside a tie of its rounding, on either side."""
+    g = gen(seed)
+    v = torch.randint(2 ** 23, 2 ** 24, shape, generator=g)
+    if out != F32:
+        low = 24 - KEPT[out]
+        v = (v >> low << low) + 2 ** (low - 1) + 2 * torch.randint(0, 2, shape, generator=g) - 1
+    return v
+
+
+# ------------------------------------------------------------------ lora
+def lora_case(T, n, m, r, R, xt, wt, out, seed):
+    """x has ones in three columns, A the three bytes of a number there; B picks one rank a row, with a sign."""
+    g = gen(seed)
+    u = whole_numbers((R, r), out, seed + 1)
+    at = torch.randperm(n, generator=g)[:3]
+    x = torch.zeros(T, n)
+    x[:, at] = 1.0
+    a = torch.zeros(R, r, n)
+    for i, shift in enumerate((16, 8, 0)):
+        a[:, :, at[i]] = (u >> shift & 255).float() * 2.0 ** (shift - 8)  # within fp16's range
+    sign = 2.0 * torch.randint(0, 2, (R, m), generator=g) - 1
+    rank = torch.randint(0, r, (R, m), generator=g)
+    b = torch.zeros(R, m, r).scatter_(2, rank[:, :, None], sign[:, :, None])
+    ids = torch.randint(0, R, (T,), generator=g, dtype=torch.int32)
+    want = (u.double().gather(1, rank) * sign * 2.0 ** -8)[ids.long()]
+    return x.to(xt), a.to(wt), b.to(wt), ids, want
+
+
+@pytest.mark.parametrize("xt,wt", [(F32, F32), (F16, F16), (BF16, BF16), (I8, F16), (I8, BF16), (E4M3, F16), (E4M3, BF16)])
+@pytest.mark.parametrize("T,n,m,r", [(1, 300, 200, 16), (5, 1500, 130, 13), (40, 700, 700, 8), (100, 96, 65, 32), (20, 200, 100, 20),  # one launch
+                                     (19, 96, 90, 130), (3, 200, 70, 512),                                              # ranks in passes
+                                     (1, 4096, 300, 64), (150, 700, 200, 13), (140, 6661, 700, 16), (200, 96, 130, 32),  # two
+                                     (130, 300, 383, 40), (70, 128, 64, 64), (300, 500, 260, 100), (300, 500, 260, 128)])
+def test_lora_holds_every_bit_between_its_products(T, n, m, r, xt, wt):
+    for out in (F32, F16, BF16):
+        x, a, b, ids, want = lora_case(T, n, m, r, 3, xt, wt, out, T + r)
+        y = bk.lora(x.cuda(), a.cuda(), b.cuda(), ids.cuda(), out_dtype=out).cpu()
+        # (the 24-bit numbers are fp32 values, so that the cast rounds once; 2^-16 keeps them in fp16's range)
+        if out == F16:
+            y = bk.lora(x.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=torch.full((3,), 2.0 ** -16, device="cuda"), out_dtype=out).cpu()
+            want = want * 2.0 ** -16
+        assert torch.equal(y, want.float().to(out)), (out, int((y != want.float().to(out)).sum()), y.numel())
