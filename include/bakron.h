@@ -493,7 +493,7 @@ int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t
  *   act: BAKRON_ACT_SILU, v / (1 + exp(-v)), or BAKRON_ACT_GELU, gelu's tanh form.
  *   Y: T x n, BAKRON_F32, F16 or BF16, ldy >= n.
  *   The products are exact with fp32 accumulation as bakron_matvec's, all sums are fp32, act and the values between the two
- *   products are formed in fp32 (they enter the second with 25 bits where Y is fp32, else with 17), and Y is rounded once.
+ *   products are formed in fp32 (they enter the second with all 24 bits), and Y is rounded once.
  *   Token t's result depends on its own row only. Deterministic.
  *   ws: at least bakron_experts_workspace_bytes(T, k, E, n, I) bytes (0 for sizes that bakron_experts refuses, and T = 0),
  *     16-byte aligned. Calls that overlap need one each.

@@ -14,10 +14,6 @@ extern template void launch_experts_first<kI8>(const ExpertArgs&, int, int, int,
 extern template void launch_experts_first_few<kI8>(const FewArgs&, int, int, hipStream_t);
 extern template void launch_experts_first<kF8>(const ExpertArgs&, int, int, int, hipStream_t);
 extern template void launch_experts_first_few<kF8>(const FewArgs&, int, int, hipStream_t);
-extern template void launch_experts_second<kH2>(const ExpertArgs&, int, int, int, hipStream_t);
-extern template void launch_experts_second<kH3>(const ExpertArgs&, int, int, int, hipStream_t);
-extern template void launch_experts_second_few<2>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
-extern template void launch_experts_second_few<3>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
 
 namespace {
 
@@ -183,7 +179,7 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     };
     if (few_tokens(T, k)) {
         l.named = take(4 * (1 + 17 * std::min(E, T * k)));
-        l.planes = take(3 * l.plane * T * k);
+        l.planes = take(kPieces * l.plane * T * k);
         const int splits = second_splits(T, k, E, n, I);
         if (splits > 1) l.part = take(4 * splits * T * n);
         l.bytes = at;
@@ -194,7 +190,7 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     l.tokens = take(4 * p);
     l.pair = take(4 * p);
     l.weight = take(4 * p);
-    l.planes = take(3 * l.plane * p);
+    l.planes = take(kPieces * l.plane * p);
     l.part = take(4 * p * n);
     l.bytes = at;
     return l;
@@ -240,7 +236,6 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     const PackShape p1 = pack_shape(I, n, bits, group), p2 = pack_shape(n, I, dbits, dgroup);
     const Layout l = layout(T, k, E, n, I);
     char* w = (char*)ws;
-    const int pieces = ytype == BAKRON_F32 ? 3 : 2;
     if (few_tokens(T, k)) {
         int fs;
         FewArgs f = {};
@@ -256,7 +251,6 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         f.E = (int32_t)E;
         f.slots = (int32_t)std::min(E, T * k);
         f.act = act;
-        f.pieces = pieces;
         const auto product = [&](const void* packed, const PackShape& p, int64_t m, int64_t cols, int64_t g) {
             const MvArgs a = layer_args(packed, p, m, cols, g, &fs);
             f.gate = a.codes;
@@ -282,8 +276,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         }
         product(down, p2, n, I, dgroup);
         const int splits = second_splits(T, k, E, n, I);
-        if (pieces == 3) launch_experts_second_few<3>(f, p2.W, fs, splits, y, ytype, ldy, stream);
-        else launch_experts_second_few<2>(f, p2.W, fs, splits, y, ytype, ldy, stream);
+        launch_experts_second_few(f, p2.W, fs, splits, y, ytype, ldy, stream);
         if (splits > 1)
             hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, f.part, splits,
                                T, n, y, ytype, ldy);
@@ -304,7 +297,6 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     e.weights = (const float*)(w + l.weight);
     e.planes = w + l.planes;
     e.plane = l.plane;
-    e.pieces = pieces;
     e.part = (float*)(w + l.part);
     e.n = n;
     e.I = I;
@@ -312,7 +304,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
     e.first.ldx = ldx;
     e.second.x = e.planes;
     e.second.n = l.plane / 2;  // zeros behind I
-    e.second.ldx = pieces * l.plane / 2;
+    e.second.ldx = kPieces * l.plane / 2;
     const int64_t xb = xtype == BAKRON_F32 ? 4 : xtype == BAKRON_I8 || xtype == BAKRON_E4M3 ? 1 : 2;
     const int64_t round = round_tokens(T, k, E, n, I);
     for (int64_t t0 = 0; t0 < T; t0 += round) {
@@ -326,8 +318,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
                       (ExpertTile*)(w + l.list), (int32_t*)(w + l.tokens), (int32_t*)(w + l.pair), (float*)(w + l.weight)};
         hipLaunchKernelGGL(k_experts_plan, dim3(1), dim3(1024), 0, stream, p);
         launch_first(e, tile, xtype, p1.W, fs1, stream);
-        if (pieces == 3) launch_experts_second<kH3>(e, tile, p2.W, fs2, stream);
-        else launch_experts_second<kH2>(e, tile, p2.W, fs2, stream);
+        launch_experts_second(e, tile, p2.W, fs2, stream);
         SumArgs s = {ids + t0 * k, e.part, (char*)y + t0 * ldy * (ytype == BAKRON_F32 ? 4 : 2), tokens, n, ldy, (int)k, (int)E, ytype};
         hipLaunchKernelGGL(k_experts_sum, dim3((unsigned)(tokens * ((n + 1023) / 1024))), dim3(256), 0, stream, s);
     }

@@ -44,7 +44,7 @@ struct ExpertArgs {
     int64_t plane;
     float* part;                  // [pair][n]
     int64_t n, I;
-    int act, pieces;
+    int act;
     int most_tiles;               // the list's bound
 };
 
@@ -62,7 +62,7 @@ struct FewArgs {
     int64_t ldx;
     int32_t T, k, E, slots;       // slots: experts, or pairs where they are fewer
     int32_t m, n, tiles, nc, ngp, gshift;
-    int32_t plane, act, pieces;
+    int32_t plane, act;
     float* part;                  // [split][token][m] of the second product
 };
 
@@ -98,21 +98,20 @@ __device__ __forceinline__ float activation(float v, int act) {
     return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
-// h between the products: bf16 pieces, the largest first, of which all but the last are cut off and the last is rounded.
-// Three hold 25 bits of h, for a y in fp32; two hold 17, for a y of 16 bits, whose own rounding is 2^5 to 2^8 times
-// theirs. (A third piece is a third more MFMAs and reads of h.) An infinity or NaN stays in the first.
+// h between the products: three bf16 pieces, the largest first, which hold all 24 bits of it (the first two are cut off, the
+// last is rounded). An infinity or NaN stays in the first.
+constexpr int kPieces = Mt<kH>::kPieces;
 template <int N>
-__device__ __forceinline__ void store_pieces(char* row, int64_t plane, int pieces, int64_t i, const float (&h)[N]) {
+__device__ __forceinline__ void store_pieces(char* row, int64_t plane, int64_t i, const float (&h)[N]) {
     float r[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) r[e] = h[e];
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-        if (p >= pieces) break;
+    for (int p = 0; p < kPieces; ++p) {
         uint16_t b[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            if (p == pieces - 1) b[e] = __builtin_bit_cast(uint16_t, (__bf16)r[e]);
+            if (p == kPieces - 1) b[e] = __builtin_bit_cast(uint16_t, (__bf16)r[e]);
             else b[e] = (uint16_t)(__float_as_uint(__builtin_canonicalizef(r[e])) >> 16);
             const float left = r[e] - __uint_as_float((uint32_t)b[e] << 16);
             r[e] = left == left ? left : 0.0f;
@@ -287,7 +286,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
             h = w * (activation(g * s, e.act) * (u * s));
         }
         const float hh[1] = {h};
-        store_pieces<1>(e.planes + to * e.pieces * e.plane, e.plane, e.pieces, row, hh);
+        store_pieces<1>(e.planes + to * kPieces * e.plane, e.plane, row, hh);
     }
 }
 
@@ -296,18 +295,20 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
 // each stages h's pieces for its next PF chunks in LDS of its own, as few_products does x: a token that does not name the
 // expert has zeros there. 16 tokens, 8 experts of 4096 x 14336: 65 us for 0.25 GB, 3.9 TB/s; one token, 6 of 2048 x 1408:
 // 6.8 us.
-template <int NP, int PF, int TB>
+template <int PF, int TB>
 struct SecondShape {
+    static constexpr int NP = kPieces;
     static constexpr int kUnits = (TB * PF * NP * 16 + 63) / 64;  // 16-byte units of a lane in a set
     static constexpr int kPiece = PF * 256;                       // from piece to piece of a token
     static constexpr int kPitch = NP * kPiece + 16;               // from token to token: 4 banks
     static constexpr int kBytes = TB * kPitch;                    // of a wave
 };
 
-template <int NP, int W, int FS, int R, int PF, int TB, int NW>
+template <int W, int FS, int R, int PF, int TB, int NW>
 __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int splits, void* y, int ytype, int64_t ldy) {
-    using M = Mt<kBF16>;
-    using Sh = SecondShape<NP, PF, TB>;
+    using M = Mt<kH>;
+    using Sh = SecondShape<PF, TB>;
+    constexpr int NP = kPieces;
     using Wd = typename Share<W>::T;
     constexpr int kScales = kSteps / FS;
     extern __shared__ __align__(16) char lds[];
@@ -493,16 +494,15 @@ void launch_experts_first_few(const FewArgs& e, int W, int fs, hipStream_t strea
     }
 }
 
-template <int NP, int W, int FS, int TB>
+template <int W, int FS, int TB>
 void launch_second_tokens(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
-    // Up to 4 tokens are waits in a row, which 16 waves shorten; above, LDS for h's pieces leaves 8 (and for three pieces one
-    // chunk ahead).
-    constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : NP == 3 ? 1 : 2;
+    // Up to 4 tokens are waits in a row, which 16 waves shorten; above, LDS for h's pieces leaves 8, with one chunk ahead.
+    constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : 1;
     const auto launch = [&](auto tiles) {
         constexpr int R = decltype(tiles)::value;
         const size_t red = sizeof(float) * NW * R * 16 * 17;
-        const size_t lds = std::max(red, (size_t)NW * SecondShape<NP, PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
-        hipLaunchKernelGGL((k_experts_second_few<NP, W, FS, R, PF, TB, NW>), dim3((unsigned)((e.tiles + R - 1) / R * splits)),
+        const size_t lds = std::max(red, (size_t)NW * SecondShape<PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
+        hipLaunchKernelGGL((k_experts_second_few<W, FS, R, PF, TB, NW>), dim3((unsigned)((e.tiles + R - 1) / R * splits)),
                            dim3(64 * NW), lds, stream, e, splits, y, ytype, ldy);
     };
     if constexpr (TB > 4) {
@@ -510,24 +510,13 @@ void launch_second_tokens(const FewArgs& e, int splits, void* y, int ytype, int6
     }
     launch(std::integral_constant<int, 1>());
 }
-template <int NP, int W, int FS>
+template <int W, int FS>
 void launch_second_few(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
-    if (e.T == 1) launch_second_tokens<NP, W, FS, 1>(e, splits, y, ytype, ldy, stream);
-    else if (e.T <= 4) launch_second_tokens<NP, W, FS, 4>(e, splits, y, ytype, ldy, stream);
-    else if (e.T <= 8) launch_second_tokens<NP, W, FS, 8>(e, splits, y, ytype, ldy, stream);
-    else launch_second_tokens<NP, W, FS, 16>(e, splits, y, ytype, ldy, stream);
+    if (e.T == 1) launch_second_tokens<W, FS, 1>(e, splits, y, ytype, ldy, stream);
+    else if (e.T <= 4) launch_second_tokens<W, FS, 4>(e, splits, y, ytype, ldy, stream);
+    else if (e.T <= 8) launch_second_tokens<W, FS, 8>(e, splits, y, ytype, ldy, stream);
+    else launch_second_tokens<W, FS, 16>(e, splits, y, ytype, ldy, stream);
 }
-template <int NP>
-void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
-    if (W == 4) {
-        if (fs == 1) launch_second_few<NP, 4, 1>(e, splits, y, ytype, ldy, stream);
-        else launch_second_few<NP, 4, 4>(e, splits, y, ytype, ldy, stream);
-    } else {
-        if (fs == 1) launch_second_few<NP, 2, 1>(e, splits, y, ytype, ldy, stream);
-        else launch_second_few<NP, 2, 4>(e, splits, y, ytype, ldy, stream);
-    }
-}
-
 // ---------------------------------------------------------------- more tokens
 // The list's tiles hold at most 16 tokens where an expert has about as few (few_products), else as many as a workgroup of
 // mm_products takes.
@@ -581,11 +570,11 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first(ExpertArgs e) {
             const float s = unit<MATH, W>() * (f.a.xs ? f.a.xs[e.tokens[at]] : 1.0f);
             h[0] = e.weights[at] * (activation(g * s, e.act) * (u * s));
         }
-        store_pieces<1>(e.planes + (int64_t)e.pairs[at] * e.pieces * e.plane, e.plane, e.pieces, row, h);
+        store_pieces<1>(e.planes + (int64_t)e.pairs[at] * kPieces * e.plane, e.plane, row, h);
     }
 }
 
-template <int MATH, int W, int FS, int R, int PF, int NW>
+template <int W, int FS, int R, int PF, int NW>
 __global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
     extern __shared__ __align__(16) char lds[];
     const uint32_t blocks = (e.second.tiles + R - 1) / R;
@@ -594,7 +583,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
     if ((int)li >= *e.tiles_used) return;
     const ExpertTile l = e.list[li];
     const MvArgs a = second_tile(e, l);
-    few_products<MATH, W, FS, R, PF, 16, NW>(a, Stream<W, FS, R, PF>(a, tile0, threadIdx.x & 63), Listed{e.pairs + l.begin}, lds);
+    few_products<kH, W, FS, R, PF, 16, NW>(a, Stream<W, FS, R, PF>(a, tile0, threadIdx.x & 63), Listed{e.pairs + l.begin}, lds);
     const float* red = reinterpret_cast<const float*>(lds);
     for (int i = threadIdx.x; i < l.count * R * 16; i += 64 * NW) {
         const int t = i / (R * 16), r = i / 16 % R;
@@ -639,7 +628,7 @@ __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)
             float h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) h[k] = row + k < e.I ? w * (activation(g[k] * s, e.act) * (u[k] * s)) : 0.0f;
-            store_pieces<4>(e.planes + (int64_t)e.pairs[at] * e.pieces * e.plane, e.plane, e.pieces, row, h);
+            store_pieces<4>(e.planes + (int64_t)e.pairs[at] * kPieces * e.plane, e.plane, row, h);
         }
     };
     mm_products<MATH, W, FS, NT, 2, KS, RW, CH>(f.a, 0, Listed{e.tokens + f.l.begin}, stream, lds, sink);
@@ -648,7 +637,7 @@ __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)
 // 16 R RW rows of D by 16 NT tokens. At the sizes above: 50 us with 256 rows by 32 tokens; 64 tokens in half as many rows
 // 55, 64 rows a wave 93, columns split over waves 64 to 104, 128 tokens 145. Matrix cores busy 25 %, vector instructions
 // 28 %, 1.3 waves a SIMD.
-template <int MATH, int W, int FS, int NT, int R, int KS, int RW, int CH>
+template <int W, int FS, int NT, int R, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
     constexpr int kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
     extern __shared__ __align__(16) char lds[];
@@ -675,7 +664,7 @@ __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)
             store4(e.part, BAKRON_F32, (int64_t)e.pairs[l.begin + t] * e.n + row, y, (int)min<int64_t>(4, e.n - row));
         }
     };
-    mm_products<MATH, W, FS, NT, R, KS, RW, CH>(a, t0, Listed{e.pairs + l.begin}, stream, lds, sink);
+    mm_products<kH, W, FS, NT, R, KS, RW, CH>(a, t0, Listed{e.pairs + l.begin}, stream, lds, sink);
 }
 
 template <int MATH, int W, int FS>
@@ -706,32 +695,25 @@ void launch_experts_first(const ExpertArgs& e, int tile, int W, int fs, hipStrea
     }
 }
 
-template <int MATH, int W, int FS>
+template <int W, int FS>
 void launch_second_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
     if (tile == kListFew) {
         constexpr int NW = 4, PF = 1, R = 2;
         constexpr size_t red = sizeof(float) * NW * R * 16 * 17;
-        constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<MATH, PF, 16>::kBytes, red);
-        hipLaunchKernelGGL((k_experts_second<MATH, W, FS, R, PF, NW>), dim3((e.second.tiles + R - 1) / R * (unsigned)e.most_tiles),
+        constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<kH, PF, 16>::kBytes, red);
+        hipLaunchKernelGGL((k_experts_second<W, FS, R, PF, NW>), dim3((e.second.tiles + R - 1) / R * (unsigned)e.most_tiles),
                            dim3(64 * NW), lds, stream, e);
     } else {
         constexpr int NT = 2, R = 2, KS = 1, RW = 8, CH = 1;
         constexpr size_t red = sizeof(float) * KS * 16 * (16 * R * RW + 4);
-        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<MATH, NT, KS * CH>::kBytes, red);
-        hipLaunchKernelGGL((k_experts_second_mm<MATH, W, FS, NT, R, KS, RW, CH>),
+        constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<kH, NT, KS * CH>::kBytes, red);
+        hipLaunchKernelGGL((k_experts_second_mm<W, FS, NT, R, KS, RW, CH>),
                            dim3((e.second.tiles + R * RW - 1) / (R * RW) * (unsigned)e.most_tiles * (kListMany / (16 * NT))),
                            dim3(64 * KS * RW), lds, stream, e);
     }
 }
-template <int MATH>
-void launch_experts_second(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream) {
-    if (W == 4) {
-        if (fs == 1) launch_second_shape<MATH, 4, 1>(e, tile, stream);
-        else launch_second_shape<MATH, 4, 4>(e, tile, stream);
-    } else {
-        if (fs == 1) launch_second_shape<MATH, 2, 1>(e, tile, stream);
-        else launch_second_shape<MATH, 2, 4>(e, tile, stream);
-    }
-}
+// in bk_experts_second.hip
+void launch_experts_second(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream);
+void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream);
 
 }  // namespace bk

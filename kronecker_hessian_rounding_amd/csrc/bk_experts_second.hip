@@ -1,9 +1,26 @@
-// bk_experts_second.hip -- the experts' second product, of rows in pieces (kernels in bk_experts.hpp).
+// bk_experts_second.hip -- the experts' second product (kernels in bk_experts.hpp).
 #include "bk_experts.hpp"
 
 namespace bk {
-template void launch_experts_second<kH2>(const ExpertArgs&, int, int, int, hipStream_t);
-template void launch_experts_second<kH3>(const ExpertArgs&, int, int, int, hipStream_t);
-template void launch_experts_second_few<2>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
-template void launch_experts_second_few<3>(const FewArgs&, int, int, int, void*, int, int64_t, hipStream_t);
+
+void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    if (W == 4) {
+        if (fs == 1) launch_second_few<4, 1>(e, splits, y, ytype, ldy, stream);
+        else launch_second_few<4, 4>(e, splits, y, ytype, ldy, stream);
+    } else {
+        if (fs == 1) launch_second_few<2, 1>(e, splits, y, ytype, ldy, stream);
+        else launch_second_few<2, 4>(e, splits, y, ytype, ldy, stream);
+    }
+}
+
+void launch_experts_second(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream) {
+    if (W == 4) {
+        if (fs == 1) launch_second_shape<4, 1>(e, tile, stream);
+        else launch_second_shape<4, 4>(e, tile, stream);
+    } else {
+        if (fs == 1) launch_second_shape<2, 1>(e, tile, stream);
+        else launch_second_shape<2, 4>(e, tile, stream);
+    }
+}
+
 }  // namespace bk

@@ -64,10 +64,10 @@ struct MvArgs {
 };
 
 // ---------------------------------------------------------------- operands
-enum Math { kBF16, kF16, kF8, kI8, kF32, kH2, kH3 };
+enum Math { kBF16, kF16, kF8, kI8, kF32, kH };
 
-// kBytes: of an element of x in memory; kLds: of one (fp32: of a piece of one) in LDS. kH2 and kH3 are rows that lie
-// in memory as two or three planes of bf16 pieces, the largest first, a.n elements each.
+// kBytes: of an element of x in memory; kLds: of one (fp32: of a piece of one) in LDS. kH are rows that lie in
+// memory as three planes of bf16 pieces, the largest first, a.n elements each.
 template <int MATH> struct Mt;
 template <> struct Mt<kBF16> {
     using Op = bf16x8;
@@ -80,10 +80,7 @@ template <> struct Mt<kBF16> {
 template <> struct Mt<kF32> : Mt<kBF16> {
     static constexpr int kBytes = 4, kPieces = 3;
 };
-template <> struct Mt<kH2> : Mt<kBF16> {
-    static constexpr int kPieces = 2, kPlanes = 2;
-};
-template <> struct Mt<kH3> : Mt<kBF16> {
+template <> struct Mt<kH> : Mt<kBF16> {
     static constexpr int kPieces = 3, kPlanes = 3;
 };
 template <> struct Mt<kF16> {

@@ -62,3 +62,46 @@ def test_lora_holds_every_bit_between_its_products(T, n, m, r, xt, wt):
             y = bk.lora(x.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=torch.full((3,), 2.0 ** -16, device="cuda"), out_dtype=out).cpu()
             want = want * 2.0 ** -16
         assert torch.equal(y, want.float().to(out)), (out, int((y != want.float().to(out)).sum()), y.numel())
+
+
+# ------------------------------------------------------------------ experts
+def experts_case(T, E, k, n, I, dbits, dgroup, xt, act, seed):
+    """Token t's columns 2 c and 2 c + 1 hold 64, the others 0, and weights are -1/2 or 1/2: Gate gives 64 in every row, which act
+    leaves, Up 64 in the one row c % I and 0 in the others, Down +-1/2 of that. So each result is +-2^11 times the router's
+    weight, by way of one column of Down's."""
+    g = gen(seed)
+    c = (torch.randint(0, n // 2, (1,), generator=g) + torch.arange(T)) % (n // 2)
+    x = torch.zeros(T, n)
+    x[torch.arange(T), 2 * c] = x[torch.arange(T), 2 * c + 1] = 64.0
+    gate = torch.full((E, I, n), 8, dtype=torch.uint8)
+    up = torch.full((E, I, n), 8, dtype=torch.uint8)
+    up[:, :, 1::2] = 7
+    pairs = torch.arange(n // 2)
+    up[:, pairs % I, 2 * pairs + 1] = 8
+    top = 2 ** (dbits - 1)
+    down = torch.randint(top - 1, top + 1, (E, n, I), generator=g, dtype=torch.uint8)
+    ids = torch.full((T, k), -1, dtype=torch.int32)
+    slot, e = torch.randint(0, k, (T,), generator=g), torch.randint(0, E, (T,), generator=g)
+    ids[torch.arange(T), slot] = e.to(torch.int32)
+    ones = lambda m, cols, group: torch.ones(E, m, -(-cols // group) if group else 1)
+    packed = [bk.pack_experts(w.cuda(), ones(m, cols, gr).cuda(), bits, gr)
+              for w, m, cols, bits, gr in ((gate, I, n, 4, 128), (up, I, n, 4, 128), (down, n, I, dbits, dgroup))]
+    half = (down.double() - (2 ** dbits - 1) / 2)[e, :, c % I]
+    return x.to(xt), packed, ids, (slot, half)
+
+
+@pytest.mark.parametrize("xt", [F32, F16, BF16, I8, E4M3])
+@pytest.mark.parametrize("T,E,k,n,I,dbits,dgroup", [(1, 3, 2, 600, 300, 4, 128), (3, 5, 2, 130, 65, 2, 0), (7, 4, 2, 600, 290, 4, 32), (16, 8, 3, 514, 257, 3, 64),
+                                                    (9, 4, 3, 4112, 4000, 4, 128), (16, 4, 3, 8200, 2048, 2, 64),  # in splits
+                                                    (20, 40, 2, 200, 100, 4, 128), (33, 12, 1, 600, 300, 2, 32),   # list tiles of 16
+                                                    (70, 2, 2, 600, 300, 4, 128), (300, 3, 1, 260, 129, 4, 32)])   # of 64
+def test_experts_hold_every_bit_between_their_products(T, E, k, n, I, dbits, dgroup, xt):
+    x, packed, ids, (slot, half) = experts_case(T, E, k, n, I, dbits, dgroup, xt, "silu", T + n)
+    for out, act in ((F32, "silu"), (F32, "gelu"), (F16, "silu"), (BF16, "gelu")):
+        w = whole_numbers((T,), out, T + k)
+        # the router's weight, of 24 bits, in one slot; others hold what must not matter. 2^11 times it stays in fp16's range
+        wt = torch.full((T, k), 3.0)
+        wt[torch.arange(T), slot] = w.float() * 2.0 ** -22
+        y = bk.experts(x.cuda(), *packed, ids.cuda(), wt.cuda(), act=act, out_dtype=out).cpu()
+        want = (w.double() * 2.0 ** -22 * 64 * 64)[:, None] * half
+        assert torch.equal(y, want.float().to(out)), (out, int((y != want.float().to(out)).sum()), y.numel())
