@@ -124,54 +124,45 @@ __device__ __forceinline__ void store_pieces(char* row, int64_t plane, int64_t i
 constexpr int kFewTokens = 16, kFewPairs = 512;  // of the few tokens' path: what LDS holds of the map
 inline bool few_tokens(int64_t T, int64_t k) { return T <= kFewTokens && T * k <= kFewPairs; }
 
-// The named experts, by one workgroup: an expert's slot is its place among the pairs that are the first to name one.
-// Row `slot` of the map: the leader of each token that names the expert, or -1.
+// The named experts, by one workgroup, in the order of their numbers. Row `slot` of the map: the leader of each token that
+// names the expert, or -1.
 __device__ __forceinline__ void list_named(const FewArgs& e, char* lds) {
-    const int pairs = e.T * e.k, threads = blockDim.x, waves = threads / 64;
-    int* id = reinterpret_cast<int*>(lds);    // [pairs]
-    int* first = id + kFewPairs;                   // [pairs]: the first pair with this pair's id
-    int* slot = first + kFewPairs;                // [pairs]: of first ones
-    int* base = slot + kFewPairs;                 // [waves]
+    constexpr int kWords = (int)(kMaxExperts / 32);
+    const int pairs = e.T * e.k, threads = blockDim.x;
+    int* id = reinterpret_cast<int*>(lds);                               // [pairs]
+    uint32_t* some = reinterpret_cast<uint32_t*>(id + kFewPairs);        // a bit an expert
+    int* before = reinterpret_cast<int*>(some + kWords);                 // experts of the words in front
+    if (threadIdx.x < kWords) some[threadIdx.x] = 0;
+    __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += threads) {
         const int x = e.ids[p];
-        id[p] = x >= 0 && x < e.E ? x : -1;
+        const bool named = x >= 0 && x < e.E;
+        id[p] = named ? x : -1;
+        if (named) atomicOr(&some[x >> 5], 1u << (x & 31));
     }
     __syncthreads();
-    int total = 0;
-    for (int p0 = 0; p0 < pairs; p0 += threads) {
-        const int p = p0 + threadIdx.x;
-        bool leader = false;
-        if (p < pairs && id[p] >= 0) {
-            int f = 0;
-            while (id[f] != id[p]) ++f;
-            first[p] = f;
-            leader = f == p;
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x, mine = lane < kWords ? __popc(some[lane]) : 0;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < kWords; d *= 2) {
+            const int v = __shfl_up(upto, d);
+            upto += lane >= d ? v : 0;
         }
-        const uint64_t b = __ballot(leader);
-        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-        if (lane == 0) base[w] = __popcll(b);
-        __syncthreads();
-        int before = total;
-        for (int i = 0; i < waves; ++i) {
-            before += i < w ? base[i] : 0;
-            total += base[i];
-        }
-        if (leader) {
-            const int s = before + __popcll(b & (((uint64_t)1 << lane) - 1));
-            slot[p] = s;
-            e.named[1 + s] = id[p];
-        }
-        __syncthreads();
+        if (lane < kWords) before[lane] = upto - mine;
+        if (lane == kWords - 1) e.named[0] = upto;
     }
-    if (threadIdx.x == 0) e.named[0] = total;
     int32_t* map = e.named + 1 + e.slots;
-    for (int i = threadIdx.x; i < total * 16; i += threads) map[i] = -1;
+    for (int i = threadIdx.x; i < e.slots * 16; i += threads) map[i] = -1;
     __syncthreads();  // (the map's own lines: written and then overwritten by this workgroup)
+    const auto slot = [&](int x) { return before[x >> 5] + __popc(some[x >> 5] & ((1u << (x & 31)) - 1)); };
+    for (int x = threadIdx.x; x < e.E; x += threads)
+        if (some[x >> 5] >> (x & 31) & 1) e.named[1 + slot(x)] = x;
     for (int p = threadIdx.x; p < pairs; p += threads)
         if (id[p] >= 0) {
             bool leader = true;
             for (int i = p / e.k * e.k; i < p; ++i) leader = leader && id[i] != id[p];
-            if (leader) map[slot[first[p]] * 16 + p / e.k] = p;
+            if (leader) map[slot(id[p]) * 16 + p / e.k] = p;
         }
 }
 
@@ -291,10 +282,11 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
 }
 
 // The second product of few tokens. A workgroup takes R row tiles of every named expert's D; its waves (and with `splits`
-// those of as many workgroups) share the chunks of all of them, wave w of W taking w, w + W, .. of slot * nc + chunk, and
-// each stages h's pieces for its next PF chunks in LDS of its own, as few_products does x: a token that does not name the
-// expert has zeros there. 16 tokens, 8 experts of 4096 x 14336: 65 us for 0.25 GB, 3.9 TB/s; one token, 6 of 2048 x 1408:
-// 6.8 us.
+// those of as many workgroups: `all` together, a power of two) share the chunks. Chunk c of expert i is wave (i nc + c) % all's, and
+// a wave takes the experts in the order of their numbers, so that a token's sums do not depend on what other tokens name. (One token
+// alone: slot in place of i, which spreads the chunks evenly.) Each wave stages h's pieces for its next PF chunks in LDS of its own,
+// as few_products does x: a token that does not name the expert has zeros there. 16 tokens, 8 experts of 4096 x 14336: 65
+// us for 0.25 GB, 3.9 TB/s; one token, 6 of 2048 x 1408: 6.8 us.
 template <int PF, int TB>
 struct SecondShape {
     static constexpr int NP = kPieces;
@@ -316,27 +308,56 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
     const int split = blockIdx.x % splits, wave = split * NW + w, all = splits * NW;
     const int64_t tile0 = (int64_t)(blockIdx.x / splits) * R;
     const int nc = e.nc;
+    int16_t* map = reinterpret_cast<int16_t*>(lds + NW * Sh::kBytes);  // [slots + 1][TB], -1 behind the named ones
+    int16_t* ids = map + (e.slots + 1) * TB;                           // [slots] of more than 64
+    const int live = __builtin_amdgcn_readfirstlane(e.named[0]);
+    int window = e.named[1 + min(lane, e.slots - 1)];  // lane: the expert of slot 64 i + lane, i that of the furthest chunk
+    if (TB > 1 && e.slots > 64) {
+        for (int i = threadIdx.x; i < e.slots; i += 64 * NW) ids[i] = (int16_t)e.named[1 + i];
+        __syncthreads();
+    }
     struct At {
-        int slot, chunk;
+        int slot, chunk, id;  // slot == live, chunk 0: behind the last
     };
-    const auto ahead = [&](At p) __attribute__((always_inline)) {  // the wave's next chunk
-        p.chunk += all;
-        while (p.chunk >= nc) {
-            p.chunk -= nc;
-            ++p.slot;
+    const auto enter = [&](At& p) __attribute__((always_inline)) {  // the wave's first chunk of a slot, if it has one
+        p.id = __builtin_amdgcn_readlane(window, p.slot & 63);
+        p.chunk = (wave - p.id * nc) & (all - 1);
+    };
+    const auto settle = [&](At p) __attribute__((always_inline)) {
+        if constexpr (TB == 1) {  // (at most 64 slots)
+            while (p.chunk >= nc) {
+                p.chunk -= nc;
+                ++p.slot;
+            }
+            p.slot = min(p.slot, live);
+            p.id = __builtin_amdgcn_readlane(window, min(p.slot, 63));
+        } else {
+            while (p.chunk >= nc && p.slot < live) {
+                ++p.slot;
+                if ((p.slot & 63) == 0) window = ids[min(p.slot + lane, e.slots - 1)];
+                enter(p);
+            }
+            if (p.slot >= live) p.chunk = 0;
         }
         return p;
     };
+    const auto ahead = [&](At p) __attribute__((always_inline)) {  // the wave's next chunk
+        p.chunk += all;
+        return settle(p);
+    };
     At next[PF];
-    next[0] = At{wave / nc, wave % nc};
+    {
+        At p = {0, wave, 0};
+        if (TB > 1) enter(p);
+        next[0] = settle(p);
+    }
 #pragma unroll
     for (int p = 1; p < PF; ++p) next[p] = ahead(next[p - 1]);
     Wd d[PF][R];
     float s[PF][R][kScales];
     // (behind the named experts' last chunk: some expert's, and never used)
     const auto fetch = [&](int p) __attribute__((always_inline)) {
-        const int id = __builtin_amdgcn_readfirstlane(e.named[1 + min(next[p].slot, e.slots - 1)]);
-        const char* codes = e.gate + min(max(id, 0), e.E - 1) * e.stride;
+        const char* codes = e.gate + min(max(next[p].id, 0), e.E - 1) * e.stride;
         const float* scales = (const float*)(codes + e.scale_offset);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -348,18 +369,15 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
         }
     };
     const int32_t* from = e.named + 1 + e.slots;
-    int16_t* map = reinterpret_cast<int16_t*>(lds + NW * Sh::kBytes);  // [slots][TB], -1 behind the named ones
-    const int live = __builtin_amdgcn_readfirstlane(e.named[0]);
 #pragma unroll
     for (int p = 0; p < PF; ++p) fetch(p);
-    for (int i = threadIdx.x; i < e.slots * TB; i += 64 * NW) {
-        const int pair = from[i / TB * 16 + i % TB];
+    for (int i = threadIdx.x; i < (e.slots + 1) * TB; i += 64 * NW) {
+        const int pair = from[min(i / TB, e.slots - 1) * 16 + i % TB];
         map[i] = (int16_t)(i / TB < live ? pair : -1);
     }
     __syncthreads();
-    const int total = live * nc, mine = total > wave ? (total - wave + all - 1) / all : 0;
     float sum[R][4] = {};
-    if (mine > 0) {
+    if (next[0].slot < live) {
         char* xs = lds + w * Sh::kBytes;
         u32x4 x[Sh::kUnits];
         uint32_t some = 0;  // units whose token names the expert
@@ -376,7 +394,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
                     c.slot = p == k ? next[k].slot : c.slot;
                     c.chunk = p == k ? next[k].chunk : c.chunk;
                 }
-                const int pair = map[min(c.slot, e.slots - 1) * TB + token];
+                const int pair = map[c.slot * TB + token];
                 some |= (uint32_t)(pair >= 0) << i;
                 x[i] = *reinterpret_cast<const u32x4*>(e.planes + ((int64_t)max(pair, 0) * NP + piece) * e.plane +
                                                        c.chunk * 256 + u * 16);
@@ -385,7 +403,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
         load();
         const char* xl = xs + min(lane & 15, TB - 1) * Sh::kPitch + (lane >> 4) * 16;
         int after = 0;  // as in few_products: keeps a set's writes behind the reads of the set before
-        for (int i0 = 0; i0 < mine; i0 += PF) {
+        while (next[0].slot < live) {
 #pragma unroll
             for (int i = 0; i < Sh::kUnits; ++i) {
                 const int v = lane + 64 * i, u = v % 16, piece = v / 16 % NP, p = v / (16 * NP) % PF, token = v / (16 * NP * PF);
@@ -409,8 +427,8 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
                 // which of the lane's tokens name the expert: the others' sums stay, whatever its scales hold
                 int16_t own[4] = {0, 0, 0, 0};
                 if constexpr (TB >= 4)
-                    __builtin_memcpy(own, __builtin_assume_aligned(map + min(now[p].slot, e.slots - 1) * TB + min(4 * (lane >> 4), TB - 4), 8), 8);
-                if (i0 + p < mine)
+                    __builtin_memcpy(own, __builtin_assume_aligned(map + now[p].slot * TB + min(4 * (lane >> 4), TB - 4), 8), 8);
+                if (now[p].slot < live)
 #pragma unroll
                     for (int f = 0; f < kScales; ++f) {
                         f32x4 acc[R] = {};
@@ -464,7 +482,7 @@ void launch_first_tokens(const FewArgs& e, hipStream_t stream) {
     // many fit side by side). Few tokens have registers for 64 bytes of codes ahead a lane; with more tokens x's pieces
     // have them.
     constexpr int NW = 4, PF = TB <= 4 ? 16 / W : 1;
-    constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17, list = sizeof(int) * (3 * kFewPairs + NW);
+    constexpr size_t red = sizeof(float) * NW * 2 * 16 * 17, list = sizeof(int) * (kFewPairs + kMaxExperts / 16);
     constexpr size_t lds = std::max<size_t>({(size_t)NW * FewShape<MATH, PF, TB>::kBytes, red, list});
     const unsigned grid = (unsigned)(e.slots * (e.plane / 32) + 1);
     if constexpr (TB > 1) {
@@ -501,7 +519,7 @@ void launch_second_tokens(const FewArgs& e, int splits, void* y, int ytype, int6
     const auto launch = [&](auto tiles) {
         constexpr int R = decltype(tiles)::value;
         const size_t red = sizeof(float) * NW * R * 16 * 17;
-        const size_t lds = std::max(red, (size_t)NW * SecondShape<PF, TB>::kBytes + sizeof(int16_t) * e.slots * TB);
+        const size_t lds = std::max(red, (size_t)NW * SecondShape<PF, TB>::kBytes + sizeof(int16_t) * ((e.slots + 1) * TB + e.slots));
         hipLaunchKernelGGL((k_experts_second_few<W, FS, R, PF, TB, NW>), dim3((unsigned)((e.tiles + R - 1) / R * splits)),
                            dim3(64 * NW), lds, stream, e, splits, y, ytype, ldy);
     };

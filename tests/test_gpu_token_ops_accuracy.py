@@ -105,3 +105,27 @@ def test_experts_hold_every_bit_between_their_products(T, E, k, n, I, dbits, dgr
         y = bk.experts(x.cuda(), *packed, ids.cuda(), wt.cuda(), act=act, out_dtype=out).cpu()
         want = (w.double() * 2.0 ** -22 * 64 * 64)[:, None] * half
         assert torch.equal(y, want.float().to(out)), (out, int((y != want.float().to(out)).sum()), y.numel())
+
+
+@pytest.mark.parametrize("T,E,k,n,I", [(2, 9, 3, 300, 200), (4, 30, 4, 200, 1400), (7, 12, 4, 513, 300), (8, 64, 6, 130, 700), (16, 6, 2, 300, 1000),
+                                       (16, 64, 8, 96, 400), (9, 8, 4, 4112, 4000), (30, 9, 3, 200, 300), (200, 4, 2, 130, 300)])
+def test_experts_other_rows_do_not_matter(T, E, k, n, I):
+    """Every token's result stays bit for bit, in fp32, when the other rows and the experts that they name change."""
+    g = gen(T + E)
+
+    def layer(m, c):
+        return bk.pack_experts(torch.randint(0, 16, (E, m, c), generator=g, dtype=torch.uint8).cuda(), torch.rand(E, m, -(-c // 128), generator=g).cuda(), 4, 128)
+
+    def choice():
+        return torch.rand(T, E, generator=g).argsort(1)[:, :k].to(torch.int32)
+    packed = [layer(I, n), layer(I, n), layer(n, I)]
+    x, ids, wt = torch.randn(T, n, generator=g), choice(), torch.rand(T, k, generator=g)
+    y = bk.experts(x.cuda(), *packed, ids.cuda(), wt.cuda()).cpu()
+    for r in range(3):
+        x2, ids2, w2 = torch.randn(T, n, generator=g), choice(), torch.rand(T, k, generator=g)
+        ids2[torch.rand(T, k, generator=g) < (0.0, 0.4, 0.9)[r]] = -1
+        for t in sorted({0, 1, T // 3, T // 2, T - 2, T - 1}):
+            x3, ids3, w3 = x2.clone(), ids2.clone(), w2.clone()
+            x3[t], ids3[t], w3[t] = x[t], ids[t], wt[t]
+            z = bk.experts(x3.cuda(), *packed, ids3.cuda(), w3.cuda()).cpu()
+            assert torch.equal(z[t], y[t]), (r, t, int((z[t] != y[t]).sum()), n)
