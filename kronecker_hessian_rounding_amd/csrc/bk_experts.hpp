@@ -380,10 +380,10 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
     if (next[0].slot < live) {
         char* xs = lds + w * Sh::kBytes;
         u32x4 x[Sh::kUnits];
-        uint32_t some = 0;  // units whose token names the expert
-        // unit of this lane: 16 bytes `u` of a piece of a token's row in chunk p of the set
+        // unit of this lane: 16 bytes `u` of a piece of a token's row in chunk p of the set. A buffer load past the buffer's end
+        // reads nothing and gives zeros: those of the tokens that do not name the expert. (All of h is below 2^31 bytes.)
+        const auto planes = __builtin_amdgcn_make_buffer_rsrc(e.planes, 0, NP * e.plane * e.T * e.k, 0x00027000);
         const auto load = [&]() __attribute__((always_inline)) {
-            some = 0;
 #pragma unroll
             for (int i = 0; i < Sh::kUnits; ++i) {
                 const int v = lane + 64 * i, u = v % 16, piece = v / 16 % NP, p = v / (16 * NP) % PF;
@@ -395,9 +395,8 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
                     c.chunk = p == k ? next[k].chunk : c.chunk;
                 }
                 const int pair = map[c.slot * TB + token];
-                some |= (uint32_t)(pair >= 0) << i;
-                x[i] = *reinterpret_cast<const u32x4*>(e.planes + ((int64_t)max(pair, 0) * NP + piece) * e.plane +
-                                                       c.chunk * 256 + u * 16);
+                const uint32_t at = (uint32_t)((pair * NP + piece) * e.plane + c.chunk * 256 + u * 16);
+                x[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(planes, pair >= 0 ? at : 0x80000000u, 0, 0));
             }
         };
         load();
@@ -408,8 +407,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
             for (int i = 0; i < Sh::kUnits; ++i) {
                 const int v = lane + 64 * i, u = v % 16, piece = v / 16 % NP, p = v / (16 * NP) % PF, token = v / (16 * NP * PF);
                 if (token < TB)
-                    *reinterpret_cast<u32x4*>(xs + token * Sh::kPitch + piece * Sh::kPiece + p * 256 + u * 16 + after) =
-                        some >> i & 1 ? x[i] : u32x4{0, 0, 0, 0};
+                    *reinterpret_cast<u32x4*>(xs + token * Sh::kPitch + piece * Sh::kPiece + p * 256 + u * 16 + after) = x[i];
             }
             wave_fence();
             At now[PF];
