@@ -650,9 +650,8 @@ __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)
     mm_products<MATH, W, FS, NT, 2, KS, RW, CH>(f.a, 0, Listed{e.tokens + f.l.begin}, stream, lds, sink);
 }
 
-// 16 R RW rows of D by 16 NT tokens. At the sizes above: 50 us with 256 rows by 32 tokens; 64 tokens in half as many rows
-// 55, 64 rows a wave 93, columns split over waves 64 to 104, 128 tokens 145. Matrix cores busy 25 %, vector instructions
-// 28 %, 1.3 waves a SIMD.
+// 16 R RW rows of D by 16 NT tokens. At the sizes above, int8 tokens: 110 us for the call with 128 rows by 32 tokens; 256 rows 116,
+// 64 rows 137; 64 tokens by 128 rows 141, by 256 rows 124; 16 tokens by 128 rows 111; 64 rows a wave spill.
 template <int W, int FS, int NT, int R, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
     constexpr int kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;
@@ -714,13 +713,25 @@ void launch_experts_first(const ExpertArgs& e, int tile, int W, int fs, hipStrea
 template <int W, int FS>
 void launch_second_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
     if (tile == kListFew) {
-        constexpr int NW = 4, PF = 1, R = 2;
-        constexpr size_t red = sizeof(float) * NW * R * 16 * 17;
-        constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<kH, PF, 16>::kBytes, red);
-        hipLaunchKernelGGL((k_experts_second<W, FS, R, PF, NW>), dim3((e.second.tiles + R - 1) / R * (unsigned)e.most_tiles),
-                           dim3(64 * NW), lds, stream, e);
+        // Four row tiles a workgroup: each stages all three pieces of its tokens' h. Two waves where the grid gives a unit more
+        // than the three workgroups of four waves that its LDS holds: 64 tokens of 6 in 64 experts 2048 x 1920 112 us for the call,
+        // with four 117; 24 of 2 in 16, 4096 x 2816, 69 and 74; on the other side 32 of 2 in 8, 4096 x 14336, 226 and with four 187.
+        // Eight where it does not give one to each: 24 of 2 in 8, 1024 x 4096, 30 and with four 34; on the other side 32 of 2 in
+        // 8 by 4096 x 14336 again, 192.
+        constexpr int PF = 1, R = 4;
+        const unsigned blocks = (e.second.tiles + R - 1) / R * (unsigned)e.most_tiles;
+        const auto launch = [&](auto waves) {
+            constexpr int NW = decltype(waves)::value;
+            constexpr size_t red = sizeof(float) * NW * R * 16 * 17;
+            constexpr size_t lds = std::max<size_t>((size_t)NW * FewShape<kH, PF, 16>::kBytes, red);
+            hipLaunchKernelGGL((k_experts_second<W, FS, R, PF, NW>), dim3(blocks), dim3(64 * NW), lds, stream, e);
+        };
+        const unsigned units = (unsigned)device_info().cus;
+        if (blocks > 3 * units) launch(std::integral_constant<int, 2>());
+        else if (blocks <= units) launch(std::integral_constant<int, 8>());
+        else launch(std::integral_constant<int, 4>());
     } else {
-        constexpr int NT = 2, R = 2, KS = 1, RW = 8, CH = 1;
+        constexpr int NT = 2, R = 2, KS = 1, RW = 4, CH = 1;
         constexpr size_t red = sizeof(float) * KS * 16 * (16 * R * RW + 4);
         constexpr size_t lds = std::max<size_t>(2 * (size_t)MmTile<kH, NT, KS * CH>::kBytes, red);
         hipLaunchKernelGGL((k_experts_second_mm<W, FS, NT, R, KS, RW, CH>),
@@ -728,6 +739,7 @@ void launch_second_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
                            dim3(64 * KS * RW), lds, stream, e);
     }
 }
+
 // in bk_experts_second.hip
 void launch_experts_second(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream);
 void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream);
