@@ -319,9 +319,11 @@ __device__ __forceinline__ f32x4 second_mma(typename Vec8<W>::type a, typename V
         return c;
     }
 }
+// What a value counts for the largest of its token: its magnitude, an infinity or NaN (which stays what it is) nothing.
+__device__ __forceinline__ float finite_magnitude(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; }
 // The power of two for fp16 pieces of values up to `top`, as the exponent; both it and its inverse are normal.
 __device__ __forceinline__ int piece_exponent(float top) {
-    return top > 0.0f && top < INFINITY ? min(max(14 - (int)((__float_as_uint(top) >> 23) - 127), -126), 126) : 0;
+    return top > 0.0f ? min(max(14 - (int)((__float_as_uint(top) >> 23) - 127), -126), 126) : 0;
 }
 __device__ __forceinline__ float power(int ex) { return __uint_as_float((uint32_t)(127 + ex) << 23); }
 // Cuts the next piece off x (the last one: rounds it).
@@ -471,7 +473,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
         float up = 1.0f;
         if constexpr (kScaled) {
             float top = 0.0f;
-            for (int s = 0; s < steps; ++s) top = fmaxf(top, fabsf(u[tk * pitch + 32 * s + part]));
+            for (int s = 0; s < steps; ++s) top = fmaxf(top, finite_magnitude(u[tk * pitch + 32 * s + part]));
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
             const int ex = piece_exponent(top);
@@ -712,7 +714,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
                 v[i] *= f;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]));
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, finite_magnitude(v[i][e]));
         }
         if constexpr (kScaled) {
             top = fmaxf(top, __shfl_xor(top, 1));

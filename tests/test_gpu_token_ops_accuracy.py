@@ -129,3 +129,20 @@ def test_experts_other_rows_do_not_matter(T, E, k, n, I):
             x3[t], ids3[t], w3[t] = x[t], ids[t], wt[t]
             z = bk.experts(x3.cuda(), *packed, ids3.cuda(), w3.cuda()).cpu()
             assert torch.equal(z[t], y[t]), (r, t, int((z[t] != y[t]).sum()), n)
+
+
+# ------------------------------------------------------------------ lora's other edges
+@pytest.mark.parametrize("T,r,m", [(5, 16, 200), (40, 13, 130), (6, 200, 70), (180, 16, 200), (150, 64, 96), (140, 5, 300)])
+@pytest.mark.parametrize("out", [F32, F16, BF16])
+def test_lora_infinity_in_one_rank(T, r, m, out):
+    """An infinite u_k leaves the token's other ranks as they are, above fp16's largest value too: the sum is infinite, not NaN."""
+    n, R = 64, 2
+    g = gen(r)
+    x = torch.full((T, n), 100.0)
+    a, b = torch.zeros(R, r, n), torch.where(torch.rand(R, m, r, generator=g) < 0.5, 1.0, -1.0)
+    a[:, :, 3] = 1000.0          # u = 10^5
+    a[1, 2, 7] = float("inf")
+    ids = torch.arange(T, dtype=torch.int32) % R
+    y = bk.lora(x.to(F16).cuda(), a.to(F16).cuda(), b.to(F16).cuda(), ids.cuda(), out_dtype=out).cpu()
+    want = torch.where(ids[:, None] == 1, b[1, :, 2] * float("inf"), 1e5 * b[0].sum(1)).to(out)
+    assert torch.equal(y, want)
