@@ -185,6 +185,11 @@ template <> struct Raw16<false, true> {
     }
     __device__ __forceinline__ f32x4 value(int j, int type) const { return value4(v[j], type); }
 };
+// The sum of a token without an adapter: -0, which leaves every base as it is, -0 too; 0 where there is no base.
+__device__ __forceinline__ f32x4 no_sum(const void* base) {
+    const float v = base ? -0.0f : 0.0f;
+    return f32x4{v, v, v, v};
+}
 // y = base + g * sum for a lane's 16 rows of 64 whole ones of a token; raw holds the base.
 template <bool kWide, bool kWideY>
 __device__ __forceinline__ void finish16(bool based, int btype, const Raw16<kWide, kWideY>& raw, float g, const f32x4 (&sum)[4],
@@ -502,7 +507,11 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora(LoraArgs a) {
         }
     };
     const auto product = [&](int64_t i0, Rows& r, f32x4 (&acc)[4]) __attribute__((always_inline)) {
-        if (ad < 0) return;
+        if (ad < 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = no_sum(a.base);
+            return;
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) step_product(s, r.b[s], acc);
         if constexpr (kPasses)
@@ -751,6 +760,9 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll 1
             for (int64_t i0 = row0; i0 < row1; i0 += 64) {
                 f32x4 sum[4] = {};
+                if (ad < 0)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sum[j] = no_sum(a.base);
 #pragma unroll 1
                 for (int s = 0; s < S && 32 * s < a.r && ad >= 0; ++s) {
                     Op b[4];
@@ -867,7 +879,10 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
         const uint64_t members = cur.members & own;
         if (members) {
             f32x4 acc[8] = {};
-            if (cur.ad >= 0)
+            if (cur.ad < 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] = no_sum(a.base);
+            } else {
 #pragma unroll
                 for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -877,6 +892,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
                         for (int j = 0; j < 8; ++j)
                             acc[j] = second_mma<W>(uo, *reinterpret_cast<const Op*>(block + ((s * 8 + j) * 64 + lane) * 8), acc[j]);
                     }
+            }
 #pragma unroll
             for (int v = 0; v < 4; ++v)
                 if (members >> token(v) & 1) {

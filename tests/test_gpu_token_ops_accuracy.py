@@ -146,3 +146,20 @@ def test_lora_infinity_in_one_rank(T, r, m, out):
     y = bk.lora(x.to(F16).cuda(), a.to(F16).cuda(), b.to(F16).cuda(), ids.cuda(), out_dtype=out).cpu()
     want = torch.where(ids[:, None] == 1, b[1, :, 2] * float("inf"), 1e5 * b[0].sum(1)).to(out)
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("T,r,m", [(5, 16, 200), (40, 13, 130), (6, 200, 70), (180, 16, 300), (150, 64, 100), (140, 5, 128)])
+def test_lora_without_an_adapter_is_the_base(T, r, m, dtype):
+    """To the sign of a zero, in every row; without a base +0."""
+    g = gen(m)
+    x, a, b = (torch.randn(s, generator=g).to(dtype).cuda() for s in ((T, 64), (2, r, 64), (2, m, r)))
+    base = torch.randn(T, m, generator=g)
+    base[torch.rand(T, m, generator=g) < 0.4] = -0.0
+    base[torch.rand(T, m, generator=g) < 0.2] = 0.0
+    base = base.to(dtype).cuda()
+    ids = torch.where(torch.arange(T) % 3 == 1, 1, -1).to(torch.int32).cuda()
+    bits = torch.int32 if dtype == F32 else torch.int16
+    y = bk.lora(x, a, b, ids, base=base)
+    assert torch.equal(y[ids < 0].view(bits), base[ids < 0].view(bits))
+    assert bool((bk.lora(x, a, b, ids)[ids < 0].view(bits) == 0).all())
