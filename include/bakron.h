@@ -469,7 +469,8 @@ int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const vo
  *     64 bits.
  *   logits: BAKRON_F32, F16 or BF16, ldl >= E. ids: T x k int32, contiguous, the experts in falling order of what they
  *     are chosen by, the lowest index first among equals. weights: T x k fp32: the scores of the chosen; with
- *     renorm != 0 divided by their sum (0 if that is 0); times scale.
+ *     renorm != 0 divided by their sum (0 if that is 0); times scale. Sigmoid's are 64-bit values, rounded once; softmax's
+ *     arithmetic is fp32.
  *   An expert whose logit or bias is -infinity or NaN is never chosen (and not in softmax's sum): slots that find none
  *     hold id -1 and weight 0. Logits of +infinity share softmax's whole weight equally.
  *   No workspace; deterministic.

@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
                 const double s = wave_add(p);
                 p = s > 0.0 ? p / s : 0.0;
             }
-            w = (float)p;
+            w = (float)(p * (double)a.scale);  // the one rounding
         } else {
             // l - mx, 0 where both are infinite
             const auto term = [&](float v) { return v == mx ? 1.0f : expf(v - mx); };
@@ -164,11 +164,11 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
                 for (int i = 0; i < NV; ++i) s += l[i] > -INFINITY ? term(l[i]) : 0.0f;
             }
             s = wave_add(s);
-            w = s > 0.0f ? w / s : 0.0f;
+            w = (s > 0.0f ? w / s : 0.0f) * a.scale;
         }
         if (lane < a.k) {
             a.ids[t * a.k + lane] = chosen;
-            a.weights[t * a.k + lane] = w * a.scale;
+            a.weights[t * a.k + lane] = w;
         }
     }
 }

@@ -163,3 +163,16 @@ def test_lora_without_an_adapter_is_the_base(T, r, m, dtype):
     y = bk.lora(x, a, b, ids, base=base)
     assert torch.equal(y[ids < 0].view(bits), base[ids < 0].view(bits))
     assert bool((bk.lora(x, a, b, ids)[ids < 0].view(bits) == 0).all())
+
+
+# ------------------------------------------------------------------ route
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("T,E,k", [(40, 256, 8), (30, 64, 6), (20, 1000, 64)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_weights_are_rounded_once(T, E, k, renorm, dtype):
+    """They are 64-bit values (off by some 2^-50) times the factor, and one rounding: half a step of fp32, at most U relative."""
+    l = (2 * torch.randn(T, E, generator=gen(E))).to(dtype)
+    ids, w = bk.route(l.cuda(), k, "sigmoid", renormalize=renorm, scale=2.7)
+    p = torch.sigmoid(l.double()).gather(1, ids.cpu().long())
+    p = (p / p.sum(1, keepdim=True) if renorm else p) * float(torch.tensor(2.7))
+    assert bool(((w.cpu().double() - p).abs() <= p * U * (1 + 2.0 ** -20)).all())
