@@ -94,8 +94,8 @@ struct Listed {  // token t is row list[t]
 __device__ __forceinline__ float activation(float v, int act) {
     // v sigmoid(v), or gelu's tanh form v sigmoid(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3)
     const float z = act == BAKRON_ACT_SILU ? v : 1.5957691216057308f * fmaf(0.044715f * v * v, v, v);
-    // (the hardware's exponential and reciprocal are within 1 ulp; the argument's rounding weighs most where v is smallest)
-    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    // (exponential and quotient of full fp32 accuracy: the hardware's exponential alone is off by some |z| steps)
+    return v / (1.0f + expf(-z));
 }
 
 // h between the products: three bf16 pieces, the largest first, which hold all 24 bits of it (the first two are cut off, the

@@ -107,6 +107,36 @@ def test_experts_hold_every_bit_between_their_products(T, E, k, n, I, dbits, dgr
         assert torch.equal(y, want.float().to(out)), (out, int((y != want.float().to(out)).sum()), y.numel())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [1, 6, 40, 400])
+def test_activation_is_formed_in_fp32(T, act):
+    """Values from -80 on by themselves through act. The exponential is within an ulp (2 U), its sum with 1, the quotient and the
+    product with u one rounding each: 5 U. gelu's argument has six roundings (two constants, four operations), 6 U |z| of the
+    result; U more for second-order terms."""
+    n = I = 64
+    E = 2
+    g = gen(T)
+    v = torch.rand(T, generator=g) * 90 - 80
+    if act == "gelu":
+        v = v.clamp_min(-9.5) if T == 1 else torch.rand(T, generator=g) * 15 - 9.5
+    x = torch.zeros(T, n)
+    x[:, 4] = x[:, 5] = v
+    gate = torch.full((E, I, n), 8, dtype=torch.uint8)
+    down = torch.full((E, n, I), 8, dtype=torch.uint8)
+    up = torch.full((E, I, n), 8, dtype=torch.uint8)
+    up[:, :, 1::2] = 7
+    up[:, 9, 5] = 8
+    one = torch.ones(E, I, 1)
+    packed = [bk.pack_experts(c.cuda(), one.cuda(), 4) for c in (gate, up, down)]
+    y = bk.experts(x.cuda(), *packed, torch.zeros(T, 1, dtype=torch.int32).cuda(), torch.ones(T, 1).cuda(), act=act).cpu().double()
+    d = v.double()
+    z = d if act == "silu" else 2 * (2 / torch.pi) ** 0.5 * (d + 0.044715 * d ** 3)
+    want = d / (1 + torch.exp(-z)) * d / 2
+    tol = want.abs() * U * (6 + (6 * z.abs() if act == "gelu" else 0.0))
+    err = (y - want[:, None]).abs()
+    assert bool((err <= tol[:, None]).all()), float((err / tol[:, None]).max())
+
+
 @pytest.mark.parametrize("T,E,k,n,I", [(2, 9, 3, 300, 200), (4, 30, 4, 200, 1400), (7, 12, 4, 513, 300), (8, 64, 6, 130, 700), (16, 6, 2, 300, 1000),
                                        (16, 64, 8, 96, 400), (9, 8, 4, 4112, 4000), (30, 9, 3, 200, 300), (200, 4, 2, 130, 300)])
 def test_experts_other_rows_do_not_matter(T, E, k, n, I):
