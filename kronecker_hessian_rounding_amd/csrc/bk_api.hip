@@ -93,27 +93,25 @@ size_t elem_size(int type) {
 }
 bool wide_type(int type) { return type == BAKRON_F32 || type == BAKRON_F16 || type == BAKRON_BF16; }
 
-// rows of `width` bytes, `pitch` bytes apart
+// rows of `width` bytes, `pitch` bytes apart; in 128 bits, where no row's address wraps
+typedef __int128 wide_t;
 struct Rows {
     const void* p;
-    int64_t rows, width, pitch;
+    wide_t rows, width, pitch;
 };
-Rows rows_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int type) {
-    const int64_t e = (int64_t)elem_size(type);
+Rows rows_of(const void* p, wide_t rows, wide_t cols, wide_t ld, int type) {
+    const wide_t e = (wide_t)elem_size(type);
     return {p, rows, cols * e, ld * e};
 }
 // Whether two arrays share a byte. Rows of one pitch may interleave (columns of one
 // buffer); with different pitches, ranges that cross count as overlapping.
 bool overlap(const Rows& a, const Rows& b) {
     if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    const uintptr_t a1 = a0 + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
-    const uintptr_t b1 = b0 + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
-    if (a1 <= b0 || b1 <= a0) return false;
+    const wide_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    if (a0 + (a.rows - 1) * a.pitch + a.width <= b0 || b0 + (b.rows - 1) * b.pitch + b.width <= a0) return false;
     if (a.pitch != b.pitch) return true;
-    const uintptr_t d = b0 >= a0 ? (b0 - a0) % (uintptr_t)a.pitch
-                                 : ((uintptr_t)a.pitch - (a0 - b0) % (uintptr_t)a.pitch) % (uintptr_t)a.pitch;
-    return d < (uintptr_t)a.width || d + (uintptr_t)b.width > (uintptr_t)a.pitch;
+    const wide_t d = b0 >= a0 ? (b0 - a0) % a.pitch : (a.pitch - (a0 - b0) % a.pitch) % a.pitch;
+    return d < a.width || d + b.width > a.pitch;
 }
 bool same_rows(const Rows& a, const Rows& b) { return a.p == b.p && a.pitch == b.pitch && a.width == b.width; }
 
@@ -131,14 +129,13 @@ bool bad_pack_shape(int64_t m, int64_t n, int32_t bits, int64_t group) {
 bool bad_heads(int64_t T, int64_t H, int64_t d, int64_t st, int64_t sh) {
     if ((H > 1 && sh < d) || (T > 1 && st < d)) return true;
     if (H <= 1 || T <= 1) return false;
-    return st < (__int128)(H - 1) * sh + d && sh < (__int128)(T - 1) * st + d;
+    return st < (wide_t)(H - 1) * sh + d && sh < (wide_t)(T - 1) * st + d;
 }
 Rows rows_of_heads(const void* p, int64_t T, int64_t H, int64_t d, int64_t st, int64_t sh, int type) {
-    const int64_t e = (int64_t)elem_size(type);
-    if (H <= 1) return {p, T, d * e, T > 1 ? st * e : d * e};
-    if (T <= 1) return {p, H, d * e, sh * e};
-    if (st >= sh) return {p, T, ((H - 1) * sh + d) * e, st * e};
-    return {p, H, ((T - 1) * st + d) * e, sh * e};
+    if (H <= 1) return rows_of(p, T, d, T > 1 ? st : d, type);
+    if (T <= 1) return rows_of(p, H, d, sh, type);
+    if (st >= sh) return rows_of(p, T, (wide_t)(H - 1) * sh + d, st, type);
+    return rows_of(p, H, (wide_t)(T - 1) * st + d, sh, type);
 }
 
 bool bad_experts(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {

@@ -147,3 +147,22 @@ def test_packed_experts_refuse_other_bytes():
             bk.PackedExperts(d, e, 64, 256, 4, 128)
     with pytest.raises(ValueError):
         bk.pack_experts(torch.zeros(2, 4, 64, dtype=torch.uint8), torch.ones(2, 4), 4)
+
+
+def test_ends_of_rows_do_not_wrap():
+    """Rows so far apart that 64 bits would take the last one's address round to the first's: an output between the first
+    two of them lies in their range."""
+    far, between = 1 << 61, at((1 << 36) + 4096)  # of 16 bits an element: 5 rows end where they begin
+    lib, nb = bk.LIB, bk.LIB.bakron_packed_bytes
+    heads = dict(Q=A, hq=4, qt=far, qh=64, K=None, hk=0, kt=0, kh=0, type=BF16, T=5, d=64, qg=None, kg=None, gtype=BF16, eps=1e-6, norm=1,
+                 pos=None, pos32=0, freq=None, rot=0, inter=0, YQ=between, yqt=256, yqh=64, YK=None, ykt=0, ykh=0, stream=None)
+    assert lib.bakron_head_norm(*heads.values()) == INVALID
+    # heads that hold tokens, as far apart
+    assert lib.bakron_head_norm(*{**heads, "hq": 5, "T": 4, "qt": 64, "qh": far}.values()) == INVALID
+    assert lib.bakron_lora(A, BF16, 5, 64, far, None, B, C, BF16, 4, 8, 32, D, E, None, 0, 0, between, BF16, 32, None, 0, None) == INVALID
+    assert lib.bakron_route(A, BF16, 5, 64, far, 2, 0, None, 1, 1.0, between, D, None) == INVALID
+    gb, wb = 4 * nb(32, 64, 4, 0), lib.bakron_experts_workspace_bytes(5, 2, 4, 64, 32)
+    assert lib.bakron_experts(B, C, gb, 4, 0, D, 4 * nb(64, 32, 4, 0), 4, 0, 4, 64, 32, A, BF16, 5, far, None, E, F, 2, 0, between, BF16, 64,
+                              at(8 << 36), wb, None) == INVALID
+    assert lib.bakron_matvec(B, nb(32, 64, 4, 0), 32, 64, 4, 0, A, BF16, 5, far, None, between, BF16, 32, None) == INVALID
+    assert lib.bakron_rmsnorm(A, BF16, 5, 64, far, None, 0, None, 0, None, BF16, 1e-6, 0, 0, between, BF16, 64, None, None) == INVALID
