@@ -452,7 +452,8 @@ int bakron_lora(const void* X, int32_t xtype, int64_t T, int64_t n, int64_t ldx,
  *   The arithmetic is fp32, rounded once at the end; angles are formed and reduced in 64 bits (the product is exact
  *   for positions below 2^29; sine and cosine within 3e-7). A head of zeros with eps = 0, or one whose sum of squares passes
  *   fp32's range, is as for bakron_rmsnorm. No workspace; deterministic; a head's result depends on its own row only.
- *   YQ may be Q itself and YK K itself (same pointer and strides); no other overlap with an output is allowed.
+ *   YQ may be Q itself and YK K itself (same pointer and strides), also where heads of equal strides lie between each other
+ *   ([token][head][q k v]); no other overlap with an output is allowed.
  * Errors: INVALID_ARG for NULL Q or YQ (with T > 0; K and YK with hk > 0), T < 0 or > 2^31 - 1, hq < 1, hk < 0, either
  *   above 65535, d < 1 or > 512, rot odd, negative or > d, missing pos or freq with rot > 0, bad types or strides, eps
  *   negative or not finite, a gain without the norm, or overlap.

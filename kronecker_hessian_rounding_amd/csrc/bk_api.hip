@@ -104,10 +104,10 @@ Rows rows_of(const void* p, wide_t rows, wide_t cols, wide_t ld, int type) {
     return {p, rows, cols * e, ld * e};
 }
 // Whether two arrays share a byte. Rows of one pitch may interleave (columns of one
-// buffer); with different pitches, ranges that cross count as overlapping.
-bool overlap(const Rows& a, const Rows& b) {
+// buffer); with different pitches, ranges that cross count as overlapping. b_at: bytes from b.p to where b is taken to lie.
+bool overlap(const Rows& a, const Rows& b, wide_t b_at = 0) {
     if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
-    const wide_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    const wide_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p + b_at;
     if (a0 + (a.rows - 1) * a.pitch + a.width <= b0 || b0 + (b.rows - 1) * b.pitch + b.width <= a0) return false;
     if (a.pitch != b.pitch) return true;
     const wide_t d = b0 >= a0 ? (b0 - a0) % a.pitch : (a.pitch - (a0 - b0) % a.pitch) % a.pitch;
@@ -131,11 +131,29 @@ bool bad_heads(int64_t T, int64_t H, int64_t d, int64_t st, int64_t sh) {
     if (H <= 1 || T <= 1) return false;
     return st < (wide_t)(H - 1) * sh + d && sh < (wide_t)(T - 1) * st + d;
 }
-Rows rows_of_heads(const void* p, int64_t T, int64_t H, int64_t d, int64_t st, int64_t sh, int type) {
+struct Heads {
+    const void* p;
+    int64_t T, H, d, st, sh;
+    int type;
+};
+Rows rows_of_heads(const Heads& a) {
+    const auto [p, T, H, d, st, sh, type] = a;
     if (H <= 1) return rows_of(p, T, d, T > 1 ? st : d, type);
     if (T <= 1) return rows_of(p, H, d, sh, type);
     if (st >= sh) return rows_of(p, T, (wide_t)(H - 1) * sh + d, st, type);
     return rows_of(p, H, (wide_t)(T - 1) * st + d, sh, type);
+}
+// Whether two arrays of as many tokens share an element. Where their ranges of heads cross, heads of one stride may still lie
+// between each other (queries and keys of one head side by side): a head of the one and the head k further of the other.
+bool overlap(const Heads& a, const Heads& b) {
+    if (!overlap(rows_of_heads(a), rows_of_heads(b))) return false;
+    if ((a.T > 1 && a.st != b.st) || (a.H > 1 && b.H > 1 && a.sh != b.sh)) return true;
+    const int64_t st = a.T > 1 ? a.st : a.d;
+    const wide_t sh = (wide_t)(a.H > 1 ? a.sh : b.sh) * (wide_t)elem_size(a.type);
+    const Rows x = rows_of(a.p, a.T, a.d, st, a.type), y = rows_of(b.p, b.T, b.d, st, b.type);
+    for (int64_t k = 1 - a.H; k < b.H; ++k)
+        if (overlap(x, y, k * sh)) return true;
+    return false;
 }
 
 bool bad_experts(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
@@ -414,9 +432,8 @@ int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const vo
     if (!Q || !YQ || (hk && (!K || !YK)) || (rot && (!pos || !freq))) return BAKRON_E_INVALID_ARG;
     if (bad_heads(T, hq, d, qt, qh) || bad_heads(T, hq, d, yqt, yqh)) return BAKRON_E_INVALID_ARG;
     if (hk && (bad_heads(T, hk, d, kt, kh) || bad_heads(T, hk, d, ykt, ykh))) return BAKRON_E_INVALID_ARG;
-    const Rows in[2] = {rows_of_heads(Q, T, hq, d, qt, qh, type), rows_of_heads(hk ? K : nullptr, T, hk, d, kt, kh, type)};
-    const Rows out[2] = {rows_of_heads(YQ, T, hq, d, yqt, yqh, type),
-                         rows_of_heads(hk ? YK : nullptr, T, hk, d, ykt, ykh, type)};
+    const Heads in[2] = {{Q, T, hq, d, qt, qh, type}, {hk ? K : nullptr, T, hk, d, kt, kh, type}};
+    const Heads out[2] = {{YQ, T, hq, d, yqt, yqh, type}, {hk ? YK : nullptr, T, hk, d, ykt, ykh, type}};
     const bool same[2] = {Q == YQ && (T == 1 || qt == yqt) && (hq == 1 || qh == yqh),
                           K == YK && (T == 1 || kt == ykt) && (hk <= 1 || kh == ykh)};
     const Rows small[4] = {rows_of(qgain, 1, d, d, gtype), rows_of(kgain, 1, d, d, gtype),
@@ -427,7 +444,7 @@ int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const vo
         for (int i = 0; i < 2; ++i)
             if (overlap(in[i], out[o]) && !(i == o && same[i])) return BAKRON_E_INVALID_ARG;
         for (const Rows& r : small)
-            if (overlap(r, out[o])) return BAKRON_E_INVALID_ARG;
+            if (overlap(r, rows_of_heads(out[o]))) return BAKRON_E_INVALID_ARG;
     }
     const bk::HeadRows q = {Q, YQ, qgain, hq, qt, qh, yqt, yqh}, k = {K, YK, kgain, hk, kt, kh, ykt, ykh};
     return bk::launch_head_norm(q, k, type, T, d, gtype, eps, norm != 0, pos, pos32 != 0, freq, rot, interleaved != 0,

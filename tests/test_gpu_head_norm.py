@@ -206,3 +206,25 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         e = step()
         assert torch.equal(y[0], e[0]) and torch.equal(y[1], e[1])
+
+
+@pytest.mark.parametrize("T,H,Hk,d", [(5, 4, 4, 64), (1, 3, 3, 80), (7, 1, 1, 33), (3, 6, 2, 128)])
+@pytest.mark.parametrize("heads_outside", [False, True])
+def test_in_place_side_by_side(T, H, Hk, d, heads_outside):
+    """A projection that leaves query, key and value of one head side by side, [token][head][3][d] (or heads outside): in place,
+    and the values stay. Fewer keys than queries use the first heads' places."""
+    buf = torch.randn((H, T, 3, d) if heads_outside else (T, H, 3, d), generator=gen(d)).to(BF16).cuda()
+    rows = buf.transpose(0, 1) if heads_outside else buf
+    q, k, v = rows[:, :, 0], rows[:, :Hk, 1], rows[:, :, 2].clone()
+    gq, gk = torch.randn(d, generator=gen(1)).cuda(), torch.randn(d, generator=gen(2)).cuda()
+    pos, freq = torch.arange(T).cuda(), torch.rand(d // 2, generator=gen(3)).cuda()
+    kw = dict(q_gain=gq, k_gain=gk, positions=pos, freq=freq)
+    wq, wk = bk.head_norm(q.contiguous(), k.contiguous(), **kw)
+    rest = rows[:, Hk:, 1].clone()
+    yq, yk = bk.head_norm(q, k, out_q=q, out_k=k, **kw)
+    assert yq.data_ptr() == q.data_ptr() and torch.equal(q, wq) and torch.equal(k, wk)
+    assert torch.equal(rows[:, :, 2], v) and torch.equal(rows[:, Hk:, 1], rest)
+    # into the values' places and back
+    u = rows[:, :, 2]
+    bk.head_norm(q, out_q=u, q_gain=gq)
+    assert torch.equal(u, bk.head_norm(wq, q_gain=gq)[0]) and torch.equal(q, wq)

@@ -166,3 +166,17 @@ def test_ends_of_rows_do_not_wrap():
                               at(8 << 36), wb, None) == INVALID
     assert lib.bakron_matvec(B, nb(32, 64, 4, 0), 32, 64, 4, 0, A, BF16, 5, far, None, between, BF16, 32, None) == INVALID
     assert lib.bakron_rmsnorm(A, BF16, 5, 64, far, None, 0, None, 0, None, BF16, 1e-6, 0, 0, between, BF16, 64, None, None) == INVALID
+
+
+def test_head_norm_refuses_heads_that_cross():
+    """Queries and keys of one head side by side, [token][head][q k v]: outputs that share an element with an input or output
+    of another head, token or place."""
+    base, e = 1 << 36, 2
+    ok = dict(Q=A, hq=4, qt=768, qh=192, K=at(base + 64 * e), hk=4, kt=768, kh=192, type=BF16, T=3, d=64, qg=None, kg=None, gtype=BF16, eps=1e-6,
+              norm=1, pos=None, pos32=0, freq=None, rot=0, inter=0, YQ=A, yqt=768, yqh=192, YK=at(base + 64 * e), ykt=768, ykh=192, stream=None)
+    for kw in (dict(YK=A), dict(YQ=at(base + 64 * e)), dict(YK=at(base + 63 * e)), dict(YK=at(base + 65 * e)), dict(YK=at(base + (128 + 1) * e)),
+               dict(YQ=at(base + 192 * e)), dict(YQ=at(base + 768 * e)), dict(YQ=at(base + (768 + 3 * 192) * e)), dict(YK=at(base - 1 * e)),
+               dict(YK=at(base - (3 * 192 - 63) * e)), dict(YK=at(base + 64 * e), ykh=191), dict(YQ=A, yqt=769), dict(YQ=at(base - 2 * 768 * e)),
+               # heads that hold tokens
+               dict(qt=192, qh=768, kt=192, kh=768, yqt=192, yqh=768, ykt=192, ykh=768, YK=at(base + 32 * e))):
+        assert bk.LIB.bakron_head_norm(*{**ok, **kw}.values()) == INVALID, kw
