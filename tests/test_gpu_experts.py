@@ -302,3 +302,51 @@ def test_a_block_of_rounded_layers(T):
     y = bk.experts(n2.y, *packed, ei, ew, out_dtype=F32)
     ref, tol = form64(n2.y.cpu(), None, (gate, up, down, 4, 128, 4, 32), ei.cpu(), ew.cpu(), "silu")
     assert bool(((y.cpu().double() - ref).abs() <= tol + (k + 1) * U * (ref.abs() + tol) * 2).all())
+
+
+def test_offsets_past_2_31():
+    """Rows of x and y more than 2^31 elements apart, and the last of many experts behind 2^31 bytes of codes in each matrix.
+    The last expert's sums may meet in another order than the second's: 64 U of the result's norm."""
+    n, I, E = 4096, 1024, 1000
+    nb = [bk.LIB.bakron_packed_bytes(*s, 4, 128) for s in ((I, n), (I, n), (n, I))]
+    assert all((E - 1) * b > 2 ** 31 for b in nb)
+    two = [bk.pack_experts(c.cuda(), s.cuda(), 4, 128) for c, s in (layers(2, I, n, 4, 128, 1), layers(2, I, n, 4, 128, 2), layers(2, n, I, 4, 128, 3))]
+    many = []
+    for w, b in zip(two, nb):
+        data = torch.zeros(E * b, dtype=torch.uint8, device="cuda")  # scales of 0 in between
+        data[:b] = w.data[:b]
+        data[(E - 1) * b:] = w.data[b:]
+        many.append(bk.PackedExperts(data, E, w.m, w.n, 4, 128))
+    g = gen(9)
+    for T in (1, 2, 9, 40):  # 40: list tiles of 16
+        x = torch.randn(T, n, generator=g).to(BF16).cuda()
+        ids = torch.randint(0, 2, (T, 1), generator=g, dtype=torch.int32).cuda()
+        ids[-1] = 1
+        wt = torch.rand(T, 1, generator=g).cuda()
+        y = bk.experts(x, *two, ids, wt, out_dtype=F32)
+        z = bk.experts(x, *many, ids * (E - 1), wt, out_dtype=F32)
+        assert float((y - z).norm()) <= 2.0 ** -18 * float(y.norm())
+    # tiles of 64: many tokens of few slots
+    T, k = 20, 64
+    x = torch.randn(T, n, generator=g).to(BF16).cuda()
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    ids[:, 0], ids[:, 1] = 0, 1
+    wt = torch.rand(T, k, generator=g).cuda()
+    y, z = bk.experts(x, *two, ids, wt, out_dtype=F32), bk.experts(x, *many, torch.where(ids == 1, E - 1, ids), wt, out_dtype=F32)
+    assert float((y - z).norm()) <= 2.0 ** -18 * float(y.norm())
+    del many, data
+    ld = (1 << 31) + 8
+    for T in (2, 1):
+        ids, wt = ids[:T, :2].contiguous(), wt[:T, :2].contiguous()
+        xb = torch.empty((T - 1) * ld + n, dtype=BF16, device="cuda").as_strided((T, n), (ld, 1))
+        xb.copy_(x[:T])
+        yb = torch.empty((T - 1) * ld + n, dtype=BF16, device="cuda").as_strided((T, n), (ld, 1))
+        assert torch.equal(bk.experts(xb, *two, ids, wt, out=yb).contiguous(), bk.experts(x[:T], *two, ids, wt))
+    # more tokens: 18 rows, ld 2^28
+    ld, T = (1 << 28) + 8, 18
+    ids, wt = torch.randint(0, 2, (T, 1), generator=g, dtype=torch.int32).cuda(), torch.rand(T, 1, generator=g).cuda()
+    xb = torch.empty((T - 1) * ld + n, dtype=I8, device="cuda").as_strided((T, n), (ld, 1))
+    x8 = torch.randint(-127, 128, (T, n), generator=g, dtype=I8).cuda()
+    xb.copy_(x8)
+    yb = torch.empty((T - 1) * ld + n, dtype=BF16, device="cuda").as_strided((T, n), (ld, 1))
+    assert torch.equal(bk.experts(xb, *two, ids, wt, out=yb).contiguous(), bk.experts(x8, *two, ids, wt))

@@ -255,3 +255,28 @@ def test_stream_and_graph(T):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, step())
+
+
+@pytest.mark.parametrize("rest", [100, 3000])
+@pytest.mark.parametrize("xt,wt", [(BF16, BF16), (I8, F16)])
+def test_tokens_past_a_round_of_launches(rest, xt, wt):
+    """More than 65536 tokens go through in rounds; the last one in one launch (100) or two (3000). Rows at the rounds' ends
+    against 64 bits, and all against calls of 5000 tokens (whose sums start in other columns: twice the tolerance's part of those)."""
+    T, n, m, r, R = 65536 + rest, 40, 24, 8, 3
+    x, a, b, ids, scales, xs = inputs(T, n, m, r, R, xt, wt, seed=rest, none=0.1, run=7)
+    base = torch.randn(T, m, generator=gen(1))
+    xb = torch.zeros(T, n + 5, dtype=xt, device="cuda")
+    xb[:, 2:2 + n] = x.cuda()
+    yb = torch.full((T, m + 3), 9.0, device="cuda")
+    args = dict(scales=scales.cuda(), out_dtype=F32)
+    y = yb[:, 1:1 + m]
+    bk.lora(xb[:, 2:2 + n], a.cuda(), b.cuda(), ids.cuda(), base=base.cuda(), x_scale=xs.cuda(), out=y, **args)
+    for s in (slice(0, 40), slice(65536 - 70, 65536 + 100), slice(T - 90, T)):
+        check(y[s], x[s], a, b, ids[s], base[s], scales, xs[s])
+    for t0 in range(0, T, 5000):
+        s = slice(t0, min(T, t0 + 5000))
+        part = bk.lora(x[s].cuda(), a.cuda(), b.cuda(), ids[s].cuda(), base=base[s].cuda(), x_scale=xs[s].cuda(), **args)
+        mag = base[s].abs() + 2 * 1.5 * 1.5 * n * r * x[s].float().abs().amax() * a.float().abs().amax() * b.float().abs().amax()
+        assert bool(((y[s] - part).abs().cpu() <= 2 * U * (n / 8 + 8 + r + 4) * 2 * mag).all())
+    y.fill_(9.0)
+    assert bool((yb == 9.0).all())

@@ -195,6 +195,22 @@ def test_lora_without_an_adapter_is_the_base(T, r, m, dtype):
     assert bool((bk.lora(x, a, b, ids)[ids < 0].view(bits) == 0).all())
 
 
+@pytest.mark.parametrize("T,n,m,r", [(50, 700, 333, 24), (190, 700, 333, 24), (170, 3000, 128, 64), (90, 300, 70, 200)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_lora_other_rows_do_not_matter(T, n, m, r, dtype):
+    """In fp32, with the others' adapters alike (more than half of a tile's tokens name one) and mixed."""
+    g = gen(T)
+    x, a, b = torch.randn(T, n, generator=g).to(dtype), (torch.randn(5, r, n, generator=g) * 0.05).to(dtype), torch.randn(5, m, r, generator=g).to(dtype)
+    ids, base = torch.randint(-1, 5, (T,), generator=g, dtype=torch.int32), torch.randn(T, m, generator=g)
+    run = lambda x, ids: bk.lora(x.cuda(), a.cuda(), b.cuda(), ids.cuda(), base=base.cuda(), out_dtype=F32).cpu()
+    y = run(x, ids)
+    for others in (torch.full((T,), 2, dtype=torch.int32), torch.full((T,), -1, dtype=torch.int32), torch.randint(-1, 5, (T,), generator=g, dtype=torch.int32)):
+        for t in (0, 17, 40, T - 1):
+            x2, ids2 = torch.randn(T, n, generator=g).to(dtype), others.clone()
+            x2[t], ids2[t] = x[t], ids[t]
+            assert torch.equal(run(x2, ids2)[t], y[t])
+
+
 # ------------------------------------------------------------------ route
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("T,E,k", [(40, 256, 8), (30, 64, 6), (20, 1000, 64)])
