@@ -142,13 +142,30 @@ __global__ __launch_bounds__(256) void k_experts_splits(const float* part, int s
     store4(y, ytype, t * ldy + i, v, count);
 }
 
-// Splits of the few tokens' second product. For more than 4 tokens a row tile alone reads twice as much of h as of codes,
-// so that large layers take four tiles a workgroup, and four workgroups share their columns to fill the chip all the same:
-// 16 tokens, 8 experts of 4096 x 14336: 68 us and 5 for the sum, where one tile and no split takes 130. Below 2^15 chunks
-// of codes (32 MB at 4 bits) there is too little for the third launch to pay.
-int second_splits(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
+// Grid of the few tokens' second product: workgroups that share the columns of a row block, and row tiles of a block. LDS holds one
+// workgroup a unit, so there are at most as many as units where that is possible: first with four splits, which cost a
+// launch for their sum, and few tiles, which cost h's way into LDS the more often. us of a call at 16 (8) tokens as chosen, and
+// the next best of 1, 2, 4 splits by 1, 2, 4 tiles, 2 of 8 experts unless said:
+//   1024 x 8192: 4 by 1 48 (36), 4 by 2 51 (40), 1 by 1 105 (71)       2048 x 5632: 4 by 2 46 (37), 4 by 4 53 (44), 1 by 1 81 (57)
+//   4096 x 14336: 4 by 4 175 (139), 2 by 2 199 (152), 1 by 1 254       7168 x 2048, 4 of 64: 2 by 4 212 (137), 4 by 4 234, 1 by 1 324
+//   16384 x 1024: 1 by 4 52 (47), 2 by 4 58 (53), 1 by 1 81 (53)       24576 x 1024: 1 by 4 98 (83), 2 by 4 97 (86)
+// 2 to 4 tokens take one tile (their waves have no room for more): 4 tokens, 2048 x 1408, 6 of 64, 2 splits 38, 1 44, 4 45; 1024 x
+// 3584, 2 of 16, 4 splits 20, 1 24; 4096 x 14336 none 144, 2 148. One token alone is waits in a row, which splits lengthen.
+// With fewer than 64 chunks of columns there is too little for the launch to pay: 4096 x 2048, 2 of 4 (64 chunks), 4 by 4 23
+// (21), 1 by 1 25 (21); 4096 x 1024, 2 of 4 (32), 4 by 4 18 (16), 1 by 1 17 (15).
+struct SecondGrid {
+    int splits, tiles;
+};
+constexpr int kMostSplits = 4;
+SecondGrid second_grid(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     const int64_t tiles = (n + kRowTile - 1) / kRowTile, chunks = (I + kChunk - 1) / kChunk * std::min(E, T * k);
-    return T > 4 && tiles * chunks >= 1 << 15 ? 4 : 1;
+    if (T == 1) return {1, 1};
+    const int64_t units = device_info().cus;
+    const int most = T <= 4 ? 1 : 4;
+    for (int splits = chunks >= 64 ? kMostSplits : 1; splits >= 1; splits /= 2)
+        for (int r = 1; r <= most; r *= 2)
+            if ((tiles + r - 1) / r * splits <= units) return {splits, r};
+    return {1, most};
 }
 
 // Tokens of one round of launches: the plan and the workspace hold 2^14 pairs at most, and a grid fewer than 2^32 threads.
@@ -180,8 +197,7 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     if (few_tokens(T, k)) {
         l.named = take(4 * (1 + 17 * std::min(E, T * k)));
         l.planes = take(kPieces * l.plane * T * k);
-        const int splits = second_splits(T, k, E, n, I);
-        if (splits > 1) l.part = take(4 * splits * T * n);
+        if (T > 1) l.part = take(4 * kMostSplits * T * n);
         l.bytes = at;
         return l;
     }
@@ -275,10 +291,10 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
             default: launch_experts_first_few<kF8>(f, p1.W, fs, stream); break;
         }
         product(down, p2, n, I, dgroup);
-        const int splits = second_splits(T, k, E, n, I);
-        launch_experts_second_few(f, p2.W, fs, splits, y, ytype, ldy, stream);
-        if (splits > 1)
-            hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, f.part, splits,
+        const SecondGrid grid = second_grid(T, k, E, n, I);
+        launch_experts_second_few(f, p2.W, fs, grid.splits, grid.tiles, y, ytype, ldy, stream);
+        if (grid.splits > 1)
+            hipLaunchKernelGGL(k_experts_splits, dim3((unsigned)(T * ((n + 1023) / 1024))), dim3(256), 0, stream, f.part, grid.splits,
                                T, n, y, ytype, ldy);
         return hipGetLastError() == hipSuccess ? BAKRON_OK : BAKRON_E_DEVICE;
     }

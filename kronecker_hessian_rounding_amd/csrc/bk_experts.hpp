@@ -511,27 +511,28 @@ void launch_experts_first_few(const FewArgs& e, int W, int fs, hipStream_t strea
 }
 
 template <int W, int FS, int TB>
-void launch_second_tokens(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_second_tokens(const FewArgs& e, int splits, int tiles, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     // Up to 4 tokens are waits in a row, which 16 waves shorten; above, LDS for h's pieces leaves 8, with one chunk ahead.
     constexpr int NW = TB <= 4 ? 16 : 8, PF = TB <= 4 ? 2 : 1;
-    const auto launch = [&](auto tiles) {
-        constexpr int R = decltype(tiles)::value;
+    const auto launch = [&](auto r) {
+        constexpr int R = decltype(r)::value;
         const size_t red = sizeof(float) * NW * R * 16 * 17;
         const size_t lds = std::max(red, (size_t)NW * SecondShape<PF, TB>::kBytes + sizeof(int16_t) * ((e.slots + 1) * TB + e.slots));
         hipLaunchKernelGGL((k_experts_second_few<W, FS, R, PF, TB, NW>), dim3((unsigned)((e.tiles + R - 1) / R * splits)),
                            dim3(64 * NW), lds, stream, e, splits, y, ytype, ldy);
     };
     if constexpr (TB > 4) {
-        if (splits > 1) return launch(std::integral_constant<int, 4>());
+        if (tiles == 4) return launch(std::integral_constant<int, 4>());
+        if (tiles == 2) return launch(std::integral_constant<int, 2>());
     }
     launch(std::integral_constant<int, 1>());
 }
 template <int W, int FS>
-void launch_second_few(const FewArgs& e, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
-    if (e.T == 1) launch_second_tokens<W, FS, 1>(e, splits, y, ytype, ldy, stream);
-    else if (e.T <= 4) launch_second_tokens<W, FS, 4>(e, splits, y, ytype, ldy, stream);
-    else if (e.T <= 8) launch_second_tokens<W, FS, 8>(e, splits, y, ytype, ldy, stream);
-    else launch_second_tokens<W, FS, 16>(e, splits, y, ytype, ldy, stream);
+void launch_second_few(const FewArgs& e, int splits, int tiles, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+    if (e.T == 1) launch_second_tokens<W, FS, 1>(e, splits, tiles, y, ytype, ldy, stream);
+    else if (e.T <= 4) launch_second_tokens<W, FS, 4>(e, splits, tiles, y, ytype, ldy, stream);
+    else if (e.T <= 8) launch_second_tokens<W, FS, 8>(e, splits, tiles, y, ytype, ldy, stream);
+    else launch_second_tokens<W, FS, 16>(e, splits, tiles, y, ytype, ldy, stream);
 }
 // ---------------------------------------------------------------- more tokens
 // The list's tiles hold at most 16 tokens where an expert has about as few (few_products), else as many as a workgroup of
@@ -742,6 +743,6 @@ void launch_second_shape(const ExpertArgs& e, int tile, hipStream_t stream) {
 
 // in bk_experts_second.hip
 void launch_experts_second(const ExpertArgs& e, int tile, int W, int fs, hipStream_t stream);
-void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream);
+void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, int tiles, void* y, int ytype, int64_t ldy, hipStream_t stream);
 
 }  // namespace bk

@@ -3,13 +3,13 @@
 
 namespace bk {
 
-void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+void launch_experts_second_few(const FewArgs& e, int W, int fs, int splits, int tiles, void* y, int ytype, int64_t ldy, hipStream_t stream) {
     if (W == 4) {
-        if (fs == 1) launch_second_few<4, 1>(e, splits, y, ytype, ldy, stream);
-        else launch_second_few<4, 4>(e, splits, y, ytype, ldy, stream);
+        if (fs == 1) launch_second_few<4, 1>(e, splits, tiles, y, ytype, ldy, stream);
+        else launch_second_few<4, 4>(e, splits, tiles, y, ytype, ldy, stream);
     } else {
-        if (fs == 1) launch_second_few<2, 1>(e, splits, y, ytype, ldy, stream);
-        else launch_second_few<2, 4>(e, splits, y, ytype, ldy, stream);
+        if (fs == 1) launch_second_few<2, 1>(e, splits, tiles, y, ytype, ldy, stream);
+        else launch_second_few<2, 4>(e, splits, tiles, y, ytype, ldy, stream);
     }
 }
 

@@ -350,3 +350,10 @@ def test_offsets_past_2_31():
     xb.copy_(x8)
     yb = torch.empty((T - 1) * ld + n, dtype=BF16, device="cuda").as_strided((T, n), (ld, 1))
     assert torch.equal(bk.experts(xb, *two, ids, wt, out=yb).contiguous(), bk.experts(x8, *two, ids, wt))
+
+
+@pytest.mark.parametrize("n,I", [(900, 1100), (1500, 1030), (4000, 1024), (7000, 1100), (9000, 1060), (7000, 100), (5000, 130)])
+@pytest.mark.parametrize("T,bits,group", [(3, 4, 128), (7, 2, 32), (12, 4, 32)])
+def test_second_product_grids(T, bits, group, n, I):
+    """Every number of splits and of row tiles a workgroup, by the number of rows and columns."""
+    check(T, 8, 3, n, I, 4, 128, bits, group, BF16, F32, none=0.1, seed=n + T)
