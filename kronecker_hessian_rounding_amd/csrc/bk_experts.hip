@@ -176,6 +176,12 @@ int64_t round_tokens(int64_t T, int64_t k, int64_t E, int64_t n, int64_t I) {
     return t;
 }
 
+// List tiles of 16 tokens up to this many of an expert on average, else of 64. us of a call in tiles of 16 and of 64 with 16, 24
+// and 32 tokens an expert, bf16 tokens: 4 of 32 experts 2048 x 1408 66 86, 74 87, 91 95; 2 of 8, 1024 x 3584, 31 59, 40 60, 45
+// 61; 2 of 8, 4096 x 14336, 266 335, 332 340, 434 346; 4 of 16, 7168 x 2048, 133 142, 170 154, 201 163. int8: the same borders (the
+// third 244 284, 296 288, 393 295); fp32, whose pieces cost the wide tiles more: 4096 x 14336 412 745, 551 748, 708 752.
+constexpr int kFewEach = 24;
+
 struct Layout {
     size_t planes, part;
     size_t used, list, tokens, pair, weight;  // more tokens
@@ -327,8 +333,7 @@ int launch_experts(const void* gate, const void* up, int bits, int64_t group, co
         const int64_t tokens = std::min(round, T - t0), pairs = tokens * k;
         e.first.x = (const char*)x + t0 * ldx * xb;
         e.first.xs = xs ? xs + t0 : nullptr;
-        // tiles of 64 tokens where an expert has more than 16 on average (512 tokens of 4 in 32: 115 us, in tiles of 16 274)
-        const int tile = pairs > kListFew * std::min(E, pairs) ? kListMany : kListFew;
+        const int tile = pairs > kFewEach * std::min(E, pairs) ? kListMany : kListFew;
         e.most_tiles = (int)(std::min(E, pairs) + pairs / tile);
         PlanArgs p = {ids + t0 * k, weights + t0 * k, pairs, (int)k, (int)E, tile, (int32_t*)(w + l.used),
                       (ExpertTile*)(w + l.list), (int32_t*)(w + l.tokens), (int32_t*)(w + l.pair), (float*)(w + l.weight)};

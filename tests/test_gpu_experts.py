@@ -357,3 +357,10 @@ def test_offsets_past_2_31():
 def test_second_product_grids(T, bits, group, n, I):
     """Every number of splits and of row tiles a workgroup, by the number of rows and columns."""
     check(T, 8, 3, n, I, 4, 128, bits, group, BF16, F32, none=0.1, seed=n + T)
+
+
+@pytest.mark.parametrize("T,E,k", [(24, 1, 1), (25, 1, 1), (48, 4, 2), (50, 4, 2), (72, 6, 2), (17, 1, 1)])
+@pytest.mark.parametrize("dtype", [F32, BF16, I8])
+def test_tokens_of_an_expert(T, E, k, dtype):
+    """Around the border between list tiles of 16 and of 64 tokens, several tiles an expert."""
+    check(T, E, k, 300, 200, 4, 128, 4, 64, dtype, F32, seed=T)
