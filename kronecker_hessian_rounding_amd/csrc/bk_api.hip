@@ -1,6 +1,7 @@
 // bk_api.hip -- the extern "C" entry points of libbakron: argument validation on
 // the host, workspace checks, then dispatch to the kernel drivers. Every check
 // happens before anything is enqueued, so an invalid call enqueues no work.
+#include <algorithm>
 #include <mutex>
 
 #include "bk_internal.hpp"
@@ -93,25 +94,36 @@ size_t elem_size(int type) {
 }
 bool wide_type(int type) { return type == BAKRON_F32 || type == BAKRON_F16 || type == BAKRON_BF16; }
 
-// rows of `width` bytes, `pitch` bytes apart; in 128 bits, where no row's address wraps
+// rows of `width` bytes, `pitch` bytes apart (what passes 63 bits: 2^63 - 1, further than any address)
 typedef __int128 wide_t;
 struct Rows {
     const void* p;
-    wide_t rows, width, pitch;
+    int64_t rows, width, pitch;
 };
-Rows rows_of(const void* p, wide_t rows, wide_t cols, wide_t ld, int type) {
-    const wide_t e = (wide_t)elem_size(type);
-    return {p, rows, cols * e, ld * e};
+int64_t bytes_of(int64_t n, int64_t size) {
+    int64_t b;
+    return __builtin_mul_overflow(n, size, &b) ? INT64_MAX : b;
+}
+Rows rows_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int type) {
+    const int64_t e = (int64_t)elem_size(type);
+    return {p, rows, bytes_of(cols, e), bytes_of(ld, e)};
+}
+template <typename I>
+bool cross(const Rows& a, const Rows& b, I a0, I b0) {
+    if (a0 + (I)(a.rows - 1) * a.pitch + a.width <= b0 || b0 + (I)(b.rows - 1) * b.pitch + b.width <= a0) return false;
+    if (a.pitch != b.pitch) return true;
+    const I d = b0 >= a0 ? (b0 - a0) % a.pitch : (a.pitch - (a0 - b0) % a.pitch) % a.pitch;
+    return d < a.width || d + b.width > a.pitch;
 }
 // Whether two arrays share a byte. Rows of one pitch may interleave (columns of one
 // buffer); with different pitches, ranges that cross count as overlapping. b_at: bytes from b.p to where b is taken to lie.
+// Where a last row's address could pass 64 bits, in 128.
 bool overlap(const Rows& a, const Rows& b, wide_t b_at = 0) {
     if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
-    const wide_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p + b_at;
-    if (a0 + (a.rows - 1) * a.pitch + a.width <= b0 || b0 + (b.rows - 1) * b.pitch + b.width <= a0) return false;
-    if (a.pitch != b.pitch) return true;
-    const wide_t d = b0 >= a0 ? (b0 - a0) % a.pitch : (a.pitch - (a0 - b0) % a.pitch) % a.pitch;
-    return d < a.width || d + b.width > a.pitch;
+    const uint64_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    const uint64_t size = (uint64_t)(a.rows | a.width | a.pitch | b.rows | b.width | b.pitch);
+    if (b_at == 0 && (size >> 31) == 0 && ((a0 | b0) >> 62) == 0) return cross<int64_t>(a, b, (int64_t)a0, (int64_t)b0);
+    return cross<wide_t>(a, b, a0, b0 + b_at);
 }
 bool same_rows(const Rows& a, const Rows& b) { return a.p == b.p && a.pitch == b.pitch && a.width == b.width; }
 
@@ -140,8 +152,9 @@ Rows rows_of_heads(const Heads& a) {
     const auto [p, T, H, d, st, sh, type] = a;
     if (H <= 1) return rows_of(p, T, d, T > 1 ? st : d, type);
     if (T <= 1) return rows_of(p, H, d, sh, type);
-    if (st >= sh) return rows_of(p, T, (wide_t)(H - 1) * sh + d, st, type);
-    return rows_of(p, H, (wide_t)(T - 1) * st + d, sh, type);
+    const auto span = [d = d](int64_t n, int64_t stride) { return std::min<wide_t>((wide_t)(n - 1) * stride + d, INT64_MAX); };
+    if (st >= sh) return rows_of(p, T, (int64_t)span(H, sh), st, type);
+    return rows_of(p, H, (int64_t)span(T, st), sh, type);
 }
 // Whether two arrays of as many tokens share an element. Where their ranges of heads cross, heads of one stride may still lie
 // between each other (queries and keys of one head side by side): a head of the one and the head k further of the other.
