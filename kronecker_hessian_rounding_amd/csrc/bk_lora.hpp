@@ -950,11 +950,18 @@ void launch_up_ranks(const LoraArgs& a, hipStream_t stream) {
     else launch_up<W, 4, true, kWideY>(a, stream);
 }
 
-// One launch or two. r = 16, 4096 x 4096, 128 tokens of mixed adapters (of one): one launch 13.1 us (14.8), two 20 (14);
-// 4096 -> 14336, 128 tokens: 24 (25.8) and 47 (15); 192 tokens: 38 (40) and 52 (14.5). Up to 128 tokens
-// one launch is ahead by more where adapters are mixed than it is behind where there is one (ids lie on the device, so the
-// choice cannot look at them). Rank 64, one token, 4096 x 4096: one launch 21.7, two 15.2, since the columns of A are
-// split over workgroups there. Above 128, u's pieces pass k_lora_up's LDS and registers.
+// One launch or two, us of a call, one and two. In one launch every range of rows forms u anew, in two a tile takes a turn an
+// adapter; ids lie on the device, so the rule cannot see whether adapters are mixed, and its sizes are those that the
+// workspace's size is asked for by, T and r.
+//   r = 16, bf16, mixed adapters (one adapter):
+//     4096 x 4096:  16 tokens 9.1 12.8; 64 10.6 19.8 (12.9 14.8); 128 13.2 22.3 (15.2 15.0); 192 17.8 31.8 (19.5 15.1)
+//     4096 -> 14336: 64 tokens 16.4 25.8 (18.7 15.0); 128 24.4 39.0 (26.2 15.2); 192 39.5 53.2 (41.1 15.6); 256 39.9 69.7
+//   Up to 128 tokens one launch is ahead by more where adapters are mixed than it is behind where there is one; above, behind by
+//   more, up to 2.6 times.
+//   fp32 and long rows, whose u takes longer, would rather have two where tokens are few: fp32, r = 16, 4096 x 4096, one token
+//     15.0 13.0, 64 18.6 28.8 (24.0 18.6); 8192 -> 4096, one token 23.5 13.3, 64 27.5 29.9 (37.8 19.0); bf16, 11008 -> 4096, one token
+//     16.6 11.2, 64 19.8 24.4 (26.4 17.0). (256 KB of an adapter's A are the border for up to 16 tokens, 512 KB for more.)
+//   Rank 64, one token, bf16, 4096 x 4096: one launch 21.7, two 15.2. Above 128, u's pieces pass k_lora_up's LDS and registers.
 inline bool lora_few(int64_t T, int64_t r) { return (T <= 128 && r <= 32) || r > 128; }
 
 template <typename X, typename W>
