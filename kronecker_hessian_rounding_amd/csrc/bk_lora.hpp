@@ -682,7 +682,6 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     W* blocks = (W*)lds;                                       // [buffer][kBlock]
     float* box = (float*)lds;                                  // [wave][kBox], where no blocks are
     W* ops = (W*)(lds + UpShape<W, S>::kBytes);                // [piece][step][tile][lane][8]
-    float* undo = (float*)(ops + NP * S * NT * 512);           // [token]
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
     const uint32_t tiles = (uint32_t)((a.T + kUpTokens - 1) / kUpTokens);
@@ -708,6 +707,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
     if (ours == 0) return;
     // four threads a token, ranks 4 part .., 16 apart
     const int ut = threadIdx.x >> 2, part = threadIdx.x & 3, uad = __shfl(mine, ut & 63);
+    float undo = 1.0f;  // of token ut; the wave's token j is its lanes' 4 j ..
     if (ut < kUpTokens) {
         const int t = ut, ad = uad;
         const float f = ad < 0 ? 0.0f : (a.scales ? a.scales[ad] : 1.0f) * (a.xs ? a.xs[t0 + t] : 1.0f);
@@ -732,7 +732,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
             const float up = power(ex);
 #pragma unroll
             for (int i = 0; i < 2 * S; ++i) v[i] *= up;
-            if (part == 0) undo[t] = power(-ex);
+            undo = power(-ex);
         }
 #pragma unroll
         for (int i = 0; i < 2 * S; ++i) {
@@ -778,7 +778,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
                     }
                 }
                 finish_cut<kWideY>(a, box + w * kBox, i0, row1, members >> (16 * w) >> c & 1, t0 + min(16 * w + c, tokens - 1),
-                                   kScaled ? undo[16 * w + c] : 1.0f, sum, lane);
+                                   kScaled ? __shfl(undo, 4 * c) : 1.0f, sum, lane);
             }
         }
         return;
@@ -835,6 +835,9 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
             for (int v = 0; v < 4; ++v)
                 raw[v].fetch(a.base, (t0 + (own >> token(v) & 1 ? token(v) : (int)__builtin_ctzll(some))) * a.ldb + i0, c);
     };
+    float g[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) g[v] = kScaled ? __shfl(undo, 4 * (4 * q + v)) : 1.0f;
     // turns: the adapters of a row block, then those of the next, for all waves alike
     struct Turn {
         int64_t i0;
@@ -899,7 +902,7 @@ __global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2
                     float f[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] = acc[j][v];
-                    finish8<kWide, kWideY>(a.base != nullptr, a.btype, raw[v], kScaled ? undo[token(v)] : 1.0f, f, a.y, a.ytype,
+                    finish8<kWide, kWideY>(a.base != nullptr, a.btype, raw[v], kScaled ? g[v] : 1.0f, f, a.y, a.ytype,
                                            (t0 + token(v)) * a.ldy + cur.i0, c);
                 }
         }
@@ -936,7 +939,7 @@ void launch_down(const LoraArgs& a, hipStream_t stream) {
 template <typename W, int S, bool kEven, bool kWideY>
 void launch_up(const LoraArgs& a, hipStream_t stream) {
     const int64_t tiles = (a.T + kUpTokens - 1) / kUpTokens;
-    constexpr size_t lds = UpShape<W, S>::kBytes + pieces<W>() * S * (kUpTokens / 16) * 512 * sizeof(W) + kUpTokens * 4;
+    constexpr size_t lds = UpShape<W, S>::kBytes + pieces<W>() * S * (kUpTokens / 16) * 512 * sizeof(W);
     const dim3 grid((unsigned)(tiles * a.row_blocks * a.up_slots)), threads(64 * kUpWaves);
     if (a.base && a.btype == BAKRON_F32) hipLaunchKernelGGL((k_lora_up<W, S, kEven, true, kWideY>), grid, threads, lds, stream, a);
     else hipLaunchKernelGGL((k_lora_up<W, S, kEven, false, kWideY>), grid, threads, lds, stream, a);
