@@ -474,7 +474,8 @@ int bakron_head_norm(const void* Q, int64_t hq, int64_t qt, int64_t qh, const vo
  *     arithmetic is fp32.
  *   An expert whose logit or bias is -infinity or NaN is never chosen (and not in softmax's sum): slots that find none
  *     hold id -1 and weight 0. Logits of +infinity share softmax's whole weight equally.
- *   No workspace; deterministic.
+ *   The choice is among all E experts (one that is limited to some groups of them first is not formed: mask the others'
+ *   logits with -infinity). No workspace; deterministic.
  * Errors: INVALID_ARG for NULL logits, ids or weights (T > 0), T < 0 or > 2^40, E < 1 or > 1024, k < 1, > 64 or > E, bad
  *   types, ldl or scoring, a bias with softmax, a scale that is not finite, or outputs that overlap each other or an input.
  */
@@ -496,7 +497,7 @@ int bakron_route(const void* logits, int32_t type, int64_t T, int64_t E, int64_t
  *   Y: T x n, BAKRON_F32, F16 or BF16, ldy >= n.
  *   The products are exact with fp32 accumulation as bakron_matvec's, all sums are fp32, act and the values between the two
  *   products are formed in fp32 (they enter the second with all 24 bits), and Y is rounded once.
- *   Token t's result depends on its own row only. Deterministic.
+ *   For given sizes and types token t's result depends, to the last bit, on its own row only. Deterministic.
  *   ws: at least bakron_experts_workspace_bytes(T, k, E, n, I) bytes (0 for sizes that bakron_experts refuses, and T = 0),
  *     16-byte aligned. Calls that overlap need one each.
  * Errors: INVALID_ARG for NULL pointers (T > 0), T < 0 or > 2^40, n or I < 1 or > 2^18, E < 1 or > 1024, k < 1 or > 64,

@@ -929,7 +929,8 @@ def route(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: Optional
     scoring "softmax" chooses by the logits; "sigmoid" by sigmoid(logit) + bias, where the bias (E,) float32 acts on the
     choice alone. The weights are the scores of the chosen, divided by their sum with renormalize, times scale. Experts
     come in falling order, the lowest index first among equals; a logit of -inf or NaN is never chosen, and slots left
-    over hold id -1 and weight 0, which experts() skips. E up to 1024, k up to 64.
+    over hold id -1 and weight 0, which experts() skips. E up to 1024, k up to 64. The choice is among all experts: one that is
+    limited to some groups of them first is not formed (logits masked with -inf leave the others).
     """
     dev = _device_of(logits, "logits")
     ldl = _rows(logits, "logits", _WIDE, dev)

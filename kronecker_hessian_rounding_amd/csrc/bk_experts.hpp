@@ -16,8 +16,8 @@
 // No result depends on the order within a list.
 //
 // Few tokens are bound by the codes' way from HBM: 16 tokens through all of 8 experts of 4096 x 14336 (4 bits, 0.74 GB with
-// scales) take 168 us, 4.4 TB/s; one token through 6 experts of 2048 x 1408 (26 MB) 16 with the router's choice, most of it
-// waits in a row (ids, codes, sums; the same again for the second product). By way of the plan that took 36. Many are bound
+// scales) take 179 us, 4.1 TB/s; one token through 6 experts of 2048 x 1408 (26 MB) 16.5 with the router's choice, most of
+// it waits in a row (ids, codes, sums; the same again for the second product). By way of the plan that took 36. Many are bound
 // by vector instructions (codes to operands, scaling) beside the matrix cores: see the kernels.
 #pragma once
 
@@ -285,8 +285,8 @@ __global__ __launch_bounds__(64 * NW) void k_experts_first_few(FewArgs e) {
 // those of as many workgroups: `all` together, a power of two) share the chunks. Chunk c of expert i is wave (i nc + c) % all's, and
 // a wave takes the experts in the order of their numbers, so that a token's sums do not depend on what other tokens name. (One token
 // alone: slot in place of i, which spreads the chunks evenly.) Each wave stages h's pieces for its next PF chunks in LDS of its own,
-// as few_products does x: a token that does not name the expert has zeros there. 16 tokens, 8 experts of 4096 x 14336: 65
-// us for 0.25 GB, 3.9 TB/s; one token, 6 of 2048 x 1408: 6.8 us.
+// as few_products does x: a token that does not name the expert has zeros there. 16 tokens, 8 experts of 4096 x 14336: 76
+// us for 0.25 GB, 3.3 TB/s (vector instructions 46 % of it, matrix cores 24 %); one token, 6 of 2048 x 1408: 6.5 us.
 template <int PF, int TB>
 struct SecondShape {
     static constexpr int NP = kPieces;
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second_few(FewArgs e, int s
     };
     const auto enter = [&](At& p) __attribute__((always_inline)) {  // the wave's first chunk of a slot, if it has one
         p.id = __builtin_amdgcn_readlane(window, p.slot & 63);
-        p.chunk = (wave - p.id * nc) & (all - 1);
+        p.chunk = (int)(((uint32_t)wave - (uint32_t)p.id * (uint32_t)nc) & (uint32_t)(all - 1));
     };
     const auto settle = [&](At p) __attribute__((always_inline)) {
         if constexpr (TB == 1) {  // (at most 64 slots)
@@ -534,6 +534,7 @@ void launch_second_few(const FewArgs& e, int splits, int tiles, void* y, int yty
     else if (e.T <= 8) launch_second_tokens<W, FS, 8>(e, splits, tiles, y, ytype, ldy, stream);
     else launch_second_tokens<W, FS, 16>(e, splits, tiles, y, ytype, ldy, stream);
 }
+
 // ---------------------------------------------------------------- more tokens
 // The list's tiles hold at most 16 tokens where an expert has about as few (few_products), else as many as a workgroup of
 // mm_products takes.
@@ -613,8 +614,8 @@ __global__ __launch_bounds__(64 * NW) void k_experts_second(ExpertArgs e) {
     }
 }
 
-// 16 RW rows of G and of U (and so of h) by 16 NT tokens. int8, 512 tokens of 4 in 32 experts of 2048 x 1408: 48 us with 64
-// rows by 64 tokens (0.49 PFLOP/s); with 128 rows 68, 32 rows 61, columns split over waves 67 to 79, 128 tokens 58 to 64.
+// 16 RW rows of G and of U (and so of h) by 16 NT tokens. int8, 512 tokens of 4 in 32 experts of 2048 x 1408: 50 us with 64
+// rows by 64 tokens (0.47 PFLOP/s); with 128 rows 68, 32 rows 61, columns split over waves 67 to 79, 128 tokens 58 to 64.
 // Vector instructions are busy 46 % of it, the matrix cores 13 %, with 1.8 waves a SIMD.
 template <int MATH, int W, int FS, int NT, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_first_mm(ExpertArgs e) {
@@ -652,7 +653,8 @@ __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2)
 }
 
 // 16 R RW rows of D by 16 NT tokens. At the sizes above, int8 tokens: 110 us for the call with 128 rows by 32 tokens; 256 rows 116,
-// 64 rows 137; 64 tokens by 128 rows 141, by 256 rows 124; 16 tokens by 128 rows 111; 64 rows a wave spill.
+// 64 rows 137; 64 tokens by 128 rows 141, by 256 rows 124; 16 tokens by 128 rows 111; 64 rows a wave spill. Alone 62 us: vector
+// instructions 38 %, matrix cores 30 %, 1.8 waves a SIMD.
 template <int W, int FS, int NT, int R, int KS, int RW, int CH>
 __global__ __launch_bounds__(64 * KS * RW) __attribute__((amdgpu_waves_per_eu(2))) void k_experts_second_mm(ExpertArgs e) {
     constexpr int kThreads = 64 * KS * RW, kRows = 16 * R * RW, kPitch = kRows + 4;

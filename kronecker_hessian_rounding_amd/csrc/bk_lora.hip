@@ -66,8 +66,8 @@ int launch_lora(const void* x, int xtype, int64_t T, int64_t n, int64_t ldx, con
             a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most_splits(a.T), blocks / kDownWaves));
             a.slots = (int)std::max<int64_t>(1, std::min<int64_t>({16, R, 4 * cus / ((a.T + kDownTokens - 1) / kDownTokens * a.splits)}));
             const int64_t whole = m / kUpRows * kUpRows;
-            // Four workgroups a unit (4096 tokens, 14336 rows, rank 64: 66 us, with two 78, with eight 68), of two row blocks
-            // at least, since each forms its tokens' operands (512 tokens: 27.6 us for both launches, with one row block 35).
+            // Four workgroups a unit (4096 tokens, 14336 rows, rank 64, with two pieces a value: 66 us, with two workgroups 78, with
+            // eight 68), of two row blocks at least, since each forms its tokens' operands (512 tokens: 27.6 us for both launches, with one row block 35).
             // Slots share a tile's adapters over workgroups where ranges alone leave units idle.
             ranges = std::max<int64_t>(1, std::min(4 * cus / ((a.T + kUpTokens - 1) / kUpTokens), whole / (2 * kUpRows)));
             a.rows_each = std::max<int64_t>(1, (whole / kUpRows + ranges - 1) / ranges) * kUpRows;
