@@ -364,3 +364,10 @@ def test_second_product_grids(T, bits, group, n, I):
 def test_tokens_of_an_expert(T, E, k, dtype):
     """Around the border between list tiles of 16 and of 64 tokens, several tiles an expert."""
     check(T, E, k, 300, 200, 4, 128, 4, 64, dtype, F32, seed=T)
+
+
+@pytest.mark.parametrize("n", [700, 2000, 6000])
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 32), (2, 0), (1, 64)])
+def test_list_tiles_of_16(n, bits, group):
+    """The second product's workgroups of 8, 4 and 2 waves, by the number of rows."""
+    check(24, 8, 2, n, 300, 4, 128, bits, group, BF16, F32, none=0.1, seed=n)

@@ -138,7 +138,8 @@ def test_activation_is_formed_in_fp32(T, act):
 
 
 @pytest.mark.parametrize("T,E,k,n,I", [(2, 9, 3, 300, 200), (4, 30, 4, 200, 1400), (7, 12, 4, 513, 300), (8, 64, 6, 130, 700), (16, 6, 2, 300, 1000),
-                                       (16, 64, 8, 96, 400), (9, 8, 4, 4112, 4000), (30, 9, 3, 200, 300), (200, 4, 2, 130, 300)])
+                                       (16, 64, 8, 96, 400), (9, 8, 4, 4112, 4000), (30, 9, 3, 200, 300), (200, 4, 2, 130, 300),
+                                       (16, 200, 8, 96, 300), (12, 1000, 40, 64, 140), (3, 400, 30, 70, 260)])
 def test_experts_other_rows_do_not_matter(T, E, k, n, I):
     """Every token's result stays bit for bit, in fp32, when the other rows and the experts that they name change."""
     g = gen(T + E)
